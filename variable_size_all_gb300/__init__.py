@@ -23,6 +23,9 @@ __all__ = [
     "COMBINE_WORKSPACE_BYTES",
     "OK", "ERR_INVALID_ARG", "ERR_UNSUPPORTED", "ERR_CUDA", "ERR_BAD_SPLITS", "ERR_TIMEOUT",
     "PATH_AUTO", "PATH_VECTOR", "PATH_BULK", "PATH_STAGED", "MAX_RANKS",
+    "a2av_route", "a2av_route_backward", "a2av_expert_matmul", "a2av_expert_matmul_backward",
+    "a2av_expert_matmul_workspace_bytes", "a2av_combine_weighted", "a2av_combine_weighted_backward",
+    "A2avRoute", "A2avExpert", "F32", "BF16", "F16", "MAX_TOPK", "MAX_ROUTE_GROUPS",
 ]
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_BAD_SPLITS, ERR_TIMEOUT = 0, -1, -2, -3, -4, -5
@@ -32,6 +35,10 @@ PATH_AUTO, PATH_VECTOR, PATH_BULK, PATH_STAGED = 0, 1, 2, 3
 MAX_RANKS = 32
 MAX_EXCHANGES = 4
 COMBINE_WORKSPACE_BYTES = 256 + 16 * 32 * 32
+F32, BF16, F16 = 0, 1, 2
+MAX_TOPK, MAX_ROUTE_GROUPS = 32, 32
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 
 _lib = None
 
@@ -43,6 +50,20 @@ class A2avExchange(ctypes.Structure):
                 ("out_ptrs", ctypes.POINTER(ctypes.c_void_p)),
                 ("out_splits_offsets_dev", ctypes.c_void_p),
                 ("row_bytes", ctypes.c_int64)]
+
+
+class A2avRoute(ctypes.Structure):
+    """``a2av_route_t``: how ``a2av_route`` chooses."""
+    _fields_ = [(n, ctypes.c_int) for n in ("experts", "topk", "dtype", "score", "groups",
+                                            "top_groups", "group_top", "renormalise")]
+    _fields_.append(("scale", ctypes.c_float))
+
+
+class A2avExpert(ctypes.Structure):
+    """``a2av_expert_t``: the shape of ``a2av_expert_matmul``."""
+    _fields_ = [("experts_per_peer", ctypes.c_int), ("in_features", ctypes.c_int64),
+                ("out_features", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("activation", ctypes.c_int), ("gated", ctypes.c_int)]
 
 
 class A2avError(RuntimeError):
@@ -86,9 +107,23 @@ def load():
     lib.a2av_error_string.argtypes = [ci]
     lib.a2av_error_string.restype = ctypes.c_char_p
     lib.a2av_version.argtypes = []
+    route_p, expert_p = ctypes.POINTER(A2avRoute), ctypes.POINTER(A2avExpert)
+    lib.a2av_route.argtypes = [vp, route_p, pp, i64p, vp, pp, pp, vp, vp]
+    lib.a2av_route_backward.argtypes = [vp, route_p, pp, i64p, pp, pp, pp, vp]
+    lib.a2av_expert_matmul.argtypes = [vp, expert_p, pp, i64p, vp, pp, pp, pp, pp, pp, vp]
+    lib.a2av_expert_matmul_backward.argtypes = [vp, expert_p, pp, i64p, vp, pp, pp, pp, pp, pp, pp,
+                                                vp, i64, vp]
+    lib.a2av_expert_matmul_workspace_bytes.argtypes = [ci, expert_p, i64]
+    lib.a2av_expert_matmul_workspace_bytes.restype = i64
+    lib.a2av_combine_weighted.argtypes = [vp, ci, ci, i64, ci, pp, i64p, vp, pp, pp, pp, i64p, pp, pp,
+                                          vp]
+    lib.a2av_combine_weighted_backward.argtypes = [vp, ci, ci, i64, ci, pp, i64p, vp, pp, pp, pp,
+                                                   i64p, pp, pp, pp, vp]
     for f in ("a2av_create", "a2av_run", "a2av_combine", "a2av_status", "a2av_destroy", "a2av_set_path",
               "a2av_set_grid", "a2av_last_launch", "a2av_version", "a2av_run_noalloc",
-              "a2av_run_multi"):
+              "a2av_run_multi", "a2av_route", "a2av_route_backward", "a2av_expert_matmul",
+              "a2av_expert_matmul_backward", "a2av_combine_weighted",
+              "a2av_combine_weighted_backward"):
         getattr(lib, f).restype = ci
     _lib = lib
     return lib
@@ -237,6 +272,83 @@ def a2av_dispatch(handle, keys_per_peer: int, rows_ptrs, rows_per_rank, src_row_
         _ptr_array(sorted_pos_ptrs), ctypes.c_void_p(int(in_splits_dev) or None),
         int(row_bytes), ctypes.c_void_p(int(workspace) or None), int(workspace_bytes),
         ctypes.c_void_p(int(stream) or None))
+
+
+def _address(p):
+    return ctypes.c_void_p(int(p) if p else None)
+
+
+def _optional_ptrs(ptrs):
+    return None if ptrs is None else _ptr_array(ptrs)
+
+
+def a2av_route(handle, route: A2avRoute, logits_ptrs, tokens_per_rank, bias: int, key_ptrs,
+               weight_ptrs, counts: int, stream: int = 0) -> int:
+    """Raw routing (include/a2av_moe.h): integer device addresses, host lists of counts."""
+    return load().a2av_route(handle, ctypes.byref(route), _ptr_array(logits_ptrs),
+                             _i64_array(tokens_per_rank), _address(bias), _ptr_array(key_ptrs),
+                             _ptr_array(weight_ptrs), _address(counts), _address(stream))
+
+
+def a2av_route_backward(handle, route: A2avRoute, logits_ptrs, tokens_per_rank, key_ptrs,
+                        d_weight_ptrs, d_logits_ptrs, stream: int = 0) -> int:
+    """Raw gradient of the routing weights."""
+    return load().a2av_route_backward(handle, ctypes.byref(route), _ptr_array(logits_ptrs),
+                                      _i64_array(tokens_per_rank), _ptr_array(key_ptrs),
+                                      _ptr_array(d_weight_ptrs), _ptr_array(d_logits_ptrs),
+                                      _address(stream))
+
+
+def a2av_expert_matmul(handle, shape: A2avExpert, rows_ptrs, rows_per_peer, counts: int,
+                       weight_ptrs, bias_ptrs, residual_ptrs, out_ptrs, pre_ptrs,
+                       stream: int = 0) -> int:
+    """Raw experts' product: integer device addresses, lists (or None) per peer."""
+    return load().a2av_expert_matmul(
+        handle, ctypes.byref(shape), _ptr_array(rows_ptrs), _i64_array(rows_per_peer),
+        _address(counts), _ptr_array(weight_ptrs), _optional_ptrs(bias_ptrs),
+        _optional_ptrs(residual_ptrs), _ptr_array(out_ptrs), _optional_ptrs(pre_ptrs),
+        _address(stream))
+
+
+def a2av_expert_matmul_workspace_bytes(world_size: int, shape: A2avExpert, total_rows: int) -> int:
+    return load().a2av_expert_matmul_workspace_bytes(int(world_size), ctypes.byref(shape),
+                                                     int(total_rows))
+
+
+def a2av_expert_matmul_backward(handle, shape: A2avExpert, rows_ptrs, rows_per_peer, counts: int,
+                                weight_ptrs, pre_ptrs, d_out_ptrs, d_rows_ptrs, d_weight_ptrs,
+                                d_bias_ptrs, workspace: int, workspace_bytes: int,
+                                stream: int = 0) -> int:
+    """Raw gradients of the experts' product."""
+    return load().a2av_expert_matmul_backward(
+        handle, ctypes.byref(shape), _ptr_array(rows_ptrs), _i64_array(rows_per_peer),
+        _address(counts), _ptr_array(weight_ptrs), _optional_ptrs(pre_ptrs),
+        _ptr_array(d_out_ptrs), _optional_ptrs(d_rows_ptrs), _optional_ptrs(d_weight_ptrs),
+        _optional_ptrs(d_bias_ptrs), _address(workspace), int(workspace_bytes), _address(stream))
+
+
+def a2av_combine_weighted(handle, keys_per_peer: int, topk: int, hidden: int, dtype: int,
+                          peer_ptrs, rows_per_peer, in_splits_dev: int, key_ptrs, sorted_pos_ptrs,
+                          weight_ptrs, tokens_per_rank, residual_ptrs, out_ptrs,
+                          stream: int = 0) -> int:
+    """Raw weighted combine: integer device addresses, lists (or None) per rank."""
+    return load().a2av_combine_weighted(
+        handle, int(keys_per_peer), int(topk), int(hidden), int(dtype), _ptr_array(peer_ptrs),
+        _i64_array(rows_per_peer), _address(in_splits_dev), _ptr_array(key_ptrs), _ptr_array(sorted_pos_ptrs),
+        _optional_ptrs(weight_ptrs), _i64_array(tokens_per_rank), _optional_ptrs(residual_ptrs),
+        _ptr_array(out_ptrs), _address(stream))
+
+
+def a2av_combine_weighted_backward(handle, keys_per_peer: int, topk: int, hidden: int, dtype: int,
+                                   peer_ptrs, rows_per_peer, in_splits_dev: int, key_ptrs,
+                                   sorted_pos_ptrs, weight_ptrs, tokens_per_rank, d_out_ptrs, d_peer_ptrs,
+                                   d_weight_ptrs, stream: int = 0) -> int:
+    """Raw gradients of the weighted combine."""
+    return load().a2av_combine_weighted_backward(
+        handle, int(keys_per_peer), int(topk), int(hidden), int(dtype), _optional_ptrs(peer_ptrs),
+        _i64_array(rows_per_peer), _address(in_splits_dev), _ptr_array(key_ptrs), _ptr_array(sorted_pos_ptrs),
+        _optional_ptrs(weight_ptrs), _i64_array(tokens_per_rank), _ptr_array(d_out_ptrs),
+        _optional_ptrs(d_peer_ptrs), _optional_ptrs(d_weight_ptrs), _address(stream))
 
 
 # --------------------------------------------------------- torch-facing --
@@ -520,6 +632,291 @@ class A2av:
             keep = (peers, in_splits, keys, sorted_pos, item_out, workspace)
             return BoundCall(self, load().a2av_combine_items, "a2av_combine_items", args, 11, keep)
         self._check(load().a2av_combine_items(*args), "a2av_combine_items")
+
+    # ------------------------------------------- the MoE layer's operators --
+    def _dtype(self, tensors, name, allowed):
+        """The element type that a list's non-empty tensors share, and its code."""
+        import torch
+        codes = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+        for t in tensors:
+            if t is not None and t.numel():
+                if codes.get(t.dtype) not in allowed:
+                    raise ValueError(f"{name}: {t.dtype} is not supported")
+                return t.dtype, codes[t.dtype]
+        return None, allowed[-1]
+
+    def _list(self, tensors, name, dtype, shapes=None):
+        """Pointer array of W contiguous CUDA tensors of a type.  ``shapes``:
+        the expected shape of each (a tensor without elements may be None)."""
+        W = self.world_size
+        if len(tensors) != W:
+            raise ValueError(f"{name}: expected {W} tensors, got {len(tensors)}")
+        arr = (ctypes.c_void_p * W)()
+        for r, t in enumerate(tensors):
+            if t is None:
+                if shapes is not None and 0 not in shapes[r]:
+                    raise ValueError(f"{name}[{r}] is missing")
+                continue
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous CUDA tensors")
+            if shapes is not None and t.shape != shapes[r]:
+                raise ValueError(f"{name}[{r}] must have shape {tuple(shapes[r])}, "
+                                 f"not {tuple(t.shape)}")
+            if t.numel():
+                if t.dtype != dtype:
+                    raise ValueError(f"{name} must be {dtype} tensors, not {t.dtype}")
+                arr[r] = t.data_ptr()
+        return arr
+
+    def _call(self, what, args, keep, bind):
+        fn = getattr(load(), what)
+        if bind:
+            return BoundCall(self, fn, what, args, len(args) - 1, keep)
+        rc = fn(*args)
+        if rc != OK:
+            raise A2avError(rc, what)
+
+    def _tokens(self, tensors, name):
+        """Rows and the common second dimension of W [rows, n] tensors."""
+        if len(tensors) != self.world_size:
+            raise ValueError(f"{name}: expected {self.world_size} tensors, got {len(tensors)}")
+        rows, width = [], None
+        for t in tensors:
+            if t is None:
+                rows.append(0)
+                continue
+            if t.dim() != 2 or (width is not None and t.shape[1] != width):
+                raise ValueError(f"{name} must be 2-D tensors of one width")
+            width = t.shape[1]
+            rows.append(t.shape[0])
+        if width is None:
+            raise ValueError(f"{name}: every tensor is missing")
+        return rows, width
+
+    def _route_args(self, logits, keys, weights, weights_name, topk, score, groups, top_groups,
+                    group_top, renormalise, scale):
+        import torch
+        if score not in _SCORES:
+            raise ValueError(f"score must be one of {sorted(_SCORES)}")
+        rows, E = self._tokens(logits, "logits")
+        dtype, code = self._dtype(logits, "logits", (F32, BF16, F16))
+        route = A2avRoute(E, int(topk), code, _SCORES[score], int(groups), int(top_groups),
+                          int(group_top), int(bool(renormalise)), float(scale))
+        W = self.world_size
+        if not 1 <= route.topk <= E:
+            raise ValueError(f"topk must be in 1..{E}")
+        shapes = [(n, route.topk) for n in rows]
+        return (dtype, ctypes.byref(route), self._list(logits, "logits", dtype),
+                (ctypes.c_int64 * W)(*rows), self._list(keys, "keys", torch.int32, shapes),
+                self._list(weights, weights_name, torch.float32, shapes), rows, E)
+
+    def route(self, logits, keys, weights, topk: int, counts=None, bias=None,
+              score: str = "softmax", groups: int = 1, top_groups: int = 1, group_top: int = 1,
+              renormalise: bool = True, scale: float = 1.0, stream=None, _bind=False):
+        """Routing to experts (see include/a2av_moe.h, a2av_route).
+
+        ``logits[r]``: rank r's [T, E] CUDA tensor (float32, bfloat16 or
+        float16).  Written: ``keys[r]`` int32 [T, topk], the keys of a
+        dispatch; ``weights[r]`` float32 [T, topk]; ``counts`` (optional)
+        int64 [W, E], rank r's items for each expert.  ``bias``: optional
+        float32 [E], added to the scores for the choice alone."""
+        import torch
+        dtype, cfg, x, n, k, w, rows, E = self._route_args(
+            logits, keys, weights, "weights", topk, score, groups, top_groups, group_top,
+            renormalise, scale)
+        W = self.world_size
+        if bias is not None and (bias.dtype != torch.float32 or not bias.is_cuda
+                                 or bias.shape != (E,) or not bias.is_contiguous()):
+            raise ValueError(f"bias must be a contiguous CUDA float32 [{E}] tensor")
+        if counts is not None:
+            self._matrix(counts, (W, E), "counts")
+        args = [self.handle, cfg, x, n, _address(None if bias is None else bias.data_ptr()), k, w,
+                _address(None if counts is None else counts.data_ptr()),
+                _address(self._stream(stream))]
+        return self._call("a2av_route", args, (logits, keys, weights, counts, bias), _bind)
+
+    def bind_route(self, logits, keys, weights, topk: int, **options) -> BoundCall:
+        """``route`` marshalled once (see BoundCall)."""
+        return self.route(logits, keys, weights, topk, **options, _bind=True)
+
+    def route_backward(self, logits, keys, d_weights, d_logits, topk: int, score: str = "softmax",
+                       renormalise: bool = True, scale: float = 1.0, stream=None):
+        """The gradient of ``route``'s weights: ``d_logits[r]`` [T, E], of the
+        logits' type, from ``d_weights[r]`` float32 [T, topk] and the keys that
+        ``route`` wrote (see include/a2av_moe.h, a2av_route_backward)."""
+        dtype, cfg, x, n, k, w, rows, E = self._route_args(
+            logits, keys, d_weights, "d_weights", topk, score, 1, 1, 1, renormalise, scale)
+        d = self._list(d_logits, "d_logits", dtype, [(m, E) for m in rows])
+        self._call("a2av_route_backward",
+                   [self.handle, cfg, x, n, k, w, d, _address(self._stream(stream))], None, False)
+
+    def _expert_args(self, rows, counts, weights, out, out_name, activation, gated):
+        """The shape, the common arguments and what the others are checked by."""
+        if activation not in _ACTIVATIONS:
+            raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}")
+        W = self.world_size
+        n, D = self._tokens(rows, "rows")
+        n_out, N = self._tokens(out, out_name)
+        if n_out != n:
+            raise ValueError(f"rows and {out_name} must have the same number of rows")
+        if len(weights) != W or any(w is None or w.dim() != 3 for w in weights):
+            raise ValueError(f"weights must be {W} tensors [experts, features, {D}]")
+        K, Z = weights[0].shape[0], 2 * N if gated else N
+        dtype, code = self._dtype(weights, "weights", (F16, BF16))
+        self._matrix(counts, (W, W * K), "counts")
+        shape = A2avExpert(K, D, N, code, _ACTIVATIONS[activation], int(bool(gated)))
+        return (shape, self._list(rows, "rows", dtype), (ctypes.c_int64 * W)(*n),
+                ctypes.c_void_p(counts.data_ptr()),
+                self._list(weights, "weights", dtype, [(K, Z, D)] * W), n, K, Z, dtype)
+
+    def expert_matmul(self, rows, counts, weights, outputs, activation: str = "none",
+                      gated: bool = False, bias=None, residual=None, pre=None, stream=None,
+                      _bind=False):
+        """One product per expert (see include/a2av_moe.h, a2av_expert_matmul).
+
+        ``rows[p]``: peer p's [rows, D] bfloat16 or float16 tensor in the
+        dispatch's order; ``counts`` int64 [W, W * K] as ``route`` writes it;
+        ``weights[p]`` [K, Z, D] with Z = N, or 2 N when ``gated``; written:
+        ``outputs[p]`` [rows, N] and, when given, ``pre[p]`` [rows, Z].
+        ``bias[p]`` [K, Z] and ``residual[p]`` [rows, N] are optional."""
+        shape, x, n, c, w, n_rows, K, Z, dtype = self._expert_args(
+            rows, counts, weights, outputs, "outputs", activation, gated)
+        N, W = shape.out_features, self.world_size
+        by_row = [(m, N) for m in n_rows]
+        args = [self.handle, ctypes.byref(shape), x, n, c, w,
+                None if bias is None else self._list(bias, "bias", dtype, [(K, Z)] * W),
+                None if residual is None else self._list(residual, "residual", dtype, by_row),
+                self._list(outputs, "outputs", dtype, by_row),
+                None if pre is None else self._list(pre, "pre", dtype, [(m, Z) for m in n_rows]),
+                _address(self._stream(stream))]
+        keep = (rows, counts, weights, outputs, bias, residual, pre)
+        return self._call("a2av_expert_matmul", args, keep, _bind)
+
+    def bind_expert_matmul(self, rows, counts, weights, outputs, **options) -> BoundCall:
+        """``expert_matmul`` marshalled once (see BoundCall): new counts and rows
+        are allowed within the buffers' row counts."""
+        return self.expert_matmul(rows, counts, weights, outputs, **options, _bind=True)
+
+    def expert_matmul_backward(self, rows, counts, weights, d_outputs, d_rows=None, d_weights=None,
+                               d_bias=None, pre=None, activation: str = "none",
+                               gated: bool = False, workspace=None, stream=None):
+        """The gradients of ``expert_matmul`` (see include/a2av_moe.h,
+        a2av_expert_matmul_backward): any of ``d_rows``, ``d_weights`` and
+        ``d_bias``, of the shapes of ``rows``, ``weights`` and the bias.
+        ``pre`` is what the forward call wrote, needed with an activation or a
+        gate.  ``workspace`` defaults to a buffer the object keeps."""
+        import torch
+        shape, x, n, c, w, n_rows, K, Z, dtype = self._expert_args(
+            rows, counts, weights, d_outputs, "d_outputs", activation, gated)
+        D, N, W = shape.in_features, shape.out_features, self.world_size
+        need = a2av_expert_matmul_workspace_bytes(W, shape, sum(n_rows))
+        if need < 0:
+            raise A2avError(ERR_UNSUPPORTED, "a2av_expert_matmul_workspace_bytes")
+        activated = activation != "none" or bool(gated)
+        if activated and pre is None:
+            raise ValueError("an activation's gradient needs pre")
+        if workspace is None and need:
+            workspace = getattr(self, "_expert_workspace", None)
+            if workspace is None or workspace.numel() < need:
+                workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
+                self._expert_workspace = workspace
+        each = [(K, Z, D)] * W
+        args = [self.handle, ctypes.byref(shape), x, n, c, w,
+                None if not activated else self._list(pre, "pre", dtype, [(m, Z) for m in n_rows]),
+                self._list(d_outputs, "d_outputs", dtype, [(m, N) for m in n_rows]),
+                None if d_rows is None else self._list(d_rows, "d_rows", dtype,
+                                                       [(m, D) for m in n_rows]),
+                None if d_weights is None else self._list(d_weights, "d_weights", dtype, each),
+                None if d_bias is None else self._list(d_bias, "d_bias", dtype, [(K, Z)] * W),
+                _address(workspace.data_ptr() if need else None),
+                int(workspace.numel()) if need else 0, _address(self._stream(stream))]
+        self._call("a2av_expert_matmul_backward", args, None, False)
+
+    def _weighted_args(self, in_splits, keys, sorted_pos, keys_per_peer, token_rows, name):
+        """What both directions of the weighted combine share."""
+        import torch
+        W = self.world_size
+        sp = self._matrix(in_splits, (W, W), "in_splits")
+        n, H = self._tokens(token_rows, name)
+        dtype, code = self._dtype(token_rows, name, (F32, BF16, F16))
+        k = None
+        for t, m in zip(keys, n):
+            if t is not None and m:
+                k = t.numel() // m
+                break
+        k = k or 1
+        items = [(m * k,) for m in n]
+        for ts, what in ((keys, "keys"), (sorted_pos, "sorted_pos")):
+            if len(ts) != W or any((0 if t is None else t.numel()) != m for t, (m,) in zip(ts, items)):
+                raise ValueError(f"{what} must have one entry per item")
+        return (int(keys_per_peer), k, H, code, sp, self._list(keys, "keys", torch.int32),
+                self._list(sorted_pos, "sorted_pos", torch.int64), (ctypes.c_int64 * W)(*n),
+                n, H, dtype)
+
+    def _item_weights(self, weights, name, n, k):
+        import torch
+        return self._list(weights, name, torch.float32, [(m, k) for m in n])
+
+    def combine_weighted(self, peers, in_splits, keys, sorted_pos, keys_per_peer: int, weights,
+                         outputs, residual=None, stream=None, _bind=False):
+        """The weighted return path (see include/a2av_moe.h, a2av_combine_weighted).
+
+        ``peers[p]``: peer p's rows, [rows, H] in the dispatch's layout;
+        ``in_splits``, ``keys`` and ``sorted_pos`` as the dispatch took or
+        wrote them (topk items a token); ``weights[r]`` float32 [T, topk], or
+        None for 1; ``outputs[r]`` and the optional ``residual[r]`` [T, H]."""
+        K, k, H, code, sp, ka, pa, na, n, H, dtype = self._weighted_args(
+            in_splits, keys, sorted_pos, keys_per_peer, outputs, "outputs")
+        shapes = [(m, H) for m in n]
+        held, (peer_arr,) = self._peer_rows((("peers", peers),), dtype, H)
+        args = [self.handle, K, k, H, code, peer_arr, held, sp, ka, pa,
+                None if weights is None else self._item_weights(weights, "weights", n, k), na,
+                None if residual is None else self._list(residual, "residual", dtype, shapes),
+                self._list(outputs, "outputs", dtype, shapes), _address(self._stream(stream))]
+        keep = (peers, in_splits, keys, sorted_pos, weights, outputs, residual)
+        return self._call("a2av_combine_weighted", args, keep, _bind)
+
+    def bind_combine_weighted(self, peers, in_splits, keys, sorted_pos, keys_per_peer: int,
+                              weights, outputs, **options) -> BoundCall:
+        """``combine_weighted`` marshalled once (see BoundCall)."""
+        return self.combine_weighted(peers, in_splits, keys, sorted_pos, keys_per_peer, weights,
+                                     outputs, **options, _bind=True)
+
+    def _peer_rows(self, lists, dtype, H):
+        """Rows of the peers' buffers, and the pointer array of each list of them."""
+        held, arrays = None, []
+        for name, ts in lists:
+            if ts is None:
+                arrays.append(None)
+                continue
+            if any(t is not None and (t.dim() != 2 or t.shape[1] != H) for t in ts):
+                raise ValueError(f"{name} must be [rows, {H}] tensors")
+            rows = [0 if t is None else t.shape[0] for t in ts]
+            if held is not None and rows != held:
+                raise ValueError("peers and d_peers must have the same number of rows")
+            held = rows
+            arrays.append(self._list(ts, name, dtype))
+        return _i64_array(held), arrays
+
+    def combine_weighted_backward(self, peers, in_splits, keys, sorted_pos, keys_per_peer: int,
+                                  weights, d_outputs, d_peers=None, d_weights=None, stream=None):
+        """The gradients of ``combine_weighted`` (see include/a2av_moe.h,
+        a2av_combine_weighted_backward): ``d_peers[p]`` in the peers' layout,
+        ``d_weights[r]`` float32 [T, topk]; either may be None (``peers`` too,
+        without ``d_weights``)."""
+        K, k, H, code, sp, ka, pa, na, n, H, dtype = self._weighted_args(
+            in_splits, keys, sorted_pos, keys_per_peer, d_outputs, "d_outputs")
+        if (d_peers is None and d_weights is None) or (d_weights is not None and peers is None):
+            raise ValueError("d_peers, or d_weights with peers, must be given")
+        held, (peer_arr, d_peer_arr) = self._peer_rows((("peers", peers), ("d_peers", d_peers)),
+                                                       dtype, H)
+        args = [self.handle, K, k, H, code, peer_arr, held, sp, ka, pa,
+                None if weights is None else self._item_weights(weights, "weights", n, k), na,
+                self._list(d_outputs, "d_outputs", dtype, [(m, H) for m in n]),
+                d_peer_arr,
+                None if d_weights is None else self._item_weights(d_weights, "d_weights", n, k),
+                _address(self._stream(stream))]
+        self._call("a2av_combine_weighted_backward", args, None, False)
 
     def status(self, stream=None) -> int:
         rc, v = a2av_status(self.handle, self._stream(stream))

@@ -7,8 +7,10 @@ import subprocess
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCES = [os.path.join(PKG, "csrc", "a2av.cu"), os.path.join(PKG, "csrc", "dispatch.cu")]
-HEADERS = [os.path.join(PKG, "csrc", "a2av_device.cuh"), os.path.join(PKG, "csrc", "a2av_handle.h")]
+SOURCES = [os.path.join(PKG, "csrc", f) for f in ("a2av.cu", "dispatch.cu", "route.cu", "experts.cu",
+                                                  "weighted.cu")]
+HEADERS = [os.path.join(PKG, "csrc", f) for f in ("a2av_device.cuh", "a2av_handle.h",
+                                                  "moe_device.cuh", "experts.cuh")]
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "liba2av.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -29,7 +31,7 @@ def command(output: str = LIBRARY, extra=()) -> list:
 def stale(output: str = LIBRARY) -> bool:
     if not os.path.exists(output):
         return True
-    deps = SOURCES + HEADERS + [os.path.join(INCLUDE, "a2av.h"), __file__]
+    deps = SOURCES + HEADERS + [os.path.join(INCLUDE, f) for f in ("a2av.h", "a2av_moe.h")] + [__file__]
     return os.path.getmtime(output) < max(os.path.getmtime(d) for d in deps)
 
 

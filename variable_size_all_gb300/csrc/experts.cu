@@ -1,0 +1,397 @@
+// experts.cu -- one product per expert over the rows a dispatch delivered
+// (a2av_expert_matmul) and its gradients; the interface is in
+// include/a2av_moe.h.
+#include "experts.cuh"
+
+namespace {
+
+struct ExpertParams {
+  GroupParams g;
+  const void* x[kW];         // rows that are multiplied (forward: x; d_rows: dz)
+  const void* w[kW];         // [K][Z][D]
+  const void* bias[kW];
+  const void* residual[kW];
+  void* out[kW];
+  void* pre[kW];
+  const void* dy[kW];        // backward
+  const void* pre_in[kW];
+  void* dz[kW];
+  void* d_w[kW];
+  void* d_bias[kW];
+  long long D, N, Z;
+  int act, gated;
+};
+
+// ------------------------------------------------- products by plain FMAs --
+// For shapes and buffers that the tensor-core kernels' copies cannot take
+// (rows that are not multiples of 16 bytes, or not aligned to them).  64 x 64
+// tiles of the result, 16 of the contraction in shared memory at a time, 4 x 4
+// results a thread.
+constexpr int kTile = 64, kDepth = 16, kPlainThreads = 256;
+
+// out rows x features: sum over c of x[row][c] * w(feature, c), where
+// w(f, c) is at w[f * wf + c * wc] of the expert.  kGated: features f and
+// f + N together.
+template <typename T, bool kGated>
+__global__ void __launch_bounds__(kPlainThreads)
+    expert_plain_kernel(const __grid_constant__ ExpertParams P, long long C, long long F,
+                        long long wf, long long wc) {
+  chain();
+  __shared__ GroupTable g;
+  __shared__ float xs[kDepth][kTile + 1], ws[kGated ? 2 : 1][kDepth][kTile + 1];
+  const int nf = (int)((F + kTile - 1) / kTile);
+  if (!build_groups(P.g, g, kTile, nf)) return;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  for (long long tile = blockIdx.x; tile < g.tiles[g.entries]; tile += gridDim.x) {
+    const GroupTile gt = find_tile(P.g, g, tile, kTile, nf);
+    const long long f0 = gt.local % nf * kTile, m0 = gt.local / nf * kTile;
+    const T* x = static_cast<const T*>(P.x[gt.p]) + (gt.first + m0) * C;
+    const T* w = static_cast<const T*>(P.w[gt.p]) + (long long)gt.e * P.Z * P.D;
+    const int rows = (int)min((long long)kTile, gt.rows - m0);
+    float acc[kGated ? 2 : 1][4][4] = {};
+    for (long long c0 = 0; c0 < C; c0 += kDepth) {
+      for (int i = tid; i < kTile * kDepth; i += kPlainThreads) {
+        const int c = i % kDepth, m = i / kDepth;
+        xs[c][m] = m < rows && c0 + c < C ? to_float(x[(long long)m * C + c0 + c]) : 0.0f;
+        const int fc = wc == 1 ? i % kDepth : i / kTile, f = wc == 1 ? i / kDepth : i % kTile;
+        const bool in = f0 + f < F && c0 + fc < C;
+        const long long at = (f0 + f) * wf + (c0 + fc) * wc;
+        ws[0][fc][f] = in ? to_float(w[at]) : 0.0f;
+        if (kGated) ws[kGated ? 1 : 0][fc][f] = in ? to_float(w[at + P.N * wf]) : 0.0f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < kDepth; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[0][i][j] += xs[c][ty + 16 * i] * ws[0][c][tx + 16 * j];
+            if (kGated) acc[kGated ? 1 : 0][i][j] += xs[c][ty + 16 * i] * ws[kGated ? 1 : 0][c][tx + 16 * j];
+          }
+      __syncthreads();
+    }
+    const T* bias = P.bias[gt.p] != nullptr
+                        ? static_cast<const T*>(P.bias[gt.p]) + gt.e * P.Z : nullptr;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int m = ty + 16 * i;
+      if (m >= rows) continue;
+      const long long row = gt.first + m0 + m;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const long long f = f0 + tx + 16 * j;
+        if (f >= F) continue;
+        float z = acc[0][i][j] + (bias != nullptr ? to_float(bias[f]) : 0.0f);
+        float y;
+        if (P.pre[gt.p] != nullptr)
+          static_cast<T*>(P.pre[gt.p])[row * P.Z + f] = from_float<T>(z);
+        if (kGated) {
+          const float u = acc[kGated ? 1 : 0][i][j] + (bias != nullptr ? to_float(bias[P.N + f]) : 0.0f);
+          if (P.pre[gt.p] != nullptr)
+            static_cast<T*>(P.pre[gt.p])[row * P.Z + P.N + f] = from_float<T>(u);
+          y = act_fn(P.act, z) * u;
+        } else {
+          y = act_fn(P.act, z);
+        }
+        if (P.residual[gt.p] != nullptr)
+          y += to_float(static_cast<const T*>(P.residual[gt.p])[row * F + f]);
+        static_cast<T*>(P.out[gt.p])[row * F + f] = from_float<T>(y);
+      }
+    }
+  }
+}
+
+// d_w[e][z][d] = sum over the expert's rows of dz[row][z] * x[row][d].
+template <typename T>
+__global__ void __launch_bounds__(kPlainThreads)
+    expert_plain_wgrad_kernel(const __grid_constant__ ExpertParams P) {
+  chain();
+  __shared__ GroupTable g;
+  __shared__ float zs[kDepth][kTile + 1], xs[kDepth][kTile + 1];
+  if (!build_groups(P.g, g, kTile, 1)) return;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int W = P.g.W, K = P.g.K;
+  const long long nz = (P.Z + kTile - 1) / kTile, nd = (P.D + kTile - 1) / kTile;
+  for (long long tile = blockIdx.x; tile < (long long)W * K * nz * nd; tile += gridDim.x) {
+    const int pe = (int)(tile / (nz * nd)), p = pe / K, e = pe % K;
+    const long long z0 = tile / nd % nz * kTile, d0 = tile % nd * kTile;
+    const T* dz = static_cast<const T*>(P.dy[p]);
+    const T* x = static_cast<const T*>(P.x[p]);
+    float acc[4][4] = {};
+    for (int r = 0; r < W; ++r) {
+      int rows;
+      const long long first = find_group(P.g, g, (p * W + r) * K + e, &rows);
+      for (int m0 = 0; m0 < rows; m0 += kDepth) {
+        for (int i = tid; i < kTile * kDepth; i += kPlainThreads) {
+          const int c = i % kTile, m = i / kTile;
+          const long long row = first + m0 + m;
+          const bool in = m0 + m < rows;
+          zs[m][c] = in && z0 + c < P.Z ? to_float(dz[row * P.Z + z0 + c]) : 0.0f;
+          xs[m][c] = in && d0 + c < P.D ? to_float(x[row * P.D + d0 + c]) : 0.0f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < kDepth; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] += zs[m][ty + 16 * i] * xs[m][tx + 16 * j];
+        __syncthreads();
+      }
+    }
+    T* out = static_cast<T*>(P.d_w[p]) + (long long)e * P.Z * P.D;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const long long z = z0 + ty + 16 * i, d = d0 + tx + 16 * j;
+        if (z < P.Z && d < P.D) out[z * P.D + d] = from_float<T>(acc[i][j]);
+      }
+  }
+}
+
+// ---------------------------------------------- activation's gradient --
+// dz from dy and the saved pre-activations, an element (or N of them) a thread.
+template <typename T, int N>
+__global__ void __launch_bounds__(256)
+    expert_dz_kernel(const __grid_constant__ ExpertParams P) {
+  chain();
+  __shared__ GroupTable g;
+  if (!build_groups(P.g, g, 1, 1)) return;
+  using V = Vec<T, N>;
+  const long long nv = P.N / N;
+  for (int p = 0; p < P.g.W; ++p) {
+    const long long total = (g.peer_base[p + 1] - g.peer_base[p]) * nv;
+    const T* dy = static_cast<const T*>(P.dy[p]);
+    const T* pre = static_cast<const T*>(P.pre_in[p]);
+    T* dz = static_cast<T*>(P.dz[p]);
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total;
+         i += (long long)gridDim.x * blockDim.x) {
+      const long long row = i / nv, c = (i - row * nv) * N;
+      const V y = *reinterpret_cast<const V*>(dy + row * P.N + c);
+      const V z = *reinterpret_cast<const V*>(pre + row * P.Z + c);
+      V a, b;
+      if (P.gated) {
+        const V u = *reinterpret_cast<const V*>(pre + row * P.Z + P.N + c);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const float d = to_float(y.v[k]), zf = to_float(z.v[k]);
+          a.v[k] = from_float<T>(d * to_float(u.v[k]) * act_slope(P.act, zf));
+          b.v[k] = from_float<T>(d * act_fn(P.act, zf));
+        }
+        *reinterpret_cast<V*>(dz + row * P.Z + P.N + c) = b;
+      } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          a.v[k] = from_float<T>(to_float(y.v[k]) * act_slope(P.act, to_float(z.v[k])));
+      }
+      *reinterpret_cast<V*>(dz + row * P.Z + c) = a;
+    }
+  }
+}
+
+// d_bias[e][z]: a block takes 32 columns of an expert, its 8 warps every
+// eighth row; their sums are joined in the order of the warps.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    expert_dbias_kernel(const __grid_constant__ ExpertParams P) {
+  chain();
+  __shared__ GroupTable g;
+  __shared__ float part[8][32];
+  if (!build_groups(P.g, g, 1, 1)) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int W = P.g.W, K = P.g.K;
+  const long long nz = (P.Z + 31) / 32;
+  for (long long tile = blockIdx.x; tile < (long long)W * K * nz; tile += gridDim.x) {
+    const int pe = (int)(tile / nz), p = pe / K, e = pe % K;
+    const long long z = tile % nz * 32 + lane;
+    float sum = 0.0f;
+    for (int r = 0; r < W; ++r) {
+      int rows;
+      const long long first = find_group(P.g, g, (p * W + r) * K + e, &rows);
+      if (z < P.Z)
+        for (int m = warp; m < rows; m += 8)
+          sum += to_float(static_cast<const T*>(P.dy[p])[(first + m) * P.Z + z]);
+    }
+    part[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && z < P.Z) {
+      for (int w = 1; w < 8; ++w) sum += part[w][lane];
+      static_cast<T*>(P.d_bias[p])[e * P.Z + z] = from_float<T>(sum);
+    }
+    __syncthreads();
+  }
+}
+
+// ----------------------------------------------------------- host side --
+int shape_ok(const a2av_expert_t* c, int W) {
+  if (c == nullptr || c->experts_per_peer < 1 || c->in_features < 1 || c->out_features < 1 ||
+      (c->dtype != A2AV_BF16 && c->dtype != A2AV_F16) || c->activation < A2AV_ACT_NONE ||
+      c->activation > A2AV_ACT_SILU)
+    return A2AV_ERR_INVALID_ARG;
+  if ((long long)W * c->experts_per_peer > A2AV_MAX_DISPATCH_KEYS ||
+      c->in_features > (1 << 24) || c->out_features > (c->gated ? 1 << 23 : 1 << 24))
+    return A2AV_ERR_UNSUPPORTED;
+  return A2AV_OK;
+}
+
+// Copies a list of W pointers (`need`: rows or experts of peer p want one).
+bool take(const void** to, const void* const* from, int W, const int64_t* rows, int size) {
+  for (int p = 0; p < W; ++p) {
+    to[p] = from != nullptr && (rows == nullptr || rows[p] > 0) ? from[p] : nullptr;
+    if (from != nullptr && (rows == nullptr || rows[p] > 0) && to[p] == nullptr) return false;
+    if (!aligned_to(to[p], size)) return false;
+  }
+  return true;
+}
+
+bool take(void** to, void* const* from, int W, const int64_t* rows, int size) {
+  return take(const_cast<const void**>(to), from, W, rows, size);
+}
+
+int expert_params(a2av_handle* h, const a2av_expert_t* c, const int64_t* rows_per_peer,
+                  const int64_t* counts, ExpertParams* P) {
+  if (h == nullptr || rows_per_peer == nullptr || counts == nullptr || !aligned_to(counts, 8))
+    return A2AV_ERR_INVALID_ARG;
+  const int rc = shape_ok(c, h->W);
+  if (rc != A2AV_OK) return rc;
+  std::memset(P, 0, sizeof(*P));
+  for (int p = 0; p < h->W; ++p) {
+    if (rows_per_peer[p] < 0) return A2AV_ERR_INVALID_ARG;
+    if (rows_per_peer[p] > kMaxCount) return A2AV_ERR_UNSUPPORTED;
+    P->g.cap[p] = rows_per_peer[p];
+  }
+  P->g.counts = reinterpret_cast<const long long*>(counts);
+  P->g.status = h->d_status;
+  P->g.W = h->W;
+  P->g.K = c->experts_per_peer;
+  P->D = c->in_features;
+  P->N = c->out_features;
+  P->Z = c->gated ? 2 * c->out_features : c->out_features;
+  P->act = c->activation;
+  P->gated = c->gated != 0;
+  return current_device(h);
+}
+
+template <typename T>
+cudaError_t launch_forward(a2av_handle* h, const ExpertParams& P, cudaStream_t s) {
+  const dim3 grid(4 * h->sms);
+  return P.gated ? launch_chained(expert_plain_kernel<T, true>, grid, kPlainThreads, 0, s, h->pdl,
+                                  P, P.D, P.N, P.D, 1LL)
+                 : launch_chained(expert_plain_kernel<T, false>, grid, kPlainThreads, 0, s, h->pdl,
+                                  P, P.D, P.N, P.D, 1LL);
+}
+
+template <typename T>
+cudaError_t launch_backward(a2av_handle* h, ExpertParams P, void* const* d_rows, bool dz_needed,
+                            cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  const dim3 grid(4 * h->sms);
+  if (dz_needed) {
+    bool vec = P.N % 8 == 0;
+    for (int p = 0; p < h->W; ++p)
+      vec = vec && aligned_to(P.dy[p], 16) && aligned_to(P.pre_in[p], 16) && aligned_to(P.dz[p], 16);
+    e = launch_chained(vec ? expert_dz_kernel<T, 8> : expert_dz_kernel<T, 1>, grid, 256, 0, s,
+                       h->pdl, P);
+    if (e != cudaSuccess) return e;
+    for (int p = 0; p < h->W; ++p) P.dy[p] = P.dz[p];
+  }
+  if (P.d_w[0] != nullptr) {
+    e = launch_chained(expert_plain_wgrad_kernel<T>, grid, kPlainThreads, 0, s, h->pdl, P);
+    if (e != cudaSuccess) return e;
+  }
+  if (P.d_bias[0] != nullptr) {
+    e = launch_chained(expert_dbias_kernel<T>, grid, 256, 0, s, h->pdl, P);
+    if (e != cudaSuccess) return e;
+  }
+  if (d_rows != nullptr) {
+    for (int p = 0; p < h->W; ++p) {
+      P.x[p] = P.dy[p];
+      P.out[p] = P.g.cap[p] > 0 ? d_rows[p] : nullptr;
+    }
+    P.act = A2AV_ACT_NONE;
+    e = launch_chained(expert_plain_kernel<T, false>, grid, kPlainThreads, 0, s, h->pdl, P, P.Z,
+                       P.D, 1LL, P.D);
+  }
+  return e;
+}
+
+}  // namespace
+
+extern "C" int a2av_expert_matmul(a2av_handle* h, const a2av_expert_t* shape,
+                                  const void* const* rows_ptrs, const int64_t* rows_per_peer,
+                                  const int64_t* counts_dev, const void* const* weight_ptrs,
+                                  const void* const* bias_ptrs, const void* const* residual_ptrs,
+                                  void* const* out_ptrs, void* const* pre_ptrs, void* stream) {
+  if (rows_ptrs == nullptr || weight_ptrs == nullptr || out_ptrs == nullptr)
+    return A2AV_ERR_INVALID_ARG;
+  ExpertParams P;
+  const int rc = expert_params(h, shape, rows_per_peer, counts_dev, &P);
+  if (rc != A2AV_OK) return rc;
+  const int W = h->W, size = dtype_bytes(shape->dtype);
+  if (!take(P.x, rows_ptrs, W, rows_per_peer, size) || !take(P.w, weight_ptrs, W, nullptr, size) ||
+      !take(P.bias, bias_ptrs, W, nullptr, size) ||
+      !take(P.residual, residual_ptrs, W, rows_per_peer, size) ||
+      !take(P.out, out_ptrs, W, rows_per_peer, size) ||
+      !take(P.pre, pre_ptrs, W, rows_per_peer, size))
+    return A2AV_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = shape->dtype == A2AV_BF16 ? launch_forward<__nv_bfloat16>(h, P, s)
+                                                  : launch_forward<__half>(h, P, s);
+  if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return A2AV_ERR_CUDA;
+  return A2AV_OK;
+}
+
+extern "C" int64_t a2av_expert_matmul_workspace_bytes(int world_size, const a2av_expert_t* shape,
+                                                      int64_t total_rows) {
+  if (world_size < 1 || world_size > kW || total_rows < 0 ||
+      total_rows > kMaxCount * world_size || shape_ok(shape, world_size) != A2AV_OK)
+    return -1;
+  if (shape->activation == A2AV_ACT_NONE && !shape->gated) return 0;
+  const int64_t Z = shape->gated ? 2 * shape->out_features : shape->out_features;
+  return total_rows * Z * dtype_bytes(shape->dtype);
+}
+
+extern "C" int a2av_expert_matmul_backward(
+    a2av_handle* h, const a2av_expert_t* shape, const void* const* rows_ptrs,
+    const int64_t* rows_per_peer, const int64_t* counts_dev, const void* const* weight_ptrs,
+    const void* const* pre_ptrs, const void* const* d_out_ptrs, void* const* d_rows_ptrs,
+    void* const* d_weight_ptrs, void* const* d_bias_ptrs, void* workspace,
+    int64_t workspace_bytes, void* stream) {
+  if (rows_ptrs == nullptr || weight_ptrs == nullptr || d_out_ptrs == nullptr ||
+      (d_rows_ptrs == nullptr && d_weight_ptrs == nullptr && d_bias_ptrs == nullptr))
+    return A2AV_ERR_INVALID_ARG;
+  ExpertParams P;
+  const int rc = expert_params(h, shape, rows_per_peer, counts_dev, &P);
+  if (rc != A2AV_OK) return rc;
+  const int W = h->W, size = dtype_bytes(shape->dtype);
+  const bool dz_needed = shape->activation != A2AV_ACT_NONE || shape->gated;
+  if (dz_needed && pre_ptrs == nullptr) return A2AV_ERR_INVALID_ARG;
+  if (!take(P.x, rows_ptrs, W, rows_per_peer, size) || !take(P.w, weight_ptrs, W, nullptr, size) ||
+      !take(P.dy, d_out_ptrs, W, rows_per_peer, size) ||
+      !take(P.pre_in, dz_needed ? pre_ptrs : nullptr, W, rows_per_peer, size) ||
+      !take(P.out, d_rows_ptrs, W, rows_per_peer, size) ||
+      !take(P.d_w, d_weight_ptrs, W, nullptr, size) ||
+      !take(P.d_bias, d_bias_ptrs, W, nullptr, size))
+    return A2AV_ERR_INVALID_ARG;
+  if (dz_needed) {
+    int64_t total = 0;
+    for (int p = 0; p < W; ++p) total += rows_per_peer[p];
+    if (total > 0 && (workspace == nullptr || !aligned_to(workspace, 256) ||
+                      workspace_bytes < total * P.Z * size))
+      return A2AV_ERR_INVALID_ARG;
+    int64_t at = 0;
+    for (int p = 0; p < W; ++p) {
+      P.dz[p] = static_cast<unsigned char*>(workspace) + at * P.Z * size;
+      at += rows_per_peer[p];
+    }
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      shape->dtype == A2AV_BF16
+          ? launch_backward<__nv_bfloat16>(h, P, d_rows_ptrs, dz_needed, s)
+          : launch_backward<__half>(h, P, d_rows_ptrs, dz_needed, s);
+  if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return A2AV_ERR_CUDA;
+  return A2AV_OK;
+}

@@ -1,0 +1,186 @@
+// experts.cuh -- the groups of rows that the experts' products work on: where
+// each begins, and which tile of work belongs to which (device side), and the
+// epilogue's activations.
+#pragma once
+
+#include "moe_device.cuh"
+
+namespace {
+
+// Groups are numbered in the order of their rows: peer p, source rank r, local
+// expert e -> (p * W + r) * K + e, its count at counts[r][p * K + e].
+struct GroupParams {
+  const long long* counts;  // [W][W * K]
+  long long cap[kW];        // rows the peer's buffers hold
+  int* status;
+  int W, K;
+};
+
+// The prefix sums over the groups' rows and tiles, kept in shared memory for
+// every 2^shift-th group; the groups between two entries are walked.
+constexpr int kEntries = 512;
+struct GroupTable {
+  long long rows[kEntries + 1];
+  long long tiles[kEntries + 1];
+  long long peer_base[kW + 1];  // rows before peer p
+  long long warp_rows[32], warp_tiles[32];
+  int shift, entries, bad;
+};
+
+struct GroupTile {
+  int p, e;          // peer, local expert
+  int rows;          // rows of the group
+  long long first;   // its first row in the peer's buffers
+  long long local;   // the tile's number within the group
+};
+
+__device__ __forceinline__ long long group_count(const GroupParams& G, int s) {
+  const int E = G.W * G.K;
+  const int p = s / E, in = s - p * E;
+  const int r = in / G.K, e = in - r * G.K;
+  return __ldcg(G.counts + (long long)r * E + p * G.K + e);
+}
+
+// Tiles of a group of n rows: `features` for each `tile_rows` of them.
+__device__ __forceinline__ long long group_tiles(long long n, int tile_rows, int features) {
+  return (n + tile_rows - 1) / tile_rows * features;
+}
+
+// By the whole block.  False (in every thread) when a count is negative or a
+// peer's rows do not fit its buffers; block 0 then records A2AV_ERR_BAD_SPLITS.
+__device__ bool build_groups(const GroupParams& G, GroupTable& g, int tile_rows, int features) {
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int E = G.W * G.K, n = G.W * E;
+  if (tid == 0) {
+    g.bad = 0;
+    int shift = 0;
+    while ((n + (1 << shift) - 1) >> shift > kEntries) ++shift;
+    g.shift = shift;
+    g.entries = (n + (1 << shift) - 1) >> shift;
+  }
+  __syncthreads();
+  const int shift = g.shift, entries = g.entries;
+  const int per = (entries + nt - 1) / nt;
+  const int e0 = min(tid * per, entries), e1 = min(e0 + per, entries);
+  const int s0 = min(e0 << shift, n), s1 = min(e1 << shift, n);
+  long long rows = 0, tiles = 0;
+  bool bad = false;
+  for (int s = s0; s < s1; ++s) {
+    const long long c = group_count(G, s);
+    if (c < 0 || c > kMaxCount) {
+      bad = true;
+    } else {
+      rows += c;
+      tiles += group_tiles(c, tile_rows, features);
+    }
+  }
+  if (bad) g.bad = 1;
+  long long ir = rows, it = tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(kAll, ir, o), b = __shfl_up_sync(kAll, it, o);
+    if (lane >= o) {
+      ir += a;
+      it += b;
+    }
+  }
+  if (lane == 31) {
+    g.warp_rows[warp] = ir;
+    g.warp_tiles[warp] = it;
+  }
+  __syncthreads();
+  long long r0 = ir - rows, t0 = it - tiles;
+  for (int w = 0; w < warp; ++w) {
+    r0 += g.warp_rows[w];
+    t0 += g.warp_tiles[w];
+  }
+  for (int s = s0; s < s1; ++s) {
+    if ((s & ((1 << shift) - 1)) == 0) {
+      g.rows[s >> shift] = r0;
+      g.tiles[s >> shift] = t0;
+    }
+    if (s % E == 0) g.peer_base[s / E] = r0;
+    const long long c = group_count(G, s);
+    if (c < 0 || c > kMaxCount) break;
+    r0 += c;
+    t0 += group_tiles(c, tile_rows, features);
+    if (s == n - 1) {
+      g.rows[entries] = r0;
+      g.tiles[entries] = t0;
+      g.peer_base[G.W] = r0;
+    }
+  }
+  __syncthreads();
+  if (!g.bad && tid < G.W && g.peer_base[tid + 1] - g.peer_base[tid] > G.cap[tid]) g.bad = 1;
+  __syncthreads();
+  if (g.bad && blockIdx.x == 0 && tid == 0) note_error(G.status, A2AV_ERR_BAD_SPLITS);
+  return !g.bad;
+}
+
+// The group that tile t (below the table's last entry) belongs to.
+__device__ __forceinline__ GroupTile find_tile(const GroupParams& G, const GroupTable& g,
+                                               long long t, int tile_rows, int features) {
+  int lo = 0, hi = g.entries;  // tiles[lo] <= t < tiles[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (g.tiles[mid] <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  int s = lo << g.shift;
+  long long first = g.rows[lo], at = g.tiles[lo];
+  long long c = group_count(G, s);
+  while (true) {
+    const long long more = group_tiles(c, tile_rows, features);
+    if (t < at + more) break;
+    at += more;
+    first += c;
+    c = group_count(G, ++s);
+  }
+  GroupTile x;
+  const int E = G.W * G.K;
+  x.p = s / E;
+  x.e = s % G.K;
+  x.rows = (int)c;
+  x.first = first - g.peer_base[x.p];
+  x.local = t - at;
+  return x;
+}
+
+// First row (in its peer's buffers) and rows of group s.
+__device__ __forceinline__ long long find_group(const GroupParams& G, const GroupTable& g, int s,
+                                                int* rows) {
+  long long first = g.rows[s >> g.shift];
+  for (int i = s >> g.shift << g.shift; i < s; ++i) first += group_count(G, i);
+  *rows = (int)group_count(G, s);
+  return first - g.peer_base[s / (G.W * G.K)];
+}
+
+// --------------------------------------------------------- activations --
+// In 32 bits.  The exponential is the fast one (2 ulp of its argument's
+// range): the result is rounded to 8 or 11 bits right after.
+__device__ __forceinline__ float act_fn(int a, float z) {
+  switch (a) {
+    case A2AV_ACT_RELU: return z < 0.0f ? 0.0f : z;  // (a NaN stays)
+    case A2AV_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    case A2AV_ACT_SILU: return __fdividef(z, 1.0f + __expf(-z));
+    default: return z;
+  }
+}
+
+__device__ __forceinline__ float act_slope(int a, float z) {
+  switch (a) {
+    case A2AV_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+    case A2AV_ACT_GELU:
+      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
+             z * __expf(-0.5f * z * z) * 0.39894228040143268f;
+    case A2AV_ACT_SILU: {
+      const float s = __fdividef(1.0f, 1.0f + __expf(-z));
+      return s * (1.0f + z * (1.0f - s));
+    }
+    default: return 1.0f;
+  }
+}
+
+}  // namespace
