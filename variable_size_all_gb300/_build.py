@@ -8,9 +8,9 @@ import subprocess
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", f) for f in ("a2av.cu", "dispatch.cu", "route.cu", "experts.cu",
-                                                  "weighted.cu")]
+                                                  "experts_mma.cu", "weighted.cu")]
 HEADERS = [os.path.join(PKG, "csrc", f) for f in ("a2av_device.cuh", "a2av_handle.h",
-                                                  "moe_device.cuh", "experts.cuh")]
+                                                  "moe_device.cuh", "experts.cuh", "mma.cuh")]
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "liba2av.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

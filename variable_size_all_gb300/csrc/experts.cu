@@ -5,23 +5,6 @@
 
 namespace {
 
-struct ExpertParams {
-  GroupParams g;
-  const void* x[kW];         // rows that are multiplied (forward: x; d_rows: dz)
-  const void* w[kW];         // [K][Z][D]
-  const void* bias[kW];
-  const void* residual[kW];
-  void* out[kW];
-  void* pre[kW];
-  const void* dy[kW];        // backward
-  const void* pre_in[kW];
-  void* dz[kW];
-  void* d_w[kW];
-  void* d_bias[kW];
-  long long D, N, Z;
-  int act, gated;
-};
-
 // ------------------------------------------------- products by plain FMAs --
 // For shapes and buffers that the tensor-core kernels' copies cannot take
 // (rows that are not multiples of 16 bytes, or not aligned to them).  64 x 64
@@ -275,7 +258,9 @@ int expert_params(a2av_handle* h, const a2av_expert_t* c, const int64_t* rows_pe
 }
 
 template <typename T>
-cudaError_t launch_forward(a2av_handle* h, const ExpertParams& P, cudaStream_t s) {
+cudaError_t launch_forward(a2av_handle* h, const ExpertParams& P, int dtype, cudaStream_t s) {
+  cudaError_t e;
+  if (a2av_expert_mma(h, P, dtype, 0, s, &e)) return e;
   const dim3 grid(4 * h->sms);
   return P.gated ? launch_chained(expert_plain_kernel<T, true>, grid, kPlainThreads, 0, s, h->pdl,
                                   P, P.D, P.N, P.D, 1LL)
@@ -285,7 +270,7 @@ cudaError_t launch_forward(a2av_handle* h, const ExpertParams& P, cudaStream_t s
 
 template <typename T>
 cudaError_t launch_backward(a2av_handle* h, ExpertParams P, void* const* d_rows, bool dz_needed,
-                            cudaStream_t s) {
+                            int dtype, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   const dim3 grid(4 * h->sms);
   if (dz_needed) {
@@ -297,10 +282,9 @@ cudaError_t launch_backward(a2av_handle* h, ExpertParams P, void* const* d_rows,
     if (e != cudaSuccess) return e;
     for (int p = 0; p < h->W; ++p) P.dy[p] = P.dz[p];
   }
-  if (P.d_w[0] != nullptr) {
+  if (P.d_w[0] != nullptr && !a2av_expert_mma(h, P, dtype, 2, s, &e))
     e = launch_chained(expert_plain_wgrad_kernel<T>, grid, kPlainThreads, 0, s, h->pdl, P);
-    if (e != cudaSuccess) return e;
-  }
+  if (e != cudaSuccess) return e;
   if (P.d_bias[0] != nullptr) {
     e = launch_chained(expert_dbias_kernel<T>, grid, 256, 0, s, h->pdl, P);
     if (e != cudaSuccess) return e;
@@ -311,8 +295,9 @@ cudaError_t launch_backward(a2av_handle* h, ExpertParams P, void* const* d_rows,
       P.out[p] = P.g.cap[p] > 0 ? d_rows[p] : nullptr;
     }
     P.act = A2AV_ACT_NONE;
-    e = launch_chained(expert_plain_kernel<T, false>, grid, kPlainThreads, 0, s, h->pdl, P, P.Z,
-                       P.D, 1LL, P.D);
+    if (!a2av_expert_mma(h, P, dtype, 1, s, &e))
+      e = launch_chained(expert_plain_kernel<T, false>, grid, kPlainThreads, 0, s, h->pdl, P,
+                         P.Z, P.D, 1LL, P.D);
   }
   return e;
 }
@@ -337,8 +322,8 @@ extern "C" int a2av_expert_matmul(a2av_handle* h, const a2av_expert_t* shape,
       !take(P.pre, pre_ptrs, W, rows_per_peer, size))
     return A2AV_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = shape->dtype == A2AV_BF16 ? launch_forward<__nv_bfloat16>(h, P, s)
-                                                  : launch_forward<__half>(h, P, s);
+  const cudaError_t e = shape->dtype == A2AV_BF16 ? launch_forward<__nv_bfloat16>(h, P, shape->dtype, s)
+                                                  : launch_forward<__half>(h, P, shape->dtype, s);
   if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return A2AV_ERR_CUDA;
   return A2AV_OK;
 }
@@ -390,8 +375,8 @@ extern "C" int a2av_expert_matmul_backward(
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
       shape->dtype == A2AV_BF16
-          ? launch_backward<__nv_bfloat16>(h, P, d_rows_ptrs, dz_needed, s)
-          : launch_backward<__half>(h, P, d_rows_ptrs, dz_needed, s);
+          ? launch_backward<__nv_bfloat16>(h, P, d_rows_ptrs, dz_needed, shape->dtype, s)
+          : launch_backward<__half>(h, P, d_rows_ptrs, dz_needed, shape->dtype, s);
   if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return A2AV_ERR_CUDA;
   return A2AV_OK;
 }

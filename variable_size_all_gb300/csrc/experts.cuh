@@ -5,16 +5,37 @@
 
 #include "moe_device.cuh"
 
-namespace {
-
 // Groups are numbered in the order of their rows: peer p, source rank r, local
 // expert e -> (p * W + r) * K + e, its count at counts[r][p * K + e].
-struct GroupParams {
+struct A2avGroups {
   const long long* counts;  // [W][W * K]
-  long long cap[kW];        // rows the peer's buffers hold
+  long long cap[A2AV_MAX_RANKS];        // rows the peer's buffers hold
   int* status;
   int W, K;
 };
+
+// One call of the experts' products.
+struct A2avExperts {
+  A2avGroups g;
+  const void* x[A2AV_MAX_RANKS];         // rows that are multiplied (forward: x; d_rows: dz)
+  const void* w[A2AV_MAX_RANKS];         // [K][Z][D]
+  const void* bias[A2AV_MAX_RANKS];
+  const void* residual[A2AV_MAX_RANKS];
+  void* out[A2AV_MAX_RANKS];
+  void* pre[A2AV_MAX_RANKS];
+  const void* dy[A2AV_MAX_RANKS];        // backward
+  const void* pre_in[A2AV_MAX_RANKS];
+  void* dz[A2AV_MAX_RANKS];
+  void* d_w[A2AV_MAX_RANKS];
+  void* d_bias[A2AV_MAX_RANKS];
+  long long D, N, Z;
+  int act, gated;
+};
+
+namespace {
+
+using GroupParams = A2avGroups;
+using ExpertParams = A2avExperts;
 
 // The prefix sums over the groups' rows and tiles, kept in shared memory for
 // every 2^shift-th group; the groups between two entries are walked.
@@ -130,7 +151,7 @@ __device__ __forceinline__ GroupTile find_tile(const GroupParams& G, const Group
   }
   int s = lo << g.shift;
   long long first = g.rows[lo], at = g.tiles[lo];
-  long long c = group_count(G, s);
+  long long c = g.shift == 0 ? g.rows[lo + 1] - first : group_count(G, s);
   while (true) {
     const long long more = group_tiles(c, tile_rows, features);
     if (t < at + more) break;
@@ -152,6 +173,10 @@ __device__ __forceinline__ GroupTile find_tile(const GroupParams& G, const Group
 __device__ __forceinline__ long long find_group(const GroupParams& G, const GroupTable& g, int s,
                                                 int* rows) {
   long long first = g.rows[s >> g.shift];
+  if (g.shift == 0) {
+    *rows = (int)(g.rows[s + 1] - first);
+    return first - g.peer_base[s / (G.W * G.K)];
+  }
   for (int i = s >> g.shift << g.shift; i < s; ++i) first += group_count(G, i);
   *rows = (int)group_count(G, s);
   return first - g.peer_base[s / (G.W * G.K)];
@@ -184,3 +209,11 @@ __device__ __forceinline__ float act_slope(int a, float z) {
 }
 
 }  // namespace
+
+// experts_mma.cu: the same products on the tensor cores.  `direction` 0: out =
+// epilogue(x w^T); 1: out = x w, x being dz; 2: d_w = dy^T x.  False when the
+// shape or a buffer is not one their copies can take (then nothing is
+// launched); *error gets the launch's error.
+__attribute__((visibility("hidden"))) bool a2av_expert_mma(a2av_handle* h, const A2avExperts& P,
+                                                           int dtype, int direction,
+                                                           cudaStream_t s, cudaError_t* error);
