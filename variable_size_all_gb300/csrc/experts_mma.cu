@@ -8,10 +8,13 @@
 // tile before from TMEM, where two tiles' sums have room, while the next tile's
 // products run.
 //
-// Experts' weights are the M = 256 side of a tile and rows (tokens) the N side:
-// N can be any multiple of 32 up to 256, so that a ragged group's last tile
-// costs what its rows cost, and a group of a few rows reads its weights with
-// little else.  The rows' own multiple of 128 would be wasted on small groups.
+// Experts' weights are the M = 256 side of a tile and rows (tokens) the N side.
+// An expert's rows lie in W groups, one from each source rank; its tiles are
+// runs of up to 32 granules, eight rows of one group each (a group's last may
+// have fewer), whatever groups they are from.  So the products cost what the
+// rows cost (to 8 a group, and 16 a tile), the weights of an expert with a few
+// rows from every rank are read once, and a granule is what the 128-byte
+// swizzle and a TMA copy can place by itself.
 #include "experts.cuh"
 #include "mma.cuh"
 
@@ -23,7 +26,9 @@ constexpr int kK = 64;                // contraction per stage: 128 bytes of a r
 constexpr int kSideBytes = 128 * 128; // one operand's part of a stage in one CTA
 constexpr int kStageBytes = 2 * kSideBytes;
 constexpr int kStages = 6;
-constexpr int kRowBox = 32;           // rows of one copy of the N side
+constexpr int kGranule = 8;
+constexpr int kTileGranules = kN / kGranule;
+constexpr int kSlots = 3;             // tiles the scheduler may be ahead
 constexpr int kMmaThreads = 256;
 constexpr unsigned kTmemColumns = 512;
 constexpr int kPitch = 80;            // bytes between staged rows: 8 of them hit all banks once
@@ -31,7 +36,9 @@ constexpr int kStaging = 32 * kPitch; // per epilogue warp
 constexpr size_t kMmaSmem = 1024 + (size_t)kStages * kStageBytes + 4 * kStaging;
 
 struct MmaParams {
-  CUtensorMap rows[kW];     // N side: [rows][C], or x of the weights' gradient
+  CUtensorMap rows[kW];     // N side: [rows][C] in boxes of a granule; x of the weights' gradient
+  CUtensorMap rows32[kW];   // the same in boxes of 32 and 128 rows
+  CUtensorMap rows128[kW];
   CUtensorMap weights[kW];  // M side: [K][..][..], or dz
   GroupParams g;
   const void* bias[kW];
@@ -49,11 +56,107 @@ struct Bars {
   unsigned long long tail[kStages];   // weights' gradient: this CTA's copies, before zeroing
   unsigned long long acc_full[2];     // a tile's sums are complete
   unsigned long long acc_empty[2];    // of the first CTA: both CTAs have taken them
+  unsigned long long slot_full[kSlots], slot_empty[kSlots];
   unsigned tmem;
 };
 
+// A tile as the scheduler (warp 3 of each CTA) describes it to the others.
+struct Slot {
+  int p, e;                // peer, local expert
+  int f;                   // its first feature
+  int granules;            // 1 .. 32
+  int row[kTileGranules];  // each granule's first row in the peer's buffers
+  int n[kTileGranules];    // and its rows, 0 past the last granule
+};
+
+// Tiles before each expert.
+struct TileTable {
+  long long first[A2AV_MAX_DISPATCH_KEYS + 1];
+};
+
+// By the whole block, after build_groups.
+__device__ void build_tiles(const GroupParams& G, GroupTable& g, TileTable& tt, int features) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int E = G.W * G.K, per = (E + kMmaThreads - 1) / kMmaThreads;
+  const int x0 = min(tid * per, E), x1 = min(x0 + per, E);
+  long long own = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long at = own;  // second pass: tiles before expert x0
+    long long sum = 0;
+    for (int x = x0; x < x1; ++x) {
+      const int p = x / G.K, e = x - p * G.K;
+      long long granules = 0;
+      for (int r = 0; r < G.W; ++r) {
+        int rows;
+        find_group(G, g, (p * G.W + r) * G.K + e, &rows);
+        granules += (rows + kGranule - 1) / kGranule;
+      }
+      if (pass == 1) tt.first[x] = at + sum;
+      sum += group_tiles(granules, kTileGranules, features);
+    }
+    if (pass == 1) {
+      if (x1 == E && x0 < E) tt.first[E] = at + sum;
+      break;
+    }
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(kAll, inc, o);
+      if (lane >= o) inc += v;
+    }
+    __syncthreads();
+    if (lane == 31) g.warp_tiles[warp] = inc;
+    __syncthreads();
+    own = inc - sum;
+    for (int w = 0; w < warp; ++w) own += g.warp_tiles[w];
+  }
+  __syncthreads();
+}
+
+// Tile t, by a whole warp.
+__device__ __forceinline__ void describe_tile(const GroupParams& G, const GroupTable& g,
+                                              const TileTable& tt, long long t, int features,
+                                              int tile_features, Slot& slot, int lane) {
+  int lo = 0, hi = G.W * G.K;  // first[lo] <= t < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tt.first[mid] <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int p = lo / G.K, e = lo - p * G.K;
+  const long long local = t - tt.first[lo];
+  int rows = 0;
+  long long first = 0;
+  if (lane < G.W) first = find_group(G, g, (p * G.W + lane) * G.K + e, &rows);
+  const int granules = (rows + kGranule - 1) / kGranule;
+  int inc = granules;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kAll, inc, o);
+    if (lane >= o) inc += v;
+  }
+  const int total = __shfl_sync(kAll, inc, 31);
+  const int g0 = (int)(local / features) * kTileGranules, mine = g0 + lane;
+  int r = 0;
+  for (int i = 0; i < G.W - 1; ++i)
+    if (__shfl_sync(kAll, inc, i) <= mine) r = i + 1;
+  const int before = __shfl_sync(kAll, inc - granules, r) * kGranule;
+  const int n = __shfl_sync(kAll, rows, r) - (mine * kGranule - before);
+  const long long row = __shfl_sync(kAll, first, r) + (mine * kGranule - before);
+  slot.row[lane] = (int)row;
+  slot.n[lane] = mine < total ? min(n, kGranule) : 0;
+  if (lane == 0) {
+    slot.p = p;
+    slot.e = e;
+    slot.f = (int)(local % features) * tile_features;
+    slot.granules = min(total - g0, kTileGranules);
+  }
+}
+
 // What the two kernels share before and after their roles.
-__device__ __forceinline__ void pair_begin(Bars& b, int warp) {
+__device__ __forceinline__ void pair_begin(Bars& b, int warp, uint32_t rank) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       bar_init(smem_addr(&b.full[s]), 2);
@@ -63,6 +166,10 @@ __device__ __forceinline__ void pair_begin(Bars& b, int warp) {
     for (int i = 0; i < 2; ++i) {
       bar_init(smem_addr(&b.acc_full[i]), 1);
       bar_init(smem_addr(&b.acc_empty[i]), 8);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      bar_init(smem_addr(&b.slot_full[i]), 1);
+      bar_init(smem_addr(&b.slot_empty[i]), rank == 0 ? 6 : 5);
     }
     bar_init_done();
   }
@@ -105,40 +212,41 @@ __device__ __forceinline__ uint32_t columns_of(long long n) {
   return n >= kN ? kN : (uint32_t)((n + 31) / 32 * 32);
 }
 
-// The warp's 32 staged rows of kPieces x 16 bytes to rows `ld` apart; pieces
-// past the first kSplit go `jump` elements further.
+// The warp's 32 staged rows (four granules, from granule j of the slot) of
+// kPieces x 16 bytes to the rows they stand for, `ld` apart; pieces past the
+// first kSplit go `jump` elements further.
 template <typename T, int kPieces, int kSplit>
-__device__ __forceinline__ void write_rows(uint32_t stage, T* to, long long ld, int rows, int f,
-                                           int F, long long jump, int lane) {
+__device__ __forceinline__ void write_rows(uint32_t stage, T* to, long long ld, const Slot& slot,
+                                           int j, int f, int F, long long jump, int lane) {
   constexpr int kPer = 32 / kPieces;
   const int piece = lane % kPieces, within = piece % kSplit;
   if (f + 8 * within >= F) return;
   T* at = to + f + 8 * within + (piece >= kSplit ? jump : 0);
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
-    const int row = lane / kPieces + kPer * i;
-    if (row < rows) {
+    const int row = lane / kPieces + kPer * i, gr = j + row / kGranule, in = row % kGranule;
+    if (in < slot.n[gr]) {
       uint4 v;
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                    : "r"(stage + row * kPitch + piece * 16));
-      *reinterpret_cast<uint4*>(at + row * ld) = v;
+      *reinterpret_cast<uint4*>(at + (long long)(slot.row[gr] + in) * ld) = v;
     }
   }
 }
 
 // The other way: rows into the warp's staging.
 template <typename T, int kPieces>
-__device__ __forceinline__ void read_rows(uint32_t stage, const T* from, long long ld, int rows,
-                                          int f, int F, int lane) {
+__device__ __forceinline__ void read_rows(uint32_t stage, const T* from, long long ld,
+                                          const Slot& slot, int j, int f, int F, int lane) {
   constexpr int kPer = 32 / kPieces;
   const int piece = lane % kPieces;
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
-    const int row = lane / kPieces + kPer * i;
+    const int row = lane / kPieces + kPer * i, gr = j + row / kGranule, in = row % kGranule;
     uint4 v = make_uint4(0, 0, 0, 0);
-    if (row < rows && f + 8 * piece < F)
-      v = *reinterpret_cast<const uint4*>(from + row * ld + f + 8 * piece);
+    if (in < slot.n[gr] && f + 8 * piece < F)
+      v = *reinterpret_cast<const uint4*>(from + (long long)(slot.row[gr] + in) * ld + f + 8 * piece);
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + row * kPitch + piece * 16),
                  "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
@@ -188,44 +296,96 @@ __device__ __forceinline__ void apply_act(int act, float (&v)[16]) {
 }
 
 // ------------------------------------------------- rows times weights --
+// A CTA's half of a tile's granules as copies of 128, 32 or 8 rows: a run of
+// consecutive rows takes the largest it fills, the last run also one that it
+// does not, where the half has room (what it brings past the run is in no
+// result).  Returns the bytes.
+struct Copies {
+  int count;
+  int row[kTileGranules / 2];
+  int at[kTileGranules / 2];    // bytes into the stage's N side
+  int size[kTileGranules / 2];  // granules
+};
+
+__device__ __forceinline__ unsigned plan_copies(const Slot& slot, uint32_t rank, Copies& c) {
+  const int half = (slot.granules + 1) / 2;
+  const int j0 = rank == 0 ? 0 : half, j1 = rank == 0 ? half : slot.granules;
+  unsigned bytes = 0;
+  int n = 0;
+  for (int j = j0; j < j1;) {
+    int run = 1;
+    while (j + run < j1 && slot.row[j + run] == slot.row[j] + kGranule * run) ++run;
+    const bool last = j + run == j1;
+    const int room = kTileGranules / 2 - (j - j0);
+    const int size = room == 16 && (run == 16 || (last && run > 8)) ? 16
+                     : run >= 4 || (last && run >= 2 && room >= 4)  ? 4
+                                                                    : 1;
+    c.row[n] = slot.row[j];
+    c.at[n] = (j - j0) * 1024;
+    c.size[n] = size;
+    ++n;
+    bytes += size * 1024;
+    j += size;
+  }
+  c.count = n;
+  return bytes;
+}
+
 // kMn: the weights' contraction runs over their rows (the rows' gradient), so
 // that they are the MN-major operand.  kGated: the tile's 256 weight rows are
-// 128 of the first half and their partners of the second, 16 and 16 in turn:
-// a thread of the epilogue finds both in its registers.
+// 128 of the first half and their partners of the second, eight and eight in
+// turn (one copy of a five-dimensional view of the weights puts them so): a
+// thread of the epilogue finds both in its registers.
 template <typename T, bool kMn, bool kGated>
 __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     expert_mma_kernel(const __grid_constant__ MmaParams P) {
   extern __shared__ unsigned char dynamic[];
   __shared__ GroupTable g;
+  __shared__ TileTable tt;
+  __shared__ Slot slots[kSlots];
+  __shared__ Copies copies;
   __shared__ Bars b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const uint32_t base = (smem_addr(dynamic) + 1023) & ~1023u;
-  constexpr int kTileF = kGated ? 128 : 256;   // features of the result per pair
-  constexpr int kMyF = kTileF / 2;             // and per CTA
+  constexpr int kTileF = kGated ? 128 : 256;  // features of the result per pair
+  constexpr int kMyF = kTileF / 2;            // and per CTA
   chain();
   const int nf = (P.F + kTileF - 1) / kTileF;
-  const bool good = build_groups(P.g, g, kN, nf);
-  pair_begin(b, warp);
-  const long long tiles = good ? g.tiles[g.entries] : 0;
+  const bool good = build_groups(P.g, g, 1, 1);
+  if (good) build_tiles(P.g, g, tt, nf);
+  pair_begin(b, warp, rank);
+  const long long tiles = good ? tt.first[P.g.W * P.g.K] : 0;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int blocks = (P.C + kK - 1) / kK;
   bool ok = true;
+  unsigned i = 0;  // tiles so far
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 3) {
+    // --------------------------------------------------- scheduler --
+    for (long long t = pair; t < tiles; t += pairs, ++i) {
+      const unsigned sl = i % kSlots;
+      ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_empty[sl]), ((i / kSlots) & 1) ^ 1));
+      if (!ok) break;
+      describe_tile(P.g, g, tt, t, nf, kTileF, slots[sl], lane);
+      __syncwarp();
+      if (lane == 0) bar_arrive_here(smem_addr(&b.slot_full[sl]));
+    }
+    if (!ok && lane == 0) note_error(P.g.status, A2AV_ERR_TIMEOUT);
+  } else if (warp == 0 && lane == 0) {
     // ------------------------------------------------------ copies --
     const uint32_t full0 = map_to(smem_addr(&b.full[0]), 0);
     unsigned it = 0;
-    for (long long t = pair; t < tiles && ok; t += pairs) {
-      const GroupTile gt = find_tile(P.g, g, t, kN, nf);
-      const int f0 = (int)(gt.local % nf) * kTileF + kMyF * rank;
-      const long long m0 = gt.local / nf * kN;
-      const uint32_t half = columns_of(gt.rows - m0) / 2;
-      const int copies = (half + kRowBox - 1) / kRowBox;
-      const int row = (int)(gt.first + m0 + half * rank);
-      const CUtensorMap* wm = &P.weights[gt.p];
-      const CUtensorMap* xm = &P.rows[gt.p];
-      const unsigned bytes = kSideBytes + copies * kRowBox * 128;
+    for (long long t = pair; t < tiles && ok; t += pairs, ++i) {
+      const unsigned sl = i % kSlots;
+      if (!bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1)) {
+        ok = false;
+        break;
+      }
+      const int p = slots[sl].p, e = slots[sl].e, f0 = slots[sl].f + kMyF * rank;
+      const unsigned bytes = kSideBytes + plan_copies(slots[sl], rank, copies);
+      bar_arrive_here(smem_addr(&b.slot_empty[sl]));
+      const CUtensorMap* wm = &P.weights[p];
       for (int kb = 0; kb < blocks; ++kb, ++it) {
         const unsigned s = it % kStages;
         if (!bar_wait(smem_addr(&b.empty[s]), ((it / kStages) & 1) ^ 1)) {
@@ -237,19 +397,19 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
         bar_arrive_tx(full, bytes);
         const int c = kb * kK;
         if (kMn) {
-          tma_load(at, wm, f0, c, gt.e, full);
-          tma_load(at + kSideBytes / 2, wm, f0 + 64, c, gt.e, full);
+          tma_load(at, wm, f0, c, e, full);
+          tma_load(at + kSideBytes / 2, wm, f0 + 64, c, e, full);
         } else if (kGated) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            tma_load(at + i * 4096, wm, c, f0 + 16 * i, gt.e, full);
-            tma_load(at + i * 4096 + 2048, wm, c, P.F + f0 + 16 * i, gt.e, full);
-          }
+          tma_load5(at, wm, c, 0, 0, f0 / 8, e, full);
         } else {
-          tma_load(at, wm, c, f0, gt.e, full);
+          tma_load(at, wm, c, f0, e, full);
         }
-        for (int i = 0; i < copies; ++i)
-          tma_load(at + kSideBytes + i * kRowBox * 128, xm, c, row + i * kRowBox, 0, full);
+        for (int n = 0; n < copies.count; ++n) {
+          const CUtensorMap* xm = copies.size[n] == 16  ? &P.rows128[p]
+                                  : copies.size[n] == 4 ? &P.rows32[p]
+                                                        : &P.rows[p];
+          tma_load(at + kSideBytes + copies.at[n], xm, c, copies.row[n], 0, full);
+        }
       }
     }
     if (!ok || !settle(b, it)) {
@@ -258,18 +418,18 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ---------------------------------------------------- products --
-    constexpr bool kBf16 = sizeof(T) == 2 && !__is_same(T, __half);
-    unsigned it = 0, n_tile = 0;
-    for (long long t = pair; t < tiles && ok; t += pairs, ++n_tile) {
-      const GroupTile gt = find_tile(P.g, g, t, kN, nf);
-      const uint32_t n = columns_of(gt.rows - gt.local / nf * kN);
-      const uint32_t idesc = product(kBf16, kMn, false, kM, n);
-      const unsigned buf = n_tile & 1;
-      const uint32_t d = b.tmem + buf * kN;
-      if (!bar_wait(smem_addr(&b.acc_empty[buf]), ((n_tile >> 1) & 1) ^ 1)) {
+    constexpr bool kBf16 = !__is_same(T, __half);
+    unsigned it = 0;
+    for (long long t = pair; t < tiles && ok; t += pairs, ++i) {
+      const unsigned sl = i % kSlots, buf = i & 1;
+      if (!bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1) ||
+          !bar_wait(smem_addr(&b.acc_empty[buf]), ((i >> 1) & 1) ^ 1)) {
         ok = false;
         break;
       }
+      const uint32_t idesc = product(kBf16, kMn, false, kM, (slots[sl].granules + 1) / 2 * 2 * kGranule);
+      bar_arrive_here(smem_addr(&b.slot_empty[sl]));
+      const uint32_t d = b.tmem + buf * kN;
       fence_after_sync();
       for (int kb = 0; kb < blocks; ++kb, ++it) {
         const unsigned s = it % kStages;
@@ -296,69 +456,75 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     const int q = warp - 4;
     const uint32_t stage = base + kStages * kStageBytes + q * kStaging;
     const uint32_t empty0 = map_to(smem_addr(&b.acc_empty[0]), 0);
-    unsigned n_tile = 0;
-    for (long long t = pair; t < tiles && ok; t += pairs, ++n_tile) {
-      const GroupTile gt = find_tile(P.g, g, t, kN, nf);
-      const long long m0 = gt.local / nf * kN;
-      const int rows = (int)min((long long)kN, gt.rows - m0);
+    for (long long t = pair; t < tiles && ok; t += pairs, ++i) {
+      const unsigned sl = i % kSlots, buf = i & 1;
+      ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
+      if (!ok) break;
+      const Slot& slot = slots[sl];
+      const int p = slot.p, columns = slot.granules * kGranule;
       // the warp's features: 32 of the result, or 16 and their partners
-      const int f = (int)(gt.local % nf) * kTileF + kMyF * rank + (kGated ? 16 : 32) * q;
-      const unsigned buf = n_tile & 1;
-      const T* bias = P.bias[gt.p] != nullptr
-                          ? static_cast<const T*>(P.bias[gt.p]) + (long long)gt.e * P.Z : nullptr;
+      const int f = slot.f + kMyF * rank + (kGated ? 16 : 32) * q;
+      const T* bias = P.bias[p] != nullptr
+                          ? static_cast<const T*>(P.bias[p]) + (long long)slot.e * P.Z : nullptr;
       float ba[2] = {0.0f, 0.0f}, bb[2] = {0.0f, 0.0f};
       if (bias != nullptr) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int fa = f + (lane >> 2) + 8 * i, fb = kGated ? fa : fa + 16;
-          if (fa < P.F) ba[i] = to_float(bias[fa]);
-          if (fb < P.F) bb[i] = to_float(bias[kGated ? P.F + fb : fb]);
+        for (int h = 0; h < 2; ++h) {
+          const int fa = f + (lane >> 2) + 8 * h, fb = kGated ? fa : fa + 16;
+          if (fa < P.F) ba[h] = to_float(bias[fa]);
+          if (fb < P.F) bb[h] = to_float(bias[kGated ? P.F + fb : fb]);
         }
       }
-      const long long row0 = gt.first + m0;
-      T* out = static_cast<T*>(P.out[gt.p]) + row0 * P.F;
-      T* pre = P.pre[gt.p] != nullptr ? static_cast<T*>(P.pre[gt.p]) + row0 * P.Z : nullptr;
-      const T* res = P.residual[gt.p] != nullptr
-                         ? static_cast<const T*>(P.residual[gt.p]) + row0 * P.F : nullptr;
-      ok = __all_sync(kAll, bar_wait(smem_addr(&b.acc_full[buf]), (n_tile >> 1) & 1));
+      T* out = static_cast<T*>(P.out[p]);
+      T* pre = static_cast<T*>(P.pre[p]);
+      const T* res = static_cast<const T*>(P.residual[p]);
+      ok = __all_sync(kAll, bar_wait(smem_addr(&b.acc_full[buf]), (i >> 1) & 1));
       if (!ok) break;
       fence_after_sync();
-      for (int c = 0; c < rows; c += 32) {
-        const int n = min(32, rows - c);
+      for (int c = 0; c < columns; c += 32) {
+        const int j = c / kGranule;
         const uint32_t at = b.tmem + buf * kN + c + ((uint32_t)(32 * q) << 16);
         float va[16], vb[16];
         tmem_load(at, va);
         tmem_load(at + (16u << 16), vb);
         tmem_load_wait();
-        if (c + 32 >= rows) {  // the last of the tile's sums: the buffer is free
+        if (c + 32 >= columns) {  // the last of the tile's sums: the buffer is free
           fence_before_sync();
           __syncwarp();
           if (lane == 0) bar_arrive(empty0 + buf * 8);
         }
+        if (kGated) {  // lanes 0..7 and 8..15 of each are partners: va the first halves, vb the second
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          va[i] += ba[(i >> 1) & 1];
-          vb[i] += bb[(i >> 1) & 1];
+          for (int n = 0; n < 16; n += 4)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float second = va[n + 2 + x];
+              va[n + 2 + x] = vb[n + x];
+              vb[n + x] = second;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          va[n] += ba[(n >> 1) & 1];
+          vb[n] += bb[(n >> 1) & 1];
         }
         if (pre != nullptr) {
           stage_block<T>(stage, 0, va, lane);
           stage_block<T>(stage, 32, vb, lane);
           __syncwarp();
-          if (kGated)
-            write_rows<T, 4, 2>(stage, pre + (long long)c * P.Z, P.Z, n, f, P.F, P.F, lane);
-          else
-            write_rows<T, 4, 4>(stage, pre + (long long)c * P.Z, P.Z, n, f, P.F, 0, lane);
+          write_rows<T, 4, kGated ? 2 : 4>(stage, pre, P.Z, slot, j, f, P.F, P.F, lane);
           __syncwarp();
         }
         apply_act(P.act, va);
         if (kGated) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) va[i] *= vb[i];
+          for (int n = 0; n < 16; ++n) va[n] *= vb[n];
         } else {
           apply_act(P.act, vb);
         }
+        constexpr int kPieces = kGated ? 2 : 4;
         if (res != nullptr) {
-          read_rows<T, kGated ? 2 : 4>(stage, res + (long long)c * P.F, P.F, n, f, P.F, lane);
+          read_rows<T, kPieces>(stage, res, P.F, slot, j, f, P.F, lane);
           __syncwarp();
           add_block<T>(stage, 0, va, lane);
           if (!kGated) add_block<T>(stage, 32, vb, lane);
@@ -367,10 +533,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
         stage_block<T>(stage, 0, va, lane);
         if (!kGated) stage_block<T>(stage, 32, vb, lane);
         __syncwarp();
-        constexpr int kPieces = kGated ? 2 : 4;
-        write_rows<T, kPieces, kPieces>(stage, out + (long long)c * P.F, P.F, n, f, P.F, 0, lane);
+        write_rows<T, kPieces, kPieces>(stage, out, P.F, slot, j, f, P.F, 0, lane);
         __syncwarp();
       }
+      if (lane == 0) bar_arrive_here(smem_addr(&b.slot_empty[sl]));
     }
     if (!ok && lane == 0) note_error(P.g.status, A2AV_ERR_TIMEOUT);
   }
@@ -395,7 +561,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t base = (smem_addr(dynamic) + 1023) & ~1023u;
   chain();
   const bool good = build_groups(P.g, g, kN, 1);
-  pair_begin(b, warp);
+  pair_begin(b, warp, rank);
   const int W = P.g.W, K = P.g.K;
   const int nz = (P.Z + kM - 1) / kM, nd = (P.D + kN - 1) / kN;
   const long long tiles = good ? (long long)W * K * nz * nd : 0;
@@ -491,6 +657,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
             ok = false;
             break;
           }
+          // (a ragged block's rows were written by the other CTA's warp 3 as well)
+          if ((rows - m) % 16 != 0 && rows - m < kK)
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
           fence_after_sync();
           const uint32_t at = base + s * kStageBytes;
           const uint64_t zd = operand(at, 8192), xd = operand(at + kSideBytes, 8192);
@@ -555,7 +724,17 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
                pack2(vb[4 * i + 6], vb[4 * i + 7], T()));
         }
         __syncwarp();
-        write_rows<T, 4, 4>(stage, out, P.D, min(32, P.Z - z0), d0 + c, P.D, 0, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int z = lane / 4 + 8 * i, d = d0 + c + 8 * (lane % 4);
+          if (z0 + z < P.Z && d < P.D) {
+            uint4 v;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(stage + z * kPitch + (lane % 4) * 16));
+            *reinterpret_cast<uint4*>(out + (long long)z * P.D + d) = v;
+          }
+        }
         __syncwarp();
       }
     }
@@ -593,6 +772,21 @@ bool encode(CUtensorMap* m, const void* p, int dtype, long long inner, long long
   return encoder()(m, dtype == A2AV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                    3, const_cast<void*>(p), dims, strides, box, steps,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A gated expert's weights [K][2][N][D] as [K][N / 8][2][8][D]: a box has
+// eight rows of the first half, their eight partners, the next eight...
+bool encode_gated(CUtensorMap* m, const void* p, int dtype, long long D, long long N, long long K) {
+  const cuuint64_t dims[5] = {(cuuint64_t)D, 8, 2, (cuuint64_t)N / 8, (cuuint64_t)K};
+  const cuuint64_t strides[4] = {(cuuint64_t)D * 2, (cuuint64_t)(N * D) * 2, (cuuint64_t)D * 16,
+                                 (cuuint64_t)(N * D) * 4};
+  const cuuint32_t box[5] = {64, 8, 2, 8, 1}, steps[5] = {1, 1, 1, 1, 1};
+  return encoder()(m, dtype == A2AV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                   5, const_cast<void*>(p), dims, strides, box, steps,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -640,9 +834,13 @@ bool a2av_expert_mma(a2av_handle* h, const A2avExperts& P, int dtype, int direct
         made = encode(&M.rows[p], n_side, dtype, P.D, rows, 1, kK) &&
                encode(&M.weights[p], m_side, dtype, P.Z, rows, 1, kK);
     } else {
-      if (rows > 0) made = encode(&M.rows[p], n_side, dtype, C, rows, 1, kRowBox);
-      made = made && encode(&M.weights[p], m_side, dtype, P.D, P.Z, P.g.K,
-                            direction == 1 ? kK : gated ? 16 : 128);
+      if (rows > 0)
+        made = encode(&M.rows[p], n_side, dtype, C, rows, 1, kGranule) &&
+               encode(&M.rows32[p], n_side, dtype, C, rows, 1, 32) &&
+               encode(&M.rows128[p], n_side, dtype, C, rows, 1, 128);
+      made = made && (gated ? encode_gated(&M.weights[p], m_side, dtype, P.D, P.N, P.g.K)
+                            : encode(&M.weights[p], m_side, dtype, P.D, P.Z, P.g.K,
+                                     direction == 1 ? kK : 128));
     }
     if (!made) return false;
     M.out[p] = out;
