@@ -147,7 +147,7 @@ typedef struct {
  * result is rounded once.  Rows of NaN stay within their own results.
  *
  *  rows_ptrs          HOST array of W: peer p's x, [rows_per_peer[p]][D].  Read only.
- *  rows_per_peer      HOST int64 [W], 0 .. 2^31 - 1: the rows each peer's buffers hold.
+ *  rows_per_peer      HOST int64 [W], up to 2^31 - 1 together: the rows each peer's buffers hold.
  *                     Rows past the sum of its groups are neither used nor written.
  *  counts_dev         DEVICE int64 [W][W * K], as a2av_route writes it.
  *  weight_ptrs        HOST array of W: [K][Z][D].

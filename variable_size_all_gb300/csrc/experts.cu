@@ -240,9 +240,11 @@ int expert_params(a2av_handle* h, const a2av_expert_t* c, const int64_t* rows_pe
   const int rc = shape_ok(c, h->W);
   if (rc != A2AV_OK) return rc;
   std::memset(P, 0, sizeof(*P));
+  int64_t all = 0;
   for (int p = 0; p < h->W; ++p) {
     if (rows_per_peer[p] < 0) return A2AV_ERR_INVALID_ARG;
-    if (rows_per_peer[p] > kMaxCount) return A2AV_ERR_UNSUPPORTED;
+    if (rows_per_peer[p] > kMaxCount - all) return A2AV_ERR_UNSUPPORTED;
+    all += rows_per_peer[p];
     P->g.cap[p] = rows_per_peer[p];
   }
   P->g.counts = reinterpret_cast<const long long*>(counts);
@@ -331,7 +333,7 @@ extern "C" int a2av_expert_matmul(a2av_handle* h, const a2av_expert_t* shape,
 extern "C" int64_t a2av_expert_matmul_workspace_bytes(int world_size, const a2av_expert_t* shape,
                                                       int64_t total_rows) {
   if (world_size < 1 || world_size > kW || total_rows < 0 ||
-      total_rows > kMaxCount * world_size || shape_ok(shape, world_size) != A2AV_OK)
+      total_rows > kMaxCount || shape_ok(shape, world_size) != A2AV_OK)
     return -1;
   if (shape->activation == A2AV_ACT_NONE && !shape->gated) return 0;
   const int64_t Z = shape->gated ? 2 * shape->out_features : shape->out_features;

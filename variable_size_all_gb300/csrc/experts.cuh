@@ -41,9 +41,9 @@ using ExpertParams = A2avExperts;
 // every 2^shift-th group; the groups between two entries are walked.
 constexpr int kEntries = 512;
 struct GroupTable {
-  long long rows[kEntries + 1];
+  int rows[kEntries + 1];
   long long tiles[kEntries + 1];
-  long long peer_base[kW + 1];  // rows before peer p
+  int peer_base[kW + 1];  // rows before peer p
   long long warp_rows[32], warp_tiles[32];
   int shift, entries, bad;
 };
@@ -117,18 +117,23 @@ __device__ bool build_groups(const GroupParams& G, GroupTable& g, int tile_rows,
   }
   for (int s = s0; s < s1; ++s) {
     if ((s & ((1 << shift) - 1)) == 0) {
-      g.rows[s >> shift] = r0;
+      g.rows[s >> shift] = (int)r0;
       g.tiles[s >> shift] = t0;
     }
-    if (s % E == 0) g.peer_base[s / E] = r0;
+    if (r0 > kMaxCount) {  // more than all the buffers hold together
+      g.bad = 1;
+      break;
+    }
+    if (s % E == 0) g.peer_base[s / E] = (int)r0;
     const long long c = group_count(G, s);
     if (c < 0 || c > kMaxCount) break;
     r0 += c;
     t0 += group_tiles(c, tile_rows, features);
     if (s == n - 1) {
-      g.rows[entries] = r0;
+      if (r0 > kMaxCount) g.bad = 1;
+      g.rows[entries] = (int)r0;
       g.tiles[entries] = t0;
-      g.peer_base[G.W] = r0;
+      g.peer_base[G.W] = (int)r0;
     }
   }
   __syncthreads();

@@ -28,17 +28,18 @@ constexpr int kStageBytes = 2 * kSideBytes;
 constexpr int kStages = 6;
 constexpr int kGranule = 8;
 constexpr int kTileGranules = kN / kGranule;
+constexpr int kBoxes = 5;
 constexpr int kSlots = 3;             // tiles the scheduler may be ahead
-constexpr int kMmaThreads = 256;
+constexpr int kEpilogueWarps = 8;     // two for each quarter of the TMEM lanes
+constexpr int kMmaThreads = 128 + 32 * kEpilogueWarps;
 constexpr unsigned kTmemColumns = 512;
 constexpr int kPitch = 80;            // bytes between staged rows: 8 of them hit all banks once
 constexpr int kStaging = 32 * kPitch; // per epilogue warp
-constexpr size_t kMmaSmem = 1024 + (size_t)kStages * kStageBytes + 4 * kStaging;
+constexpr size_t kMmaSmem = 1024 + (size_t)kStages * kStageBytes + kEpilogueWarps * kStaging;
 
 struct MmaParams {
-  CUtensorMap rows[kW];     // N side: [rows][C] in boxes of a granule; x of the weights' gradient
-  CUtensorMap rows32[kW];   // the same in boxes of 32 and 128 rows
-  CUtensorMap rows128[kW];
+  CUtensorMap rows[kBoxes][kW];  // N side: [rows][C] in boxes of 1, 2 .. 16 granules
+                                 // (weights' gradient: x, in [0])
   CUtensorMap weights[kW];  // M side: [K][..][..], or dz
   GroupParams g;
   const void* bias[kW];
@@ -71,7 +72,7 @@ struct Slot {
 
 // Tiles before each expert.
 struct TileTable {
-  long long first[A2AV_MAX_DISPATCH_KEYS + 1];
+  int first[A2AV_MAX_DISPATCH_KEYS + 1];
 };
 
 // By the whole block, after build_groups.
@@ -91,11 +92,11 @@ __device__ void build_tiles(const GroupParams& G, GroupTable& g, TileTable& tt, 
         find_group(G, g, (p * G.W + r) * G.K + e, &rows);
         granules += (rows + kGranule - 1) / kGranule;
       }
-      if (pass == 1) tt.first[x] = at + sum;
+      if (pass == 1) tt.first[x] = (int)(at + sum);
       sum += group_tiles(granules, kTileGranules, features);
     }
     if (pass == 1) {
-      if (x1 == E && x0 < E) tt.first[E] = at + sum;
+      if (x1 == E && x0 < E) tt.first[E] = (int)(at + sum);
       break;
     }
     long long inc = sum;
@@ -165,11 +166,11 @@ __device__ __forceinline__ void pair_begin(Bars& b, int warp, uint32_t rank) {
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(smem_addr(&b.acc_full[i]), 1);
-      bar_init(smem_addr(&b.acc_empty[i]), 8);
+      bar_init(smem_addr(&b.acc_empty[i]), 2 * kEpilogueWarps);
     }
     for (int i = 0; i < kSlots; ++i) {
       bar_init(smem_addr(&b.slot_full[i]), 1);
-      bar_init(smem_addr(&b.slot_empty[i]), rank == 0 ? 6 : 5);
+      bar_init(smem_addr(&b.slot_empty[i]), kEpilogueWarps + (rank == 0 ? 2 : 1));
     }
     bar_init_done();
   }
@@ -235,22 +236,31 @@ __device__ __forceinline__ void write_rows(uint32_t stage, T* to, long long ld, 
   }
 }
 
-// The other way: rows into the warp's staging.
+// The other way, in two steps: rows into registers, and from there into the
+// warp's staging (the loads are in flight while the sums are taken).
 template <typename T, int kPieces>
-__device__ __forceinline__ void read_rows(uint32_t stage, const T* from, long long ld,
+__device__ __forceinline__ void load_rows(uint4 (&v)[kPieces], const T* from, long long ld,
                                           const Slot& slot, int j, int f, int F, int lane) {
   constexpr int kPer = 32 / kPieces;
   const int piece = lane % kPieces;
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     const int row = lane / kPieces + kPer * i, gr = j + row / kGranule, in = row % kGranule;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (in < slot.n[gr] && f + 8 * piece < F)
-      v = *reinterpret_cast<const uint4*>(from + (long long)(slot.row[gr] + in) * ld + f + 8 * piece);
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + row * kPitch + piece * 16),
-                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (gr < kTileGranules && in < slot.n[gr] && f + 8 * piece < F)
+      v[i] = *reinterpret_cast<const uint4*>(from + (long long)(slot.row[gr] + in) * ld + f + 8 * piece);
   }
+}
+
+template <int kPieces>
+__device__ __forceinline__ void keep_rows(uint32_t stage, const uint4 (&v)[kPieces], int lane) {
+  constexpr int kPer = 32 / kPieces;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                     stage + (lane / kPieces + kPer * i) * kPitch + lane % kPieces * 16),
+                 "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w)
+                 : "memory");
 }
 
 // Sums of 16 features (lanes) x 32 rows (columns) to the staged rows' bytes
@@ -296,39 +306,47 @@ __device__ __forceinline__ void apply_act(int act, float (&v)[16]) {
 }
 
 // ------------------------------------------------- rows times weights --
-// A CTA's half of a tile's granules as copies of 128, 32 or 8 rows: a run of
-// consecutive rows takes the largest it fills, the last run also one that it
-// does not, where the half has room (what it brings past the run is in no
-// result).  Returns the bytes.
+// A CTA's half of a tile's granules as copies: a run of g consecutive granules
+// takes the largest box of 2^b granules that it fills, and the same again so
+// that it ends with the run (both bring the same bytes where they overlap).
+// The half's last run takes one larger box instead where there is room: what
+// that brings past the run is in no result.  So a run costs one or two copies;
+// issuing them is what bounds tiles of many short groups.  Returns the bytes.
 struct Copies {
   int count;
   int row[kTileGranules / 2];
-  int at[kTileGranules / 2];    // bytes into the stage's N side
-  int size[kTileGranules / 2];  // granules
+  int at[kTileGranules / 2];   // granules into the stage's N side
+  int box[kTileGranules / 2];  // 2^box granules
 };
 
 __device__ __forceinline__ unsigned plan_copies(const Slot& slot, uint32_t rank, Copies& c) {
   const int half = (slot.granules + 1) / 2;
   const int j0 = rank == 0 ? 0 : half, j1 = rank == 0 ? half : slot.granules;
-  unsigned bytes = 0;
+  unsigned granules = 0;
   int n = 0;
   for (int j = j0; j < j1;) {
+    const int row = slot.row[j];
     int run = 1;
-    while (j + run < j1 && slot.row[j + run] == slot.row[j] + kGranule * run) ++run;
-    const bool last = j + run == j1;
-    const int room = kTileGranules / 2 - (j - j0);
-    const int size = room == 16 && (run == 16 || (last && run > 8)) ? 16
-                     : run >= 4 || (last && run >= 2 && room >= 4)  ? 4
-                                                                    : 1;
-    c.row[n] = slot.row[j];
-    c.at[n] = (j - j0) * 1024;
-    c.size[n] = size;
+    while (j + run < j1 && slot.row[j + run] == row + kGranule * run) ++run;
+    int box = 31 - __clz(run);
+    if (j + run == j1 && (1 << box) < run && j - j0 + (2 << box) <= kTileGranules / 2) ++box;
+    c.row[n] = row;
+    c.at[n] = j - j0;
+    c.box[n] = box;
     ++n;
-    bytes += size * 1024;
-    j += size;
+    granules += 1u << box;
+    if ((1 << box) < run) {
+      const int by = run - (1 << box);
+      c.row[n] = row + by * kGranule;
+      c.at[n] = j - j0 + by;
+      c.box[n] = box;
+      ++n;
+      granules += 1u << box;
+    }
+    j += run;
   }
   c.count = n;
-  return bytes;
+  return granules * 1024;
 }
 
 // kMn: the weights' contraction runs over their rows (the rows' gradient), so
@@ -372,47 +390,55 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
       if (lane == 0) bar_arrive_here(smem_addr(&b.slot_full[sl]));
     }
     if (!ok && lane == 0) note_error(P.g.status, A2AV_ERR_TIMEOUT);
-  } else if (warp == 0 && lane == 0) {
+  } else if (warp == 0) {
     // ------------------------------------------------------ copies --
+    // lane l issues the l-th copy of every stage: the weights' first
+    constexpr int kOwn = kMn ? 2 : 1;
     const uint32_t full0 = map_to(smem_addr(&b.full[0]), 0);
     unsigned it = 0;
     for (long long t = pair; t < tiles && ok; t += pairs, ++i) {
       const unsigned sl = i % kSlots;
-      if (!bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1)) {
-        ok = false;
-        break;
-      }
+      ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
+      if (!ok) break;
       const int p = slots[sl].p, e = slots[sl].e, f0 = slots[sl].f + kMyF * rank;
-      const unsigned bytes = kSideBytes + plan_copies(slots[sl], rank, copies);
-      bar_arrive_here(smem_addr(&b.slot_empty[sl]));
-      const CUtensorMap* wm = &P.weights[p];
+      unsigned bytes = 0;
+      if (lane == 0) {
+        bytes = kSideBytes + plan_copies(slots[sl], rank, copies);
+        bar_arrive_here(smem_addr(&b.slot_empty[sl]));
+      }
+      __syncwarp();
+      const int n = lane - kOwn;
+      const bool mine = n < copies.count;
+      const CUtensorMap* map = &P.weights[p];
+      int row = 0;
+      uint32_t to = kMn && n == -1 ? kSideBytes / 2 : 0;
+      if (n >= 0 && mine) {
+        map = &P.rows[copies.box[n]][p];
+        row = copies.row[n];
+        to = kSideBytes + copies.at[n] * 1024;
+      }
       for (int kb = 0; kb < blocks; ++kb, ++it) {
         const unsigned s = it % kStages;
-        if (!bar_wait(smem_addr(&b.empty[s]), ((it / kStages) & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(kAll, bar_wait(smem_addr(&b.empty[s]), ((it / kStages) & 1) ^ 1));
+        if (!ok) break;
         const uint32_t full = full0 + s * 8;
-        const uint32_t at = base + s * kStageBytes;
-        bar_arrive_tx(full, bytes);
+        const uint32_t at = base + s * kStageBytes + to;
         const int c = kb * kK;
-        if (kMn) {
-          tma_load(at, wm, f0, c, e, full);
-          tma_load(at + kSideBytes / 2, wm, f0 + 64, c, e, full);
+        if (lane == 0) bar_arrive_tx(full, bytes);
+        __syncwarp();
+        if (n >= 0) {
+          if (mine) tma_load(at, map, c, row, 0, full);
+        } else if (kMn) {
+          tma_load(at, map, f0 + 64 * lane, c, e, full);
         } else if (kGated) {
-          tma_load5(at, wm, c, 0, 0, f0 / 8, e, full);
+          tma_load5(at, map, c, 0, 0, f0 / 8, e, full);
         } else {
-          tma_load(at, wm, c, f0, e, full);
-        }
-        for (int n = 0; n < copies.count; ++n) {
-          const CUtensorMap* xm = copies.size[n] == 16  ? &P.rows128[p]
-                                  : copies.size[n] == 4 ? &P.rows32[p]
-                                                        : &P.rows[p];
-          tma_load(at + kSideBytes + copies.at[n], xm, c, copies.row[n], 0, full);
+          tma_load(at, map, c, f0, e, full);
         }
       }
+      __syncwarp();
     }
-    if (!ok || !settle(b, it)) {
+    if (lane == 0 && (!ok || !settle(b, it))) {
       note_error(P.g.status, A2AV_ERR_TIMEOUT);
       drain(b, rank, it);
     }
@@ -453,9 +479,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     if (!ok) note_error(P.g.status, A2AV_ERR_TIMEOUT);
   } else if (warp >= 4) {
     // ---------------------------------------------------- epilogue --
-    const int q = warp - 4;
-    const uint32_t stage = base + kStages * kStageBytes + q * kStaging;
+    // two warps share a quarter of the lanes, with every other 32 columns each
+    const int q = warp % 4, c0 = warp >= 8 ? 32 : 0;
+    const uint32_t stage = base + kStages * kStageBytes + (warp - 4) * kStaging;
     const uint32_t empty0 = map_to(smem_addr(&b.acc_empty[0]), 0);
+    constexpr int kPieces = kGated ? 2 : 4;
     for (long long t = pair; t < tiles && ok; t += pairs, ++i) {
       const unsigned sl = i % kSlots, buf = i & 1;
       ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
@@ -478,17 +506,20 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
       T* out = static_cast<T*>(P.out[p]);
       T* pre = static_cast<T*>(P.pre[p]);
       const T* res = static_cast<const T*>(P.residual[p]);
+      uint4 held[kPieces];  // of the residual
+      if (res != nullptr) load_rows<T, kPieces>(held, res, P.F, slot, c0 / kGranule, f, P.F, lane);
       ok = __all_sync(kAll, bar_wait(smem_addr(&b.acc_full[buf]), (i >> 1) & 1));
       if (!ok) break;
       fence_after_sync();
-      for (int c = 0; c < columns; c += 32) {
+      if (c0 >= columns && lane == 0) bar_arrive(empty0 + buf * 8);  // nothing to take
+      for (int c = c0; c < columns; c += 64) {
         const int j = c / kGranule;
         const uint32_t at = b.tmem + buf * kN + c + ((uint32_t)(32 * q) << 16);
         float va[16], vb[16];
         tmem_load(at, va);
         tmem_load(at + (16u << 16), vb);
         tmem_load_wait();
-        if (c + 32 >= columns) {  // the last of the tile's sums: the buffer is free
+        if (c + 64 >= columns) {  // the warp's last of the tile's sums: its share of the buffer is free
           fence_before_sync();
           __syncwarp();
           if (lane == 0) bar_arrive(empty0 + buf * 8);
@@ -522,9 +553,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
         } else {
           apply_act(P.act, vb);
         }
-        constexpr int kPieces = kGated ? 2 : 4;
         if (res != nullptr) {
-          read_rows<T, kPieces>(stage, res, P.F, slot, j, f, P.F, lane);
+          keep_rows<kPieces>(stage, held, lane);
+          load_rows<T, kPieces>(held, res, P.F, slot, j + 8, f, P.F, lane);
           __syncwarp();
           add_block<T>(stage, 0, va, lane);
           if (!kGated) add_block<T>(stage, 32, vb, lane);
@@ -594,7 +625,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
           tma_load(at, &P.weights[p], z0, row, 0, bar);
           tma_load(at + 8192, &P.weights[p], z0 + 64, row, 0, bar);
           for (int i = 0; i < copies; ++i)
-            tma_load(at + kSideBytes + i * 8192, &P.rows[p], d0 + half * rank + 64 * i, row, 0, bar);
+            tma_load(at + kSideBytes + i * 8192, &P.rows[0][p], d0 + half * rank + 64 * i, row, 0, bar);
         }
       }
     }
@@ -678,8 +709,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     }
     if (!ok) note_error(P.g.status, A2AV_ERR_TIMEOUT);
   } else if (warp >= 4) {
-    const int q = warp - 4;
-    const uint32_t stage = base + kStages * kStageBytes + q * kStaging;
+    const int q = warp % 4, c0 = warp >= 8 ? 32 : 0;
+    const uint32_t stage = base + kStages * kStageBytes + (warp - 4) * kStaging;
     const uint32_t empty0 = map_to(smem_addr(&b.acc_empty[0]), 0);
     // the address a lane gives for its row of the 8 x 8 blocks (below)
     const uint32_t put = stage + (((lane >> 3) & 1) * 8 + (lane & 7)) * kPitch + (lane >> 4) * 16;
@@ -702,14 +733,15 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
       }
       const int columns = min(kN, P.D - d0);
       T* out = static_cast<T*>(P.out[p]) + ((long long)e * P.Z + z0) * P.D;
-      for (int c = 0; c < columns; c += 32) {
+      if (c0 >= columns && all > 0 && lane == 0) bar_arrive(empty0 + buf * 8);
+      for (int c = c0; c < columns; c += 64) {
         float va[16] = {}, vb[16] = {};
         if (all > 0) {
           const uint32_t at = b.tmem + buf * kN + c + ((uint32_t)(32 * q) << 16);
           tmem_load(at, va);
           tmem_load(at + (16u << 16), vb);
           tmem_load_wait();
-          if (c + 32 >= columns) {
+          if (c + 64 >= columns) {
             fence_before_sync();
             __syncwarp();
             if (lane == 0) bar_arrive(empty0 + buf * 8);
@@ -831,13 +863,11 @@ bool a2av_expert_mma(a2av_handle* h, const A2avExperts& P, int dtype, int direct
     bool made = true;
     if (direction == 2) {
       if (rows > 0)
-        made = encode(&M.rows[p], n_side, dtype, P.D, rows, 1, kK) &&
+        made = encode(&M.rows[0][p], n_side, dtype, P.D, rows, 1, kK) &&
                encode(&M.weights[p], m_side, dtype, P.Z, rows, 1, kK);
     } else {
-      if (rows > 0)
-        made = encode(&M.rows[p], n_side, dtype, C, rows, 1, kGranule) &&
-               encode(&M.rows32[p], n_side, dtype, C, rows, 1, 32) &&
-               encode(&M.rows128[p], n_side, dtype, C, rows, 1, 128);
+      for (int i = 0; i < kBoxes && made && rows > 0; ++i)
+        made = encode(&M.rows[i][p], n_side, dtype, C, rows, 1, kGranule << i);
       made = made && (gated ? encode_gated(&M.weights[p], m_side, dtype, P.D, P.N, P.g.K)
                             : encode(&M.weights[p], m_side, dtype, P.D, P.Z, P.g.K,
                                      direction == 1 ? kK : 128));
