@@ -170,9 +170,9 @@ int a2av_expert_matmul(a2av_handle *h, const a2av_expert_t *shape, const void *c
 
 /*
  * a2av_expert_matmul_workspace_bytes -- device workspace that
- * a2av_expert_matmul_backward needs for W peers of `total_rows` rows together;
- * 0 when the shape has neither activation nor gate, -1 for a shape that would
- * be rejected.
+ * a2av_expert_matmul_backward needs for W peers of `total_rows` rows together
+ * (dz, where there is an activation or a gate, and what the groups have over
+ * multiples of 64 rows); -1 for a shape or a count that would be rejected.
  */
 int64_t a2av_expert_matmul_workspace_bytes(int world_size, const a2av_expert_t *shape,
                                            int64_t total_rows);
@@ -195,7 +195,7 @@ int64_t a2av_expert_matmul_workspace_bytes(int world_size, const a2av_expert_t *
  *  d_bias_ptrs        HOST array of W: [K][Z], or NULL.
  *  workspace          DEVICE scratch, 256-byte aligned, at least
  *                     a2av_expert_matmul_workspace_bytes(W, shape, sum of rows_per_peer),
- *                     not shared with a call in flight; NULL when that is 0.
+ *                     not shared with a call in flight (NULL for no rows at all).
  */
 int a2av_expert_matmul_backward(a2av_handle *h, const a2av_expert_t *shape,
                                 const void *const *rows_ptrs, const int64_t *rows_per_peer,

@@ -313,7 +313,10 @@ def test_refusals():
         shape = a2av.A2avExpert(2, 64, 32, a2av.F32, 0, 0)
         assert a2av.a2av_expert_matmul_workspace_bytes(1, shape, 10) == -1
         shape = a2av.A2avExpert(2, 64, 32, a2av.BF16, 3, 1)
-        assert a2av.a2av_expert_matmul_workspace_bytes(1, shape, 10) == 10 * 64 * 2
+        # dz, and the packed remainders of dz and x: at most every row, and 63 rows of zeros an expert
+        assert a2av.a2av_expert_matmul_workspace_bytes(1, shape, 10) == 10 * 64 * 2 + (10 + 2 * 63) * (64 + 64) * 2
+        assert a2av.a2av_expert_matmul_workspace_bytes(1, shape, -1) == -1
+        assert a2av.a2av_expert_matmul_workspace_bytes(1, shape, 1 << 31) == -1
         n, ptr = c["held"], lambda ts: [t.data_ptr() for t in ts]
         call = lambda shape, **kw: a2av.a2av_expert_matmul(
             eng.handle, shape, kw.get("x", ptr(c["x"])), kw.get("n", n), kw.get("c", c["d_counts"].data_ptr()),

@@ -21,12 +21,13 @@ __global__ void __launch_bounds__(kPlainThreads)
                         long long wf, long long wc) {
   chain();
   __shared__ GroupTable g;
+  __shared__ GroupTiles tiles;
   __shared__ float xs[kDepth][kTile + 1], ws[kGated ? 2 : 1][kDepth][kTile + 1];
   const int nf = (int)((F + kTile - 1) / kTile);
-  if (!build_groups(P.g, g, kTile, nf)) return;
+  if (!build_groups(P.g, g, &tiles, kTile, nf)) return;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  for (long long tile = blockIdx.x; tile < g.tiles[g.entries]; tile += gridDim.x) {
-    const GroupTile gt = find_tile(P.g, g, tile, kTile, nf);
+  for (long long tile = blockIdx.x; tile < tiles.first[g.entries]; tile += gridDim.x) {
+    const GroupTile gt = find_tile(P.g, g, tiles, tile, kTile, nf);
     const long long f0 = gt.local % nf * kTile, m0 = gt.local / nf * kTile;
     const T* x = static_cast<const T*>(P.x[gt.p]) + (gt.first + m0) * C;
     const T* w = static_cast<const T*>(P.w[gt.p]) + (long long)gt.e * P.Z * P.D;
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(kPlainThreads)
   chain();
   __shared__ GroupTable g;
   __shared__ float zs[kDepth][kTile + 1], xs[kDepth][kTile + 1];
-  if (!build_groups(P.g, g, kTile, 1)) return;
+  if (!build_groups(P.g, g)) return;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int W = P.g.W, K = P.g.K;
   const long long nz = (P.Z + kTile - 1) / kTile, nd = (P.D + kTile - 1) / kTile;
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(256)
     expert_dz_kernel(const __grid_constant__ ExpertParams P) {
   chain();
   __shared__ GroupTable g;
-  if (!build_groups(P.g, g, 1, 1)) return;
+  if (!build_groups(P.g, g)) return;
   using V = Vec<T, N>;
   const long long nv = P.N / N;
   for (int p = 0; p < P.g.W; ++p) {
@@ -174,34 +175,56 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// d_bias[e][z]: a block takes 32 columns of an expert, its 8 warps every
-// eighth row; their sums are joined in the order of the warps.
-template <typename T>
-__global__ void __launch_bounds__(256)
+// d_bias[e][z]: a block takes 16 vectors of N columns of an expert, each of its
+// 32 half warps every 32nd row; their sums are joined in shared memory in a
+// fixed order.  It reads dz once, so the memory's rate is its floor.
+constexpr int kBiasThreads = 512, kBiasRows = kBiasThreads / 16;
+
+template <typename T, int N>
+__global__ void __launch_bounds__(kBiasThreads)
     expert_dbias_kernel(const __grid_constant__ ExpertParams P) {
   chain();
   __shared__ GroupTable g;
-  __shared__ float part[8][32];
-  if (!build_groups(P.g, g, 1, 1)) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ float part[kBiasRows][16 * N + 1];
+  if (!build_groups(P.g, g)) return;
+  using V = Vec<T, N>;
+  const int at = threadIdx.x % 16, team = threadIdx.x / 16;
   const int W = P.g.W, K = P.g.K;
-  const long long nz = (P.Z + 31) / 32;
+  const long long nz = (P.Z + 16 * N - 1) / (16 * N);
   for (long long tile = blockIdx.x; tile < (long long)W * K * nz; tile += gridDim.x) {
     const int pe = (int)(tile / nz), p = pe / K, e = pe % K;
-    const long long z = tile % nz * 32 + lane;
-    float sum = 0.0f;
+    const long long z = tile % nz * 16 * N + at * N;
+    float sum[N] = {};
     for (int r = 0; r < W; ++r) {
       int rows;
       const long long first = find_group(P.g, g, (p * W + r) * K + e, &rows);
-      if (z < P.Z)
-        for (int m = warp; m < rows; m += 8)
-          sum += to_float(static_cast<const T*>(P.dy[p])[(first + m) * P.Z + z]);
+      if (z >= P.Z) continue;
+      const T* from = static_cast<const T*>(P.dy[p]) + first * P.Z + z;
+      constexpr int kAhead = 4;  // loads in flight
+      for (int m = team; m < rows; m += kAhead * kBiasRows) {
+        V v[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          if (m + u * kBiasRows < rows)
+            v[u] = *reinterpret_cast<const V*>(from + (long long)(m + u * kBiasRows) * P.Z);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          if (m + u * kBiasRows < rows) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) sum[k] += to_float(v[u].v[k]);
+          }
+      }
     }
-    part[warp][lane] = sum;
+#pragma unroll
+    for (int k = 0; k < N; ++k) part[team][at * N + k] = sum[k];
     __syncthreads();
-    if (warp == 0 && z < P.Z) {
-      for (int w = 1; w < 8; ++w) sum += part[w][lane];
-      static_cast<T*>(P.d_bias[p])[e * P.Z + z] = from_float<T>(sum);
+    for (int c = threadIdx.x; c < 16 * N; c += kBiasThreads) {
+      const long long col = tile % nz * 16 * N + c;
+      if (col < P.Z) {
+        float all = 0.0f;
+        for (int i = 0; i < kBiasRows; ++i) all += part[i][c];
+        static_cast<T*>(P.d_bias[p])[e * P.Z + col] = from_float<T>(all);
+      }
     }
     __syncthreads();
   }
@@ -288,7 +311,10 @@ cudaError_t launch_backward(a2av_handle* h, ExpertParams P, void* const* d_rows,
     e = launch_chained(expert_plain_wgrad_kernel<T>, grid, kPlainThreads, 0, s, h->pdl, P);
   if (e != cudaSuccess) return e;
   if (P.d_bias[0] != nullptr) {
-    e = launch_chained(expert_dbias_kernel<T>, grid, 256, 0, s, h->pdl, P);
+    bool vec = P.Z % 8 == 0;
+    for (int p = 0; p < h->W; ++p) vec = vec && aligned_to(P.dy[p], 16);
+    e = launch_chained(vec ? expert_dbias_kernel<T, 8> : expert_dbias_kernel<T, 1>, grid,
+                       kBiasThreads, 0, s, h->pdl, P);
     if (e != cudaSuccess) return e;
   }
   if (d_rows != nullptr) {
@@ -335,9 +361,11 @@ extern "C" int64_t a2av_expert_matmul_workspace_bytes(int world_size, const a2av
   if (world_size < 1 || world_size > kW || total_rows < 0 ||
       total_rows > kMaxCount || shape_ok(shape, world_size) != A2AV_OK)
     return -1;
-  if (shape->activation == A2AV_ACT_NONE && !shape->gated) return 0;
   const int64_t Z = shape->gated ? 2 * shape->out_features : shape->out_features;
-  return total_rows * Z * dtype_bytes(shape->dtype);
+  const int64_t dz = shape->activation == A2AV_ACT_NONE && !shape->gated ? 0 : total_rows * Z;
+  const int64_t tails = a2av_expert_tail_rows(world_size, shape->experts_per_peer, total_rows);
+  const int64_t size = dtype_bytes(shape->dtype);
+  return (dz * size + 255) / 256 * 256 + tails * (Z + shape->in_features) * size;
 }
 
 extern "C" int a2av_expert_matmul_backward(
@@ -362,18 +390,18 @@ extern "C" int a2av_expert_matmul_backward(
       !take(P.d_w, d_weight_ptrs, W, nullptr, size) ||
       !take(P.d_bias, d_bias_ptrs, W, nullptr, size))
     return A2AV_ERR_INVALID_ARG;
-  if (dz_needed) {
-    int64_t total = 0;
-    for (int p = 0; p < W; ++p) total += rows_per_peer[p];
-    if (total > 0 && (workspace == nullptr || !aligned_to(workspace, 256) ||
-                      workspace_bytes < total * P.Z * size))
-      return A2AV_ERR_INVALID_ARG;
-    int64_t at = 0;
-    for (int p = 0; p < W; ++p) {
-      P.dz[p] = static_cast<unsigned char*>(workspace) + at * P.Z * size;
-      at += rows_per_peer[p];
-    }
+  int64_t total = 0;
+  for (int p = 0; p < W; ++p) total += rows_per_peer[p];
+  const int64_t need = a2av_expert_matmul_workspace_bytes(W, shape, total);
+  if (workspace_bytes < need || !aligned_to(workspace, 256) || (need > 0 && workspace == nullptr))
+    return A2AV_ERR_INVALID_ARG;
+  int64_t at = 0;
+  for (int p = 0; p < W && dz_needed; ++p) {
+    P.dz[p] = static_cast<unsigned char*>(workspace) + at * P.Z * size;
+    at += rows_per_peer[p];
   }
+  P.tails = static_cast<unsigned char*>(workspace) + (at * P.Z * size + 255) / 256 * 256;
+  P.tail_rows = a2av_expert_tail_rows(W, P.g.K, total);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
       shape->dtype == A2AV_BF16

@@ -28,6 +28,8 @@ struct A2avExperts {
   void* dz[A2AV_MAX_RANKS];
   void* d_w[A2AV_MAX_RANKS];
   void* d_bias[A2AV_MAX_RANKS];
+  void* tails;               // workspace of the weights' gradient
+  long long tail_rows;
   long long D, N, Z;
   int act, gated;
 };
@@ -42,10 +44,15 @@ using ExpertParams = A2avExperts;
 constexpr int kEntries = 512;
 struct GroupTable {
   int rows[kEntries + 1];
-  long long tiles[kEntries + 1];
   int peer_base[kW + 1];  // rows before peer p
   long long warp_rows[32], warp_tiles[32];
   int shift, entries, bad;
+};
+
+// The tiles before every 2^shift-th group, for kernels whose tiles are cut
+// from single groups.
+struct GroupTiles {
+  long long first[kEntries + 1];
 };
 
 struct GroupTile {
@@ -69,7 +76,8 @@ __device__ __forceinline__ long long group_tiles(long long n, int tile_rows, int
 
 // By the whole block.  False (in every thread) when a count is negative or a
 // peer's rows do not fit its buffers; block 0 then records A2AV_ERR_BAD_SPLITS.
-__device__ bool build_groups(const GroupParams& G, GroupTable& g, int tile_rows, int features) {
+__device__ bool build_groups(const GroupParams& G, GroupTable& g, GroupTiles* gt = nullptr,
+                             int tile_rows = 1, int features = 1) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int E = G.W * G.K, n = G.W * E;
   if (tid == 0) {
@@ -118,7 +126,7 @@ __device__ bool build_groups(const GroupParams& G, GroupTable& g, int tile_rows,
   for (int s = s0; s < s1; ++s) {
     if ((s & ((1 << shift) - 1)) == 0) {
       g.rows[s >> shift] = (int)r0;
-      g.tiles[s >> shift] = t0;
+      if (gt != nullptr) gt->first[s >> shift] = t0;
     }
     if (r0 > kMaxCount) {  // more than all the buffers hold together
       g.bad = 1;
@@ -132,7 +140,7 @@ __device__ bool build_groups(const GroupParams& G, GroupTable& g, int tile_rows,
     if (s == n - 1) {
       if (r0 > kMaxCount) g.bad = 1;
       g.rows[entries] = (int)r0;
-      g.tiles[entries] = t0;
+      if (gt != nullptr) gt->first[entries] = t0;
       g.peer_base[G.W] = (int)r0;
     }
   }
@@ -145,17 +153,18 @@ __device__ bool build_groups(const GroupParams& G, GroupTable& g, int tile_rows,
 
 // The group that tile t (below the table's last entry) belongs to.
 __device__ __forceinline__ GroupTile find_tile(const GroupParams& G, const GroupTable& g,
-                                               long long t, int tile_rows, int features) {
-  int lo = 0, hi = g.entries;  // tiles[lo] <= t < tiles[hi]
+                                               const GroupTiles& gt, long long t, int tile_rows,
+                                               int features) {
+  int lo = 0, hi = g.entries;  // first[lo] <= t < first[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (g.tiles[mid] <= t)
+    if (gt.first[mid] <= t)
       lo = mid;
     else
       hi = mid;
   }
   int s = lo << g.shift;
-  long long first = g.rows[lo], at = g.tiles[lo];
+  long long first = g.rows[lo], at = gt.first[lo];
   long long c = g.shift == 0 ? g.rows[lo + 1] - first : group_count(G, s);
   while (true) {
     const long long more = group_tiles(c, tile_rows, features);
@@ -222,3 +231,7 @@ __device__ __forceinline__ float act_slope(int a, float z) {
 __attribute__((visibility("hidden"))) bool a2av_expert_mma(a2av_handle* h, const A2avExperts& P,
                                                            int dtype, int direction,
                                                            cudaStream_t s, cudaError_t* error);
+
+// Rows of the weights' gradient's packed remainders (see experts_mma.cu), at
+// most; and their place: Z elements each for dz, then D each for x.
+__attribute__((visibility("hidden"))) int64_t a2av_expert_tail_rows(int W, int K, int64_t rows);

@@ -40,6 +40,7 @@ constexpr size_t kMmaSmem = 1024 + (size_t)kStages * kStageBytes + kEpilogueWarp
 struct MmaParams {
   CUtensorMap rows[kBoxes][kW];  // N side: [rows][C] in boxes of 1, 2 .. 16 granules
                                  // (weights' gradient: x, in [0])
+  CUtensorMap tail_dz, tail_x;   // weights' gradient: the packed remainders
   CUtensorMap weights[kW];  // M side: [K][..][..], or dz
   GroupParams g;
   const void* bias[kW];
@@ -54,7 +55,6 @@ struct MmaParams {
 struct Bars {
   unsigned long long full[kStages];   // of the first CTA: both CTAs' copies have arrived
   unsigned long long empty[kStages];  // the products that read the stage are done
-  unsigned long long tail[kStages];   // weights' gradient: this CTA's copies, before zeroing
   unsigned long long acc_full[2];     // a tile's sums are complete
   unsigned long long acc_empty[2];    // of the first CTA: both CTAs have taken them
   unsigned long long slot_full[kSlots], slot_empty[kSlots];
@@ -162,7 +162,6 @@ __device__ __forceinline__ void pair_begin(Bars& b, int warp, uint32_t rank) {
     for (int s = 0; s < kStages; ++s) {
       bar_init(smem_addr(&b.full[s]), 2);
       bar_init(smem_addr(&b.empty[s]), 1);
-      bar_init(smem_addr(&b.tail[s]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(smem_addr(&b.acc_full[i]), 1);
@@ -370,7 +369,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
   constexpr int kMyF = kTileF / 2;            // and per CTA
   chain();
   const int nf = (P.F + kTileF - 1) / kTileF;
-  const bool good = build_groups(P.g, g, 1, 1);
+  const bool good = build_groups(P.g, g);
   if (good) build_tiles(P.g, g, tt, nf);
   pair_begin(b, warp, rank);
   const long long tiles = good ? tt.first[P.g.W * P.g.K] : 0;
@@ -576,139 +575,194 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
 }
 
 // --------------------------------------------------- weights' gradient --
-// d_w[e] = dz_e^T x_e: both operands are MN-major, the contraction is over the
-// expert's rows, group after group.  The rows of a block past its group's end
-// are the next group's; where they share a step of 16 with the group's own,
-// warp 3 zeroes them in both operands (a zero in one would not stop a NaN in
-// the other) between their arrival and the products.
+// d_w[e] = dz_e^T x_e: both operands are MN-major and the contraction is over
+// the expert's rows, in blocks of 64.  A block has rows of one expert only (a
+// foreign row's NaN would not be stopped by a zero in the other operand), so
+// what each group has over a multiple of 64 is copied together first
+// (expert_tails_kernel): the remainders of an expert's W groups one after the
+// other, zeros up to the next multiple of 64.  The products then run over the
+// groups' whole blocks where they lie and over the packed ones.
+struct TailTable {
+  int first[A2AV_MAX_DISPATCH_KEYS + 1];       // packed row of each expert, multiples of 64
+  unsigned short rows[A2AV_MAX_DISPATCH_KEYS]; // its packed rows without the zeros
+  int whole[A2AV_MAX_DISPATCH_KEYS];           // its groups' whole blocks
+};
+
+// By the whole block (of up to 1024 threads), after build_groups.
+__device__ void build_tails(const GroupParams& G, GroupTable& g, TailTable& tt) {
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int E = G.W * G.K, per = (E + nt - 1) / nt;
+  const int x0 = min(tid * per, E), x1 = min(x0 + per, E);
+  int sum = 0;
+  for (int x = x0; x < x1; ++x) {
+    const int p = x / G.K, e = x - p * G.K;
+    int tail = 0, whole = 0;
+    for (int r = 0; r < G.W; ++r) {
+      int rows;
+      find_group(G, g, (p * G.W + r) * G.K + e, &rows);
+      tail += rows % kK;
+      whole += rows / kK;
+    }
+    tt.rows[x] = (unsigned short)tail;
+    tt.whole[x] = whole;
+    sum += (tail + kK - 1) / kK * kK;
+  }
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kAll, inc, o);
+    if (lane >= o) inc += v;
+  }
+  __syncthreads();
+  if (lane == 31) g.warp_rows[warp] = inc;
+  __syncthreads();
+  int at = inc - sum;
+  for (int w = 0; w < warp; ++w) at += (int)g.warp_rows[w];
+  for (int x = x0; x < x1; ++x) {
+    tt.first[x] = at;
+    at += (tt.rows[x] + kK - 1) / kK * kK;
+    if (x == E - 1) tt.first[E] = at;
+  }
+  __syncthreads();
+}
+
+// The packed remainders: a warp takes a packed row of dz and of x.
+struct TailParams {
+  GroupParams g;
+  const void* dz[kW];
+  const void* x[kW];
+  void* to_dz;
+  void* to_x;
+  int Z, D;
+};
+
+__global__ void __launch_bounds__(256) expert_tails_kernel(const __grid_constant__ TailParams P) {
+  chain();
+  __shared__ GroupTable g;
+  __shared__ TailTable tt;
+  if (!build_groups(P.g, g)) return;
+  build_tails(P.g, g, tt);
+  const int lane = threadIdx.x & 31, W = P.g.W, K = P.g.K, E = W * K;
+  const int zv = P.Z / 8, xv = P.D / 8;  // 16-byte vectors of a row
+  const int warps = gridDim.x * (blockDim.x / 32);
+  for (int row = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; row < tt.first[E]; row += warps) {
+    int lo = 0, hi = E;  // first[lo] <= row < first[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tt.first[mid] <= row)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int p = lo / K, e = lo - p * K;
+    int in = row - tt.first[lo];
+    long long from = -1;
+    for (int r = 0; r < W && from < 0; ++r) {
+      int rows;
+      const long long first = find_group(P.g, g, (p * W + r) * K + e, &rows);
+      const int tail = rows % kK;
+      if (in < tail) from = first + (rows - tail) + in;
+      in -= tail;
+    }
+    uint4* z = static_cast<uint4*>(P.to_dz) + (long long)row * zv;
+    uint4* x = static_cast<uint4*>(P.to_x) + (long long)row * xv;
+    const uint4* z0 = static_cast<const uint4*>(P.dz[p]) + from * zv;
+    const uint4* x0 = static_cast<const uint4*>(P.x[p]) + from * xv;
+#pragma unroll 4
+    for (int i = lane; i < zv; i += 32) z[i] = from < 0 ? make_uint4(0, 0, 0, 0) : z0[i];
+#pragma unroll 4
+    for (int i = lane; i < xv; i += 32) x[i] = from < 0 ? make_uint4(0, 0, 0, 0) : x0[i];
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     expert_wgrad_kernel(const __grid_constant__ MmaParams P) {
   extern __shared__ unsigned char dynamic[];
   __shared__ GroupTable g;
+  __shared__ TailTable tt;
   __shared__ Bars b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const uint32_t base = (smem_addr(dynamic) + 1023) & ~1023u;
   chain();
-  const bool good = build_groups(P.g, g, kN, 1);
+  const bool good = build_groups(P.g, g);
+  if (good) build_tails(P.g, g, tt);
   pair_begin(b, warp, rank);
   const int W = P.g.W, K = P.g.K;
   const int nz = (P.Z + kM - 1) / kM, nd = (P.D + kN - 1) / kN;
   const long long tiles = good ? (long long)W * K * nz * nd : 0;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   bool ok = true;
-  unsigned it = 0;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
+    // ------------------------------------------------------ copies --
+    // lanes 0 and 1 copy the CTA's 128 columns of dz, lanes 2 and 3 its up to
+    // 128 columns of x, in boxes of 64 columns x 64 rows
     const uint32_t full0 = map_to(smem_addr(&b.full[0]), 0);
+    unsigned it = 0;
     for (long long t = pair; t < tiles && ok; t += pairs) {
       const int pe = (int)(t / ((long long)nz * nd)), p = pe / K, e = pe % K;
       const int z0 = (int)(t / nd % nz) * kM + 128 * rank, d0 = (int)(t % nd) * kN;
       const uint32_t half = columns_of(P.D - d0) / 2;
-      const int copies = (half + 63) / 64;
-      const unsigned bytes = kSideBytes + copies * 8192;
-      for (int r = 0; r < W && ok; ++r) {
-        int rows;
-        const long long first = find_group(P.g, g, (p * W + r) * K + e, &rows);
-        for (int m = 0; m < rows; m += kK, ++it) {
+      const int copies = 2 + (half + 63) / 64;
+      const unsigned bytes = copies * 8192;
+      const int column = lane < 2 ? z0 + 64 * lane : d0 + (int)half * (int)rank + 64 * (lane - 2);
+      for (int r = 0; r <= W && ok; ++r) {  // the groups, then the packed rows
+        int rows = tt.rows[pe];
+        long long first = tt.first[pe];
+        if (r < W) first = find_group(P.g, g, (p * W + r) * K + e, &rows);
+        const int n = r < W ? rows / kK : (rows + kK - 1) / kK;
+        const CUtensorMap* map = r < W ? (lane < 2 ? &P.weights[p] : &P.rows[0][p])
+                                       : (lane < 2 ? &P.tail_dz : &P.tail_x);
+        for (int m = 0; m < n; ++m, ++it) {
           const unsigned s = it % kStages;
-          if (!bar_wait(smem_addr(&b.empty[s]), ((it / kStages) & 1) ^ 1)) {
-            ok = false;
-            break;
-          }
-          const bool ragged = rows - m < kK && (rows - m) % 16 != 0;
-          const uint32_t bar = ragged ? smem_addr(&b.tail[s]) : full0 + s * 8;
-          const uint32_t at = base + s * kStageBytes;
-          const int row = (int)(first + m);
-          bar_arrive_tx(ragged ? map_to(bar, rank) : bar, bytes);
-          tma_load(at, &P.weights[p], z0, row, 0, bar);
-          tma_load(at + 8192, &P.weights[p], z0 + 64, row, 0, bar);
-          for (int i = 0; i < copies; ++i)
-            tma_load(at + kSideBytes + i * 8192, &P.rows[0][p], d0 + half * rank + 64 * i, row, 0, bar);
+          ok = __all_sync(kAll, bar_wait(smem_addr(&b.empty[s]), ((it / kStages) & 1) ^ 1));
+          if (!ok) break;
+          const uint32_t full = full0 + s * 8;
+          if (lane == 0) bar_arrive_tx(full, bytes);
+          __syncwarp();
+          if (lane < copies)
+            tma_load(base + s * kStageBytes + lane * 8192, map, column, (int)(first + m * kK), 0, full);
         }
       }
     }
-    if (!ok || !settle(b, it)) {
+    if (lane == 0 && (!ok || !settle(b, it))) {
       note_error(P.g.status, A2AV_ERR_TIMEOUT);
       drain(b, rank, it);
     }
-  } else if (warp == 3) {
-    const uint32_t full0 = map_to(smem_addr(&b.full[0]), 0);
-    unsigned parity = 0;  // a bit a stage
-    for (long long t = pair; t < tiles && ok; t += pairs) {
-      const int pe = (int)(t / ((long long)nz * nd)), p = pe / K, e = pe % K;
-      const int d0 = (int)(t % nd) * kN;
-      const uint32_t half = columns_of(P.D - d0) / 2;
-      const int boxes = 2 + (half + 63) / 64;
-      for (int r = 0; r < W && ok; ++r) {
-        int rows;
-        find_group(P.g, g, (p * W + r) * K + e, &rows);
-        const unsigned n = (rows + kK - 1) / kK;
-        const int left = rows % kK;
-        it += n;
-        if (left % 16 == 0) continue;
-        const unsigned s = (it - 1) % kStages;
-        ok = __all_sync(kAll, bar_wait(smem_addr(&b.tail[s]), (parity >> s) & 1));
-        if (!ok) break;
-        parity ^= 1u << s;
-        const int lines = 16 - left % 16;
-        const uint32_t at = base + s * kStageBytes + left * 128;
-        for (int i = lane; i < boxes * lines * 8; i += 32) {
-          const int box = i / (lines * 8), in = i % (lines * 8);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + box * 8192 + in * 16),
-                       "r"(0)
-                       : "memory");
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) bar_arrive(full0 + s * 8);
-      }
-    }
-    if (!ok && lane == 0) note_error(P.g.status, A2AV_ERR_TIMEOUT);
   } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ---------------------------------------------------- products --
     constexpr bool kBf16 = !__is_same(T, __half);
-    unsigned n_tile = 0;
+    unsigned it = 0, n_tile = 0;
     for (long long t = pair; t < tiles && ok; t += pairs) {
-      const int pe = (int)(t / ((long long)nz * nd)), p = pe / K, e = pe % K;
+      const int pe = (int)(t / ((long long)nz * nd));
+      const int blocks = tt.whole[pe] + (tt.rows[pe] + kK - 1) / kK;
+      if (blocks == 0) continue;
+      const int last = tt.rows[pe] % kK == 0 ? 4 : (tt.rows[pe] % kK + 15) / 16;
       const uint32_t idesc = product(kBf16, true, true, kM, columns_of(P.D - t % nd * kN));
       const unsigned buf = n_tile & 1;
       const uint32_t d = b.tmem + buf * kN;
-      bool any = false;
-      for (int r = 0; r < W && ok; ++r) {
-        int rows;
-        find_group(P.g, g, (p * W + r) * K + e, &rows);
-        for (int m = 0; m < rows; m += kK, ++it) {
-          if (!any && !bar_wait(smem_addr(&b.acc_empty[buf]), ((n_tile >> 1) & 1) ^ 1)) {
-            ok = false;
-            break;
-          }
-          const unsigned s = it % kStages;
-          if (!bar_wait(smem_addr(&b.full[s]), (it / kStages) & 1)) {
-            ok = false;
-            break;
-          }
-          // (a ragged block's rows were written by the other CTA's warp 3 as well)
-          if ((rows - m) % 16 != 0 && rows - m < kK)
-            asm volatile("fence.acq_rel.cluster;" ::: "memory");
-          fence_after_sync();
-          const uint32_t at = base + s * kStageBytes;
-          const uint64_t zd = operand(at, 8192), xd = operand(at + kSideBytes, 8192);
-          const int left = rows - m, steps = left >= kK ? 4 : (left + 15) / 16;
-          for (int k = 0; k < steps; ++k) {
-            mma(d, zd + k * (2048 >> 4), xd + k * (2048 >> 4), idesc, any);
-            any = true;
-          }
-          mma_commit(smem_addr(&b.empty[s]));
-        }
+      ok = bar_wait(smem_addr(&b.acc_empty[buf]), ((n_tile >> 1) & 1) ^ 1);
+      if (!ok) break;
+      ++n_tile;
+      for (int kb = 0; kb < blocks; ++kb, ++it) {
+        const unsigned s = it % kStages;
+        ok = bar_wait(smem_addr(&b.full[s]), (it / kStages) & 1);
+        if (!ok) break;
+        fence_after_sync();
+        const uint32_t at = base + s * kStageBytes;
+        const uint64_t zd = operand(at, 8192), xd = operand(at + kSideBytes, 8192);
+        const int steps = kb == blocks - 1 ? last : 4;
+        for (int k = 0; k < steps; ++k)
+          mma(d, zd + k * (2048 >> 4), xd + k * (2048 >> 4), idesc, kb > 0 || k > 0);
+        mma_commit(smem_addr(&b.empty[s]));
       }
-      if (any && ok) {
-        mma_commit(smem_addr(&b.acc_full[buf]));
-        ++n_tile;
-      }
+      if (ok) mma_commit(smem_addr(&b.acc_full[buf]));
     }
     if (!ok) note_error(P.g.status, A2AV_ERR_TIMEOUT);
   } else if (warp >= 4) {
+    // ---------------------------------------------------- epilogue --
     const int q = warp % 4, c0 = warp >= 8 ? 32 : 0;
     const uint32_t stage = base + kStages * kStageBytes + (warp - 4) * kStaging;
     const uint32_t empty0 = map_to(smem_addr(&b.acc_empty[0]), 0);
@@ -718,25 +772,20 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     for (long long t = pair; t < tiles && ok; t += pairs) {
       const int pe = (int)(t / ((long long)nz * nd)), p = pe / K, e = pe % K;
       const int z0 = (int)(t / nd % nz) * kM + 128 * rank + 32 * q, d0 = (int)(t % nd) * kN;
-      long long all = 0;
-      for (int r = 0; r < W; ++r) {
-        int rows;
-        find_group(P.g, g, (p * W + r) * K + e, &rows);
-        all += rows;
-      }
+      const bool any = tt.whole[pe] + tt.rows[pe] > 0;  // else the gradient is 0
       const unsigned buf = n_tile & 1;
-      if (all > 0) {
+      const int columns = min(kN, P.D - d0);
+      if (any) {
         ok = __all_sync(kAll, bar_wait(smem_addr(&b.acc_full[buf]), (n_tile >> 1) & 1));
         if (!ok) break;
         fence_after_sync();
         ++n_tile;
+        if (c0 >= columns && lane == 0) bar_arrive(empty0 + buf * 8);
       }
-      const int columns = min(kN, P.D - d0);
       T* out = static_cast<T*>(P.out[p]) + ((long long)e * P.Z + z0) * P.D;
-      if (c0 >= columns && all > 0 && lane == 0) bar_arrive(empty0 + buf * 8);
       for (int c = c0; c < columns; c += 64) {
         float va[16] = {}, vb[16] = {};
-        if (all > 0) {
+        if (any) {
           const uint32_t at = b.tmem + buf * kN + c + ((uint32_t)(32 * q) << 16);
           tmem_load(at, va);
           tmem_load(at + (16u << 16), vb);
@@ -835,6 +884,13 @@ MmaKernel mma_kernel_of(int direction, bool gated) {
 
 }  // namespace
 
+int64_t a2av_expert_tail_rows(int W, int K, int64_t rows) {
+  // at most 63 of each group, and zeros up to a multiple of 64 for each expert
+  const int64_t groups = (int64_t)W * W * K, experts = (int64_t)W * K;
+  const int64_t most = rows < groups * (kK - 1) ? rows : groups * (kK - 1);
+  return rows == 0 ? 0 : most + experts * (kK - 1);
+}
+
 bool a2av_expert_mma(a2av_handle* h, const A2avExperts& P, int dtype, int direction,
                      cudaStream_t s, cudaError_t* error) {
   *error = cudaSuccess;
@@ -880,10 +936,31 @@ bool a2av_expert_mma(a2av_handle* h, const A2avExperts& P, int dtype, int direct
       M.pre[p] = P.pre[p];
     }
   }
+  if (direction == 2) {
+    if (!aligned_to(P.tails, 16)) return false;
+    void* tail_x = static_cast<unsigned char*>(P.tails) + P.tail_rows * P.Z * 2;
+    if (P.tail_rows > 0 && (!encode(&M.tail_dz, P.tails, dtype, P.Z, P.tail_rows, 1, kK) ||
+                            !encode(&M.tail_x, tail_x, dtype, P.D, P.tail_rows, 1, kK)))
+      return false;
+    TailParams R;
+    std::memset(&R, 0, sizeof(R));
+    R.g = P.g;
+    for (int p = 0; p < h->W; ++p) {
+      R.dz[p] = P.dy[p];
+      R.x[p] = P.x[p];
+    }
+    R.to_dz = P.tails;
+    R.to_x = tail_x;
+    R.Z = (int)P.Z;
+    R.D = (int)P.D;
+    *error = launch_chained(expert_tails_kernel, dim3(4 * h->sms), 256, 0, s, h->pdl, R);
+    if (*error != cudaSuccess) return true;
+  }
   const MmaKernel kernel = dtype == A2AV_BF16 ? mma_kernel_of<__nv_bfloat16>(direction, gated)
                                               : mma_kernel_of<__half>(direction, gated);
   *error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMmaSmem);
   if (*error != cudaSuccess) return true;
-  *error = launch_chained(kernel, dim3(h->sms / 2 * 2), kMmaThreads, kMmaSmem, s, h->pdl, M);
+  *error = launch_chained(kernel, dim3(h->sms / 2 * 2), kMmaThreads,
+                          kMmaSmem, s, h->pdl, M);
   return true;
 }
