@@ -38,6 +38,13 @@ CASES = [
     ([700], 24, 3, "sigmoid", True, 6, 6, 1, True),
     ([19], 512, 16, "sigmoid", False, 16, 5, 2, False),
     ([14], 33, 4, "softmax", False, 11, 3, 1, False),
+    # tokens enough for a thread a token
+    ([2100], 64, 2, "softmax", False, 1, 1, 1, True),
+    ([1500, 0, 700], 256, 8, "sigmoid", True, 8, 4, 2, True),
+    ([2049], 24, 3, "softmax", False, 6, 2, 1, False),
+    ([1100, 1000], 128, 1, "sigmoid", False, 1, 1, 1, False),
+    ([33, 2200], 160, 7, "softmax", False, 5, 3, 1, False),
+    ([2300], 8, 8, "sigmoid", True, 2, 2, 2, True),
 ]
 
 

@@ -352,6 +352,29 @@ def a2av_combine_weighted_backward(handle, keys_per_peer: int, topk: int, hidden
 
 
 # --------------------------------------------------------- torch-facing --
+def _plain_pointers(tensors, dtype, shapes, address):
+    """``_marshal.pointers`` (csrc/marshal.c) without the compiled module."""
+    try:
+        if not all(t.is_cuda and t.dtype == dtype and t.is_contiguous() for t in tensors) or (
+                shapes is not None and [t.shape for t in tensors] != shapes):
+            return False
+    except AttributeError:  # None among them
+        return False
+    for r, t in enumerate(tensors):
+        ctypes.c_void_p.from_address(address + 8 * r).value = t.data_ptr()
+    return True
+
+
+def _pointers(*args):
+    """The compiled check, from the first call on (it may be built after the import)."""
+    global _pointers
+    try:
+        from ._marshal import pointers as _pointers
+    except ImportError:
+        _pointers = _plain_pointers
+    return _pointers(*args)
+
+
 class BoundCall:
     """One library call whose arguments were marshalled once (``A2av.bind_run``,
     ``bind_run_multi``, ``bind_dispatch``).  Calling it enqueues the same
@@ -392,6 +415,8 @@ class A2av:
         if rc != OK:
             raise A2avError(rc, "a2av_create")
         self.handle, self.world_size, self._path = h, int(world_size), int(path)
+        import torch
+        self._device = torch.cuda.current_device()
         if path != PATH_AUTO:
             self._check(a2av_set_path(h, path), "a2av_set_path")
         if ctas_per_sm:
@@ -408,6 +433,14 @@ class A2av:
         if stream is None:
             stream = torch.cuda.current_stream()
         return int(getattr(stream, "cuda_stream", stream))
+
+    def _queue(self, stream):
+        """The cudaStream_t to enqueue on: ``stream``, or torch's current one."""
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if stream is not None or raw is None:
+            return _address(self._stream(stream))
+        return ctypes.c_void_p(raw(self._device) or None)
 
     def _buffers(self, tensors, what):
         """Pointer array for W buffers; True when one lives in pinned host memory."""
@@ -635,15 +668,15 @@ class A2av:
 
     # ------------------------------------------- the MoE layer's operators --
     def _dtype(self, tensors, name, allowed):
-        """The element type that a list's non-empty tensors share, and its code."""
+        """The element type that a list's tensors share, and its code."""
         import torch
-        codes = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
         for t in tensors:
-            if t is not None and t.numel():
-                if codes.get(t.dtype) not in allowed:
+            if t is not None:
+                code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(t.dtype)
+                if code not in allowed:
                     raise ValueError(f"{name}: {t.dtype} is not supported")
-                return t.dtype, codes[t.dtype]
-        return None, allowed[-1]
+                return t.dtype, code
+        raise ValueError(f"{name}: every tensor is missing")
 
     def _list(self, tensors, name, dtype, shapes=None):
         """Pointer array of W contiguous CUDA tensors of a type.  ``shapes``:
@@ -651,6 +684,9 @@ class A2av:
         W = self.world_size
         if len(tensors) != W:
             raise ValueError(f"{name}: expected {W} tensors, got {len(tensors)}")
+        arr = (ctypes.c_void_p * W)()
+        if _pointers(tensors, dtype, shapes, ctypes.addressof(arr)):
+            return arr
         arr = (ctypes.c_void_p * W)()
         for r, t in enumerate(tensors):
             if t is None:
@@ -662,10 +698,9 @@ class A2av:
             if shapes is not None and t.shape != shapes[r]:
                 raise ValueError(f"{name}[{r}] must have shape {tuple(shapes[r])}, "
                                  f"not {tuple(t.shape)}")
-            if t.numel():
-                if t.dtype != dtype:
-                    raise ValueError(f"{name} must be {dtype} tensors, not {t.dtype}")
-                arr[r] = t.data_ptr()
+            if t.dtype != dtype:
+                raise ValueError(f"{name} must be {dtype} tensors, not {t.dtype}")
+            arr[r] = t.data_ptr()
         return arr
 
     def _call(self, what, args, keep, bind):
@@ -680,18 +715,11 @@ class A2av:
         """Rows and the common second dimension of W [rows, n] tensors."""
         if len(tensors) != self.world_size:
             raise ValueError(f"{name}: expected {self.world_size} tensors, got {len(tensors)}")
-        rows, width = [], None
-        for t in tensors:
-            if t is None:
-                rows.append(0)
-                continue
-            if t.dim() != 2 or (width is not None and t.shape[1] != width):
-                raise ValueError(f"{name} must be 2-D tensors of one width")
-            width = t.shape[1]
-            rows.append(t.shape[0])
-        if width is None:
-            raise ValueError(f"{name}: every tensor is missing")
-        return rows, width
+        shapes = [(0, None) if t is None else t.shape for t in tensors]
+        widths = {s[-1] for s in shapes if s[-1:] != (None,)}
+        if len(widths) != 1 or any(len(s) != 2 for s in shapes):
+            raise ValueError(f"{name} must be 2-D tensors of one width")
+        return [s[0] for s in shapes], widths.pop()
 
     def _route_args(self, logits, keys, weights, weights_name, topk, score, groups, top_groups,
                     group_top, renormalise, scale):
@@ -732,7 +760,7 @@ class A2av:
             self._matrix(counts, (W, E), "counts")
         args = [self.handle, cfg, x, n, _address(None if bias is None else bias.data_ptr()), k, w,
                 _address(None if counts is None else counts.data_ptr()),
-                _address(self._stream(stream))]
+                self._queue(stream)]
         return self._call("a2av_route", args, (logits, keys, weights, counts, bias), _bind)
 
     def bind_route(self, logits, keys, weights, topk: int, **options) -> BoundCall:
@@ -748,7 +776,7 @@ class A2av:
             logits, keys, d_weights, "d_weights", topk, score, 1, 1, 1, renormalise, scale)
         d = self._list(d_logits, "d_logits", dtype, [(m, E) for m in rows])
         self._call("a2av_route_backward",
-                   [self.handle, cfg, x, n, k, w, d, _address(self._stream(stream))], None, False)
+                   [self.handle, cfg, x, n, k, w, d, self._queue(stream)], None, False)
 
     def _expert_args(self, rows, counts, weights, out, out_name, activation, gated):
         """The shape, the common arguments and what the others are checked by."""
@@ -788,7 +816,7 @@ class A2av:
                 None if residual is None else self._list(residual, "residual", dtype, by_row),
                 self._list(outputs, "outputs", dtype, by_row),
                 None if pre is None else self._list(pre, "pre", dtype, [(m, Z) for m in n_rows]),
-                _address(self._stream(stream))]
+                self._queue(stream)]
         keep = (rows, counts, weights, outputs, bias, residual, pre)
         return self._call("a2av_expert_matmul", args, keep, _bind)
 
@@ -829,7 +857,7 @@ class A2av:
                 None if d_weights is None else self._list(d_weights, "d_weights", dtype, each),
                 None if d_bias is None else self._list(d_bias, "d_bias", dtype, [(K, Z)] * W),
                 _address(workspace.data_ptr() if need else None),
-                int(workspace.numel()) if need else 0, _address(self._stream(stream))]
+                int(workspace.numel()) if need else 0, self._queue(stream)]
         self._call("a2av_expert_matmul_backward", args, None, False)
 
     def _weighted_args(self, in_splits, keys, sorted_pos, keys_per_peer, token_rows, name):
@@ -839,16 +867,11 @@ class A2av:
         sp = self._matrix(in_splits, (W, W), "in_splits")
         n, H = self._tokens(token_rows, name)
         dtype, code = self._dtype(token_rows, name, (F32, BF16, F16))
-        k = None
-        for t, m in zip(keys, n):
-            if t is not None and m:
-                k = t.numel() // m
-                break
-        k = k or 1
-        items = [(m * k,) for m in n]
-        for ts, what in ((keys, "keys"), (sorted_pos, "sorted_pos")):
-            if len(ts) != W or any((0 if t is None else t.numel()) != m for t, (m,) in zip(ts, items)):
-                raise ValueError(f"{what} must have one entry per item")
+        sizes = [[0 if t is None else t.numel() for t in ts] for ts in (keys, sorted_pos)]
+        k = next((m // T for m, T in zip(sizes[0], n) if T), 1) or 1
+        for m, what in zip(sizes, ("keys", "sorted_pos")):
+            if m != [T * k for T in n]:
+                raise ValueError(f"{what} must have one entry per item of each rank")
         return (int(keys_per_peer), k, H, code, sp, self._list(keys, "keys", torch.int32),
                 self._list(sorted_pos, "sorted_pos", torch.int64), (ctypes.c_int64 * W)(*n),
                 n, H, dtype)
@@ -872,7 +895,7 @@ class A2av:
         args = [self.handle, K, k, H, code, peer_arr, held, sp, ka, pa,
                 None if weights is None else self._item_weights(weights, "weights", n, k), na,
                 None if residual is None else self._list(residual, "residual", dtype, shapes),
-                self._list(outputs, "outputs", dtype, shapes), _address(self._stream(stream))]
+                self._list(outputs, "outputs", dtype, shapes), self._queue(stream)]
         keep = (peers, in_splits, keys, sorted_pos, weights, outputs, residual)
         return self._call("a2av_combine_weighted", args, keep, _bind)
 
@@ -915,7 +938,7 @@ class A2av:
                 self._list(d_outputs, "d_outputs", dtype, [(m, H) for m in n]),
                 d_peer_arr,
                 None if d_weights is None else self._item_weights(d_weights, "d_weights", n, k),
-                _address(self._stream(stream))]
+                self._queue(stream)]
         self._call("a2av_combine_weighted_backward", args, None, False)
 
     def status(self, stream=None) -> int:

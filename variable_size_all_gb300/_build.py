@@ -4,6 +4,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -13,6 +14,8 @@ HEADERS = [os.path.join(PKG, "csrc", f) for f in ("a2av_device.cuh", "a2av_handl
                                                   "moe_device.cuh", "experts.cuh", "mma.cuh")]
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "liba2av.so")
+MARSHAL_SOURCE = os.path.join(PKG, "csrc", "marshal.c")
+MARSHAL = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -35,8 +38,20 @@ def stale(output: str = LIBRARY) -> bool:
     return os.path.getmtime(output) < max(os.path.getmtime(d) for d in deps)
 
 
+def build_marshal(force: bool = False) -> None:
+    """The binding's argument checks in C; without Python's headers the binding does them itself."""
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        return
+    if force or not os.path.exists(MARSHAL) or os.path.getmtime(MARSHAL) < os.path.getmtime(MARSHAL_SOURCE):
+        subprocess.run(["gcc", "-O2", "-shared", "-fPIC", "-I", include, "-o", MARSHAL + ".tmp",
+                        MARSHAL_SOURCE], check=True)
+        os.replace(MARSHAL + ".tmp", MARSHAL)
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     """Build ``liba2av.so`` unless it is up to date; returns its path."""
+    build_marshal(force)
     if force or stale():
         cmd = command(extra=extra)
         if verbose:

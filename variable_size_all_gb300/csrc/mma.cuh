@@ -204,19 +204,4 @@ __device__ __forceinline__ void get4_t(uint32_t a, uint32_t (&v)[4]) {
                : "memory");
 }
 
-__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
-  const __half2 v = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ float2 unpack2(uint32_t x, __nv_bfloat16) {
-  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x));
-}
-__device__ __forceinline__ float2 unpack2(uint32_t x, __half) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&x));
-}
-
 }  // namespace

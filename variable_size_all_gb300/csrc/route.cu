@@ -1,12 +1,20 @@
 // route.cu -- routing to experts (a2av_route) and its gradient
 // (a2av_route_backward); the interface is in include/a2av_moe.h.
 //
-// A warp takes a token.  Lane l holds the experts [l NJ, (l + 1) NJ), NJ the
-// power of two >= E / 32, so that among equal choices the lowest expert is the
-// lowest lane's lowest: a round of the top-k is one redux.max over the lanes'
-// best, one ballot for the first lane that has it, and a search of that lane's
-// NJ values.  Choices are compared as unsigned integers in the order of the
-// floats they stand for (0 = not an expert, or already taken).
+// L lanes of a warp take a token, the warp 32 / L tokens.  Lane l of them holds
+// the experts [l NJ, (l + 1) NJ), so that the order of (lane, place) is that of
+// the experts, which decides ties.  With few tokens L is 32, for the shortest
+// way through one; with many, NJ is 16 and L as many as the experts need:
+// what is done once a token, whatever its experts (prefix sums, rounds,
+// ranking, the weights), is then shared by the tokens of the warp.
+//
+// The top k without k rounds over all the experts: the k-th largest of the
+// maxima of eight is at most the k-th largest of all, so only choices that
+// reach it are candidates, a little over k of them.  They are written side by
+// side, and each one's place is the number of candidates that come before it.
+// A round over the maxima is a few instructions; one that also removes a choice
+// and finds the next costs some for every expert.  (Many equal choices can make
+// more candidates than there is room for; then those rounds are run.)
 #include "moe_device.cuh"
 
 namespace {
@@ -25,6 +33,7 @@ struct RouteParams {
   int* status;
   int E, k, score, groups, top_groups, group_top, renormalise;
   int group_size;
+  int group_lanes;  // lanes of a group, where that is a power of two of whole lanes; else 0
   float scale;
   int add_counts;  // several blocks a rank: counts (cleared before) are added to
 };
@@ -42,21 +51,35 @@ __device__ __forceinline__ float float_of(unsigned o) {
   return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Over the L lanes of a token.
+template <int L = 32>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
   return v;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
+template <int L = 32>
+__device__ __forceinline__ float lanes_max(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+
+template <int L>
+__device__ __forceinline__ unsigned lanes_max(unsigned v) {
+  if constexpr (L == 32) {
+    v = __reduce_max_sync(kAll, v);
+  } else {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+  }
   return v;
 }
 
 // The accurate exponential and an IEEE division: choices are decided by these
 // scores, and equal logits must give equal ones on every path.
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+__device__ __forceinline__ float sigmoid(float x) { return __frcp_rn(1.0f + expf(-x)); }
 
 // exp(x - m) where m is the largest of the x's it belongs to; 0 where all are -inf.
 __device__ __forceinline__ float exp_below(float x, float m) {
@@ -89,11 +112,108 @@ __device__ __forceinline__ void load_logits(const T* row, int E, int lane, float
   }
 }
 
-template <typename T, int NJ, bool kVec>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_constant__ RouteParams P) {
+// Whether the lane's group is one of the top_groups, when every lane's experts
+// are of one group and a group has a power of two of lanes (`width`).
+template <int L, int NJ>
+__device__ __forceinline__ bool keep_by_lanes(const RouteParams& P, const float (&c)[NJ], int width,
+                                              int sl) {
+  float a = -INFINITY, b = -INFINITY;  // the group's two best
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    b = fmaxf(b, fminf(a, c[j]));
+    a = fmaxf(a, c[j]);
+  }
+  for (int o = 1; o < width; o <<= 1) {
+    const float a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
+    b = fmaxf(fmaxf(b, b2), fminf(a, a2));
+    a = fmaxf(a, a2);
+  }
+  const unsigned score = order_of(P.group_top == 2 ? a + b : a);
+  const int mine = sl / width;
+  int before = 0;  // groups chosen before this one
+  for (int g = 0; g < P.groups; ++g) {
+    const unsigned s = __shfl_sync(kAll, score, g * width, L);
+    before += s > score || (s == score && g < mine);
+  }
+  return before < P.top_groups;
+}
+
+// The same for groups of any size (L = 32): a bit for each group that stays.
+template <int NJ>
+__device__ __forceinline__ unsigned keep_groups(const RouteParams& P, const float (&c)[NJ], int lane) {
+  unsigned score = 0;  // lane g: of group g
+  for (int g = 0; g < P.groups; ++g) {
+    unsigned a = 0, b = 0;  // this lane's two best in group g
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int e = lane * NJ + j;
+      if (e >= g * P.group_size && e < (g + 1) * P.group_size) {
+        const unsigned o = order_of(c[j]);
+        b = max(b, min(a, o));
+        a = max(a, o);
+      }
+    }
+    unsigned best = __reduce_max_sync(kAll, a);
+    if (P.group_top == 2) {
+      const int first = __ffs(__ballot_sync(kAll, a == best)) - 1;
+      const unsigned second = __reduce_max_sync(kAll, lane == first ? b : a);
+      best = order_of(float_of(best) + float_of(second));
+    }
+    if (lane == g) score = best;
+  }
+  unsigned keep = 0;
+  for (int i = 0; i < P.top_groups; ++i) {
+    const unsigned best = __reduce_max_sync(kAll, score);
+    const int g = __ffs(__ballot_sync(kAll, score == best)) - 1;
+    keep |= 1u << g;
+    if (lane == g) score = 0;
+  }
+  return keep;
+}
+
+constexpr int kListed = 32;  // candidates a token has room for
+struct Candidate {
+  float c;
+  int e;
+};
+
+// The top k by k rounds, to `chosen`.
+template <int L, int NJ>
+__device__ __forceinline__ void choose_by_rounds(const float (&c)[NJ], int k, int sl, int* chosen) {
+  unsigned o[NJ], mine = 0;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    o[j] = c[j] == c[j] ? order_of(c[j]) : 0u;
+    mine = max(mine, o[j]);
+  }
+  for (int i = 0; i < k; ++i) {
+    const unsigned best = lanes_max<L>(mine);
+    // the first lane that has it, and its first expert
+    int at = 32 * NJ;
+#pragma unroll
+    for (int j = NJ - 1; j >= 0; --j)
+      if (o[j] == best) at = sl * NJ + j;
+#pragma unroll
+    for (int s = L / 2; s > 0; s >>= 1) at = min(at, __shfl_xor_sync(kAll, at, s));
+    mine = 0;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      if (sl * NJ + j == at) o[j] = 0;
+      mine = max(mine, o[j]);
+    }
+    if (sl == 0) chosen[i] = at;
+  }
+}
+
+template <typename T, int L, int NJ, bool kVec>
+__global__ void __launch_bounds__(32 * kRouteWarps, L < 32 ? 4 : 1) route_kernel(const __grid_constant__ RouteParams P) {
   chain();
+  constexpr int kTokens = 32 / L;  // of a warp
   extern __shared__ int hist[];
+  __shared__ Candidate lists[kRouteWarps * kTokens][kListed];
+  __shared__ int picks[kRouteWarps * kTokens][A2AV_MAX_TOPK];
   const int r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = lane / L, sl = lane % L;
   const int E = P.E, k = P.k;
   if (P.counts != nullptr) {
     for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
@@ -103,123 +223,134 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
   const bool softmax = P.score == A2AV_SCORE_SOFTMAX;
   const bool need_sum = softmax && (!by_logit || !P.renormalise);
   const int n = P.tokens[r];
-  for (int t = blockIdx.x * kRouteWarps + warp; t < n; t += gridDim.x * kRouteWarps) {
-    float x[NJ];
-    load_logits<T, NJ, kVec>(static_cast<const T*>(P.logits[r]) + (long long)t * E, E, lane, x);
+  Candidate* list = lists[warp * kTokens + sub];
+  int* chosen = picks[warp * kTokens + sub];
+  for (int t0 = (blockIdx.x * kRouteWarps + warp) * kTokens; t0 < n;
+       t0 += gridDim.x * kRouteWarps * kTokens) {
+    const bool live = t0 + sub < n;
+    const int t = live ? t0 + sub : n - 1;  // (lanes without a token repeat the last one)
+    const T* row = static_cast<const T*>(P.logits[r]) + (long long)t * E;
+    float c[NJ];  // the logits, then the choices
+    load_logits<T, NJ, kVec>(row, E, sl, c);
     float m = 0.0f, total = 1.0f;
     if (need_sum) {
-      m = x[0];
+      m = c[0];
 #pragma unroll
-      for (int j = 1; j < NJ; ++j) m = fmaxf(m, x[j]);
-      m = warp_max(m);
+      for (int j = 1; j < NJ; ++j) m = fmaxf(m, c[j]);
+      m = lanes_max<L>(m);
       total = 0.0f;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) total += exp_below(x[j], m);
-      total = warp_sum(total);
+      for (int j = 0; j < NJ; ++j) total += exp_below(c[j], m);
+      total = lanes_sum<L>(total);
     }
-    unsigned c[NJ];
+    // (a choice that is NaN counts as -inf; from here on NaN is no expert at all)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int e = lane * NJ + j;
-      float v = x[j];
+      float v = c[j];
       if (!softmax)
         v = sigmoid(v);
       else if (!by_logit)
         v = m == -INFINITY ? 0.0f : expf(v - m) / total;
-      if (P.bias != nullptr && e < E) v += P.bias[e];
-      c[j] = e < E ? order_of(v) : 0u;
+      const int e = sl * NJ + j;
+      if (P.bias != nullptr && e < E) v += __ldg(P.bias + e);
+      if (v != v) v = -INFINITY;
+      c[j] = e < E ? v : NAN;
     }
     if (P.groups > 1) {
-      // lane g gets group g's score: its best choice, or its two best, summed
-      unsigned score = 0;
-      for (int g = 0; g < P.groups; ++g) {
-        unsigned a = 0, b = 0;  // this lane's two best in group g
+      if (L < 32 || P.group_lanes > 0) {
+        const bool keep = keep_by_lanes<L>(P, c, P.group_lanes, sl);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          const int e = lane * NJ + j;
-          if (e >= g * P.group_size && e < (g + 1) * P.group_size) {
-            if (c[j] > a) {
-              b = a;
-              a = c[j];
-            } else if (c[j] > b) {
-              b = c[j];
-            }
-          }
-        }
-        unsigned best = __reduce_max_sync(kAll, a);
-        if (P.group_top == 2) {
-          const int first = __ffs(__ballot_sync(kAll, a == best)) - 1;
-          const unsigned second = __reduce_max_sync(kAll, lane == first ? b : a);
-          best = order_of(float_of(best) + float_of(second));
-        }
-        if (lane == g) score = best;
-      }
-      unsigned keep = 0;
-      for (int i = 0; i < P.top_groups; ++i) {
-        const unsigned best = __reduce_max_sync(kAll, score);
-        const int g = __ffs(__ballot_sync(kAll, score == best)) - 1;
-        keep |= 1u << g;
-        if (lane == g) score = 0;
-      }
+        for (int j = 0; j < NJ; ++j)
+          if (!keep && c[j] == c[j]) c[j] = -INFINITY;
+      } else {
+        const unsigned keep = keep_groups(P, c, lane);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int e = lane * NJ + j;
-        if (e < E && !((keep >> (e / P.group_size)) & 1)) c[j] = kNegInf;
+        for (int j = 0; j < NJ; ++j)
+          if (c[j] == c[j] && !((keep >> ((lane * NJ + j) / P.group_size)) & 1)) c[j] = -INFINITY;
       }
     }
-    // top k: lane i keeps the i-th choice and its logit
-    int my_key = 0;
-    float my_x = -INFINITY;
-    unsigned mine = 0;
+    // the k-th largest of the maxima of eight
+    constexpr int kEight = NJ < 8 ? NJ : 8, kMaxima = NJ / kEight;
+    unsigned most[kMaxima], best = 0;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) mine = max(mine, c[j]);
+    for (int q = 0; q < kMaxima; ++q) {
+      float v = c[q * kEight];
+#pragma unroll
+      for (int j = 1; j < kEight; ++j) v = fmaxf(v, c[q * kEight + j]);
+      most[q] = v == v ? order_of(v) : 0u;
+    }
     for (int i = 0; i < k; ++i) {
-      const unsigned best = __reduce_max_sync(kAll, mine);
-      const int owner = __ffs(__ballot_sync(kAll, mine == best)) - 1;
-      int at = 0;
-      float xv = 0.0f;
-      if (lane == owner) {
+      unsigned v = most[0];
 #pragma unroll
-        for (int j = NJ - 1; j >= 0; --j)
-          if (c[j] == best) {
-            at = j;
-            xv = x[j];
-          }
-        mine = 0;
+      for (int q = 1; q < kMaxima; ++q) v = max(v, most[q]);
+      best = lanes_max<L>(v);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          if (j == at) c[j] = 0;
-          mine = max(mine, c[j]);
+      for (int q = 0; q < kMaxima; ++q)
+        if (most[q] == best) most[q] = 0;
+    }
+    const float least = best != 0 ? float_of(best) : -INFINITY;
+    unsigned marks = 0;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) marks |= (c[j] >= least ? 1u : 0u) << j;
+    const int own = __popc(marks);
+    int upto = own;
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) {
+      const int v = __shfl_up_sync(kAll, upto, o, L);
+      if (sl >= o) upto += v;
+    }
+    const int count = __shfl_sync(kAll, upto, L - 1, L);
+    if (!__any_sync(kAll, count > kListed)) {
+      Candidate* to = list + (upto - own);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        if ((marks >> j) & 1) *to++ = Candidate{c[j], sl * NJ + j};
+      __syncwarp();
+      for (int i = sl; i < count; i += L) {
+        const Candidate x = list[i];
+        int place = 0;
+        for (int q = 0; q < count; ++q) {
+          const float other = list[q].c;
+          place += other > x.c || (other == x.c && q < i);
         }
-        at += lane * NJ;
+        if (place < k) chosen[place] = x.e;
       }
-      at = __shfl_sync(kAll, at, owner);
-      xv = __shfl_sync(kAll, xv, owner);
-      if (lane == i) {
-        my_key = at;
-        my_x = xv;
-      }
-    }
-    // weights, from the chosen logits alone where they are renormalised
-    float w;
-    if (!softmax) {
-      w = sigmoid(my_x);
-    } else if (P.renormalise) {
-      // NaN logits are chosen last; fmaxf passes them over and the sum does not
-      w = exp_below(my_x, warp_max(lane < k ? my_x : -INFINITY));
     } else {
-      w = m == -INFINITY ? 0.0f : expf(my_x - m) / total;
+      choose_by_rounds<L, NJ>(c, k, sl, chosen);
     }
-    if (P.renormalise) {
-      const float sum = warp_sum(lane < k ? w : 0.0f);
-      w = sum == 0.0f ? 0.0f : w / sum;
+    __syncwarp();
+    // weights, from the chosen logits alone where they are renormalised
+    float w[kTokens];
+    float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int s = 0; s < kTokens; ++s) {
+      const int i = sl + L * s;
+      w[s] = i < k ? to_float(row[chosen[i]]) : -INFINITY;
+      top = fmaxf(top, w[s]);  // (passes NaN over; the sum does not)
     }
-    if (lane < k) {
-      const long long i = (long long)t * k + lane;
-      P.key[r][i] = my_key;
-      P.weight[r][i] = w * P.scale;
-      if (P.counts != nullptr) atomicAdd(&hist[my_key], 1);
+    if (softmax && P.renormalise) top = lanes_max<L>(top);
+#pragma unroll
+    for (int s = 0; s < kTokens; ++s)
+      if (sl + L * s < k) {
+        w[s] = !softmax             ? sigmoid(w[s])
+               : P.renormalise      ? exp_below(w[s], top)
+               : m == -INFINITY     ? 0.0f
+                                    : expf(w[s] - m) / total;
+        sum += w[s];
+      }
+    if (P.renormalise) sum = lanes_sum<L>(sum);
+#pragma unroll
+    for (int s = 0; s < kTokens; ++s) {
+      const int i = sl + L * s;
+      if (i < k && live) {
+        if (P.renormalise) w[s] = sum == 0.0f ? 0.0f : w[s] / sum;
+        const int e = chosen[i];
+        P.key[r][(long long)t * k + i] = e;
+        P.weight[r][(long long)t * k + i] = w[s] * P.scale;
+        if (P.counts != nullptr) atomicAdd(&hist[e], 1);
+      }
     }
+    __syncwarp();
   }
   if (P.counts == nullptr) return;
   __syncthreads();
@@ -264,33 +395,33 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
         float m = x[0];
 #pragma unroll
         for (int j = 1; j < NJ; ++j) m = fmaxf(m, x[j]);
-        m = warp_max(m);
+        m = lanes_max<32>(m);
         float total = 0.0f;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
           x[j] = exp_below(x[j], m);
           total += x[j];
         }
-        total = warp_sum(total);
+        total = lanes_sum<32>(total);
         const float inv = m == -INFINITY ? 0.0f : 1.0f / total;
         const float p = lane < k ? exp_below(xs, m) * inv : 0.0f;
-        const float dot = warp_sum(lane < k ? g * p : 0.0f);
+        const float dot = lanes_sum<32>(lane < k ? g * p : 0.0f);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) d[j] = -(x[j] * inv) * dot;
         onto = p * g;  // added to -p * dot of the same expert
       } else if (softmax) {
-        const float m = warp_max(xs);  // (xs is -inf in the lanes past k)
+        const float m = lanes_max<32>(xs);  // (xs is -inf in the lanes past k)
         const float e = lane < k ? exp_below(xs, m) : 0.0f;
-        const float sum = warp_sum(e);
+        const float sum = lanes_sum<32>(e);
         const float q = sum == 0.0f ? 0.0f : e / sum;
-        const float dot = warp_sum(lane < k ? g * q : 0.0f);
+        const float dot = lanes_sum<32>(lane < k ? g * q : 0.0f);
         onto = q * (g - dot);
       } else {
         const float s = lane < k ? sigmoid(xs) : 0.0f;
         float ds = g;
         if (P.renormalise) {
-          const float sum = warp_sum(s);
-          const float dot = warp_sum(lane < k ? g * s : 0.0f);
+          const float sum = lanes_sum<32>(s);
+          const float dot = lanes_sum<32>(lane < k ? g * s : 0.0f);
           ds = sum == 0.0f ? 0.0f : (g - dot / sum) / sum;
         }
         onto = ds * s * (1.0f - s);
@@ -328,33 +459,62 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
 
 using RouteKernel = void (*)(RouteParams);
 
+// Lanes and experts a lane for a call: few tokens, or many.  (Measured at 65,536
+// tokens over 256 experts in 8 groups: 16 lanes x 16 experts with four blocks an
+// SM 65 us, 8 x 32 with two or three 84, 32 x 8 73.)
+constexpr int kManyNj = 16;
+struct RouteShape {
+  int lanes, nj;
+};
+
 template <typename T, bool kVec>
-RouteKernel route_kernel_of(int nj, bool backward) {
-  switch (nj) {
-    case 1: return backward ? route_backward_kernel<T, 1, kVec> : route_kernel<T, 1, kVec>;
-    case 2: return backward ? route_backward_kernel<T, 2, kVec> : route_kernel<T, 2, kVec>;
-    case 4: return backward ? route_backward_kernel<T, 4, kVec> : route_kernel<T, 4, kVec>;
-    case 8: return backward ? route_backward_kernel<T, 8, kVec> : route_kernel<T, 8, kVec>;
-    case 16: return backward ? route_backward_kernel<T, 16, kVec> : route_kernel<T, 16, kVec>;
-    default: return backward ? route_backward_kernel<T, 32, kVec> : route_kernel<T, 32, kVec>;
+RouteKernel route_kernel_of(RouteShape f) {
+  if constexpr (kVec) {  // (many tokens)
+    if (f.lanes == 4) return route_kernel<T, 4, kManyNj, true>;
+    if (f.lanes == 8) return route_kernel<T, 8, kManyNj, true>;
+    if (f.lanes == 16) return route_kernel<T, 16, kManyNj, true>;
+  }
+  switch (f.nj) {
+    case 1: return route_kernel<T, 32, 1, kVec>;
+    case 2: return route_kernel<T, 32, 2, kVec>;
+    case 4: return route_kernel<T, 32, 4, kVec>;
+    case 8: return route_kernel<T, 32, 8, kVec>;
+    case 16: return route_kernel<T, 32, 16, kVec>;
+    default: return route_kernel<T, 32, 32, kVec>;
   }
 }
 
-RouteKernel route_kernel_of(int dtype, int nj, bool vec, bool backward) {
-  if (dtype == A2AV_F32)
-    return vec ? route_kernel_of<float, true>(nj, backward)
-               : route_kernel_of<float, false>(nj, backward);
-  if (dtype == A2AV_BF16)
-    return vec ? route_kernel_of<__nv_bfloat16, true>(nj, backward)
-               : route_kernel_of<__nv_bfloat16, false>(nj, backward);
-  return vec ? route_kernel_of<__half, true>(nj, backward)
-             : route_kernel_of<__half, false>(nj, backward);
+template <typename T, bool kVec>
+RouteKernel backward_kernel_of(int nj) {
+  switch (nj) {
+    case 1: return route_backward_kernel<T, 1, kVec>;
+    case 2: return route_backward_kernel<T, 2, kVec>;
+    case 4: return route_backward_kernel<T, 4, kVec>;
+    case 8: return route_backward_kernel<T, 8, kVec>;
+    case 16: return route_backward_kernel<T, 16, kVec>;
+    default: return route_backward_kernel<T, 32, kVec>;
+  }
 }
+
+template <typename T>
+RouteKernel route_kernel_of(RouteShape f, bool vec, bool backward) {
+  if (backward) return vec ? backward_kernel_of<T, true>(f.nj) : backward_kernel_of<T, false>(f.nj);
+  return vec ? route_kernel_of<T, true>(f) : route_kernel_of<T, false>(f);
+}
+
+RouteKernel route_kernel_of(int dtype, RouteShape f, bool vec, bool backward) {
+  if (dtype == A2AV_F32) return route_kernel_of<float>(f, vec, backward);
+  if (dtype == A2AV_BF16) return route_kernel_of<__nv_bfloat16>(f, vec, backward);
+  return route_kernel_of<__half>(f, vec, backward);
+}
+
+// Tokens from which on several share a warp.
+constexpr long long kManyTokens = 2048;
 
 // The checks both calls share; fills what both need.
 int route_params(a2av_handle* h, const a2av_route_t* c, const void* const* logits,
                  const int64_t* tokens, const int32_t* const* keys, const float* const* weights,
-                 void* const* d_logits, RouteParams* P, int* nj, bool* vec, int* most) {
+                 void* const* d_logits, RouteParams* P, RouteShape* shape, bool* vec, int* most) {
   if (h == nullptr || c == nullptr || logits == nullptr || tokens == nullptr || keys == nullptr ||
       weights == nullptr)
     return A2AV_ERR_INVALID_ARG;
@@ -371,12 +531,8 @@ int route_params(a2av_handle* h, const a2av_route_t* c, const void* const* logit
   if (c->topk > c->top_groups * group_size || c->group_top > group_size)
     return A2AV_ERR_INVALID_ARG;
   std::memset(P, 0, sizeof(*P));
-  *nj = 1;
-  while (*nj * 32 < c->experts) *nj *= 2;
-  // Vectors when every lane's run of NJ logits is whole and aligned: the row
-  // is a multiple of a lane's vector and every buffer is aligned to it.
-  const int lane_bytes = *nj * size < 16 ? *nj * size : 16;
-  *vec = (long long)c->experts * size % lane_bytes == 0;
+  bool aligned = true;
+  long long all = 0;
   *most = 0;
   for (int r = 0; r < h->W; ++r) {
     const int64_t n = tokens[r];
@@ -385,11 +541,12 @@ int route_params(a2av_handle* h, const a2av_route_t* c, const void* const* logit
     P->tokens[r] = (int)n;
     if (n == 0) continue;
     const void* d = d_logits != nullptr ? d_logits[r] : logits[r];
+    all += n;
     if (logits[r] == nullptr || keys[r] == nullptr || weights[r] == nullptr || d == nullptr ||
         !aligned_to(logits[r], size) || !aligned_to(d, size) || !aligned_to(keys[r], 4) ||
         !aligned_to(weights[r], 4))
       return A2AV_ERR_INVALID_ARG;
-    *vec = *vec && aligned_to(logits[r], lane_bytes) && aligned_to(d, lane_bytes);
+    aligned = aligned && aligned_to(logits[r], 16) && aligned_to(d, 16);
     P->logits[r] = logits[r];
     P->key[r] = const_cast<int*>(keys[r]);
     if (n > *most) *most = (int)n;
@@ -401,15 +558,35 @@ int route_params(a2av_handle* h, const a2av_route_t* c, const void* const* logit
   P->top_groups = c->top_groups;
   P->group_top = c->group_top;
   P->group_size = group_size;
+  // A group's lanes, where they are a power of two of whole lanes.
+  const auto group_lanes = [&](int nj) {
+    const int lanes = group_size / nj;
+    return group_size % nj == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+  };
+  shape->lanes = 32;
+  shape->nj = 1;
+  while (shape->nj * 32 < c->experts) shape->nj *= 2;
+  if (d_logits == nullptr && all >= kManyTokens && c->experts <= 16 * kManyNj && aligned &&
+      (long long)c->experts * size % 16 == 0) {
+    RouteShape many = {4, kManyNj};
+    while (many.lanes * many.nj < c->experts) many.lanes *= 2;
+    if (c->groups == 1 || group_lanes(many.nj) > 0) *shape = many;
+  }
+  P->group_lanes = group_lanes(shape->nj);
+  // Vectors when every lane's run of NJ logits is whole and aligned: the row
+  // is a multiple of a lane's vector, and the buffers are aligned.
+  const int lane_bytes = shape->nj * size < 16 ? shape->nj * size : 16;
+  *vec = aligned && (long long)c->experts * size % lane_bytes == 0;
   P->renormalise = c->renormalise != 0;
   P->scale = c->scale;
   P->status = h->d_status;
   return current_device(h);
 }
 
-// Blocks a rank: enough for every token to have its warp, up to eight blocks an SM.
-int route_blocks(const a2av_handle* h, int most) {
-  const int all = (most + kRouteWarps - 1) / kRouteWarps;
+// Blocks a rank: enough for every token to have its lanes, up to eight blocks an SM.
+int route_blocks(const a2av_handle* h, int most, int lanes) {
+  const int tokens = kRouteWarps * 32 / lanes;
+  const int all = (most + tokens - 1) / tokens;
   const int fit = (8 * h->sms + h->W - 1) / h->W;
   return all < 1 ? 1 : all < fit ? all : fit;
 }
@@ -421,10 +598,11 @@ extern "C" int a2av_route(a2av_handle* h, const a2av_route_t* route,
                           const float* bias_dev, int32_t* const* key_ptrs,
                           float* const* weight_ptrs, int64_t* counts_dev, void* stream) {
   RouteParams P;
-  int nj = 0, most = 0;
+  RouteShape shape;
+  int most = 0;
   bool vec = false;
   const int rc = route_params(h, route, logits_ptrs, tokens_per_rank, key_ptrs, weight_ptrs,
-                              nullptr, &P, &nj, &vec, &most);
+                              nullptr, &P, &shape, &vec, &most);
   if (rc != A2AV_OK) return rc;
   if (!aligned_to(bias_dev, 4) || !aligned_to(counts_dev, 8)) return A2AV_ERR_INVALID_ARG;
   for (int r = 0; r < h->W; ++r) P.weight[r] = P.tokens[r] > 0 ? weight_ptrs[r] : nullptr;
@@ -432,14 +610,14 @@ extern "C" int a2av_route(a2av_handle* h, const a2av_route_t* route,
   P.counts = reinterpret_cast<unsigned long long*>(counts_dev);
   if (most == 0 && counts_dev == nullptr) return A2AV_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int blocks = route_blocks(h, most);
+  const int blocks = route_blocks(h, most, shape.lanes);
   if (P.counts != nullptr && blocks > 1) {
     P.add_counts = 1;
     if (cudaMemsetAsync(counts_dev, 0, sizeof(int64_t) * h->W * P.E, s) != cudaSuccess)
       return A2AV_ERR_CUDA;
   }
   const cudaError_t e =
-      launch_chained(route_kernel_of(route->dtype, nj, vec, false), dim3(blocks, h->W),
+      launch_chained(route_kernel_of(route->dtype, shape, vec, false), dim3(blocks, h->W),
                      32 * kRouteWarps, sizeof(int) * P.E, s, h->pdl, P);
   if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return A2AV_ERR_CUDA;
   return A2AV_OK;
@@ -452,18 +630,19 @@ extern "C" int a2av_route_backward(a2av_handle* h, const a2av_route_t* route,
                                    void* stream) {
   if (d_logits_ptrs == nullptr) return A2AV_ERR_INVALID_ARG;
   RouteParams P;
-  int nj = 0, most = 0;
+  RouteShape shape;
+  int most = 0;
   bool vec = false;
   const int rc = route_params(h, route, logits_ptrs, tokens_per_rank, key_ptrs, d_weight_ptrs,
-                              d_logits_ptrs, &P, &nj, &vec, &most);
+                              d_logits_ptrs, &P, &shape, &vec, &most);
   if (rc != A2AV_OK) return rc;
   for (int r = 0; r < h->W; ++r) {
     P.d_weight[r] = P.tokens[r] > 0 ? d_weight_ptrs[r] : nullptr;
     P.d_logits[r] = P.tokens[r] > 0 ? d_logits_ptrs[r] : nullptr;
   }
   if (most == 0) return A2AV_OK;
-  const cudaError_t e = launch_chained(route_kernel_of(route->dtype, nj, vec, true),
-                                       dim3(route_blocks(h, most), h->W), 32 * kRouteWarps, 0,
+  const cudaError_t e = launch_chained(route_kernel_of(route->dtype, shape, vec, true),
+                                       dim3(route_blocks(h, most, 32), h->W), 32 * kRouteWarps, 0,
                                        static_cast<cudaStream_t>(stream), h->pdl, P);
   if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return A2AV_ERR_CUDA;
   return A2AV_OK;

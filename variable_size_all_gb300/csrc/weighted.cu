@@ -2,10 +2,15 @@
 // (a2av_combine_weighted) and its gradient; the interface is in
 // include/a2av_moe.h.
 //
-// A block takes a token: its first k threads read the items' keys and
-// positions and turn them into row addresses (the split matrix's prefix sums
-// are in shared memory), then the block's threads walk the row, 16 bytes of it
-// at a time, with all k rows' loads in flight together.
+// Memory bound: each row is read once and each token written once.  A warp takes
+// 2 KiB of a token's rows (the backward pass, which sums over the row, a token,
+// 1 KiB of it at a time): its first k lanes read the items' keys, positions and weights and turn them into
+// row addresses (the split matrix's prefix sums are in shared memory), those of
+// its next piece being in flight meanwhile; then two rows at a time are read,
+// with no barrier between an SM's warps.  Neighbouring warps are in the same
+// rows, which memory likes better than one row a warp: 131,072 rows of 14 KiB
+// summed by twos 449 us (0.93 of the copy rate) against 466 to 585, and the more
+// warps an SM holds in other rows the slower (two blocks of eight: 466, four: 585).
 #include "moe_device.cuh"
 
 namespace {
@@ -72,74 +77,175 @@ __device__ __forceinline__ bool build_offsets(const WeightedParams& P, Offsets& 
   return !o.bad;
 }
 
-template <typename T>
-__device__ __forceinline__ void find_items(const WeightedParams& P, const Offsets& o, int r,
-                                           long long t, const T** row, T** d_row, float* w,
-                                           int* bad) {
-  const int j = threadIdx.x;
-  if (j < P.k) {
-    const long long i = t * P.k + j;
-    const int key = P.key[r][i];
-    const long long pos = P.pos[r][i];
-    bool ok = key >= 0 && key < P.W * P.K;
-    const int p = ok ? key / P.K : 0;
-    ok = ok && pos >= o.in_off[r][p] && pos < o.in_off[r][p + 1];
-    const long long at = ok ? (o.base[r][p] + pos) * P.H : 0;
-    row[j] = static_cast<const T*>(P.peer[p]) + at;
-    if (d_row != nullptr) d_row[j] = static_cast<T*>(P.d_peer[p]) + at;
-    w[j] = P.weight[r] != nullptr ? P.weight[r][i] : 1.0f;
-    if (!ok) *bad = 1;
+// One lane's item of a token.
+struct Item {
+  int r, key;
+  long long t, pos;
+  float w;
+};
+
+// Token g of all ranks' (rank-major); its item j to lane j < k.
+__device__ __forceinline__ Item fetch_item(const WeightedParams& P, long long g, int lane) {
+  Item x;
+  x.r = 0;
+  while (P.token_first[x.r + 1] <= g) ++x.r;
+  x.t = g - P.token_first[x.r];
+  x.key = 0;
+  x.pos = 0;
+  x.w = 1.0f;
+  if (lane < P.k) {
+    const long long i = x.t * P.k + lane;
+    x.key = P.key[x.r][i];
+    x.pos = P.pos[x.r][i];
+    if (P.weight[x.r] != nullptr) x.w = P.weight[x.r][i];
   }
+  return x;
+}
+
+// The item's peer and row (lanes below k); false, in every lane, when one of
+// the token's items has none.
+__device__ __forceinline__ bool find_row(const WeightedParams& P, const Offsets& o, const Item& x,
+                                         int lane, int* peer, long long* row) {
+  bool ok = x.key >= 0 && x.key < P.W * P.K;
+  const int p = ok ? x.key / P.K : 0;
+  ok = ok && x.pos >= o.in_off[x.r][p] && x.pos < o.in_off[x.r][p + 1];
+  *peer = p;
+  *row = o.base[x.r][p] + x.pos;
+  const bool all = __all_sync(kAll, ok || lane >= P.k);
+  if (!all && lane == 0) note_error(P.status, A2AV_ERR_BAD_INDEX);
+  return all;
+}
+
+template <typename P>
+__device__ __forceinline__ P* from_lane(P* p, int lane) {
+  return reinterpret_cast<P*>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(p), lane));
 }
 
 constexpr int kWeightedThreads = 256;
 
+// N elements as 32-bit words (or one element): unpacked and packed in pairs.
 template <typename T, int N>
-__global__ void __launch_bounds__(kWeightedThreads)
+struct Piece {
+  static constexpr int kWords = N * sizeof(T) / 4;
+  struct alignas(4 * kWords) Raw {
+    uint32_t w[kWords];
+  };
+  static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        f[i] = __uint_as_float(r.w[i]);
+      } else {
+        const float2 v = unpack2(r.w[i], T());
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+      }
+    }
+  }
+  static __device__ __forceinline__ Raw pack(const float (&f)[N]) {
+    Raw r;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 4)
+        r.w[i] = __float_as_uint(f[i]);
+      else
+        r.w[i] = pack2(f[2 * i], f[2 * i + 1], T());
+    }
+    return r;
+  }
+};
+
+template <typename T>
+struct Piece<T, 1> {
+  using Raw = T;
+  static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[1]) { f[0] = to_float(r); }
+  static __device__ __forceinline__ Raw pack(const float (&f)[1]) { return from_float<T>(f[0]); }
+};
+
+// U vectors of a row, 32 apart.
+template <typename T, int N, int U>
+__device__ __forceinline__ void load_slice(typename Piece<T, N>::Raw (&x)[U], const T* row,
+                                           long long v0, long long nv) {
+  using V = typename Piece<T, N>::Raw;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (v0 + 32 * u < nv) x[u] = reinterpret_cast<const V*>(row)[v0 + 32 * u];
+}
+
+template <typename T, int N>
+__global__ void __launch_bounds__(kWeightedThreads, 2)
     combine_weighted_kernel(const __grid_constant__ WeightedParams P) {
   chain();
   __shared__ Offsets o;
-  __shared__ const T* row[A2AV_MAX_TOPK];
-  __shared__ float w[A2AV_MAX_TOPK];
-  __shared__ int bad;
+  using Q = Piece<T, N>;
+  using V = typename Q::Raw;
+  constexpr int kVectors = N * sizeof(T) == 16 ? 4 : 8, kSlice = 32 * kVectors;
+  const int lane = threadIdx.x & 31;
+  const long long nv = P.H / N, slices = (nv + kSlice - 1) / kSlice;
+  const long long warps = (long long)gridDim.x * (kWeightedThreads / 32);
+  const long long first = (long long)blockIdx.x * (kWeightedThreads / 32) + threadIdx.x / 32;
+  const long long tokens = P.token_first[P.W];
+  // token and slice of this warp, and the way to its next
+  long long g = first / slices, s = first - g * slices;
+  const long long g_on = warps / slices, s_on = warps - g_on * slices;
+  Item item;
+  if (g < tokens) item = fetch_item(P, g, lane);
   if (!build_offsets(P, o)) return;
-  using V = Vec<T, N>;
-  const long long nv = P.H / N;
-  for (long long g = blockIdx.x; g < P.token_first[P.W]; g += gridDim.x) {
-    int r = 0;
-    while (P.token_first[r + 1] <= g) ++r;
-    const long long t = g - P.token_first[r];
-    if (threadIdx.x == 0) bad = 0;
-    __syncthreads();
-    find_items<T>(P, o, r, t, row, nullptr, w, &bad);
-    __syncthreads();
-    if (bad) {
-      if (threadIdx.x == 0) note_error(P.status, A2AV_ERR_BAD_INDEX);
-    } else {
-      const T* res = P.token_in[r] != nullptr
-                         ? static_cast<const T*>(P.token_in[r]) + t * P.H : nullptr;
-      T* out = static_cast<T*>(P.out[r]) + t * P.H;
-      for (long long v = threadIdx.x; v < nv; v += blockDim.x) {
-        float acc[N];
+  while (g < tokens) {
+    const Item it = item;
+    const long long v0 = s * kSlice + lane;
+    g += g_on;
+    s += s_on;
+    if (s >= slices) {
+      s -= slices;
+      ++g;
+    }
+    if (g < tokens) item = fetch_item(P, g, lane);
+    int p;
+    long long at;
+    if (!find_row(P, o, it, lane, &p, &at)) continue;
+    const T* row = static_cast<const T*>(P.peer[p]) + at * P.H;  // (lanes below k)
+    const T* res = static_cast<const T*>(P.token_in[it.r]);
+    if (res != nullptr) res += it.t * P.H;
+    V* out = reinterpret_cast<V*>(static_cast<T*>(P.out[it.r]) + it.t * P.H);
+    V z[kVectors];
+    if (res != nullptr) load_slice<T, N, kVectors>(z, res, v0, nv);
+    float acc[kVectors][N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = 0.0f;
-        for (int j = 0; j < P.k; ++j) {
-          const V x = reinterpret_cast<const V*>(row[j])[v];
+    for (int u = 0; u < kVectors; ++u)
 #pragma unroll
-          for (int i = 0; i < N; ++i) acc[i] += w[j] * to_float(x.v[i]);
+      for (int i = 0; i < N; ++i) acc[u][i] = 0.0f;
+    for (int j = 0; j < P.k; j += 2) {
+      V x[kVectors], y[kVectors];
+      const bool two = j + 1 < P.k;
+      load_slice<T, N, kVectors>(x, from_lane(row, j), v0, nv);
+      const T* next = from_lane(row, two ? j + 1 : j);
+      if (two) load_slice<T, N, kVectors>(y, next, v0, nv);
+      const float wx = __shfl_sync(kAll, it.w, j), wy = __shfl_sync(kAll, it.w, two ? j + 1 : j);
+#pragma unroll
+      for (int u = 0; u < kVectors; ++u) {
+        float f[N];
+        Q::unpack(x[u], f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[u][i] += wx * f[i];
+        if (two) {
+          Q::unpack(y[u], f);
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[u][i] += wy * f[i];
         }
-        if (res != nullptr) {
-          const V x = reinterpret_cast<const V*>(res)[v];
-#pragma unroll
-          for (int i = 0; i < N; ++i) acc[i] += to_float(x.v[i]);
-        }
-        V y;
-#pragma unroll
-        for (int i = 0; i < N; ++i) y.v[i] = from_float<T>(acc[i]);
-        reinterpret_cast<V*>(out)[v] = y;
       }
     }
-    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kVectors; ++u)
+      if (v0 + 32 * u < nv) {
+        if (res != nullptr) {
+          float f[N];
+          Q::unpack(z[u], f);
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[u][i] += f[i];
+        }
+        out[v0 + 32 * u] = Q::pack(acc[u]);
+      }
   }
 }
 
@@ -148,76 +254,101 @@ __global__ void __launch_bounds__(kWeightedThreads)
     combine_weighted_backward_kernel(const __grid_constant__ WeightedParams P) {
   chain();
   __shared__ Offsets o;
-  __shared__ const T* row[A2AV_MAX_TOPK];
-  __shared__ T* d_row[A2AV_MAX_TOPK];
-  __shared__ float w[A2AV_MAX_TOPK];
-  __shared__ float part[kWeightedThreads / 32];
-  __shared__ int bad;
+  using Q = Piece<T, N>;
+  using V = typename Q::Raw;
+  constexpr int kVectors = N == 1 ? 8 : 16 / N, kSlice = 32 * kVectors;
+  const int lane = threadIdx.x & 31;
+  const long long nv = P.H / N, tokens = P.token_first[P.W];
+  const long long warps = (long long)gridDim.x * (kWeightedThreads / 32);
+  long long g = (long long)blockIdx.x * (kWeightedThreads / 32) + threadIdx.x / 32;
+  Item item;
+  if (g < tokens) item = fetch_item(P, g, lane);
   if (!build_offsets(P, o)) return;
-  using V = Vec<T, N>;
-  const long long nv = P.H / N;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (long long g = blockIdx.x; g < P.token_first[P.W]; g += gridDim.x) {
-    int r = 0;
-    while (P.token_first[r + 1] <= g) ++r;
-    const long long t = g - P.token_first[r];
-    if (threadIdx.x == 0) bad = 0;
-    __syncthreads();
-    find_items<T>(P, o, r, t, row, d_row, w, &bad);
-    __syncthreads();
-    if (bad) {
-      if (threadIdx.x == 0) note_error(P.status, A2AV_ERR_BAD_INDEX);
-      __syncthreads();
-      continue;
-    }
-    const T* dy = static_cast<const T*>(P.token_in[r]) + t * P.H;
-    for (int j = 0; j < P.k; ++j) {
-      float dot = 0.0f;
-      for (long long v = threadIdx.x; v < nv; v += blockDim.x) {
-        const V x = reinterpret_cast<const V*>(dy)[v];
+  while (g < tokens) {
+    const Item it = item;
+    g += warps;
+    if (g < tokens) item = fetch_item(P, g, lane);
+    int p;
+    long long at;
+    if (!find_row(P, o, it, lane, &p, &at)) continue;
+    const T* row = static_cast<const T*>(P.peer[p]) + at * P.H;
+    T* d_row = static_cast<T*>(P.d_peer[p]) + at * P.H;
+    const T* dy = static_cast<const T*>(P.token_in[it.r]) + it.t * P.H;
+    for (int j = 0; j < P.k; j += 2) {
+      const bool two = j + 1 < P.k;
+      const int j1 = two ? j + 1 : j;
+      const T *r0 = from_lane(row, j), *r1 = from_lane(row, j1);
+      T *d0 = from_lane(d_row, j), *d1 = from_lane(d_row, j1);
+      const float w0 = __shfl_sync(kAll, it.w, j), w1 = __shfl_sync(kAll, it.w, j1);
+      float dot0 = 0.0f, dot1 = 0.0f;
+      for (long long v0 = lane; v0 < nv; v0 += kSlice) {
+        V d[kVectors], x[kVectors], y[kVectors];
+        load_slice<T, N, kVectors>(d, dy, v0, nv);
         if (P.reads) {
-          const V y = reinterpret_cast<const V*>(row[j])[v];
-#pragma unroll
-          for (int i = 0; i < N; ++i) dot += to_float(x.v[i]) * to_float(y.v[i]);
+          load_slice<T, N, kVectors>(x, r0, v0, nv);
+          if (two) load_slice<T, N, kVectors>(y, r1, v0, nv);
         }
-        if (P.writes) {
-          V d;
 #pragma unroll
-          for (int i = 0; i < N; ++i) d.v[i] = from_float<T>(w[j] * to_float(x.v[i]));
-          reinterpret_cast<V*>(d_row[j])[v] = d;
+        for (int u = 0; u < kVectors; ++u) {
+          const long long v = v0 + 32 * u;
+          if (v >= nv) continue;
+          float f[N], h[N];
+          Q::unpack(d[u], f);
+          if (P.reads) {
+            Q::unpack(x[u], h);
+#pragma unroll
+            for (int i = 0; i < N; ++i) dot0 += f[i] * h[i];
+            if (two) {
+              Q::unpack(y[u], h);
+#pragma unroll
+              for (int i = 0; i < N; ++i) dot1 += f[i] * h[i];
+            }
+          }
+          if (P.writes) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) h[i] = w0 * f[i];
+            reinterpret_cast<V*>(d0)[v] = Q::pack(h);
+            if (two) {
+#pragma unroll
+              for (int i = 0; i < N; ++i) h[i] = w1 * f[i];
+              reinterpret_cast<V*>(d1)[v] = Q::pack(h);
+            }
+          }
         }
       }
       if (P.reads) {
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(kAll, dot, s);
-        if (lane == 0) part[warp] = dot;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-          float sum = 0.0f;
-          for (int i = 0; i < (int)blockDim.x / 32; ++i) sum += part[i];
-          P.d_weight[r][t * P.k + j] = sum;
+        for (int s = 16; s > 0; s >>= 1) {
+          dot0 += __shfl_xor_sync(kAll, dot0, s);
+          dot1 += __shfl_xor_sync(kAll, dot1, s);
         }
-        __syncthreads();
+        float* dw = P.d_weight[it.r] + it.t * P.k + j;
+        if (lane == 0) dw[0] = dot0;
+        if (lane == 1 && two) dw[1] = dot1;
       }
     }
-    __syncthreads();
   }
 }
 
 using WeightedKernel = void (*)(WeightedParams);
 
-template <typename T>
-WeightedKernel weighted_kernel_of(bool vec, bool backward) {
-  constexpr int kV = 16 / sizeof(T);
-  if (backward)
-    return vec ? combine_weighted_backward_kernel<T, kV> : combine_weighted_backward_kernel<T, 1>;
-  return vec ? combine_weighted_kernel<T, kV> : combine_weighted_kernel<T, 1>;
+// `bytes`: of a vector, 16, 4 or one element, as every row and buffer allows.
+template <typename T, int N>
+WeightedKernel weighted_kernel_of(bool backward) {
+  return backward ? combine_weighted_backward_kernel<T, N> : combine_weighted_kernel<T, N>;
 }
 
-WeightedKernel weighted_kernel_of(int dtype, bool vec, bool backward) {
-  if (dtype == A2AV_F32) return weighted_kernel_of<float>(vec, backward);
-  if (dtype == A2AV_BF16) return weighted_kernel_of<__nv_bfloat16>(vec, backward);
-  return weighted_kernel_of<__half>(vec, backward);
+template <typename T>
+WeightedKernel weighted_kernel_of(int bytes, bool backward) {
+  if (bytes == 16) return weighted_kernel_of<T, 16 / sizeof(T)>(backward);
+  return bytes == 4 ? weighted_kernel_of<T, 4 / sizeof(T)>(backward)
+                    : weighted_kernel_of<T, 1>(backward);
+}
+
+WeightedKernel weighted_kernel_of(int dtype, int bytes, bool backward) {
+  if (dtype == A2AV_F32) return weighted_kernel_of<float>(bytes, backward);
+  if (dtype == A2AV_BF16) return weighted_kernel_of<__nv_bfloat16>(bytes, backward);
+  return weighted_kernel_of<__half>(bytes, backward);
 }
 
 // Both directions: `peers` read, `d_peers` written (either may be NULL as the
@@ -236,7 +367,7 @@ int weighted_call(a2av_handle* h, int K, int k, int64_t H, int dtype, const void
     return A2AV_ERR_UNSUPPORTED;
   WeightedParams P;
   std::memset(&P, 0, sizeof(P));
-  bool vec = H * size % 16 == 0;
+  uintptr_t low = (uintptr_t)(H * size);  // the bits below a common alignment
   for (int r = 0; r < W; ++r) {
     const int64_t n = tokens[r];
     if (n < 0 || rows_per_peer[r] < 0) return A2AV_ERR_INVALID_ARG;
@@ -249,7 +380,7 @@ int weighted_call(a2av_handle* h, int K, int k, int64_t H, int dtype, const void
                                  (d_peers != nullptr && P.d_peer[r] == nullptr)))
       return A2AV_ERR_INVALID_ARG;
     if (!aligned_to(P.peer[r], size) || !aligned_to(P.d_peer[r], size)) return A2AV_ERR_INVALID_ARG;
-    vec = vec && aligned_to(P.peer[r], 16) && aligned_to(P.d_peer[r], 16);
+    low |= (uintptr_t)P.peer[r] | (uintptr_t)P.d_peer[r];
     if (n == 0) continue;
     P.key[r] = keys[r];
     P.pos[r] = reinterpret_cast<const long long*>(pos[r]);
@@ -264,7 +395,7 @@ int weighted_call(a2av_handle* h, int K, int k, int64_t H, int dtype, const void
         !aligned_to(P.token_in[r], size) || !aligned_to(P.out[r], size) ||
         !aligned_to(P.d_weight[r], 4))
       return A2AV_ERR_INVALID_ARG;
-    vec = vec && aligned_to(P.token_in[r], 16) && aligned_to(P.out[r], 16);
+    low |= (uintptr_t)P.token_in[r] | (uintptr_t)P.out[r];
   }
   const int rc = current_device(h);
   if (rc != A2AV_OK) return rc;
@@ -278,11 +409,18 @@ int weighted_call(a2av_handle* h, int K, int k, int64_t H, int dtype, const void
   P.k = k;
   P.reads = peers != nullptr;
   P.writes = d_peers != nullptr;
-  const long long fit = 8LL * h->sms;
-  const unsigned grid = (unsigned)(P.token_first[W] < fit ? P.token_first[W] : fit);
-  const cudaError_t e =
-      launch_chained(weighted_kernel_of(dtype, vec, backward), dim3(grid), kWeightedThreads, 0,
-                     static_cast<cudaStream_t>(stream), h->pdl, P);
+  const int bytes = low % 16 == 0 ? 16 : low % 4 == 0 ? 4 : size;
+  const WeightedKernel kernel = weighted_kernel_of(dtype, bytes, backward);
+  int fit = 0;  // blocks an SM holds
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, kWeightedThreads, 0) != cudaSuccess)
+    return A2AV_ERR_CUDA;
+  const long long most = (long long)fit * h->sms, warps = kWeightedThreads / 32;
+  const int slice = bytes == 16 ? 128 : 256;  // vectors of a forward warp's slice
+  const long long slices = backward ? 1 : (H * size / bytes + slice - 1) / slice;
+  const long long blocks = (P.token_first[W] * slices + warps - 1) / warps;
+  const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+  const cudaError_t e = launch_chained(kernel, dim3(grid), kWeightedThreads, 0,
+                                       static_cast<cudaStream_t>(stream), h->pdl, P);
   if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return A2AV_ERR_CUDA;
   return A2AV_OK;
 }
