@@ -352,27 +352,45 @@ def a2av_combine_weighted_backward(handle, keys_per_peer: int, topk: int, hidden
 
 
 # --------------------------------------------------------- torch-facing --
-def _plain_pointers(tensors, dtype, shapes, address):
-    """``_marshal.pointers`` (csrc/marshal.c) without the compiled module."""
-    try:
-        if not all(t.is_cuda and t.dtype == dtype and t.is_contiguous() for t in tensors) or (
-                shapes is not None and [t.shape for t in tensors] != shapes):
+class _PlainMarshal:
+    """``_marshal`` (csrc/marshal.c) without the compiled module."""
+
+    @staticmethod
+    def pointers(tensors, dtype, shapes, address):
+        try:
+            if not all(t.is_cuda and t.dtype == dtype and t.is_contiguous() for t in tensors) or (
+                    shapes is not None and [t.shape for t in tensors] != shapes):
+                return False
+        except AttributeError:  # None among them
             return False
-    except AttributeError:  # None among them
-        return False
-    for r, t in enumerate(tensors):
-        ctypes.c_void_p.from_address(address + 8 * r).value = t.data_ptr()
-    return True
+        for r, t in enumerate(tensors):
+            ctypes.c_void_p.from_address(address + 8 * r).value = t.data_ptr()
+        return True
+
+    @staticmethod
+    def rows(tensors):
+        try:
+            shapes = [t.shape for t in tensors]
+        except AttributeError:
+            return None
+        if not shapes or any(len(s) != 2 or s[1] != shapes[0][-1] for s in shapes):
+            return None
+        return [s[0] for s in shapes], shapes[0][1]
+
+    @staticmethod
+    def sizes(tensors):
+        try:
+            return [t.numel() for t in tensors]
+        except AttributeError:
+            return None
 
 
-def _pointers(*args):
-    """The compiled check, from the first call on (it may be built after the import)."""
-    global _pointers
+def _load_marshal():
     try:
-        from ._marshal import pointers as _pointers
+        from . import _marshal
+        return _marshal
     except ImportError:
-        _pointers = _plain_pointers
-    return _pointers(*args)
+        return _PlainMarshal
 
 
 class BoundCall:
@@ -417,6 +435,11 @@ class A2av:
         self.handle, self.world_size, self._path = h, int(world_size), int(path)
         import torch
         self._device = torch.cuda.current_device()
+        self._marshal = _load_marshal()
+        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._codes = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+        self._int32, self._int64, self._float = torch.int32, torch.int64, torch.float32
+        self._pointers, self._counts = ctypes.c_void_p * self.world_size, ctypes.c_int64 * self.world_size
         if path != PATH_AUTO:
             self._check(a2av_set_path(h, path), "a2av_set_path")
         if ctas_per_sm:
@@ -436,11 +459,9 @@ class A2av:
 
     def _queue(self, stream):
         """The cudaStream_t to enqueue on: ``stream``, or torch's current one."""
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if stream is not None or raw is None:
+        if stream is not None or self._raw_stream is None:
             return _address(self._stream(stream))
-        return ctypes.c_void_p(raw(self._device) or None)
+        return ctypes.c_void_p(self._raw_stream(self._device) or None)
 
     def _buffers(self, tensors, what):
         """Pointer array for W buffers; True when one lives in pinned host memory."""
@@ -669,10 +690,9 @@ class A2av:
     # ------------------------------------------- the MoE layer's operators --
     def _dtype(self, tensors, name, allowed):
         """The element type that a list's tensors share, and its code."""
-        import torch
         for t in tensors:
             if t is not None:
-                code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(t.dtype)
+                code = self._codes.get(t.dtype)
                 if code not in allowed:
                     raise ValueError(f"{name}: {t.dtype} is not supported")
                 return t.dtype, code
@@ -684,10 +704,10 @@ class A2av:
         W = self.world_size
         if len(tensors) != W:
             raise ValueError(f"{name}: expected {W} tensors, got {len(tensors)}")
-        arr = (ctypes.c_void_p * W)()
-        if _pointers(tensors, dtype, shapes, ctypes.addressof(arr)):
+        arr = self._pointers()
+        if self._marshal.pointers(tensors, dtype, shapes, ctypes.addressof(arr)):
             return arr
-        arr = (ctypes.c_void_p * W)()
+        arr = self._pointers()
         for r, t in enumerate(tensors):
             if t is None:
                 if shapes is not None and 0 not in shapes[r]:
@@ -715,6 +735,9 @@ class A2av:
         """Rows and the common second dimension of W [rows, n] tensors."""
         if len(tensors) != self.world_size:
             raise ValueError(f"{name}: expected {self.world_size} tensors, got {len(tensors)}")
+        found = self._marshal.rows(tensors)
+        if found is not None:
+            return found
         shapes = [(0, None) if t is None else t.shape for t in tensors]
         widths = {s[-1] for s in shapes if s[-1:] != (None,)}
         if len(widths) != 1 or any(len(s) != 2 for s in shapes):
@@ -723,20 +746,18 @@ class A2av:
 
     def _route_args(self, logits, keys, weights, weights_name, topk, score, groups, top_groups,
                     group_top, renormalise, scale):
-        import torch
         if score not in _SCORES:
             raise ValueError(f"score must be one of {sorted(_SCORES)}")
         rows, E = self._tokens(logits, "logits")
         dtype, code = self._dtype(logits, "logits", (F32, BF16, F16))
         route = A2avRoute(E, int(topk), code, _SCORES[score], int(groups), int(top_groups),
                           int(group_top), int(bool(renormalise)), float(scale))
-        W = self.world_size
         if not 1 <= route.topk <= E:
             raise ValueError(f"topk must be in 1..{E}")
         shapes = [(n, route.topk) for n in rows]
         return (dtype, ctypes.byref(route), self._list(logits, "logits", dtype),
-                (ctypes.c_int64 * W)(*rows), self._list(keys, "keys", torch.int32, shapes),
-                self._list(weights, weights_name, torch.float32, shapes), rows, E)
+                self._counts(*rows), self._list(keys, "keys", self._int32, shapes),
+                self._list(weights, weights_name, self._float, shapes), rows, E)
 
     def route(self, logits, keys, weights, topk: int, counts=None, bias=None,
               score: str = "softmax", groups: int = 1, top_groups: int = 1, group_top: int = 1,
@@ -748,12 +769,11 @@ class A2av:
         dispatch; ``weights[r]`` float32 [T, topk]; ``counts`` (optional)
         int64 [W, E], rank r's items for each expert.  ``bias``: optional
         float32 [E], added to the scores for the choice alone."""
-        import torch
         dtype, cfg, x, n, k, w, rows, E = self._route_args(
             logits, keys, weights, "weights", topk, score, groups, top_groups, group_top,
             renormalise, scale)
         W = self.world_size
-        if bias is not None and (bias.dtype != torch.float32 or not bias.is_cuda
+        if bias is not None and (bias.dtype != self._float or not bias.is_cuda
                                  or bias.shape != (E,) or not bias.is_contiguous()):
             raise ValueError(f"bias must be a contiguous CUDA float32 [{E}] tensor")
         if counts is not None:
@@ -793,7 +813,7 @@ class A2av:
         dtype, code = self._dtype(weights, "weights", (F16, BF16))
         self._matrix(counts, (W, W * K), "counts")
         shape = A2avExpert(K, D, N, code, _ACTIVATIONS[activation], int(bool(gated)))
-        return (shape, self._list(rows, "rows", dtype), (ctypes.c_int64 * W)(*n),
+        return (shape, self._list(rows, "rows", dtype), self._counts(*n),
                 ctypes.c_void_p(counts.data_ptr()),
                 self._list(weights, "weights", dtype, [(K, Z, D)] * W), n, K, Z, dtype)
 
@@ -862,23 +882,22 @@ class A2av:
 
     def _weighted_args(self, in_splits, keys, sorted_pos, keys_per_peer, token_rows, name):
         """What both directions of the weighted combine share."""
-        import torch
         W = self.world_size
         sp = self._matrix(in_splits, (W, W), "in_splits")
         n, H = self._tokens(token_rows, name)
         dtype, code = self._dtype(token_rows, name, (F32, BF16, F16))
-        sizes = [[0 if t is None else t.numel() for t in ts] for ts in (keys, sorted_pos)]
+        sizes = [self._marshal.sizes(ts) or [0 if t is None else t.numel() for t in ts]
+                 for ts in (keys, sorted_pos)]
         k = next((m // T for m, T in zip(sizes[0], n) if T), 1) or 1
+        items = [T * k for T in n]
         for m, what in zip(sizes, ("keys", "sorted_pos")):
-            if m != [T * k for T in n]:
+            if m != items:
                 raise ValueError(f"{what} must have one entry per item of each rank")
-        return (int(keys_per_peer), k, H, code, sp, self._list(keys, "keys", torch.int32),
-                self._list(sorted_pos, "sorted_pos", torch.int64), (ctypes.c_int64 * W)(*n),
-                n, H, dtype)
+        return (int(keys_per_peer), k, H, code, sp, self._list(keys, "keys", self._int32),
+                self._list(sorted_pos, "sorted_pos", self._int64), self._counts(*n), n, H, dtype)
 
     def _item_weights(self, weights, name, n, k):
-        import torch
-        return self._list(weights, name, torch.float32, [(m, k) for m in n])
+        return self._list(weights, name, self._float, [(m, k) for m in n])
 
     def combine_weighted(self, peers, in_splits, keys, sorted_pos, keys_per_peer: int, weights,
                          outputs, residual=None, stream=None, _bind=False):
@@ -912,14 +931,19 @@ class A2av:
             if ts is None:
                 arrays.append(None)
                 continue
-            if any(t is not None and (t.dim() != 2 or t.shape[1] != H) for t in ts):
+            found = self._marshal.rows(ts)
+            if found is None:  # None among them, or of other shapes
+                if any(t is not None and (t.dim() != 2 or t.shape[1] != H) for t in ts):
+                    raise ValueError(f"{name} must be [rows, {H}] tensors")
+                found = [0 if t is None else t.shape[0] for t in ts], H
+            rows, width = found
+            if width != H:
                 raise ValueError(f"{name} must be [rows, {H}] tensors")
-            rows = [0 if t is None else t.shape[0] for t in ts]
             if held is not None and rows != held:
                 raise ValueError("peers and d_peers must have the same number of rows")
             held = rows
             arrays.append(self._list(ts, name, dtype))
-        return _i64_array(held), arrays
+        return self._counts(*held), arrays
 
     def combine_weighted_backward(self, peers, in_splits, keys, sorted_pos, keys_per_peer: int,
                                   weights, d_outputs, d_peers=None, d_weights=None, stream=None):

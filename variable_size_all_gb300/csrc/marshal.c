@@ -6,11 +6,16 @@
  * a contiguous CUDA tensor of `dtype` and of its shape in the list `shapes`
  * (None: any); their data pointers are then at `address`, 8 bytes each.  False
  * otherwise (the binding then finds out which, and says so).
+ *
+ * rows(tensors) -> (rows of each, their common width), or None when they are
+ * not all 2-D tensors of one width.
+ *
+ * sizes(tensors) -> the number of elements of each, or None.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
-static PyObject *s_is_cuda, *s_is_contiguous, *s_dtype, *s_shape, *s_data_ptr;
+static PyObject *s_is_cuda, *s_is_contiguous, *s_dtype, *s_shape, *s_data_ptr, *s_numel;
 
 /* 1: the attribute is `want`; 0: it is not, or there is none. */
 static int is_attr(PyObject *t, PyObject *name, PyObject *want) {
@@ -66,9 +71,61 @@ static PyObject *pointers(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   return PyBool_FromLong(good);
 }
 
+static PyObject *rows(PyObject *self, PyObject *tensors) {
+  (void)self;
+  PyObject *list = PySequence_Fast(tensors, "a sequence of tensors");
+  if (list == NULL) return NULL;
+  const Py_ssize_t count = PySequence_Fast_GET_SIZE(list);
+  PyObject *out = PyList_New(count), *width = NULL;
+  int good = out != NULL && count > 0;
+  for (Py_ssize_t i = 0; i < count && good; ++i) {
+    PyObject *shape = PyObject_GetAttr(PySequence_Fast_GET_ITEM(list, i), s_shape);
+    good = shape != NULL && PyTuple_Check(shape) && PyTuple_GET_SIZE(shape) == 2;
+    if (good) {
+      PyObject *w = PyTuple_GET_ITEM(shape, 1), *n = PyTuple_GET_ITEM(shape, 0);
+      if (width == NULL) {
+        width = w;
+        Py_INCREF(width);
+      } else {
+        good = PyObject_RichCompareBool(width, w, Py_EQ) == 1;
+      }
+      Py_INCREF(n);
+      PyList_SET_ITEM(out, i, n);
+    }
+    Py_XDECREF(shape);
+  }
+  Py_DECREF(list);
+  PyErr_Clear();
+  PyObject *result = good ? PyTuple_Pack(2, out, width) : Py_NewRef(Py_None);
+  Py_XDECREF(out);
+  Py_XDECREF(width);
+  return result;
+}
+
+static PyObject *sizes(PyObject *self, PyObject *tensors) {
+  (void)self;
+  PyObject *list = PySequence_Fast(tensors, "a sequence of tensors");
+  if (list == NULL) return NULL;
+  const Py_ssize_t count = PySequence_Fast_GET_SIZE(list);
+  PyObject *out = PyList_New(count);
+  int good = out != NULL;
+  for (Py_ssize_t i = 0; i < count && good; ++i) {
+    PyObject *n = PyObject_CallMethodNoArgs(PySequence_Fast_GET_ITEM(list, i), s_numel);
+    good = n != NULL;
+    if (good) PyList_SET_ITEM(out, i, n);
+  }
+  Py_DECREF(list);
+  PyErr_Clear();
+  if (good) return out;
+  Py_XDECREF(out);
+  Py_RETURN_NONE;
+}
+
 static PyMethodDef methods[] = {
     {"pointers", (PyCFunction)(void (*)(void))pointers, METH_FASTCALL,
      "Checks a list of tensors and stores their data pointers."},
+    {"rows", rows, METH_O, "Rows and common width of a list of 2-D tensors."},
+    {"sizes", sizes, METH_O, "The number of elements of each tensor."},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", NULL, -1, methods,
@@ -80,8 +137,9 @@ PyMODINIT_FUNC PyInit__marshal(void) {
   s_dtype = PyUnicode_InternFromString("dtype");
   s_shape = PyUnicode_InternFromString("shape");
   s_data_ptr = PyUnicode_InternFromString("data_ptr");
+  s_numel = PyUnicode_InternFromString("numel");
   if (s_is_cuda == NULL || s_is_contiguous == NULL || s_dtype == NULL || s_shape == NULL ||
-      s_data_ptr == NULL)
+      s_data_ptr == NULL || s_numel == NULL)
     return NULL;
   return PyModule_Create(&module);
 }

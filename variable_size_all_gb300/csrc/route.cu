@@ -210,20 +210,29 @@ __global__ void __launch_bounds__(32 * kRouteWarps, L < 32 ? 4 : 1) route_kernel
   chain();
   constexpr int kTokens = 32 / L;  // of a warp
   extern __shared__ int hist[];
+  constexpr int kEight = NJ < 8 ? NJ : 8, kMaxima = NJ / kEight;
+  __shared__ __align__(16) float choices[kRouteWarps * kTokens][L * NJ];
+  __shared__ __align__(16) float biases[L * NJ];
   __shared__ Candidate lists[kRouteWarps * kTokens][kListed];
   __shared__ int picks[kRouteWarps * kTokens][A2AV_MAX_TOPK];
   const int r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / L, sl = lane % L;
   const int E = P.E, k = P.k;
-  if (P.counts != nullptr) {
+  if (P.counts != nullptr)
     for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
-    __syncthreads();
-  }
+  if (P.bias != nullptr)
+    for (int e = threadIdx.x; e < L * NJ; e += blockDim.x) biases[e] = e < E ? P.bias[e] : 0.0f;
+  __syncthreads();
   const bool by_logit = P.score == A2AV_SCORE_SOFTMAX && P.bias == nullptr && P.group_top == 1;
   const bool softmax = P.score == A2AV_SCORE_SOFTMAX;
   const bool need_sum = softmax && (!by_logit || !P.renormalise);
   const int n = P.tokens[r];
+  // the experts of this lane (the first `present` of its NJ; -inf where a group
+  // that is dropped has one, NaN where there is none)
+  const int present = E - sl * NJ;
+  const bool whole = E == L * NJ;
   Candidate* list = lists[warp * kTokens + sub];
+  float* row_c = choices[warp * kTokens + sub];
   int* chosen = picks[warp * kTokens + sub];
   for (int t0 = (blockIdx.x * kRouteWarps + warp) * kTokens; t0 < n;
        t0 += gridDim.x * kRouteWarps * kTokens) {
@@ -243,25 +252,29 @@ __global__ void __launch_bounds__(32 * kRouteWarps, L < 32 ? 4 : 1) route_kernel
       for (int j = 0; j < NJ; ++j) total += exp_below(c[j], m);
       total = lanes_sum<L>(total);
     }
-    // (a choice that is NaN counts as -inf; from here on NaN is no expert at all)
+    if (!softmax || !by_logit) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        c[j] = !softmax         ? sigmoid(c[j])
+               : m == -INFINITY ? 0.0f
+                                : expf(c[j] - m) / total;
+    }
+    if (P.bias != nullptr) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) c[j] += biases[sl * NJ + j];
+    }
+    // a choice that is NaN counts as -inf; from here on NaN is no expert at all
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      float v = c[j];
-      if (!softmax)
-        v = sigmoid(v);
-      else if (!by_logit)
-        v = m == -INFINITY ? 0.0f : expf(v - m) / total;
-      const int e = sl * NJ + j;
-      if (P.bias != nullptr && e < E) v += __ldg(P.bias + e);
-      if (v != v) v = -INFINITY;
-      c[j] = e < E ? v : NAN;
+      c[j] = fmaxf(c[j], -INFINITY);
+      if (!whole && j >= present) c[j] = NAN;
     }
     if (P.groups > 1) {
       if (L < 32 || P.group_lanes > 0) {
         const bool keep = keep_by_lanes<L>(P, c, P.group_lanes, sl);
+        const float gone = present > 0 ? -INFINITY : NAN;  // (lanes are whole here)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-          if (!keep && c[j] == c[j]) c[j] = -INFINITY;
+        for (int j = 0; j < NJ; ++j) c[j] = keep ? c[j] : gone;
       } else {
         const unsigned keep = keep_groups(P, c, lane);
 #pragma unroll
@@ -270,7 +283,6 @@ __global__ void __launch_bounds__(32 * kRouteWarps, L < 32 ? 4 : 1) route_kernel
       }
     }
     // the k-th largest of the maxima of eight
-    constexpr int kEight = NJ < 8 ? NJ : 8, kMaxima = NJ / kEight;
     unsigned most[kMaxima], best = 0;
 #pragma unroll
     for (int q = 0; q < kMaxima; ++q) {
@@ -301,10 +313,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps, L < 32 ? 4 : 1) route_kernel
     }
     const int count = __shfl_sync(kAll, upto, L - 1, L);
     if (!__any_sync(kAll, count > kListed)) {
-      Candidate* to = list + (upto - own);
+      // (a lane has one or two: taken by their numbers from its choices in memory)
+      float* to_c = row_c + sl * NJ;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        if ((marks >> j) & 1) *to++ = Candidate{c[j], sl * NJ + j};
+      for (int j = 0; j < NJ; ++j) to_c[j] = c[j];
+      Candidate* to = list + (upto - own);
+      for (; marks != 0; marks &= marks - 1) {
+        const int j = __ffs(marks) - 1;
+        *to++ = Candidate{to_c[j], sl * NJ + j};
+      }
       __syncwarp();
       for (int i = sl; i < count; i += L) {
         const Candidate x = list[i];
@@ -367,6 +384,10 @@ template <typename T, int NJ, bool kVec>
 __global__ void __launch_bounds__(32 * kRouteWarps)
     route_backward_kernel(const __grid_constant__ RouteParams P) {
   chain();
+  // what the chosen experts get, at their places in the row: zeros between tokens
+  __shared__ __align__(16) float scatter[kRouteWarps][32 * NJ];
+  for (int i = threadIdx.x; i < kRouteWarps * 32 * NJ; i += blockDim.x) (&scatter[0][0])[i] = 0.0f;
+  __syncthreads();
   const int r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = P.E, k = P.k;
   const bool softmax = P.score == A2AV_SCORE_SOFTMAX;
@@ -387,8 +408,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
     float d[NJ];  // the row's gradient
 #pragma unroll
     for (int j = 0; j < NJ; ++j) d[j] = 0.0f;
-    float onto = 0.0f;  // what the lane's choice gets
     if (!bad) {
+      float* own = scatter[warp] + lane * NJ;
       if (dense) {
         float x[NJ];
         load_logits<T, NJ, kVec>(row, E, lane, x);
@@ -406,33 +427,35 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
         const float inv = m == -INFINITY ? 0.0f : 1.0f / total;
         const float p = lane < k ? exp_below(xs, m) * inv : 0.0f;
         const float dot = lanes_sum<32>(lane < k ? g * p : 0.0f);
+        if (lane < k) scatter[warp][key] = g;
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) d[j] = -(x[j] * inv) * dot;
-        onto = p * g;  // added to -p * dot of the same expert
-      } else if (softmax) {
-        const float m = lanes_max<32>(xs);  // (xs is -inf in the lanes past k)
-        const float e = lane < k ? exp_below(xs, m) : 0.0f;
-        const float sum = lanes_sum<32>(e);
-        const float q = sum == 0.0f ? 0.0f : e / sum;
-        const float dot = lanes_sum<32>(lane < k ? g * q : 0.0f);
-        onto = q * (g - dot);
+        for (int j = 0; j < NJ; ++j) d[j] = x[j] * inv * (own[j] - dot);
       } else {
-        const float s = lane < k ? sigmoid(xs) : 0.0f;
-        float ds = g;
-        if (P.renormalise) {
-          const float sum = lanes_sum<32>(s);
-          const float dot = lanes_sum<32>(lane < k ? g * s : 0.0f);
-          ds = sum == 0.0f ? 0.0f : (g - dot / sum) / sum;
+        float onto;  // what the lane's choice gets
+        if (softmax) {
+          const float m = lanes_max<32>(xs);  // (xs is -inf in the lanes past k)
+          const float e = lane < k ? exp_below(xs, m) : 0.0f;
+          const float sum = lanes_sum<32>(e);
+          const float q = sum == 0.0f ? 0.0f : e / sum;
+          onto = q * (g - lanes_sum<32>(lane < k ? g * q : 0.0f));
+        } else {
+          const float s = lane < k ? sigmoid(xs) : 0.0f;
+          float ds = g;
+          if (P.renormalise) {
+            const float sum = lanes_sum<32>(s);
+            const float dot = lanes_sum<32>(lane < k ? g * s : 0.0f);
+            ds = sum == 0.0f ? 0.0f : (g - dot / sum) / sum;
+          }
+          onto = ds * s * (1.0f - s);
         }
-        onto = ds * s * (1.0f - s);
-      }
-      for (int i = 0; i < k; ++i) {
-        const int e = __shfl_sync(kAll, key, i);
-        const float v = __shfl_sync(kAll, onto, i);
+        if (lane < k) scatter[warp][key] = onto;
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-          if (e == lane * NJ + j) d[j] += v;
+        for (int j = 0; j < NJ; ++j) d[j] = own[j];
       }
+      __syncwarp();
+      if (lane < k) scatter[warp][key] = 0.0f;
     }
     T* out = static_cast<T*>(P.d_logits[r]) + (long long)t * E;
     if (kVec) {
