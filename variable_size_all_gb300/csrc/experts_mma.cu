@@ -61,6 +61,15 @@ struct Bars {
   unsigned tmem;
 };
 
+// The copies that bring a CTA's half of a tile's granules.
+struct Copies {
+  int count;
+  unsigned bytes;
+  int row[kTileGranules / 2];
+  int at[kTileGranules / 2];   // granules into the stage's N side
+  int box[kTileGranules / 2];  // 2^box granules
+};
+
 // A tile as the scheduler (warp 3 of each CTA) describes it to the others.
 struct Slot {
   int p, e;                // peer, local expert
@@ -68,6 +77,7 @@ struct Slot {
   int granules;            // 1 .. 32
   int row[kTileGranules];  // each granule's first row in the peer's buffers
   int n[kTileGranules];    // and its rows, 0 past the last granule
+  Copies copies;           // of this CTA
 };
 
 // Tiles before each expert.
@@ -310,15 +320,9 @@ __device__ __forceinline__ void apply_act(int act, float (&v)[16]) {
 // that it ends with the run (both bring the same bytes where they overlap).
 // The half's last run takes one larger box instead where there is room: what
 // that brings past the run is in no result.  So a run costs one or two copies;
-// issuing them is what bounds tiles of many short groups.  Returns the bytes.
-struct Copies {
-  int count;
-  int row[kTileGranules / 2];
-  int at[kTileGranules / 2];   // granules into the stage's N side
-  int box[kTileGranules / 2];  // 2^box granules
-};
-
-__device__ __forceinline__ unsigned plan_copies(const Slot& slot, uint32_t rank, Copies& c) {
+// issuing them is what bounds tiles of many short groups.
+__device__ __forceinline__ void plan_copies(Slot& slot, uint32_t rank) {
+  Copies& c = slot.copies;
   const int half = (slot.granules + 1) / 2;
   const int j0 = rank == 0 ? 0 : half, j1 = rank == 0 ? half : slot.granules;
   unsigned granules = 0;
@@ -345,7 +349,7 @@ __device__ __forceinline__ unsigned plan_copies(const Slot& slot, uint32_t rank,
     j += run;
   }
   c.count = n;
-  return granules * 1024;
+  c.bytes = granules * 1024;
 }
 
 // kMn: the weights' contraction runs over their rows (the rows' gradient), so
@@ -360,7 +364,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
   __shared__ GroupTable g;
   __shared__ TileTable tt;
   __shared__ Slot slots[kSlots];
-  __shared__ Copies copies;
   __shared__ Bars b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -386,6 +389,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
       if (!ok) break;
       describe_tile(P.g, g, tt, t, nf, kTileF, slots[sl], lane);
       __syncwarp();
+      if (lane == 0) plan_copies(slots[sl], rank);
       if (lane == 0) bar_arrive_here(smem_addr(&b.slot_full[sl]));
     }
     if (!ok && lane == 0) note_error(P.g.status, A2AV_ERR_TIMEOUT);
@@ -400,12 +404,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
       ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
       if (!ok) break;
       const int p = slots[sl].p, e = slots[sl].e, f0 = slots[sl].f + kMyF * rank;
-      unsigned bytes = 0;
-      if (lane == 0) {
-        bytes = kSideBytes + plan_copies(slots[sl], rank, copies);
-        bar_arrive_here(smem_addr(&b.slot_empty[sl]));
-      }
-      __syncwarp();
+      const Copies& copies = slots[sl].copies;
+      const unsigned bytes = kSideBytes + copies.bytes;
       const int n = lane - kOwn;
       const bool mine = n < copies.count;
       const CUtensorMap* map = &P.weights[p];
@@ -416,6 +416,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
         row = copies.row[n];
         to = kSideBytes + copies.at[n] * 1024;
       }
+      __syncwarp();
+      if (lane == 0) bar_arrive_here(smem_addr(&b.slot_empty[sl]));
       for (int kb = 0; kb < blocks; ++kb, ++it) {
         const unsigned s = it % kStages;
         ok = __all_sync(kAll, bar_wait(smem_addr(&b.empty[s]), ((it / kStages) & 1) ^ 1));
@@ -675,12 +677,20 @@ __global__ void __launch_bounds__(256) expert_tails_kernel(const __grid_constant
   }
 }
 
+// A tile as the scheduler describes it.
+struct GradSlot {
+  int p, e, z, d;                     // peer, local expert, first row and column of d_w
+  int blocks, last;                   // blocks of 64 rows; steps of 16 in the last
+  int first[kW + 1], n[kW + 1];       // first row and blocks of each group, then of the packed rows
+};
+
 template <typename T>
 __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     expert_wgrad_kernel(const __grid_constant__ MmaParams P) {
   extern __shared__ unsigned char dynamic[];
   __shared__ GroupTable g;
   __shared__ TailTable tt;
+  __shared__ GradSlot slots[kSlots];
   __shared__ Bars b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -690,29 +700,59 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
   if (good) build_tails(P.g, g, tt);
   pair_begin(b, warp, rank);
   const int W = P.g.W, K = P.g.K;
-  const int nz = (P.Z + kM - 1) / kM, nd = (P.D + kN - 1) / kN;
-  const long long tiles = good ? (long long)W * K * nz * nd : 0;
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const unsigned nz = (P.Z + kM - 1) / kM, nd = (P.D + kN - 1) / kN;
+  const unsigned tiles = good ? (unsigned)(W * K) * nz * nd : 0;
+  const unsigned pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   bool ok = true;
+  unsigned i = 0;  // tiles so far
 
-  if (warp == 0) {
+  if (warp == 3) {
+    // --------------------------------------------------- scheduler --
+    for (unsigned t = pair; t < tiles; t += pairs, ++i) {
+      const unsigned sl = i % kSlots;
+      ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_empty[sl]), ((i / kSlots) & 1) ^ 1));
+      if (!ok) break;
+      GradSlot& slot = slots[sl];
+      const unsigned pe = t / (nz * nd), in = t - pe * (nz * nd);
+      const int p = pe / K, e = pe - p * K, tail = tt.rows[pe];
+      if (lane < W) {
+        int rows;
+        slot.first[lane] = (int)find_group(P.g, g, (p * W + lane) * K + e, &rows);
+        slot.n[lane] = rows / kK;
+      }
+      if (lane == 0) {
+        slot.first[W] = tt.first[pe];  // the packed rows
+        slot.n[W] = (tail + kK - 1) / kK;
+        slot.p = p;
+        slot.e = e;
+        slot.z = in / nd * kM;
+        slot.d = in % nd * kN;
+        slot.blocks = tt.whole[pe] + (tail + kK - 1) / kK;
+        slot.last = tail % kK == 0 ? 4 : (tail % kK + 15) / 16;
+      }
+      __syncwarp();
+      if (lane == 0) bar_arrive_here(smem_addr(&b.slot_full[sl]));
+    }
+    if (!ok && lane == 0) note_error(P.g.status, A2AV_ERR_TIMEOUT);
+  } else if (warp == 0) {
     // ------------------------------------------------------ copies --
     // lanes 0 and 1 copy the CTA's 128 columns of dz, lanes 2 and 3 its up to
     // 128 columns of x, in boxes of 64 columns x 64 rows
     const uint32_t full0 = map_to(smem_addr(&b.full[0]), 0);
     unsigned it = 0;
-    for (long long t = pair; t < tiles && ok; t += pairs) {
-      const int pe = (int)(t / ((long long)nz * nd)), p = pe / K, e = pe % K;
-      const int z0 = (int)(t / nd % nz) * kM + 128 * rank, d0 = (int)(t % nd) * kN;
-      const uint32_t half = columns_of(P.D - d0) / 2;
+    for (unsigned t = pair; t < tiles && ok; t += pairs, ++i) {
+      const unsigned sl = i % kSlots;
+      ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
+      if (!ok) break;
+      const GradSlot& slot = slots[sl];
+      const int p = slot.p;
+      const uint32_t half = columns_of(P.D - slot.d) / 2;
       const int copies = 2 + (half + 63) / 64;
       const unsigned bytes = copies * 8192;
-      const int column = lane < 2 ? z0 + 64 * lane : d0 + (int)half * (int)rank + 64 * (lane - 2);
+      const int column = lane < 2 ? slot.z + 128 * (int)rank + 64 * lane
+                                  : slot.d + (int)half * (int)rank + 64 * (lane - 2);
       for (int r = 0; r <= W && ok; ++r) {  // the groups, then the packed rows
-        int rows = tt.rows[pe];
-        long long first = tt.first[pe];
-        if (r < W) first = find_group(P.g, g, (p * W + r) * K + e, &rows);
-        const int n = r < W ? rows / kK : (rows + kK - 1) / kK;
+        const int n = slot.n[r], first = slot.first[r];
         const CUtensorMap* map = r < W ? (lane < 2 ? &P.weights[p] : &P.rows[0][p])
                                        : (lane < 2 ? &P.tail_dz : &P.tail_x);
         for (int m = 0; m < n; ++m, ++it) {
@@ -723,9 +763,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
           if (lane == 0) bar_arrive_tx(full, bytes);
           __syncwarp();
           if (lane < copies)
-            tma_load(base + s * kStageBytes + lane * 8192, map, column, (int)(first + m * kK), 0, full);
+            tma_load(base + s * kStageBytes + lane * 8192, map, column, first + m * kK, 0, full);
         }
       }
+      __syncwarp();
+      if (lane == 0) bar_arrive_here(smem_addr(&b.slot_empty[sl]));
     }
     if (lane == 0 && (!ok || !settle(b, it))) {
       note_error(P.g.status, A2AV_ERR_TIMEOUT);
@@ -735,16 +777,19 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     // ---------------------------------------------------- products --
     constexpr bool kBf16 = !__is_same(T, __half);
     unsigned it = 0, n_tile = 0;
-    for (long long t = pair; t < tiles && ok; t += pairs) {
-      const int pe = (int)(t / ((long long)nz * nd));
-      const int blocks = tt.whole[pe] + (tt.rows[pe] + kK - 1) / kK;
+    for (unsigned t = pair; t < tiles && ok; t += pairs, ++i) {
+      const unsigned sl = i % kSlots;
+      ok = bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1);
+      if (!ok) break;
+      const int blocks = slots[sl].blocks, last = slots[sl].last;
+      const uint32_t idesc = product(kBf16, true, true, kM, columns_of(P.D - slots[sl].d));
+      bar_arrive_here(smem_addr(&b.slot_empty[sl]));
       if (blocks == 0) continue;
-      const int last = tt.rows[pe] % kK == 0 ? 4 : (tt.rows[pe] % kK + 15) / 16;
-      const uint32_t idesc = product(kBf16, true, true, kM, columns_of(P.D - t % nd * kN));
       const unsigned buf = n_tile & 1;
       const uint32_t d = b.tmem + buf * kN;
       ok = bar_wait(smem_addr(&b.acc_empty[buf]), ((n_tile >> 1) & 1) ^ 1);
       if (!ok) break;
+      fence_after_sync();
       ++n_tile;
       for (int kb = 0; kb < blocks; ++kb, ++it) {
         const unsigned s = it % kStages;
@@ -769,10 +814,15 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     // the address a lane gives for its row of the 8 x 8 blocks (below)
     const uint32_t put = stage + (((lane >> 3) & 1) * 8 + (lane & 7)) * kPitch + (lane >> 4) * 16;
     unsigned n_tile = 0;
-    for (long long t = pair; t < tiles && ok; t += pairs) {
-      const int pe = (int)(t / ((long long)nz * nd)), p = pe / K, e = pe % K;
-      const int z0 = (int)(t / nd % nz) * kM + 128 * rank + 32 * q, d0 = (int)(t % nd) * kN;
-      const bool any = tt.whole[pe] + tt.rows[pe] > 0;  // else the gradient is 0
+    for (unsigned t = pair; t < tiles && ok; t += pairs, ++i) {
+      const unsigned sl = i % kSlots;
+      ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
+      if (!ok) break;
+      const int p = slots[sl].p, e = slots[sl].e, d0 = slots[sl].d;
+      const int z0 = slots[sl].z + 128 * (int)rank + 32 * q;
+      const bool any = slots[sl].blocks > 0;  // else the gradient is 0
+      __syncwarp();
+      if (lane == 0) bar_arrive_here(smem_addr(&b.slot_empty[sl]));
       const unsigned buf = n_tile & 1;
       const int columns = min(kN, P.D - d0);
       if (any) {
@@ -906,6 +956,8 @@ bool a2av_expert_mma(a2av_handle* h, const A2avExperts& P, int dtype, int direct
   M.F = (int)(direction == 0 ? P.N : P.D);
   M.Z = (int)P.Z;
   M.D = (int)P.D;
+  if (direction == 2 && (long long)h->W * P.g.K * ((P.Z + kM - 1) / kM) * ((P.D + kN - 1) / kN) > kMaxCount)
+    return false;
   M.act = direction == 0 ? P.act : A2AV_ACT_NONE;
   const long long C = M.C;
   for (int p = 0; p < h->W; ++p) {
