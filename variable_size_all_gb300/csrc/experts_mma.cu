@@ -80,64 +80,111 @@ struct Slot {
   Copies copies;           // of this CTA
 };
 
-// Tiles before each expert.
+// The order of tiles.  Two kinds of experts: those of several tiles of rows,
+// whose products are what takes time (their weights come from L2 after the
+// first), and those whose rows fit one, which take as long as reading their
+// weights does.  Each kind keeps its own order, and the two are dealt out
+// evenly, so that at any time some pairs keep the tensor cores busy and others
+// the memory.  (16,384 rows, Zipf-skewed over 64 experts, 2048 -> 7168: one kind
+// after the other took the sum of both times.)
 struct TileTable {
-  int first[A2AV_MAX_DISPATCH_KEYS + 1];
+  int first[A2AV_MAX_DISPATCH_KEYS + 1];        // tiles of the first kind before each expert
+  unsigned short single[A2AV_MAX_DISPATCH_KEYS];  // the experts of the second kind
+  int singles;
 };
 
-// By the whole block, after build_groups.
-__device__ void build_tiles(const GroupParams& G, GroupTable& g, TileTable& tt, int features) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int E = G.W * G.K, per = (E + kMmaThreads - 1) / kMmaThreads;
-  const int x0 = min(tid * per, E), x1 = min(x0 + per, E);
-  long long own = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    long long at = own;  // second pass: tiles before expert x0
-    long long sum = 0;
-    for (int x = x0; x < x1; ++x) {
-      const int p = x / G.K, e = x - p * G.K;
-      long long granules = 0;
-      for (int r = 0; r < G.W; ++r) {
-        int rows;
-        find_group(G, g, (p * G.W + r) * G.K + e, &rows);
-        granules += (rows + kGranule - 1) / kGranule;
-      }
-      if (pass == 1) tt.first[x] = (int)(at + sum);
-      sum += group_tiles(granules, kTileGranules, features);
-    }
-    if (pass == 1) {
-      if (x1 == E && x0 < E) tt.first[E] = (int)(at + sum);
-      break;
-    }
-    long long inc = sum;
+// Number `t` of `tiles` dealt out of two kinds, `seconds` of the second: sets
+// *index to its number within its kind, and returns whether that is the second.
+__device__ __forceinline__ bool deal(long long t, long long tiles, long long seconds, int* index) {
+  const long long before = t * seconds / tiles;
+  const bool second = (t + 1) * seconds / tiles > before;
+  *index = (int)(second ? before : t - before);
+  return second;
+}
+
+// A pair's i-th tile: every pair takes one of each round, a place further each
+// time (the kinds would else alternate in step with the pairs).
+__device__ __forceinline__ long long tile_of(unsigned i, unsigned pair, unsigned pairs) {
+  return (long long)i * pairs + (pair + i) % pairs;
+}
+
+// Rows of tiles that are taken together, for the sake of L2: a weight tile is
+// read by this many pairs at about the same time.
+constexpr int kBand = 8;
+
+// Exclusive prefix sum of one value a thread over the block.
+__device__ __forceinline__ int block_prefix(int x, GroupTable& g) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = x;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(kAll, inc, o);
-      if (lane >= o) inc += v;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kAll, inc, o);
+    if (lane >= o) inc += v;
+  }
+  __syncthreads();
+  if (lane == 31) g.warp_tiles[warp] = inc;
+  __syncthreads();
+  int base = 0;
+  for (int w = 0; w < warp; ++w) base += (int)g.warp_tiles[w];
+  return base + inc - x;
+}
+
+// By the whole block, after build_groups; `features`: tiles of a row of them.
+__device__ void build_tiles(const GroupParams& G, GroupTable& g, TileTable& tt, int features) {
+  const int tid = threadIdx.x, E = G.W * G.K, per = (E + kMmaThreads - 1) / kMmaThreads;
+  const int x0 = min(tid * per, E), x1 = min(x0 + per, E);
+  int tiles = 0, singles = 0;
+  const auto tile_rows = [&](int x) {
+    const int p = x / G.K, e = x - p * G.K;
+    int granules = 0;
+    for (int r = 0; r < G.W; ++r) {
+      int rows;
+      find_group(G, g, (p * G.W + r) * G.K + e, &rows);
+      granules += (rows + kGranule - 1) / kGranule;
     }
-    __syncthreads();
-    if (lane == 31) g.warp_tiles[warp] = inc;
-    __syncthreads();
-    own = inc - sum;
-    for (int w = 0; w < warp; ++w) own += g.warp_tiles[w];
+    return (granules + kTileGranules - 1) / kTileGranules;
+  };
+  for (int x = x0; x < x1; ++x) {
+    const int n = tile_rows(x);
+    if (n == 1) ++singles;
+    if (n > 1) tiles += n * features;
+  }
+  int at = block_prefix(tiles, g), single = block_prefix(singles, g);
+  for (int x = x0; x < x1; ++x) {
+    const int n = tile_rows(x);
+    tt.first[x] = at;
+    if (n == 1) tt.single[single++] = (unsigned short)x;
+    if (n > 1) at += n * features;
+    if (x == E - 1) {
+      tt.first[E] = at;
+      tt.singles = single;
+    }
   }
   __syncthreads();
 }
 
 // Tile t, by a whole warp.
 __device__ __forceinline__ void describe_tile(const GroupParams& G, const GroupTable& g,
-                                              const TileTable& tt, long long t, int features,
-                                              int tile_features, Slot& slot, int lane) {
-  int lo = 0, hi = G.W * G.K;  // first[lo] <= t < first[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (tt.first[mid] <= t)
-      lo = mid;
-    else
-      hi = mid;
+                                              const TileTable& tt, long long t, long long tiles,
+                                              int features, int tile_features, Slot& slot,
+                                              int lane) {
+  int at, lo;
+  if (deal(t, tiles, (long long)tt.singles * features, &at)) {
+    lo = tt.single[at / features];
+    at %= features;
+  } else {
+    int hi = G.W * G.K;  // first[lo] <= at < first[hi]
+    lo = 0;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tt.first[mid] <= at)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    at -= tt.first[lo];
   }
   const int p = lo / G.K, e = lo - p * G.K;
-  const long long local = t - tt.first[lo];
   int rows = 0;
   long long first = 0;
   if (lane < G.W) first = find_group(G, g, (p * G.W + lane) * G.K + e, &rows);
@@ -149,7 +196,11 @@ __device__ __forceinline__ void describe_tile(const GroupParams& G, const GroupT
     if (lane >= o) inc += v;
   }
   const int total = __shfl_sync(kAll, inc, 31);
-  const int g0 = (int)(local / features) * kTileGranules, mine = g0 + lane;
+  // bands of kBand rows of tiles: down a band first, then along it
+  const int row_tiles = (total + kTileGranules - 1) / kTileGranules;
+  const int band = at / (kBand * features), in = at - band * kBand * features;
+  const int high = min(kBand, row_tiles - band * kBand), f = in / high;
+  const int g0 = (band * kBand + in - f * high) * kTileGranules, mine = g0 + lane;
   int r = 0;
   for (int i = 0; i < G.W - 1; ++i)
     if (__shfl_sync(kAll, inc, i) <= mine) r = i + 1;
@@ -161,7 +212,7 @@ __device__ __forceinline__ void describe_tile(const GroupParams& G, const GroupT
   if (lane == 0) {
     slot.p = p;
     slot.e = e;
-    slot.f = (int)(local % features) * tile_features;
+    slot.f = f * tile_features;
     slot.granules = min(total - g0, kTileGranules);
   }
 }
@@ -375,19 +426,19 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
   const bool good = build_groups(P.g, g);
   if (good) build_tiles(P.g, g, tt, nf);
   pair_begin(b, warp, rank);
-  const long long tiles = good ? tt.first[P.g.W * P.g.K] : 0;
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const long long tiles = good ? tt.first[P.g.W * P.g.K] + (long long)tt.singles * nf : 0;
+  const unsigned pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int blocks = (P.C + kK - 1) / kK;
   bool ok = true;
   unsigned i = 0;  // tiles so far
 
   if (warp == 3) {
     // --------------------------------------------------- scheduler --
-    for (long long t = pair; t < tiles; t += pairs, ++i) {
+    for (long long t; (t = tile_of(i, pair, pairs)) < tiles; ++i) {
       const unsigned sl = i % kSlots;
       ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_empty[sl]), ((i / kSlots) & 1) ^ 1));
       if (!ok) break;
-      describe_tile(P.g, g, tt, t, nf, kTileF, slots[sl], lane);
+      describe_tile(P.g, g, tt, t, tiles, nf, kTileF, slots[sl], lane);
       __syncwarp();
       if (lane == 0) plan_copies(slots[sl], rank);
       if (lane == 0) bar_arrive_here(smem_addr(&b.slot_full[sl]));
@@ -395,89 +446,85 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     if (!ok && lane == 0) note_error(P.g.status, A2AV_ERR_TIMEOUT);
   } else if (warp == 0) {
     // ------------------------------------------------------ copies --
-    // lane l issues the l-th copy of every stage: the weights' first
-    constexpr int kOwn = kMn ? 2 : 1;
     const uint32_t full0 = map_to(smem_addr(&b.full[0]), 0);
     unsigned it = 0;
-    for (long long t = pair; t < tiles && ok; t += pairs, ++i) {
+    for (; ok && tile_of(i, pair, pairs) < tiles; ++i) {
       const unsigned sl = i % kSlots;
       ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
       if (!ok) break;
-      const int p = slots[sl].p, e = slots[sl].e, f0 = slots[sl].f + kMyF * rank;
-      const Copies& copies = slots[sl].copies;
+      const Slot& slot = slots[sl];
+      const Copies& copies = slot.copies;
+      const int p = slot.p, e = slot.e, f0 = slot.f + kMyF * rank, count = copies.count;
       const unsigned bytes = kSideBytes + copies.bytes;
-      const int n = lane - kOwn;
-      const bool mine = n < copies.count;
-      const CUtensorMap* map = &P.weights[p];
-      int row = 0;
-      uint32_t to = kMn && n == -1 ? kSideBytes / 2 : 0;
-      if (n >= 0 && mine) {
-        map = &P.rows[copies.box[n]][p];
-        row = copies.row[n];
-        to = kSideBytes + copies.at[n] * 1024;
-      }
-      __syncwarp();
-      if (lane == 0) bar_arrive_here(smem_addr(&b.slot_empty[sl]));
+      const CUtensorMap* wm = &P.weights[p];
       for (int kb = 0; kb < blocks; ++kb, ++it) {
         const unsigned s = it % kStages;
         ok = __all_sync(kAll, bar_wait(smem_addr(&b.empty[s]), ((it / kStages) & 1) ^ 1));
         if (!ok) break;
-        const uint32_t full = full0 + s * 8;
-        const uint32_t at = base + s * kStageBytes + to;
-        const int c = kb * kK;
-        if (lane == 0) bar_arrive_tx(full, bytes);
-        __syncwarp();
-        if (n >= 0) {
-          if (mine) tma_load(at, map, c, row, 0, full);
-        } else if (kMn) {
-          tma_load(at, map, f0 + 64 * lane, c, e, full);
-        } else if (kGated) {
-          tma_load5(at, map, c, 0, 0, f0 / 8, e, full);
-        } else {
-          tma_load(at, map, c, f0, e, full);
+        if (elect_one()) {
+          const uint32_t full = full0 + s * 8;
+          const uint32_t at = base + s * kStageBytes;
+          const int c = kb * kK;
+          bar_arrive_tx(full, bytes);
+          if (kMn) {
+            tma_load(at, wm, f0, c, e, full);
+            tma_load(at + kSideBytes / 2, wm, f0 + 64, c, e, full);
+          } else if (kGated) {
+            tma_load5(at, wm, c, 0, 0, f0 / 8, e, full);
+          } else {
+            tma_load(at, wm, c, f0, e, full);
+          }
+          for (int n = 0; n < count; ++n)
+            tma_load(at + kSideBytes + copies.at[n] * 1024, &P.rows[copies.box[n]][p], c,
+                     copies.row[n], 0, full);
         }
+        __syncwarp();
       }
-      __syncwarp();
+      if (lane == 0) bar_arrive_here(smem_addr(&b.slot_empty[sl]));
     }
     if (lane == 0 && (!ok || !settle(b, it))) {
       note_error(P.g.status, A2AV_ERR_TIMEOUT);
       drain(b, rank, it);
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // ---------------------------------------------------- products --
+    // (the whole warp waits and one elected lane issues: under a lane's own
+    // branch an instruction of the warp, as these are, takes a hundred cycles)
     constexpr bool kBf16 = !__is_same(T, __half);
     unsigned it = 0;
-    for (long long t = pair; t < tiles && ok; t += pairs, ++i) {
+    for (; ok && tile_of(i, pair, pairs) < tiles; ++i) {
       const unsigned sl = i % kSlots, buf = i & 1;
-      if (!bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1) ||
-          !bar_wait(smem_addr(&b.acc_empty[buf]), ((i >> 1) & 1) ^ 1)) {
-        ok = false;
-        break;
-      }
+      ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1) &&
+                                bar_wait(smem_addr(&b.acc_empty[buf]), ((i >> 1) & 1) ^ 1));
+      if (!ok) break;
       const uint32_t idesc = product(kBf16, kMn, false, kM, (slots[sl].granules + 1) / 2 * 2 * kGranule);
-      bar_arrive_here(smem_addr(&b.slot_empty[sl]));
+      __syncwarp();
+      if (lane == 0) bar_arrive_here(smem_addr(&b.slot_empty[sl]));
       const uint32_t d = b.tmem + buf * kN;
       fence_after_sync();
       for (int kb = 0; kb < blocks; ++kb, ++it) {
         const unsigned s = it % kStages;
-        if (!bar_wait(smem_addr(&b.full[s]), (it / kStages) & 1)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(kAll, bar_wait(smem_addr(&b.full[s]), (it / kStages) & 1));
+        if (!ok) break;
         fence_after_sync();
         const uint32_t at = base + s * kStageBytes;
         const uint64_t wd = operand(at, kMn ? kSideBytes / 2 : 16);
         const uint64_t xd = operand(at + kSideBytes, 16);
         // (the contraction's last block may have fewer steps of 16)
         const int left = P.C - kb * kK, steps = left >= kK ? 4 : (left + 15) / 16;
-        for (int k = 0; k < steps; ++k)
-          mma(d, wd + (kMn ? k * (2048 >> 4) : k * (32 >> 4)), xd + k * (32 >> 4), idesc,
-              kb > 0 || k > 0);
-        mma_commit(smem_addr(&b.empty[s]));
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < steps)
+              mma(d, wd + (kMn ? k * (2048 >> 4) : k * (32 >> 4)), xd + k * (32 >> 4), idesc,
+                  kb > 0 || k > 0);
+          mma_commit(smem_addr(&b.empty[s]));
+          if (kb == blocks - 1) mma_commit(smem_addr(&b.acc_full[buf]));
+        }
+        __syncwarp();
       }
-      if (ok) mma_commit(smem_addr(&b.acc_full[buf]));
     }
-    if (!ok) note_error(P.g.status, A2AV_ERR_TIMEOUT);
+    if (!ok && lane == 0) note_error(P.g.status, A2AV_ERR_TIMEOUT);
   } else if (warp >= 4) {
     // ---------------------------------------------------- epilogue --
     // two warps share a quarter of the lanes, with every other 32 columns each
@@ -485,7 +532,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t stage = base + kStages * kStageBytes + (warp - 4) * kStaging;
     const uint32_t empty0 = map_to(smem_addr(&b.acc_empty[0]), 0);
     constexpr int kPieces = kGated ? 2 : 4;
-    for (long long t = pair; t < tiles && ok; t += pairs, ++i) {
+    for (; ok && tile_of(i, pair, pairs) < tiles; ++i) {
       const unsigned sl = i % kSlots, buf = i & 1;
       ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
       if (!ok) break;
@@ -585,45 +632,55 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
 // other, zeros up to the next multiple of 64.  The products then run over the
 // groups' whole blocks where they lie and over the packed ones.
 struct TailTable {
-  int first[A2AV_MAX_DISPATCH_KEYS + 1];       // packed row of each expert, multiples of 64
-  unsigned short rows[A2AV_MAX_DISPATCH_KEYS]; // its packed rows without the zeros
-  int whole[A2AV_MAX_DISPATCH_KEYS];           // its groups' whole blocks
+  int first[A2AV_MAX_DISPATCH_KEYS + 1];  // packed row of each expert, multiples of 64
 };
 
-// By the whole block (of up to 1024 threads), after build_groups.
-__device__ void build_tails(const GroupParams& G, GroupTable& g, TailTable& tt) {
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+// The experts of many blocks and, from the end, those of few: their tiles are
+// dealt out evenly as in the forward product (a tile of few blocks takes as
+// long as writing its part of the gradient does).
+struct GradOrder {
+  unsigned short expert[A2AV_MAX_DISPATCH_KEYS];
+  int few;
+};
+constexpr int kFewBlocks = 6;
+
+// Rows and remainders of an expert (by one thread): whole blocks, packed rows.
+__device__ __forceinline__ void expert_blocks(const GroupParams& G, const GroupTable& g, int x,
+                                              int* whole, int* tail) {
+  const int p = x / G.K, e = x - p * G.K;
+  *whole = *tail = 0;
+  for (int r = 0; r < G.W; ++r) {
+    int rows;
+    find_group(G, g, (p * G.W + r) * G.K + e, &rows);
+    *tail += rows % kK;
+    *whole += rows / kK;
+  }
+}
+
+// By the whole block, after build_groups.
+__device__ void build_tails(const GroupParams& G, GroupTable& g, TailTable& tt,
+                            GradOrder* order = nullptr) {
+  const int tid = threadIdx.x, nt = blockDim.x;
   const int E = G.W * G.K, per = (E + nt - 1) / nt;
   const int x0 = min(tid * per, E), x1 = min(x0 + per, E);
-  int sum = 0;
+  int sum = 0, few = 0, whole, tail;
   for (int x = x0; x < x1; ++x) {
-    const int p = x / G.K, e = x - p * G.K;
-    int tail = 0, whole = 0;
-    for (int r = 0; r < G.W; ++r) {
-      int rows;
-      find_group(G, g, (p * G.W + r) * G.K + e, &rows);
-      tail += rows % kK;
-      whole += rows / kK;
-    }
-    tt.rows[x] = (unsigned short)tail;
-    tt.whole[x] = whole;
+    expert_blocks(G, g, x, &whole, &tail);
     sum += (tail + kK - 1) / kK * kK;
+    few += whole + (tail + kK - 1) / kK <= kFewBlocks;
   }
-  int inc = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(kAll, inc, o);
-    if (lane >= o) inc += v;
-  }
-  __syncthreads();
-  if (lane == 31) g.warp_rows[warp] = inc;
-  __syncthreads();
-  int at = inc - sum;
-  for (int w = 0; w < warp; ++w) at += (int)g.warp_rows[w];
+  int at = block_prefix(sum, g), few_at = block_prefix(few, g);
   for (int x = x0; x < x1; ++x) {
+    expert_blocks(G, g, x, &whole, &tail);
     tt.first[x] = at;
-    at += (tt.rows[x] + kK - 1) / kK * kK;
-    if (x == E - 1) tt.first[E] = at;
+    at += (tail + kK - 1) / kK * kK;
+    const bool is_few = whole + (tail + kK - 1) / kK <= kFewBlocks;
+    if (order != nullptr) order->expert[is_few ? E - 1 - few_at : x - few_at] = (unsigned short)x;
+    few_at += is_few;
+    if (x == E - 1) {
+      tt.first[E] = at;
+      if (order != nullptr) order->few = few_at;
+    }
   }
   __syncthreads();
 }
@@ -690,6 +747,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
   extern __shared__ unsigned char dynamic[];
   __shared__ GroupTable g;
   __shared__ TailTable tt;
+  __shared__ GradOrder order;
   __shared__ GradSlot slots[kSlots];
   __shared__ Bars b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -697,7 +755,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t base = (smem_addr(dynamic) + 1023) & ~1023u;
   chain();
   const bool good = build_groups(P.g, g);
-  if (good) build_tails(P.g, g, tt);
+  if (good) build_tails(P.g, g, tt, &order);
   pair_begin(b, warp, rank);
   const int W = P.g.W, K = P.g.K;
   const unsigned nz = (P.Z + kM - 1) / kM, nd = (P.D + kN - 1) / kN;
@@ -708,18 +766,25 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
 
   if (warp == 3) {
     // --------------------------------------------------- scheduler --
-    for (unsigned t = pair; t < tiles; t += pairs, ++i) {
+    for (long long t; (t = tile_of(i, pair, pairs)) < tiles; ++i) {
       const unsigned sl = i % kSlots;
       ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_empty[sl]), ((i / kSlots) & 1) ^ 1));
       if (!ok) break;
       GradSlot& slot = slots[sl];
-      const unsigned pe = t / (nz * nd), in = t - pe * (nz * nd);
-      const int p = pe / K, e = pe - p * K, tail = tt.rows[pe];
+      int at;
+      const bool few = deal(t, tiles, (long long)order.few * nz * nd, &at);
+      const unsigned which = (unsigned)at / (nz * nd), in = (unsigned)at - which * (nz * nd);
+      const int pe = order.expert[few ? W * K - 1 - which : which];
+      const int p = pe / K, e = pe - p * K;
+      int tail = 0, whole = 0;
       if (lane < W) {
         int rows;
         slot.first[lane] = (int)find_group(P.g, g, (p * W + lane) * K + e, &rows);
-        slot.n[lane] = rows / kK;
+        slot.n[lane] = whole = rows / kK;
+        tail = rows % kK;
       }
+      tail = __reduce_add_sync(kAll, tail);
+      whole = __reduce_add_sync(kAll, whole);
       if (lane == 0) {
         slot.first[W] = tt.first[pe];  // the packed rows
         slot.n[W] = (tail + kK - 1) / kK;
@@ -727,7 +792,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
         slot.e = e;
         slot.z = in / nd * kM;
         slot.d = in % nd * kN;
-        slot.blocks = tt.whole[pe] + (tail + kK - 1) / kK;
+        slot.blocks = whole + (tail + kK - 1) / kK;
         slot.last = tail % kK == 0 ? 4 : (tail % kK + 15) / 16;
       }
       __syncwarp();
@@ -736,34 +801,38 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     if (!ok && lane == 0) note_error(P.g.status, A2AV_ERR_TIMEOUT);
   } else if (warp == 0) {
     // ------------------------------------------------------ copies --
-    // lanes 0 and 1 copy the CTA's 128 columns of dz, lanes 2 and 3 its up to
-    // 128 columns of x, in boxes of 64 columns x 64 rows
+    // the CTA's 128 columns of dz and its up to 128 columns of x, in boxes of 64
+    // columns x 64 rows
     const uint32_t full0 = map_to(smem_addr(&b.full[0]), 0);
     unsigned it = 0;
-    for (unsigned t = pair; t < tiles && ok; t += pairs, ++i) {
+    for (; ok && tile_of(i, pair, pairs) < tiles; ++i) {
       const unsigned sl = i % kSlots;
       ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
       if (!ok) break;
       const GradSlot& slot = slots[sl];
       const int p = slot.p;
       const uint32_t half = columns_of(P.D - slot.d) / 2;
-      const int copies = 2 + (half + 63) / 64;
-      const unsigned bytes = copies * 8192;
-      const int column = lane < 2 ? slot.z + 128 * (int)rank + 64 * lane
-                                  : slot.d + (int)half * (int)rank + 64 * (lane - 2);
+      const bool two = half > 64;
+      const unsigned bytes = two ? 4 * 8192 : 3 * 8192;
+      const int z = slot.z + 128 * (int)rank, column = slot.d + (int)half * (int)rank;
       for (int r = 0; r <= W && ok; ++r) {  // the groups, then the packed rows
         const int n = slot.n[r], first = slot.first[r];
-        const CUtensorMap* map = r < W ? (lane < 2 ? &P.weights[p] : &P.rows[0][p])
-                                       : (lane < 2 ? &P.tail_dz : &P.tail_x);
+        const CUtensorMap* dz = r < W ? &P.weights[p] : &P.tail_dz;
+        const CUtensorMap* x = r < W ? &P.rows[0][p] : &P.tail_x;
         for (int m = 0; m < n; ++m, ++it) {
           const unsigned s = it % kStages;
           ok = __all_sync(kAll, bar_wait(smem_addr(&b.empty[s]), ((it / kStages) & 1) ^ 1));
           if (!ok) break;
-          const uint32_t full = full0 + s * 8;
-          if (lane == 0) bar_arrive_tx(full, bytes);
+          if (elect_one()) {
+            const uint32_t full = full0 + s * 8, at = base + s * kStageBytes;
+            const int row = first + m * kK;
+            bar_arrive_tx(full, bytes);
+            tma_load(at, dz, z, row, 0, full);
+            tma_load(at + 8192, dz, z + 64, row, 0, full);
+            tma_load(at + kSideBytes, x, column, row, 0, full);
+            if (two) tma_load(at + kSideBytes + 8192, x, column + 64, row, 0, full);
+          }
           __syncwarp();
-          if (lane < copies)
-            tma_load(base + s * kStageBytes + lane * 8192, map, column, first + m * kK, 0, full);
         }
       }
       __syncwarp();
@@ -773,39 +842,44 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
       note_error(P.g.status, A2AV_ERR_TIMEOUT);
       drain(b, rank, it);
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // ---------------------------------------------------- products --
     constexpr bool kBf16 = !__is_same(T, __half);
     unsigned it = 0, n_tile = 0;
-    for (unsigned t = pair; t < tiles && ok; t += pairs, ++i) {
+    for (; ok && tile_of(i, pair, pairs) < tiles; ++i) {
       const unsigned sl = i % kSlots;
-      ok = bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1);
+      ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
       if (!ok) break;
       const int blocks = slots[sl].blocks, last = slots[sl].last;
       const uint32_t idesc = product(kBf16, true, true, kM, columns_of(P.D - slots[sl].d));
-      bar_arrive_here(smem_addr(&b.slot_empty[sl]));
+      __syncwarp();
+      if (lane == 0) bar_arrive_here(smem_addr(&b.slot_empty[sl]));
       if (blocks == 0) continue;
       const unsigned buf = n_tile & 1;
       const uint32_t d = b.tmem + buf * kN;
-      ok = bar_wait(smem_addr(&b.acc_empty[buf]), ((n_tile >> 1) & 1) ^ 1);
+      ok = __all_sync(kAll, bar_wait(smem_addr(&b.acc_empty[buf]), ((n_tile >> 1) & 1) ^ 1));
       if (!ok) break;
       fence_after_sync();
       ++n_tile;
       for (int kb = 0; kb < blocks; ++kb, ++it) {
         const unsigned s = it % kStages;
-        ok = bar_wait(smem_addr(&b.full[s]), (it / kStages) & 1);
+        ok = __all_sync(kAll, bar_wait(smem_addr(&b.full[s]), (it / kStages) & 1));
         if (!ok) break;
         fence_after_sync();
         const uint32_t at = base + s * kStageBytes;
         const uint64_t zd = operand(at, 8192), xd = operand(at + kSideBytes, 8192);
         const int steps = kb == blocks - 1 ? last : 4;
-        for (int k = 0; k < steps; ++k)
-          mma(d, zd + k * (2048 >> 4), xd + k * (2048 >> 4), idesc, kb > 0 || k > 0);
-        mma_commit(smem_addr(&b.empty[s]));
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < steps) mma(d, zd + k * (2048 >> 4), xd + k * (2048 >> 4), idesc, kb > 0 || k > 0);
+          mma_commit(smem_addr(&b.empty[s]));
+          if (kb == blocks - 1) mma_commit(smem_addr(&b.acc_full[buf]));
+        }
+        __syncwarp();
       }
-      if (ok) mma_commit(smem_addr(&b.acc_full[buf]));
     }
-    if (!ok) note_error(P.g.status, A2AV_ERR_TIMEOUT);
+    if (!ok && lane == 0) note_error(P.g.status, A2AV_ERR_TIMEOUT);
   } else if (warp >= 4) {
     // ---------------------------------------------------- epilogue --
     const int q = warp % 4, c0 = warp >= 8 ? 32 : 0;
@@ -814,7 +888,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     // the address a lane gives for its row of the 8 x 8 blocks (below)
     const uint32_t put = stage + (((lane >> 3) & 1) * 8 + (lane & 7)) * kPitch + (lane >> 4) * 16;
     unsigned n_tile = 0;
-    for (unsigned t = pair; t < tiles && ok; t += pairs, ++i) {
+    for (; ok && tile_of(i, pair, pairs) < tiles; ++i) {
       const unsigned sl = i % kSlots;
       ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
       if (!ok) break;
