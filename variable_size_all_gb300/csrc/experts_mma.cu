@@ -197,10 +197,13 @@ __device__ __forceinline__ void describe_tile(const GroupParams& G, const GroupT
   }
   const int total = __shfl_sync(kAll, inc, 31);
   // bands of kBand rows of tiles: down a band first, then along it
+  // (its tiles have about the same number of granules: a tile of a few rows
+  // costs half of a full one for its weights alone)
   const int row_tiles = (total + kTileGranules - 1) / kTileGranules;
+  const int each = (total + row_tiles - 1) / row_tiles;
   const int band = at / (kBand * features), in = at - band * kBand * features;
   const int high = min(kBand, row_tiles - band * kBand), f = in / high;
-  const int g0 = (band * kBand + in - f * high) * kTileGranules, mine = g0 + lane;
+  const int g0 = (band * kBand + in - f * high) * each, mine = g0 + lane;
   int r = 0;
   for (int i = 0; i < G.W - 1; ++i)
     if (__shfl_sync(kAll, inc, i) <= mine) r = i + 1;
@@ -208,17 +211,17 @@ __device__ __forceinline__ void describe_tile(const GroupParams& G, const GroupT
   const int n = __shfl_sync(kAll, rows, r) - (mine * kGranule - before);
   const long long row = __shfl_sync(kAll, first, r) + (mine * kGranule - before);
   slot.row[lane] = (int)row;
-  slot.n[lane] = mine < total ? min(n, kGranule) : 0;
+  slot.n[lane] = lane < each && mine < total ? min(n, kGranule) : 0;
   if (lane == 0) {
     slot.p = p;
     slot.e = e;
     slot.f = f * tile_features;
-    slot.granules = min(total - g0, kTileGranules);
+    slot.granules = min(total - g0, each);
   }
 }
 
 // What the two kernels share before and after their roles.
-__device__ __forceinline__ void pair_begin(Bars& b, int warp, uint32_t rank) {
+__device__ __forceinline__ void pair_begin(Bars& b, int warp, uint32_t rank, int copy_warps) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       bar_init(smem_addr(&b.full[s]), 2);
@@ -230,7 +233,7 @@ __device__ __forceinline__ void pair_begin(Bars& b, int warp, uint32_t rank) {
     }
     for (int i = 0; i < kSlots; ++i) {
       bar_init(smem_addr(&b.slot_full[i]), 1);
-      bar_init(smem_addr(&b.slot_empty[i]), kEpilogueWarps + (rank == 0 ? 2 : 1));
+      bar_init(smem_addr(&b.slot_empty[i]), kEpilogueWarps + copy_warps + (rank == 0 ? 1 : 0));
     }
     bar_init_done();
   }
@@ -425,7 +428,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
   const int nf = (P.F + kTileF - 1) / kTileF;
   const bool good = build_groups(P.g, g);
   if (good) build_tiles(P.g, g, tt, nf);
-  pair_begin(b, warp, rank);
+  pair_begin(b, warp, rank, 2);
   const long long tiles = good ? tt.first[P.g.W * P.g.K] + (long long)tt.singles * nf : 0;
   const unsigned pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int blocks = (P.C + kK - 1) / kK;
@@ -444,8 +447,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
       if (lane == 0) bar_arrive_here(smem_addr(&b.slot_full[sl]));
     }
     if (!ok && lane == 0) note_error(P.g.status, A2AV_ERR_TIMEOUT);
-  } else if (warp == 0) {
+  } else if (warp == 0 || warp == 2) {
     // ------------------------------------------------------ copies --
+    // warp 0 announces a stage's bytes and copies the weights and the first half
+    // of the rows' runs, warp 2 the others
     const uint32_t full0 = map_to(smem_addr(&b.full[0]), 0);
     unsigned it = 0;
     for (; ok && tile_of(i, pair, pairs) < tiles; ++i) {
@@ -454,7 +459,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
       if (!ok) break;
       const Slot& slot = slots[sl];
       const Copies& copies = slot.copies;
-      const int p = slot.p, e = slot.e, f0 = slot.f + kMyF * rank, count = copies.count;
+      const int p = slot.p, e = slot.e, f0 = slot.f + kMyF * rank;
+      const int from = warp == 0 ? 0 : copies.count / 2, to = warp == 0 ? copies.count / 2 : copies.count;
       const unsigned bytes = kSideBytes + copies.bytes;
       const CUtensorMap* wm = &P.weights[p];
       for (int kb = 0; kb < blocks; ++kb, ++it) {
@@ -465,16 +471,18 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
           const uint32_t full = full0 + s * 8;
           const uint32_t at = base + s * kStageBytes;
           const int c = kb * kK;
-          bar_arrive_tx(full, bytes);
-          if (kMn) {
-            tma_load(at, wm, f0, c, e, full);
-            tma_load(at + kSideBytes / 2, wm, f0 + 64, c, e, full);
-          } else if (kGated) {
-            tma_load5(at, wm, c, 0, 0, f0 / 8, e, full);
-          } else {
-            tma_load(at, wm, c, f0, e, full);
+          if (warp == 0) {
+            bar_arrive_tx(full, bytes);
+            if (kMn) {
+              tma_load(at, wm, f0, c, e, full);
+              tma_load(at + kSideBytes / 2, wm, f0 + 64, c, e, full);
+            } else if (kGated) {
+              tma_load5(at, wm, c, 0, 0, f0 / 8, e, full);
+            } else {
+              tma_load(at, wm, c, f0, e, full);
+            }
           }
-          for (int n = 0; n < count; ++n)
+          for (int n = from; n < to; ++n)
             tma_load(at + kSideBytes + copies.at[n] * 1024, &P.rows[copies.box[n]][p], c,
                      copies.row[n], 0, full);
         }
@@ -482,7 +490,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
       }
       if (lane == 0) bar_arrive_here(smem_addr(&b.slot_empty[sl]));
     }
-    if (lane == 0 && (!ok || !settle(b, it))) {
+    // (warp 2 may leave: what it copied is counted on the same stages)
+    if (warp == 2 && lane == 0 && !ok) note_error(P.g.status, A2AV_ERR_TIMEOUT);
+    if (warp == 0 && lane == 0 && (!ok || !settle(b, it))) {
       note_error(P.g.status, A2AV_ERR_TIMEOUT);
       drain(b, rank, it);
     }
@@ -559,7 +569,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
       ok = __all_sync(kAll, bar_wait(smem_addr(&b.acc_full[buf]), (i >> 1) & 1));
       if (!ok) break;
       fence_after_sync();
-      if (c0 >= columns && lane == 0) bar_arrive(empty0 + buf * 8);  // nothing to take
+      if (c0 >= columns && lane == 0) bar_arrive_relaxed(empty0 + buf * 8);  // nothing to take
       for (int c = c0; c < columns; c += 64) {
         const int j = c / kGranule;
         const uint32_t at = b.tmem + buf * kN + c + ((uint32_t)(32 * q) << 16);
@@ -570,7 +580,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
         if (c + 64 >= columns) {  // the warp's last of the tile's sums: its share of the buffer is free
           fence_before_sync();
           __syncwarp();
-          if (lane == 0) bar_arrive(empty0 + buf * 8);
+          if (lane == 0) bar_arrive_relaxed(empty0 + buf * 8);
         }
         if (kGated) {  // lanes 0..7 and 8..15 of each are partners: va the first halves, vb the second
 #pragma unroll
@@ -756,7 +766,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
   chain();
   const bool good = build_groups(P.g, g);
   if (good) build_tails(P.g, g, tt, &order);
-  pair_begin(b, warp, rank);
+  pair_begin(b, warp, rank, 1);
   const int W = P.g.W, K = P.g.K;
   const unsigned nz = (P.Z + kM - 1) / kM, nd = (P.D + kN - 1) / kN;
   const unsigned tiles = good ? (unsigned)(W * K) * nz * nd : 0;
@@ -904,7 +914,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
         if (!ok) break;
         fence_after_sync();
         ++n_tile;
-        if (c0 >= columns && lane == 0) bar_arrive(empty0 + buf * 8);
+        if (c0 >= columns && lane == 0) bar_arrive_relaxed(empty0 + buf * 8);
       }
       T* out = static_cast<T*>(P.out[p]) + ((long long)e * P.Z + z0) * P.D;
       for (int c = c0; c < columns; c += 64) {
@@ -917,7 +927,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
           if (c + 64 >= columns) {
             fence_before_sync();
             __syncwarp();
-            if (lane == 0) bar_arrive(empty0 + buf * 8);
+            if (lane == 0) bar_arrive_relaxed(empty0 + buf * 8);
           }
         }
 #pragma unroll
