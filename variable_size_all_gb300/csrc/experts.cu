@@ -136,48 +136,52 @@ __global__ void __launch_bounds__(kPlainThreads)
 }
 
 // ---------------------------------------------- activation's gradient --
-// dz from dy and the saved pre-activations, an element (or N of them) a thread.
+// dz from dy and the saved pre-activations: a warp takes a row, a vector of N
+// elements a lane at a time.  Memory bound (5 N reads and writes of 2 bytes a
+// row with a gate).
 template <typename T, int N>
 __global__ void __launch_bounds__(256)
     expert_dz_kernel(const __grid_constant__ ExpertParams P) {
   chain();
   __shared__ GroupTable g;
   if (!build_groups(P.g, g)) return;
-  using V = Vec<T, N>;
-  const long long nv = P.N / N;
-  for (int p = 0; p < P.g.W; ++p) {
-    const long long total = (g.peer_base[p + 1] - g.peer_base[p]) * nv;
-    const T* dy = static_cast<const T*>(P.dy[p]);
-    const T* pre = static_cast<const T*>(P.pre_in[p]);
-    T* dz = static_cast<T*>(P.dz[p]);
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total;
-         i += (long long)gridDim.x * blockDim.x) {
-      const long long row = i / nv, c = (i - row * nv) * N;
-      const V y = *reinterpret_cast<const V*>(dy + row * P.N + c);
-      const V z = *reinterpret_cast<const V*>(pre + row * P.Z + c);
-      V a, b;
+  using Q = Piece<T, N>;
+  using V = typename Q::Raw;
+  const int nv = (int)(P.N / N), lane = threadIdx.x & 31;
+  const int warps = gridDim.x * (blockDim.x / 32), all = g.peer_base[P.g.W];
+  int p = 0;
+  for (int at = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; at < all; at += warps) {
+    while (at >= g.peer_base[p + 1]) ++p;
+    const long long row = at - g.peer_base[p];
+    const V* dy = reinterpret_cast<const V*>(static_cast<const T*>(P.dy[p]) + row * P.N);
+    const V* pre = reinterpret_cast<const V*>(static_cast<const T*>(P.pre_in[p]) + row * P.Z);
+    V* dz = reinterpret_cast<V*>(static_cast<T*>(P.dz[p]) + row * P.Z);
+#pragma unroll 2
+    for (int v = lane; v < nv; v += 32) {
+      float d[N], z[N], u[N];
+      Q::unpack(dy[v], d);
+      Q::unpack(pre[v], z);
       if (P.gated) {
-        const V u = *reinterpret_cast<const V*>(pre + row * P.Z + P.N + c);
+        Q::unpack(pre[nv + v], u);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-          const float d = to_float(y.v[k]), zf = to_float(z.v[k]);
-          a.v[k] = from_float<T>(d * to_float(u.v[k]) * act_slope(P.act, zf));
-          b.v[k] = from_float<T>(d * act_fn(P.act, zf));
+          u[k] *= d[k] * act_slope(P.act, z[k]);
+          d[k] *= act_fn(P.act, z[k]);
         }
-        *reinterpret_cast<V*>(dz + row * P.Z + P.N + c) = b;
+        dz[v] = Q::pack(u);
+        dz[nv + v] = Q::pack(d);
       } else {
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-          a.v[k] = from_float<T>(to_float(y.v[k]) * act_slope(P.act, to_float(z.v[k])));
+        for (int k = 0; k < N; ++k) d[k] *= act_slope(P.act, z[k]);
+        dz[v] = Q::pack(d);
       }
-      *reinterpret_cast<V*>(dz + row * P.Z + c) = a;
     }
   }
 }
 
 // d_bias[e][z]: a block takes 16 vectors of N columns of an expert, each of its
-// 32 half warps every 32nd row; their sums are joined in shared memory in a
-// fixed order.  It reads dz once, so the memory's rate is its floor.
+// 32 half warps every 32nd row of a group; their sums are joined in shared
+// memory in a fixed order.  It reads dz once, so the memory's rate is its floor.
 constexpr int kBiasThreads = 512, kBiasRows = kBiasThreads / 16;
 
 template <typename T, int N>
@@ -187,7 +191,8 @@ __global__ void __launch_bounds__(kBiasThreads)
   __shared__ GroupTable g;
   __shared__ float part[kBiasRows][16 * N + 1];
   if (!build_groups(P.g, g)) return;
-  using V = Vec<T, N>;
+  using Q = Piece<T, N>;
+  using V = typename Q::Raw;
   const int at = threadIdx.x % 16, team = threadIdx.x / 16;
   const int W = P.g.W, K = P.g.K;
   const long long nz = (P.Z + 16 * N - 1) / (16 * N);
@@ -210,8 +215,10 @@ __global__ void __launch_bounds__(kBiasThreads)
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
           if (m + u * kBiasRows < rows) {
+            float f[N];
+            Q::unpack(v[u], f);
 #pragma unroll
-            for (int k = 0; k < N; ++k) sum[k] += to_float(v[u].v[k]);
+            for (int k = 0; k < N; ++k) sum[k] += f[k];
           }
       }
     }

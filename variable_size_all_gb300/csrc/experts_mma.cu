@@ -424,11 +424,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t base = (smem_addr(dynamic) + 1023) & ~1023u;
   constexpr int kTileF = kGated ? 128 : 256;  // features of the result per pair
   constexpr int kMyF = kTileF / 2;            // and per CTA
+  pair_begin(b, warp, rank, 2);
   chain();
   const int nf = (P.F + kTileF - 1) / kTileF;
   const bool good = build_groups(P.g, g);
   if (good) build_tiles(P.g, g, tt, nf);
-  pair_begin(b, warp, rank, 2);
   const long long tiles = good ? tt.first[P.g.W * P.g.K] + (long long)tt.singles * nf : 0;
   const unsigned pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int blocks = (P.C + kK - 1) / kK;
@@ -640,19 +640,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
 // what each group has over a multiple of 64 is copied together first
 // (expert_tails_kernel): the remainders of an expert's W groups one after the
 // other, zeros up to the next multiple of 64.  The products then run over the
-// groups' whole blocks where they lie and over the packed ones.
+// groups' whole blocks where they lie and over the packed ones.  (The tiles go
+// expert by expert: dealing large and small experts out evenly, as the forward
+// product does, took 5 to 9 % longer here.)
 struct TailTable {
   int first[A2AV_MAX_DISPATCH_KEYS + 1];  // packed row of each expert, multiples of 64
 };
-
-// The experts of many blocks and, from the end, those of few: their tiles are
-// dealt out evenly as in the forward product (a tile of few blocks takes as
-// long as writing its part of the gradient does).
-struct GradOrder {
-  unsigned short expert[A2AV_MAX_DISPATCH_KEYS];
-  int few;
-};
-constexpr int kFewBlocks = 6;
 
 // Rows and remainders of an expert (by one thread): whole blocks, packed rows.
 __device__ __forceinline__ void expert_blocks(const GroupParams& G, const GroupTable& g, int x,
@@ -668,29 +661,21 @@ __device__ __forceinline__ void expert_blocks(const GroupParams& G, const GroupT
 }
 
 // By the whole block, after build_groups.
-__device__ void build_tails(const GroupParams& G, GroupTable& g, TailTable& tt,
-                            GradOrder* order = nullptr) {
+__device__ void build_tails(const GroupParams& G, GroupTable& g, TailTable& tt) {
   const int tid = threadIdx.x, nt = blockDim.x;
   const int E = G.W * G.K, per = (E + nt - 1) / nt;
   const int x0 = min(tid * per, E), x1 = min(x0 + per, E);
-  int sum = 0, few = 0, whole, tail;
+  int sum = 0, whole, tail;
   for (int x = x0; x < x1; ++x) {
     expert_blocks(G, g, x, &whole, &tail);
     sum += (tail + kK - 1) / kK * kK;
-    few += whole + (tail + kK - 1) / kK <= kFewBlocks;
   }
-  int at = block_prefix(sum, g), few_at = block_prefix(few, g);
+  int at = block_prefix(sum, g);
   for (int x = x0; x < x1; ++x) {
     expert_blocks(G, g, x, &whole, &tail);
     tt.first[x] = at;
     at += (tail + kK - 1) / kK * kK;
-    const bool is_few = whole + (tail + kK - 1) / kK <= kFewBlocks;
-    if (order != nullptr) order->expert[is_few ? E - 1 - few_at : x - few_at] = (unsigned short)x;
-    few_at += is_few;
-    if (x == E - 1) {
-      tt.first[E] = at;
-      if (order != nullptr) order->few = few_at;
-    }
+    if (x == E - 1) tt.first[E] = at;
   }
   __syncthreads();
 }
@@ -757,16 +742,15 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
   extern __shared__ unsigned char dynamic[];
   __shared__ GroupTable g;
   __shared__ TailTable tt;
-  __shared__ GradOrder order;
   __shared__ GradSlot slots[kSlots];
   __shared__ Bars b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const uint32_t base = (smem_addr(dynamic) + 1023) & ~1023u;
+  pair_begin(b, warp, rank, 1);
   chain();
   const bool good = build_groups(P.g, g);
-  if (good) build_tails(P.g, g, tt, &order);
-  pair_begin(b, warp, rank, 1);
+  if (good) build_tails(P.g, g, tt);
   const int W = P.g.W, K = P.g.K;
   const unsigned nz = (P.Z + kM - 1) / kM, nd = (P.D + kN - 1) / kN;
   const unsigned tiles = good ? (unsigned)(W * K) * nz * nd : 0;
@@ -776,15 +760,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
 
   if (warp == 3) {
     // --------------------------------------------------- scheduler --
-    for (long long t; (t = tile_of(i, pair, pairs)) < tiles; ++i) {
+    for (unsigned t = pair; t < tiles; t += pairs, ++i) {
       const unsigned sl = i % kSlots;
       ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_empty[sl]), ((i / kSlots) & 1) ^ 1));
       if (!ok) break;
       GradSlot& slot = slots[sl];
-      int at;
-      const bool few = deal(t, tiles, (long long)order.few * nz * nd, &at);
-      const unsigned which = (unsigned)at / (nz * nd), in = (unsigned)at - which * (nz * nd);
-      const int pe = order.expert[few ? W * K - 1 - which : which];
+      const unsigned pe = t / (nz * nd), in = t - pe * (nz * nd);
       const int p = pe / K, e = pe - p * K;
       int tail = 0, whole = 0;
       if (lane < W) {
@@ -815,7 +796,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     // columns x 64 rows
     const uint32_t full0 = map_to(smem_addr(&b.full[0]), 0);
     unsigned it = 0;
-    for (; ok && tile_of(i, pair, pairs) < tiles; ++i) {
+    for (unsigned t = pair; ok && t < tiles; t += pairs, ++i) {
       const unsigned sl = i % kSlots;
       ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
       if (!ok) break;
@@ -856,7 +837,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     // ---------------------------------------------------- products --
     constexpr bool kBf16 = !__is_same(T, __half);
     unsigned it = 0, n_tile = 0;
-    for (; ok && tile_of(i, pair, pairs) < tiles; ++i) {
+    for (unsigned t = pair; ok && t < tiles; t += pairs, ++i) {
       const unsigned sl = i % kSlots;
       ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
       if (!ok) break;
@@ -898,7 +879,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     // the address a lane gives for its row of the 8 x 8 blocks (below)
     const uint32_t put = stage + (((lane >> 3) & 1) * 8 + (lane & 7)) * kPitch + (lane >> 4) * 16;
     unsigned n_tile = 0;
-    for (; ok && tile_of(i, pair, pairs) < tiles; ++i) {
+    for (unsigned t = pair; ok && t < tiles; t += pairs, ++i) {
       const unsigned sl = i % kSlots;
       ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
       if (!ok) break;

@@ -54,6 +54,45 @@ struct alignas(sizeof(T) * N) Vec {
   T v[N];
 };
 
+// N elements as 32-bit words (or one element): unpacked and packed in pairs.
+template <typename T, int N>
+struct Piece {
+  static constexpr int kWords = N * sizeof(T) / 4;
+  struct alignas(4 * kWords) Raw {
+    uint32_t w[kWords];
+  };
+  static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        f[i] = __uint_as_float(r.w[i]);
+      } else {
+        const float2 v = unpack2(r.w[i], T());
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+      }
+    }
+  }
+  static __device__ __forceinline__ Raw pack(const float (&f)[N]) {
+    Raw r;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 4)
+        r.w[i] = __float_as_uint(f[i]);
+      else
+        r.w[i] = pack2(f[2 * i], f[2 * i + 1], T());
+    }
+    return r;
+  }
+};
+
+template <typename T>
+struct Piece<T, 1> {
+  using Raw = T;
+  static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[1]) { f[0] = to_float(r); }
+  static __device__ __forceinline__ Raw pack(const float (&f)[1]) { return from_float<T>(f[0]); }
+};
+
 // Programmatic dependent launch, as in the exchange's kernels: let the next
 // kernel of the stream be scheduled, then wait until the previous one is done
 // and its writes are visible.  Both are no-ops in a plain launch.
