@@ -498,9 +498,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     }
   } else if (warp == 1 && rank == 0) {
     // ---------------------------------------------------- products --
-    // (the whole warp waits and one elected lane issues: under a lane's own
-    // branch an instruction of the warp, as these are, takes a hundred cycles)
+    // (the whole warp goes through the loop, and a predicate has one lane issue:
+    // under a branch of its own an instruction of the warp, as these are, takes
+    // up to a hundred cycles)
     constexpr bool kBf16 = !__is_same(T, __half);
+    const bool issuer = elect_one();
+    const uint32_t tmem = __shfl_sync(kAll, b.tmem, 0);
     unsigned it = 0;
     for (; ok && tile_of(i, pair, pairs) < tiles; ++i) {
       const unsigned sl = i % kSlots, buf = i & 1;
@@ -510,29 +513,32 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
       const uint32_t idesc = product(kBf16, kMn, false, kM, (slots[sl].granules + 1) / 2 * 2 * kGranule);
       __syncwarp();
       if (lane == 0) bar_arrive_here(smem_addr(&b.slot_empty[sl]));
-      const uint32_t d = b.tmem + buf * kN;
+      const uint32_t d = tmem + buf * kN;
       fence_after_sync();
+      bool ready = false;
       for (int kb = 0; kb < blocks; ++kb, ++it) {
         const unsigned s = it % kStages;
-        ok = __all_sync(kAll, bar_wait(smem_addr(&b.full[s]), (it / kStages) & 1));
-        if (!ok) break;
+        if (!__all_sync(kAll, ready)) {
+          ok = __all_sync(kAll, bar_wait(smem_addr(&b.full[s]), (it / kStages) & 1));
+          if (!ok) break;
+        }
         fence_after_sync();
+        // (the next stage is looked at while this one's products are issued)
+        const unsigned next = (it + 1) % kStages;
+        ready = bar_test(smem_addr(&b.full[next]), ((it + 1) / kStages) & 1);
         const uint32_t at = base + s * kStageBytes;
         const uint64_t wd = operand(at, kMn ? kSideBytes / 2 : 16);
         const uint64_t xd = operand(at + kSideBytes, 16);
         // (the contraction's last block may have fewer steps of 16)
         const int left = P.C - kb * kK, steps = left >= kK ? 4 : (left + 15) / 16;
-        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < steps)
-              mma(d, wd + (kMn ? k * (2048 >> 4) : k * (32 >> 4)), xd + k * (32 >> 4), idesc,
-                  kb > 0 || k > 0);
-          mma_commit(smem_addr(&b.empty[s]));
-          if (kb == blocks - 1) mma_commit(smem_addr(&b.acc_full[buf]));
-        }
-        __syncwarp();
+        for (int k = 0; k < 4; ++k)
+          if (k < steps)
+            mma(d, wd + (kMn ? k * (2048 >> 4) : k * (32 >> 4)), xd + k * (32 >> 4), idesc,
+                kb > 0 || k > 0, issuer);
+        mma_commit(smem_addr(&b.empty[s]), issuer);
       }
+      if (ok) mma_commit(smem_addr(&b.acc_full[buf]), issuer);
     }
     if (!ok && lane == 0) note_error(P.g.status, A2AV_ERR_TIMEOUT);
   } else if (warp >= 4) {
@@ -836,6 +842,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (warp == 1 && rank == 0) {
     // ---------------------------------------------------- products --
     constexpr bool kBf16 = !__is_same(T, __half);
+    const bool issuer = elect_one();
+    const uint32_t tmem = __shfl_sync(kAll, b.tmem, 0);
     unsigned it = 0, n_tile = 0;
     for (unsigned t = pair; ok && t < tiles; t += pairs, ++i) {
       const unsigned sl = i % kSlots;
@@ -847,28 +855,32 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
       if (lane == 0) bar_arrive_here(smem_addr(&b.slot_empty[sl]));
       if (blocks == 0) continue;
       const unsigned buf = n_tile & 1;
-      const uint32_t d = b.tmem + buf * kN;
+      const uint32_t d = tmem + buf * kN;
       ok = __all_sync(kAll, bar_wait(smem_addr(&b.acc_empty[buf]), ((n_tile >> 1) & 1) ^ 1));
       if (!ok) break;
       fence_after_sync();
       ++n_tile;
+      bool ready = false;
       for (int kb = 0; kb < blocks; ++kb, ++it) {
         const unsigned s = it % kStages;
-        ok = __all_sync(kAll, bar_wait(smem_addr(&b.full[s]), (it / kStages) & 1));
-        if (!ok) break;
+        if (!__all_sync(kAll, ready)) {
+          ok = __all_sync(kAll, bar_wait(smem_addr(&b.full[s]), (it / kStages) & 1));
+          if (!ok) break;
+        }
         fence_after_sync();
+        // (the next stage is looked at while this one's products are issued)
+        const unsigned next = (it + 1) % kStages;
+        ready = bar_test(smem_addr(&b.full[next]), ((it + 1) / kStages) & 1);
         const uint32_t at = base + s * kStageBytes;
         const uint64_t zd = operand(at, 8192), xd = operand(at + kSideBytes, 8192);
         const int steps = kb == blocks - 1 ? last : 4;
-        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < steps) mma(d, zd + k * (2048 >> 4), xd + k * (2048 >> 4), idesc, kb > 0 || k > 0);
-          mma_commit(smem_addr(&b.empty[s]));
-          if (kb == blocks - 1) mma_commit(smem_addr(&b.acc_full[buf]));
-        }
-        __syncwarp();
+        for (int k = 0; k < 4; ++k)
+          if (k < steps)
+            mma(d, zd + k * (2048 >> 4), xd + k * (2048 >> 4), idesc, kb > 0 || k > 0, issuer);
+        mma_commit(smem_addr(&b.empty[s]), issuer);
       }
+      if (ok) mma_commit(smem_addr(&b.acc_full[buf]), issuer);
     }
     if (!ok && lane == 0) note_error(P.g.status, A2AV_ERR_TIMEOUT);
   } else if (warp >= 4) {
