@@ -108,17 +108,18 @@ def load():
     lib.a2av_error_string.restype = ctypes.c_char_p
     lib.a2av_version.argtypes = []
     route_p, expert_p = ctypes.POINTER(A2avRoute), ctypes.POINTER(A2avExpert)
-    lib.a2av_route.argtypes = [vp, route_p, pp, i64p, vp, pp, pp, vp, vp]
-    lib.a2av_route_backward.argtypes = [vp, route_p, pp, i64p, pp, pp, pp, vp]
-    lib.a2av_expert_matmul.argtypes = [vp, expert_p, pp, i64p, vp, pp, pp, pp, pp, pp, vp]
-    lib.a2av_expert_matmul_backward.argtypes = [vp, expert_p, pp, i64p, vp, pp, pp, pp, pp, pp, pp,
+    # (the pointer arrays of these calls go as addresses)
+    lib.a2av_route.argtypes = [vp, route_p, vp, i64p, vp, vp, vp, vp, vp]
+    lib.a2av_route_backward.argtypes = [vp, route_p, vp, i64p, vp, vp, vp, vp]
+    lib.a2av_expert_matmul.argtypes = [vp, expert_p, vp, i64p, vp, vp, vp, vp, vp, vp, vp]
+    lib.a2av_expert_matmul_backward.argtypes = [vp, expert_p, vp, i64p, vp, vp, vp, vp, vp, vp, vp,
                                                 vp, i64, vp]
     lib.a2av_expert_matmul_workspace_bytes.argtypes = [ci, expert_p, i64]
     lib.a2av_expert_matmul_workspace_bytes.restype = i64
-    lib.a2av_combine_weighted.argtypes = [vp, ci, ci, i64, ci, pp, i64p, vp, pp, pp, pp, i64p, pp, pp,
+    lib.a2av_combine_weighted.argtypes = [vp, ci, ci, i64, ci, vp, i64p, vp, vp, vp, vp, i64p, vp, vp,
                                           vp]
-    lib.a2av_combine_weighted_backward.argtypes = [vp, ci, ci, i64, ci, pp, i64p, vp, pp, pp, pp,
-                                                   i64p, pp, pp, pp, vp]
+    lib.a2av_combine_weighted_backward.argtypes = [vp, ci, ci, i64, ci, vp, i64p, vp, vp, vp, vp,
+                                                   i64p, vp, vp, vp, vp]
     for f in ("a2av_create", "a2av_run", "a2av_combine", "a2av_status", "a2av_destroy", "a2av_set_path",
               "a2av_set_grid", "a2av_last_launch", "a2av_version", "a2av_run_noalloc",
               "a2av_run_multi", "a2av_route", "a2av_route_backward", "a2av_expert_matmul",
@@ -353,18 +354,23 @@ def a2av_combine_weighted_backward(handle, keys_per_peer: int, topk: int, hidden
 
 # --------------------------------------------------------- torch-facing --
 class _PlainMarshal:
-    """``_marshal`` (csrc/marshal.c) without the compiled module."""
+    """``_marshal`` (csrc/marshal.cpp) without the compiled module."""
 
     @staticmethod
-    def pointers(tensors, dtype, shapes, address):
-        try:
-            if not all(t.is_cuda and t.dtype == dtype and t.is_contiguous() for t in tensors) or (
-                    shapes is not None and [t.shape for t in tensors] != shapes):
+    def pointers(address, count, *lists):
+        for tensors, dtype, shapes in lists:
+            if tensors is None:
+                continue
+            try:
+                if len(tensors) != count or not all(
+                        t.is_cuda and t.dtype == dtype and t.is_contiguous() for t in tensors) or (
+                        shapes is not None and [t.shape for t in tensors] != shapes):
+                    return False
+            except AttributeError:  # None among them
                 return False
-        except AttributeError:  # None among them
-            return False
-        for r, t in enumerate(tensors):
-            ctypes.c_void_p.from_address(address + 8 * r).value = t.data_ptr()
+            for r, t in enumerate(tensors):
+                ctypes.c_void_p.from_address(address + 8 * r).value = t.data_ptr()
+            address += 8 * count
         return True
 
     @staticmethod
@@ -439,7 +445,8 @@ class A2av:
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._codes = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
         self._int32, self._int64, self._float = torch.int32, torch.int64, torch.float32
-        self._pointers, self._counts = ctypes.c_void_p * self.world_size, ctypes.c_int64 * self.world_size
+        self._counts = ctypes.c_int64 * self.world_size
+        self._room = [ctypes.c_void_p * max(1, self.world_size * n) for n in range(9)]
         if path != PATH_AUTO:
             self._check(a2av_set_path(h, path), "a2av_set_path")
         if ctas_per_sm:
@@ -698,16 +705,33 @@ class A2av:
                 return t.dtype, code
         raise ValueError(f"{name}: every tensor is missing")
 
-    def _list(self, tensors, name, dtype, shapes=None):
-        """Pointer array of W contiguous CUDA tensors of a type.  ``shapes``:
-        the expected shape of each (a tensor without elements may be None)."""
+    def _lists(self, *lists):
+        """The pointer arrays of lists of W contiguous CUDA tensors, each
+        (tensors, dtype, shapes, name): the expected shapes, or None for any.
+        A list may be None, and so may a tensor without elements.  Returns the
+        addresses (None for None) and what has to live as long as they do."""
+        W = self.world_size
+        arr = self._room[len(lists)]()
+        base = ctypes.addressof(arr)
+        if self._marshal.pointers(base, W, *[x[:3] for x in lists]):
+            at = base
+            out = []
+            for x in lists:
+                if x[0] is None:
+                    out.append(None)
+                else:
+                    out.append(at)
+                    at += 8 * W
+            return out, arr
+        arrays = [None if x[0] is None else self._list(*x) for x in lists]
+        return [None if a is None else ctypes.addressof(a) for a in arrays], arrays
+
+    def _list(self, tensors, dtype, shapes, name):
+        """One of these arrays, tensor by tensor: says what is wrong with it."""
         W = self.world_size
         if len(tensors) != W:
             raise ValueError(f"{name}: expected {W} tensors, got {len(tensors)}")
-        arr = self._pointers()
-        if self._marshal.pointers(tensors, dtype, shapes, ctypes.addressof(arr)):
-            return arr
-        arr = self._pointers()
+        arr = (ctypes.c_void_p * W)()
         for r, t in enumerate(tensors):
             if t is None:
                 if shapes is not None and 0 not in shapes[r]:
@@ -745,19 +769,22 @@ class A2av:
         return [s[0] for s in shapes], widths.pop()
 
     def _route_args(self, logits, keys, weights, weights_name, topk, score, groups, top_groups,
-                    group_top, renormalise, scale):
+                    group_top, renormalise, scale, d_logits=None):
         if score not in _SCORES:
             raise ValueError(f"score must be one of {sorted(_SCORES)}")
         rows, E = self._tokens(logits, "logits")
         dtype, code = self._dtype(logits, "logits", (F32, BF16, F16))
-        route = A2avRoute(E, int(topk), code, _SCORES[score], int(groups), int(top_groups),
-                          int(group_top), int(bool(renormalise)), float(scale))
-        if not 1 <= route.topk <= E:
+        topk = int(topk)
+        if not 1 <= topk <= E:
             raise ValueError(f"topk must be in 1..{E}")
-        shapes = [(n, route.topk) for n in rows]
-        return (dtype, ctypes.byref(route), self._list(logits, "logits", dtype),
-                self._counts(*rows), self._list(keys, "keys", self._int32, shapes),
-                self._list(weights, weights_name, self._float, shapes), rows, E)
+        route = A2avRoute(E, topk, code, _SCORES[score], int(groups), int(top_groups),
+                          int(group_top), 1 if renormalise else 0, scale)
+        shapes = [(n, topk) for n in rows]
+        arrays, keep = self._lists(
+            (logits, dtype, None, "logits"), (keys, self._int32, shapes, "keys"),
+            (weights, self._float, shapes, weights_name),
+            (d_logits, dtype, [(n, E) for n in rows] if d_logits is not None else None, "d_logits"))
+        return route, arrays, self._counts(*rows), E, keep
 
     def route(self, logits, keys, weights, topk: int, counts=None, bias=None,
               score: str = "softmax", groups: int = 1, top_groups: int = 1, group_top: int = 1,
@@ -769,19 +796,17 @@ class A2av:
         dispatch; ``weights[r]`` float32 [T, topk]; ``counts`` (optional)
         int64 [W, E], rank r's items for each expert.  ``bias``: optional
         float32 [E], added to the scores for the choice alone."""
-        dtype, cfg, x, n, k, w, rows, E = self._route_args(
+        cfg, (x, k, w, _), n, E, arrays = self._route_args(
             logits, keys, weights, "weights", topk, score, groups, top_groups, group_top,
             renormalise, scale)
-        W = self.world_size
         if bias is not None and (bias.dtype != self._float or not bias.is_cuda
                                  or bias.shape != (E,) or not bias.is_contiguous()):
             raise ValueError(f"bias must be a contiguous CUDA float32 [{E}] tensor")
         if counts is not None:
-            self._matrix(counts, (W, E), "counts")
-        args = [self.handle, cfg, x, n, _address(None if bias is None else bias.data_ptr()), k, w,
-                _address(None if counts is None else counts.data_ptr()),
-                self._queue(stream)]
-        return self._call("a2av_route", args, (logits, keys, weights, counts, bias), _bind)
+            self._matrix(counts, (self.world_size, E), "counts")
+        args = [self.handle, ctypes.byref(cfg), x, n, None if bias is None else bias.data_ptr(), k, w,
+                None if counts is None else counts.data_ptr(), self._queue(stream)]
+        return self._call("a2av_route", args, (logits, keys, weights, counts, bias, arrays), _bind)
 
     def bind_route(self, logits, keys, weights, topk: int, **options) -> BoundCall:
         """``route`` marshalled once (see BoundCall)."""
@@ -792,11 +817,12 @@ class A2av:
         """The gradient of ``route``'s weights: ``d_logits[r]`` [T, E], of the
         logits' type, from ``d_weights[r]`` float32 [T, topk] and the keys that
         ``route`` wrote (see include/a2av_moe.h, a2av_route_backward)."""
-        dtype, cfg, x, n, k, w, rows, E = self._route_args(
-            logits, keys, d_weights, "d_weights", topk, score, 1, 1, 1, renormalise, scale)
-        d = self._list(d_logits, "d_logits", dtype, [(m, E) for m in rows])
+        if d_logits is None:
+            raise ValueError("d_logits is missing")
+        cfg, (x, k, w, d), n, E, arrays = self._route_args(
+            logits, keys, d_weights, "d_weights", topk, score, 1, 1, 1, renormalise, scale, d_logits)
         self._call("a2av_route_backward",
-                   [self.handle, cfg, x, n, k, w, d, self._queue(stream)], None, False)
+                   [self.handle, ctypes.byref(cfg), x, n, k, w, d, self._queue(stream)], None, False)
 
     def _expert_args(self, rows, counts, weights, out, out_name, activation, gated):
         """The shape, the common arguments and what the others are checked by."""
@@ -813,9 +839,7 @@ class A2av:
         dtype, code = self._dtype(weights, "weights", (F16, BF16))
         self._matrix(counts, (W, W * K), "counts")
         shape = A2avExpert(K, D, N, code, _ACTIVATIONS[activation], int(bool(gated)))
-        return (shape, self._list(rows, "rows", dtype), self._counts(*n),
-                ctypes.c_void_p(counts.data_ptr()),
-                self._list(weights, "weights", dtype, [(K, Z, D)] * W), n, K, Z, dtype)
+        return shape, n, K, Z, dtype
 
     def expert_matmul(self, rows, counts, weights, outputs, activation: str = "none",
                       gated: bool = False, bias=None, residual=None, pre=None, stream=None,
@@ -827,17 +851,17 @@ class A2av:
         ``weights[p]`` [K, Z, D] with Z = N, or 2 N when ``gated``; written:
         ``outputs[p]`` [rows, N] and, when given, ``pre[p]`` [rows, Z].
         ``bias[p]`` [K, Z] and ``residual[p]`` [rows, N] are optional."""
-        shape, x, n, c, w, n_rows, K, Z, dtype = self._expert_args(
-            rows, counts, weights, outputs, "outputs", activation, gated)
-        N, W = shape.out_features, self.world_size
-        by_row = [(m, N) for m in n_rows]
-        args = [self.handle, ctypes.byref(shape), x, n, c, w,
-                None if bias is None else self._list(bias, "bias", dtype, [(K, Z)] * W),
-                None if residual is None else self._list(residual, "residual", dtype, by_row),
-                self._list(outputs, "outputs", dtype, by_row),
-                None if pre is None else self._list(pre, "pre", dtype, [(m, Z) for m in n_rows]),
-                self._queue(stream)]
-        keep = (rows, counts, weights, outputs, bias, residual, pre)
+        shape, n, K, Z, dtype = self._expert_args(rows, counts, weights, outputs, "outputs",
+                                                  activation, gated)
+        D, N, W = shape.in_features, shape.out_features, self.world_size
+        by_row = [(m, N) for m in n]
+        (x, w, b, r, y, z), arrays = self._lists(
+            (rows, dtype, None, "rows"), (weights, dtype, [(K, Z, D)] * W, "weights"),
+            (bias, dtype, [(K, Z)] * W, "bias"), (residual, dtype, by_row, "residual"),
+            (outputs, dtype, by_row, "outputs"), (pre, dtype, [(m, Z) for m in n], "pre"))
+        args = [self.handle, ctypes.byref(shape), x, self._counts(*n), counts.data_ptr(), w, b, r, y,
+                z, self._queue(stream)]
+        keep = (rows, counts, weights, outputs, bias, residual, pre, arrays)
         return self._call("a2av_expert_matmul", args, keep, _bind)
 
     def bind_expert_matmul(self, rows, counts, weights, outputs, **options) -> BoundCall:
@@ -854,10 +878,10 @@ class A2av:
         ``pre`` is what the forward call wrote, needed with an activation or a
         gate.  ``workspace`` defaults to a buffer the object keeps."""
         import torch
-        shape, x, n, c, w, n_rows, K, Z, dtype = self._expert_args(
-            rows, counts, weights, d_outputs, "d_outputs", activation, gated)
+        shape, n, K, Z, dtype = self._expert_args(rows, counts, weights, d_outputs, "d_outputs",
+                                                  activation, gated)
         D, N, W = shape.in_features, shape.out_features, self.world_size
-        need = a2av_expert_matmul_workspace_bytes(W, shape, sum(n_rows))
+        need = a2av_expert_matmul_workspace_bytes(W, shape, sum(n))
         if need < 0:
             raise A2avError(ERR_UNSUPPORTED, "a2av_expert_matmul_workspace_bytes")
         activated = activation != "none" or bool(gated)
@@ -868,22 +892,22 @@ class A2av:
             if workspace is None or workspace.numel() < need:
                 workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
                 self._expert_workspace = workspace
-        each = [(K, Z, D)] * W
-        args = [self.handle, ctypes.byref(shape), x, n, c, w,
-                None if not activated else self._list(pre, "pre", dtype, [(m, Z) for m in n_rows]),
-                self._list(d_outputs, "d_outputs", dtype, [(m, N) for m in n_rows]),
-                None if d_rows is None else self._list(d_rows, "d_rows", dtype,
-                                                       [(m, D) for m in n_rows]),
-                None if d_weights is None else self._list(d_weights, "d_weights", dtype, each),
-                None if d_bias is None else self._list(d_bias, "d_bias", dtype, [(K, Z)] * W),
-                _address(workspace.data_ptr() if need else None),
-                int(workspace.numel()) if need else 0, self._queue(stream)]
+        each, by_row = [(K, Z, D)] * W, [(m, D) for m in n]
+        (x, w, z, dy, dx, dw, db), arrays = self._lists(
+            (rows, dtype, by_row, "rows"), (weights, dtype, each, "weights"),
+            (pre if activated else None, dtype, [(m, Z) for m in n], "pre"),
+            (d_outputs, dtype, [(m, N) for m in n], "d_outputs"), (d_rows, dtype, by_row, "d_rows"),
+            (d_weights, dtype, each, "d_weights"), (d_bias, dtype, [(K, Z)] * W, "d_bias"))
+        args = [self.handle, ctypes.byref(shape), x, self._counts(*n), counts.data_ptr(), w, z, dy, dx,
+                dw, db, workspace.data_ptr() if need else None, workspace.numel() if need else 0,
+                self._queue(stream)]
         self._call("a2av_expert_matmul_backward", args, None, False)
 
-    def _weighted_args(self, in_splits, keys, sorted_pos, keys_per_peer, token_rows, name):
-        """What both directions of the weighted combine share."""
-        W = self.world_size
-        sp = self._matrix(in_splits, (W, W), "in_splits")
+    def _weighted_args(self, in_splits, keys, sorted_pos, keys_per_peer, token_rows, name, peers):
+        """What both directions of the weighted combine share: K, k, H, the type
+        and its code, the rows of the ranks and of the peers' buffers (lists of
+        which are in ``peers``, as (tensors or None, name))."""
+        self._matrix(in_splits, (self.world_size, self.world_size), "in_splits")
         n, H = self._tokens(token_rows, name)
         dtype, code = self._dtype(token_rows, name, (F32, BF16, F16))
         sizes = [self._marshal.sizes(ts) or [0 if t is None else t.numel() for t in ts]
@@ -893,11 +917,23 @@ class A2av:
         for m, what in zip(sizes, ("keys", "sorted_pos")):
             if m != items:
                 raise ValueError(f"{what} must have one entry per item of each rank")
-        return (int(keys_per_peer), k, H, code, sp, self._list(keys, "keys", self._int32),
-                self._list(sorted_pos, "sorted_pos", self._int64), self._counts(*n), n, H, dtype)
-
-    def _item_weights(self, weights, name, n, k):
-        return self._list(weights, name, self._float, [(m, k) for m in n])
+        held = None
+        for ts, what in peers:
+            if ts is None:
+                continue
+            if len(ts) != self.world_size:
+                raise ValueError(f"{what}: expected {self.world_size} tensors, got {len(ts)}")
+            found = self._marshal.rows(ts)
+            if found is None:  # None among them, or of other shapes
+                if any(t is not None and (t.dim() != 2 or t.shape[1] != H) for t in ts):
+                    raise ValueError(f"{what} must be [rows, {H}] tensors")
+                found = [0 if t is None else t.shape[0] for t in ts], H
+            if found[1] != H:
+                raise ValueError(f"{what} must be [rows, {H}] tensors")
+            if held is not None and found[0] != held:
+                raise ValueError("peers and d_peers must have the same number of rows")
+            held = found[0]
+        return int(keys_per_peer), k, H, dtype, code, n, held
 
     def combine_weighted(self, peers, in_splits, keys, sorted_pos, keys_per_peer: int, weights,
                          outputs, residual=None, stream=None, _bind=False):
@@ -907,15 +943,17 @@ class A2av:
         ``in_splits``, ``keys`` and ``sorted_pos`` as the dispatch took or
         wrote them (topk items a token); ``weights[r]`` float32 [T, topk], or
         None for 1; ``outputs[r]`` and the optional ``residual[r]`` [T, H]."""
-        K, k, H, code, sp, ka, pa, na, n, H, dtype = self._weighted_args(
-            in_splits, keys, sorted_pos, keys_per_peer, outputs, "outputs")
+        K, k, H, dtype, code, n, held = self._weighted_args(
+            in_splits, keys, sorted_pos, keys_per_peer, outputs, "outputs", ((peers, "peers"),))
         shapes = [(m, H) for m in n]
-        held, (peer_arr,) = self._peer_rows((("peers", peers),), dtype, H)
-        args = [self.handle, K, k, H, code, peer_arr, held, sp, ka, pa,
-                None if weights is None else self._item_weights(weights, "weights", n, k), na,
-                None if residual is None else self._list(residual, "residual", dtype, shapes),
-                self._list(outputs, "outputs", dtype, shapes), self._queue(stream)]
-        keep = (peers, in_splits, keys, sorted_pos, weights, outputs, residual)
+        (x, ka, pa, w, r, y), arrays = self._lists(
+            (peers, dtype, None, "peers"), (keys, self._int32, None, "keys"),
+            (sorted_pos, self._int64, None, "sorted_pos"),
+            (weights, self._float, [(m, k) for m in n], "weights"),
+            (residual, dtype, shapes, "residual"), (outputs, dtype, shapes, "outputs"))
+        args = [self.handle, K, k, H, code, x, self._counts(*held), in_splits.data_ptr(), ka, pa, w,
+                self._counts(*n), r, y, self._queue(stream)]
+        keep = (peers, in_splits, keys, sorted_pos, weights, outputs, residual, arrays)
         return self._call("a2av_combine_weighted", args, keep, _bind)
 
     def bind_combine_weighted(self, peers, in_splits, keys, sorted_pos, keys_per_peer: int,
@@ -924,45 +962,25 @@ class A2av:
         return self.combine_weighted(peers, in_splits, keys, sorted_pos, keys_per_peer, weights,
                                      outputs, **options, _bind=True)
 
-    def _peer_rows(self, lists, dtype, H):
-        """Rows of the peers' buffers, and the pointer array of each list of them."""
-        held, arrays = None, []
-        for name, ts in lists:
-            if ts is None:
-                arrays.append(None)
-                continue
-            found = self._marshal.rows(ts)
-            if found is None:  # None among them, or of other shapes
-                if any(t is not None and (t.dim() != 2 or t.shape[1] != H) for t in ts):
-                    raise ValueError(f"{name} must be [rows, {H}] tensors")
-                found = [0 if t is None else t.shape[0] for t in ts], H
-            rows, width = found
-            if width != H:
-                raise ValueError(f"{name} must be [rows, {H}] tensors")
-            if held is not None and rows != held:
-                raise ValueError("peers and d_peers must have the same number of rows")
-            held = rows
-            arrays.append(self._list(ts, name, dtype))
-        return self._counts(*held), arrays
-
     def combine_weighted_backward(self, peers, in_splits, keys, sorted_pos, keys_per_peer: int,
                                   weights, d_outputs, d_peers=None, d_weights=None, stream=None):
         """The gradients of ``combine_weighted`` (see include/a2av_moe.h,
         a2av_combine_weighted_backward): ``d_peers[p]`` in the peers' layout,
         ``d_weights[r]`` float32 [T, topk]; either may be None (``peers`` too,
         without ``d_weights``)."""
-        K, k, H, code, sp, ka, pa, na, n, H, dtype = self._weighted_args(
-            in_splits, keys, sorted_pos, keys_per_peer, d_outputs, "d_outputs")
         if (d_peers is None and d_weights is None) or (d_weights is not None and peers is None):
             raise ValueError("d_peers, or d_weights with peers, must be given")
-        held, (peer_arr, d_peer_arr) = self._peer_rows((("peers", peers), ("d_peers", d_peers)),
-                                                       dtype, H)
-        args = [self.handle, K, k, H, code, peer_arr, held, sp, ka, pa,
-                None if weights is None else self._item_weights(weights, "weights", n, k), na,
-                self._list(d_outputs, "d_outputs", dtype, [(m, H) for m in n]),
-                d_peer_arr,
-                None if d_weights is None else self._item_weights(d_weights, "d_weights", n, k),
-                self._queue(stream)]
+        K, k, H, dtype, code, n, held = self._weighted_args(
+            in_splits, keys, sorted_pos, keys_per_peer, d_outputs, "d_outputs",
+            ((peers, "peers"), (d_peers, "d_peers")))
+        shapes = [(m, k) for m in n]
+        (x, ka, pa, w, dy, dx, dw), arrays = self._lists(
+            (peers, dtype, None, "peers"), (keys, self._int32, None, "keys"),
+            (sorted_pos, self._int64, None, "sorted_pos"), (weights, self._float, shapes, "weights"),
+            (d_outputs, dtype, [(m, H) for m in n], "d_outputs"), (d_peers, dtype, None, "d_peers"),
+            (d_weights, self._float, shapes, "d_weights"))
+        args = [self.handle, K, k, H, code, x, self._counts(*held), in_splits.data_ptr(), ka, pa, w,
+                self._counts(*n), dy, dx, dw, self._queue(stream)]
         self._call("a2av_combine_weighted_backward", args, None, False)
 
     def status(self, stream=None) -> int:

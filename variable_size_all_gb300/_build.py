@@ -14,7 +14,7 @@ HEADERS = [os.path.join(PKG, "csrc", f) for f in ("a2av_device.cuh", "a2av_handl
                                                   "moe_device.cuh", "experts.cuh", "mma.cuh")]
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "liba2av.so")
-MARSHAL_SOURCE = os.path.join(PKG, "csrc", "marshal.c")
+MARSHAL_SOURCE = os.path.join(PKG, "csrc", "marshal.cpp")
 MARSHAL = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -38,20 +38,33 @@ def stale(output: str = LIBRARY) -> bool:
     return os.path.getmtime(output) < max(os.path.getmtime(d) for d in deps)
 
 
-def build_marshal(force: bool = False) -> None:
-    """The binding's argument checks in C; without Python's headers the binding does them itself."""
-    include = sysconfig.get_paths()["include"]
-    if not os.path.exists(os.path.join(include, "Python.h")):
-        return
-    if force or not os.path.exists(MARSHAL) or os.path.getmtime(MARSHAL) < os.path.getmtime(MARSHAL_SOURCE):
-        subprocess.run(["gcc", "-O2", "-shared", "-fPIC", "-I", include, "-o", MARSHAL + ".tmp",
-                        MARSHAL_SOURCE], check=True)
+def start_marshal(force: bool = False):
+    """Begins to compile the binding's argument checks (csrc/marshal.cpp) against
+    the installed torch; returns the process, or None when there is nothing to
+    do.  Without a compiler or the headers the binding does the checks itself."""
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__))
+    include, python = os.path.join(base, "include"), sysconfig.get_paths()["include"]
+    if not force and os.path.exists(MARSHAL) and \
+            os.path.getmtime(MARSHAL) >= os.path.getmtime(MARSHAL_SOURCE):
+        return None
+    if shutil.which("g++") is None or not os.path.exists(os.path.join(python, "Python.h")):
+        return None
+    return subprocess.Popen(
+        ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w", "-I", include, "-I",
+         os.path.join(include, "torch", "csrc", "api", "include"), "-I", python,
+         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-o", MARSHAL + ".tmp",
+         MARSHAL_SOURCE, "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"])
+
+
+def finish_marshal(process) -> None:
+    if process is not None and process.wait() == 0:
         os.replace(MARSHAL + ".tmp", MARSHAL)
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     """Build ``liba2av.so`` unless it is up to date; returns its path."""
-    build_marshal(force)
+    marshal = start_marshal(force)
     if force or stale():
         cmd = command(extra=extra)
         if verbose:
@@ -60,6 +73,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         subprocess.run(cmd[:-len(SOURCES) - 2] + ["-o", tmp, *SOURCES, "--threads", "0"],
                        check=True)
         os.replace(tmp, LIBRARY)
+    finish_marshal(marshal)
     return LIBRARY
 
 
