@@ -1051,7 +1051,8 @@ bool a2av_expert_mma(a2av_handle* h, const A2avExperts& P, int dtype, int direct
         made = encode(&M.rows[0][p], n_side, dtype, P.D, rows, 1, kK) &&
                encode(&M.weights[p], m_side, dtype, P.Z, rows, 1, kK);
     } else {
-      for (int i = 0; i < kBoxes && made && rows > 0; ++i)
+      // (no run of granules takes a box of twice the buffer's rows)
+      for (int i = 0; i < kBoxes && made && rows > 0 && (i == 0 || (kGranule << i) < 2 * rows); ++i)
         made = encode(&M.rows[i][p], n_side, dtype, C, rows, 1, kGranule << i);
       made = made && (gated ? encode_gated(&M.weights[p], m_side, dtype, P.D, P.N, P.g.K)
                             : encode(&M.weights[p], m_side, dtype, P.D, P.Z, P.g.K,
