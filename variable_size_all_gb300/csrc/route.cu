@@ -15,6 +15,13 @@
 // A round over the maxima is a few instructions; one that also removes a choice
 // and finds the next costs some for every expert.  (Many equal choices can make
 // more candidates than there is room for; then those rounds are run.)
+//
+// Bound by instruction issue with many experts: 65,536 tokens of 256 experts
+// (f32, sigmoid, 4 of 8 groups, top 8) take 55 us against 10.5 for the memory,
+// 608 instructions a token, the issue slots 66 % busy; most are the exact
+// exponential and division of every score, which decide ties.  65,536 tokens of
+// 64 experts (bf16, top 2) take 14 us with the clearing of the counts, 4 tokens
+// on each of 8 ranks 10, of which the kernel is about 4 and the rest its launch.
 #include "moe_device.cuh"
 
 namespace {
@@ -380,6 +387,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps, L < 32 ? 4 : 1) route_kernel
   }
 }
 
+// A warp takes a token, a lane NJ experts.  Memory bound: the logits are read
+// (softmax over all the experts) and their gradients written once, 65,536 tokens
+// of 256 experts, f32: 139 MB in 27 us, 0.75 of the copy rate.
 template <typename T, int NJ, bool kVec>
 __global__ void __launch_bounds__(32 * kRouteWarps)
     route_backward_kernel(const __grid_constant__ RouteParams P) {
