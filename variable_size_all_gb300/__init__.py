@@ -390,6 +390,12 @@ class _PlainMarshal:
         except AttributeError:
             return None
 
+    @staticmethod
+    def route(*args):
+        return None  # (the method goes through its arguments itself)
+
+    route_backward = expert_matmul = combine_weighted = combine_weighted_backward = route
+
 
 def _load_marshal():
     try:
@@ -442,6 +448,10 @@ class A2av:
         import torch
         self._device = torch.cuda.current_device()
         self._marshal = _load_marshal()
+        self._address = getattr(h, "value", h)
+        self._entries = {what: ctypes.cast(getattr(load(), "a2av_" + what), ctypes.c_void_p).value
+                         for what in ("route", "route_backward", "expert_matmul", "combine_weighted",
+                                      "combine_weighted_backward")}
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._codes = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
         self._int32, self._int64, self._float = torch.int32, torch.int64, torch.float32
@@ -747,6 +757,23 @@ class A2av:
             arr[r] = t.data_ptr()
         return arr
 
+    def _whole(self, what, stream, *args):
+        """The call made by the compiled module in one go.  False when it has
+        found something to look at: nothing has been enqueued then."""
+        if self.handle is None:
+            return False
+        if stream is not None or self._raw_stream is None:
+            stream = self._stream(stream)
+        else:
+            stream = self._raw_stream(self._device)
+        rc = getattr(self._marshal, what)(self._entries[what], self._address, stream, self.world_size,
+                                          *args)
+        if rc is None:
+            return False
+        if rc != OK:
+            raise A2avError(rc, "a2av_" + what)
+        return True
+
     def _call(self, what, args, keep, bind):
         fn = getattr(load(), what)
         if bind:
@@ -796,6 +823,10 @@ class A2av:
         dispatch; ``weights[r]`` float32 [T, topk]; ``counts`` (optional)
         int64 [W, E], rank r's items for each expert.  ``bias``: optional
         float32 [E], added to the scores for the choice alone."""
+        if not _bind and self._whole("route", stream, logits, keys, weights, topk, counts, bias,
+                                     _SCORES.get(score), groups, top_groups, group_top, renormalise,
+                                     scale):
+            return
         cfg, (x, k, w, _), n, E, arrays = self._route_args(
             logits, keys, weights, "weights", topk, score, groups, top_groups, group_top,
             renormalise, scale)
@@ -819,6 +850,9 @@ class A2av:
         ``route`` wrote (see include/a2av_moe.h, a2av_route_backward)."""
         if d_logits is None:
             raise ValueError("d_logits is missing")
+        if self._whole("route_backward", stream, logits, keys, d_weights, d_logits, topk,
+                       _SCORES.get(score), renormalise, scale):
+            return
         cfg, (x, k, w, d), n, E, arrays = self._route_args(
             logits, keys, d_weights, "d_weights", topk, score, 1, 1, 1, renormalise, scale, d_logits)
         self._call("a2av_route_backward",
@@ -851,6 +885,9 @@ class A2av:
         ``weights[p]`` [K, Z, D] with Z = N, or 2 N when ``gated``; written:
         ``outputs[p]`` [rows, N] and, when given, ``pre[p]`` [rows, Z].
         ``bias[p]`` [K, Z] and ``residual[p]`` [rows, N] are optional."""
+        if not _bind and self._whole("expert_matmul", stream, rows, counts, weights, outputs,
+                                     _ACTIVATIONS.get(activation), gated, bias, residual, pre):
+            return
         shape, n, K, Z, dtype = self._expert_args(rows, counts, weights, outputs, "outputs",
                                                   activation, gated)
         D, N, W = shape.in_features, shape.out_features, self.world_size
@@ -943,6 +980,9 @@ class A2av:
         ``in_splits``, ``keys`` and ``sorted_pos`` as the dispatch took or
         wrote them (topk items a token); ``weights[r]`` float32 [T, topk], or
         None for 1; ``outputs[r]`` and the optional ``residual[r]`` [T, H]."""
+        if not _bind and self._whole("combine_weighted", stream, peers, in_splits, keys, sorted_pos,
+                                     keys_per_peer, weights, outputs, residual):
+            return
         K, k, H, dtype, code, n, held = self._weighted_args(
             in_splits, keys, sorted_pos, keys_per_peer, outputs, "outputs", ((peers, "peers"),))
         shapes = [(m, H) for m in n]
@@ -970,6 +1010,9 @@ class A2av:
         without ``d_weights``)."""
         if (d_peers is None and d_weights is None) or (d_weights is not None and peers is None):
             raise ValueError("d_peers, or d_weights with peers, must be given")
+        if self._whole("combine_weighted_backward", stream, peers, in_splits, keys, sorted_pos,
+                       keys_per_peer, weights, d_outputs, d_peers, d_weights):
+            return
         K, k, H, dtype, code, n, held = self._weighted_args(
             in_splits, keys, sorted_pos, keys_per_peer, d_outputs, "d_outputs",
             ((peers, "peers"), (d_peers, "d_peers")))

@@ -46,12 +46,13 @@ def start_marshal(force: bool = False):
     base = os.path.join(os.path.dirname(torch.__file__))
     include, python = os.path.join(base, "include"), sysconfig.get_paths()["include"]
     if not force and os.path.exists(MARSHAL) and \
-            os.path.getmtime(MARSHAL) >= os.path.getmtime(MARSHAL_SOURCE):
+            os.path.getmtime(MARSHAL) >= max(map(os.path.getmtime, (
+                MARSHAL_SOURCE, os.path.join(INCLUDE, "a2av.h"), os.path.join(INCLUDE, "a2av_moe.h")))):
         return None
     if shutil.which("g++") is None or not os.path.exists(os.path.join(python, "Python.h")):
         return None
     return subprocess.Popen(
-        ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w", "-I", include, "-I",
+        ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w", "-I", INCLUDE, "-I", include, "-I",
          os.path.join(include, "torch", "csrc", "api", "include"), "-I", python,
          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-o", MARSHAL + ".tmp",
          MARSHAL_SOURCE, "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"])

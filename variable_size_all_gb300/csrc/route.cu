@@ -21,7 +21,7 @@
 // 608 instructions a token, the issue slots 66 % busy; most are the exact
 // exponential and division of every score, which decide ties.  65,536 tokens of
 // 64 experts (bf16, top 2) take 14 us with the clearing of the counts, 4 tokens
-// on each of 8 ranks 10, of which the kernel is about 4 and the rest its launch.
+// on each of 8 ranks 3.5, one small launch.
 #include "moe_device.cuh"
 
 namespace {
