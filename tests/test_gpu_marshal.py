@@ -34,8 +34,8 @@ class _Counting:
 
         def counted(*args):
             result = f(*args)
-            if name in ("route", "route_backward", "expert_matmul", "combine_weighted",
-                        "combine_weighted_backward") and result is not None:
+            if name in ("route", "route_backward", "expert_matmul", "expert_matmul_backward",
+                        "combine_weighted", "combine_weighted_backward") and result is not None:
                 self.whole += 1
             return result
         return counted
@@ -69,8 +69,14 @@ def test_layer_is_the_same(side, dtype):
             y, dx = layer.forward(x), layer.backward(dy)
         stream.synchronize()
         assert layer.engine.status() == a2av.OK
-        # route, two products, combine; combine's gradient, the dispatch's, route's
-        assert layer.engine._marshal.whole == (0 if plain else 7)
+        # route, two products, combine; combine's gradient, the dispatch's, route's, and one
+        # product's: the first, and the second if it needs more, make the workspace first
+        assert layer.engine._marshal.whole in ((0,) if plain else (7, 8))
+        if not plain:
+            with torch.cuda.stream(stream):
+                layer.backward(dy)
+            stream.synchronize()
+            assert layer.engine._marshal.whole in (12, 13)
         results.append([t.clone() for t in [*y, *dx, *layer.keys, *layer.weights, layer.counts,
                                             *layer.d_up, *layer.d_down, layer.d_gate]])
         layer.engine.close()
@@ -124,7 +130,22 @@ def test_options_are_the_same():
             stream.synchronize()
             assert eng.status() == a2av.OK
             assert eng._marshal.whole == (6 if module is a2av._marshal else 0)
-            results.append([*keys, *weights, counts, *d_logits, *out, *pre, *y, *d_out, *d_w])
+            d_rows, d_up, d_b = rows_like(rows), rows_like(up), rows_like(b)
+            need = a2av.a2av_expert_matmul_workspace_bytes(
+                W, a2av.A2avExpert(E // W, H, N, a2av.F16, 2, 1), sum(held))
+            space = torch.empty(need, dtype=torch.uint8, device="cuda")
+            stream.wait_stream(torch.cuda.current_stream())
+            for given in (dict(d_rows=d_rows, d_bias=d_b), dict(d_weights=d_up)):
+                eng.expert_matmul_backward(rows, counts, up, res, pre=pre, activation="gelu", gated=True,
+                                           workspace=space, stream=stream, **given)
+            stream.synchronize()
+            assert eng.status() == a2av.OK
+            assert eng._marshal.whole == (8 if module is a2av._marshal else 0)
+            with pytest.raises(a2av.A2avError):  # (a workspace that is too small)
+                eng.expert_matmul_backward(rows, counts, up, res, d_rows, pre=pre, activation="gelu",
+                                           gated=True, workspace=space[:need - 256])
+            results.append([*keys, *weights, counts, *d_logits, *out, *pre, *y, *d_out, *d_w, *d_rows,
+                            *d_up, *d_b])
     for a, c in zip(*results):
         assert torch.equal(a, c)
 

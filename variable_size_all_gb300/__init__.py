@@ -394,7 +394,8 @@ class _PlainMarshal:
     def route(*args):
         return None  # (the method goes through its arguments itself)
 
-    route_backward = expert_matmul = combine_weighted = combine_weighted_backward = route
+    route_backward = expert_matmul = expert_matmul_backward = route
+    combine_weighted = combine_weighted_backward = route
 
 
 def _load_marshal():
@@ -450,8 +451,9 @@ class A2av:
         self._marshal = _load_marshal()
         self._address = getattr(h, "value", h)
         self._entries = {what: ctypes.cast(getattr(load(), "a2av_" + what), ctypes.c_void_p).value
-                         for what in ("route", "route_backward", "expert_matmul", "combine_weighted",
-                                      "combine_weighted_backward")}
+                         for what in ("route", "route_backward", "expert_matmul",
+                                      "expert_matmul_backward", "expert_matmul_workspace_bytes",
+                                      "combine_weighted", "combine_weighted_backward")}
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._codes = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
         self._int32, self._int64, self._float = torch.int32, torch.int64, torch.float32
@@ -915,6 +917,11 @@ class A2av:
         ``pre`` is what the forward call wrote, needed with an activation or a
         gate.  ``workspace`` defaults to a buffer the object keeps."""
         import torch
+        kept = workspace if workspace is not None else getattr(self, "_expert_workspace", None)
+        if self._whole("expert_matmul_backward", stream, rows, counts, weights, d_outputs, d_rows,
+                       d_weights, d_bias, pre, _ACTIVATIONS.get(activation), gated, kept,
+                       self._entries["expert_matmul_workspace_bytes"]):
+            return
         shape, n, K, Z, dtype = self._expert_args(rows, counts, weights, d_outputs, "d_outputs",
                                                   activation, gated)
         D, N, W = shape.in_features, shape.out_features, self.world_size

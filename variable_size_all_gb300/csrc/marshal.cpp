@@ -3,8 +3,8 @@
 // small tensors, and reading five attributes of each through Python took longer
 // (12 us of a combine's 27 on 8 ranks) than the kernel does.
 //
-// route, route_backward, expert_matmul, combine_weighted and
-// combine_weighted_backward(function, handle, stream, W, the method's arguments)
+// route, route_backward, expert_matmul, expert_matmul_backward, combine_weighted
+// and combine_weighted_backward(function, handle, stream, W, the method's arguments)
 // -> the library's return value: the whole call, where every list has W good
 // tensors and every number is in its range.  None where one is not, or is
 // missing: nothing has been called, and the binding goes through its arguments
@@ -326,48 +326,108 @@ PyObject* route_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
       });
 }
 
-// (..., rows, counts, weights, outputs, activation, gated, bias, residual, pre)
-PyObject* expert_matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
+// The lists an expert's product has in either direction; `out` are its results
+// or their gradients.
+struct Product {
   Call c;
   a2av_expert_t shape;
-  int64_t held[kRanks], D = 0, N = 0;
-  const int64_t* counts = nullptr;
-  void *x[kRanks], *w[kRanks], *y[kRanks], *b[kRanks], *r[kRanks], *z[kRanks];
+  at::ScalarType type;
+  int64_t held[kRanks], K, Z, D, N;
+  const int64_t* counts;
+  void *rows[kRanks], *weights[kRanks], *out[kRanks];
+
+  bool take_all(PyObject* x, PyObject* s, PyObject* w, PyObject* y, PyObject* activation,
+                PyObject* gated) {
+    int64_t n[kRanks];
+    if (!type_of(w, false, &type, &shape.dtype) || !take_any_rows(x, c.W, type, rows, held, &D) ||
+        !take_any_rows(y, c.W, type, out, n, &N) || !int_of(activation, &shape.activation))
+      return false;
+    for (int p = 0; p < c.W; ++p)
+      if (n[p] != held[p]) return false;
+    shape.gated = PyObject_IsTrue(gated) == 1;
+    Z = shape.gated ? 2 * N : N;
+    if (!take(w, c.W, type, weights, [&](const at::Tensor& t, int i) {
+          if (t.dim() != 3 || (i > 0 && t.size(0) != K)) return false;
+          K = t.size(0);
+          return t.size(1) == Z && t.size(2) == D;
+        }))
+      return false;
+    shape.experts_per_peer = (int)K;
+    shape.in_features = D;
+    shape.out_features = N;
+    return K <= INT_MAX && matrix_of(s, c.W, c.W * K, &counts);
+  }
+
+  // Optional lists of [rows, width], [K, Z] and [K, Z, D].
+  bool take_by_row(PyObject* list, int64_t width, void** to) const {
+    return list == Py_None || take_rows(list, c.W, type, to, held, width);
+  }
+  bool take_bias(PyObject* list, void** to) const {
+    return list == Py_None || take(list, c.W, type, to, [&](const at::Tensor& t, int) {
+             return has_sizes(t, K, Z);
+           });
+  }
+  bool take_weights(PyObject* list, void** to) const {
+    return list == Py_None || take(list, c.W, type, to, [&](const at::Tensor& t, int) {
+             return t.dim() == 3 && t.size(0) == K && t.size(1) == Z && t.size(2) == D;
+           });
+  }
+};
+
+// (..., rows, counts, weights, outputs, activation, gated, bias, residual, pre)
+PyObject* expert_matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  Product m;
+  void *bias[kRanks], *residual[kRanks], *pre[kRanks];
   return whole(
       n, 13,
       [&] {
-        at::ScalarType type;
-        if (!call_of(args, &c) || !type_of(args[6], false, &type, &shape.dtype) ||
-            !take_any_rows(args[4], c.W, type, x, held, &D))
-          return false;
-        int64_t rows[kRanks], K = 0, Z = 0;
-        if (!take_any_rows(args[7], c.W, type, y, rows, &N)) return false;
-        for (int p = 0; p < c.W; ++p)
-          if (rows[p] != held[p]) return false;
-        if (!int_of(args[8], &shape.activation)) return false;
-        shape.gated = PyObject_IsTrue(args[9]) == 1;
-        Z = shape.gated ? 2 * N : N;
-        if (!take(args[6], c.W, type, w, [&](const at::Tensor& t, int i) {
-              if (t.dim() != 3 || (i > 0 && t.size(0) != K)) return false;
-              K = t.size(0);
-              return t.size(1) == Z && t.size(2) == D;
-            }))
-          return false;
-        if (K > INT_MAX || !matrix_of(args[5], c.W, c.W * K, &counts)) return false;
-        shape.experts_per_peer = (int)K;
-        shape.in_features = D;
-        shape.out_features = N;
-        return (args[10] == Py_None || take(args[10], c.W, type, b, [&](const at::Tensor& t, int) {
-                  return has_sizes(t, K, Z);
-                })) &&
-               (args[11] == Py_None || take_rows(args[11], c.W, type, r, held, N)) &&
-               (args[12] == Py_None || take_rows(args[12], c.W, type, z, held, Z));
+        return call_of(args, &m.c) &&
+               m.take_all(args[4], args[5], args[6], args[7], args[8], args[9]) &&
+               m.take_bias(args[10], bias) && m.take_by_row(args[11], m.N, residual) &&
+               m.take_by_row(args[12], m.Z, pre);
       },
       [&] {
-        return reinterpret_cast<decltype(&a2av_expert_matmul)>(c.function)(
-            static_cast<a2av_handle*>(c.handle), &shape, x, held, counts, w,
-            args[10] == Py_None ? nullptr : b, args[11] == Py_None ? nullptr : r, y,
-            args[12] == Py_None ? nullptr : z, c.stream);
+        return reinterpret_cast<decltype(&a2av_expert_matmul)>(m.c.function)(
+            static_cast<a2av_handle*>(m.c.handle), &m.shape, m.rows, m.held, m.counts, m.weights,
+            args[10] == Py_None ? nullptr : bias, args[11] == Py_None ? nullptr : residual, m.out,
+            args[12] == Py_None ? nullptr : pre, m.c.stream);
+      });
+}
+
+// (..., rows, counts, weights, d_outputs, d_rows, d_weights, d_bias, pre, activation, gated,
+// workspace, a2av_expert_matmul_workspace_bytes); None as well where the workspace is too small.
+PyObject* expert_matmul_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  Product m;
+  void *d_rows[kRanks], *d_weights[kRanks], *d_bias[kRanks], *pre[kRanks], *workspace = nullptr;
+  int64_t bytes = 0;
+  bool activated = false;
+  return whole(
+      n, 16,
+      [&] {
+        if (!call_of(args, &m.c) ||
+            !m.take_all(args[4], args[5], args[6], args[7], args[12], args[13]) ||
+            !m.take_by_row(args[8], m.D, d_rows) || !m.take_weights(args[9], d_weights) ||
+            !m.take_bias(args[10], d_bias))
+          return false;
+        activated = m.shape.activation != A2AV_ACT_NONE || m.shape.gated;
+        if (activated && (args[11] == Py_None || !m.take_by_row(args[11], m.Z, pre))) return false;
+        const at::Tensor* t = tensor_of(args[14]);
+        void* size_of = PyLong_Check(args[15]) ? PyLong_AsVoidPtr(args[15]) : nullptr;
+        if (!is_good(t, at::kByte) || size_of == nullptr) return false;
+        int64_t total = 0;
+        for (int p = 0; p < m.c.W; ++p) total += m.held[p];
+        const int64_t need = reinterpret_cast<decltype(&a2av_expert_matmul_workspace_bytes)>(size_of)(
+            m.c.W, &m.shape, total);
+        workspace = t->data_ptr();
+        bytes = t->numel();
+        return need > 0 && bytes >= need;
+      },
+      [&] {
+        return reinterpret_cast<decltype(&a2av_expert_matmul_backward)>(m.c.function)(
+            static_cast<a2av_handle*>(m.c.handle), &m.shape, m.rows, m.held, m.counts, m.weights,
+            activated ? pre : nullptr, m.out, args[8] == Py_None ? nullptr : d_rows,
+            args[9] == Py_None ? nullptr : d_weights, args[10] == Py_None ? nullptr : d_bias, workspace,
+            bytes, m.c.stream);
       });
 }
 
@@ -467,6 +527,7 @@ PyMethodDef methods[] = {
     A2AV_WHOLE(route),
     A2AV_WHOLE(route_backward),
     A2AV_WHOLE(expert_matmul),
+    A2AV_WHOLE(expert_matmul_backward),
     A2AV_WHOLE(combine_weighted),
     A2AV_WHOLE(combine_weighted_backward),
     {nullptr, nullptr, 0, nullptr}};
