@@ -294,3 +294,24 @@ def test_refusals():
         assert eng.status() == a2av.OK
     assert a2av.load().a2av_route(None, ctypes.byref(cfg), None, None, None, None, None, None,
                                   None) == a2av.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("tokens", [(1, 0, 3), (8, 9, 0), (64, 1, 33), (65, 64, 130), (0, 700, 2047)])
+@pytest.mark.parametrize("E,k", [(8, 2), (60, 3), (300, 8)])
+def test_counts_of_uneven_ranks(tokens, E, k):
+    """One block a rank or several; and ranks with fewer tokens than they were
+    launched for, or none.  The counts are those of the keys, twice in a row into
+    the same tensor."""
+    W = len(tokens)
+    gen = torch.Generator("cuda").manual_seed(sum(tokens) + E)
+    counts = torch.full((W, E), 99, dtype=torch.int64, device="cuda")
+    keys = [torch.empty(t, k, dtype=torch.int32, device="cuda") for t in tokens]
+    weights = [torch.empty(t, k, device="cuda") for t in tokens]
+    with a2av.A2av(W) as eng:
+        for _ in range(2):
+            logits = [torch.randn(t, E, device="cuda", generator=gen) for t in tokens]
+            eng.route(logits, keys, weights, k, counts=counts)
+            assert eng.status() == a2av.OK
+            for r in range(W):
+                assert torch.equal(logits[r].topk(k, dim=1).indices.int(), keys[r])
+                assert torch.equal(torch.bincount(keys[r].view(-1).long(), minlength=E), counts[r])

@@ -17,10 +17,10 @@
 // more candidates than there is room for; then those rounds are run.)
 //
 // Bound by instruction issue with many experts: 65,536 tokens of 256 experts
-// (f32, sigmoid, 4 of 8 groups, top 8) take 55 us against 10.5 for the memory,
+// (f32, sigmoid, 4 of 8 groups, top 8) take 52 us against 10.5 for the memory,
 // 608 instructions a token, the issue slots 66 % busy; most are the exact
 // exponential and division of every score, which decide ties.  65,536 tokens of
-// 64 experts (bf16, top 2) take 14 us with the clearing of the counts, 4 tokens
+// 64 experts (bf16, top 2) take 10.7 us with the clearing of the counts, 4 tokens
 // on each of 8 ranks 3.5, one small launch.
 #include "moe_device.cuh"
 
@@ -42,7 +42,7 @@ struct RouteParams {
   int group_size;
   int group_lanes;  // lanes of a group, where that is a power of two of whole lanes; else 0
   float scale;
-  int add_counts;  // several blocks a rank: counts (cleared before) are added to
+  int add_counts;  // several blocks a rank: counts (cleared by a kernel before) are added to
 };
 
 constexpr unsigned kNegInf = 0x007fffffu;  // order_of(-inf)
@@ -490,6 +490,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
   }
 }
 
+// (A kernel, which the router's chains to, and no memset, which it would have to
+// wait out: 65,536 tokens of 64 experts take 10.7 us against 14.3, 256 tokens on
+// each of 8 ranks 5.0 against 8.2.  A cluster for the blocks of a rank, which
+// read each other's counts, took 4.1 against 5.0 for 64 cheap tokens a rank, one
+// launch instead of two, and 6.4 against 5.2 for dear ones; not kept.)
+__global__ void clear_counts_kernel(unsigned long long* counts, int n) {
+  chain();
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) counts[i] = 0;
+}
+
 using RouteKernel = void (*)(RouteParams);
 
 // Lanes and experts a lane for a call: few tokens, or many.  (Measured at 65,536
@@ -648,7 +658,9 @@ extern "C" int a2av_route(a2av_handle* h, const a2av_route_t* route,
   const int blocks = route_blocks(h, most, shape.lanes);
   if (P.counts != nullptr && blocks > 1) {
     P.add_counts = 1;
-    if (cudaMemsetAsync(counts_dev, 0, sizeof(int64_t) * h->W * P.E, s) != cudaSuccess)
+    const int n = h->W * P.E, clear = (n + 255) / 256;
+    if (launch_chained(clear_counts_kernel, dim3(clear < h->sms ? clear : h->sms), 256, 0, s, h->pdl,
+                       P.counts, n) != cudaSuccess)
       return A2AV_ERR_CUDA;
   }
   const cudaError_t e =
