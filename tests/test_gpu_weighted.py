@@ -62,7 +62,7 @@ def _rows_of(c, r):
 
 SHAPES = [([1], 1, 1, 8), ([1], 4, 2, 7168), ([5, 0, 3], 2, 3, 64), ([33, 1], 8, 2, 1000),
           ([7, 7], 3, 6, 65), ([1, 0], 5, 1, 1), ([50, 49, 3, 8], 16, 2, 513), ([2] * 8, 8, 4, 2056),
-          ([3], 32, 32, 40), ([300], 2, 1, 24)]
+          ([3], 32, 32, 40), ([300], 2, 1, 24), ([600, 500], 8, 2, 512), ([200] * 8, 8, 3, 1544)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])

@@ -13,6 +13,8 @@
 // warps an SM holds in other rows the slower (two blocks of eight: 466, four: 585).
 // The backward pass of the same rows (dy and the rows read, their gradients
 // written) takes 695 us, the copy rate.
+// (Of few tokens a block takes one: a decoding step of 16 tokens on each of 8
+// ranks, 5.6 us against 13.)
 #include "moe_device.cuh"
 
 namespace {
@@ -212,24 +214,28 @@ __global__ void __launch_bounds__(kWeightedThreads, 2)
   }
 }
 
-template <typename T, int N>
+// kBlock: a block takes a token, its warps every eighth slice of the rows; else
+// a warp does.
+template <typename T, int N, bool kBlock>
 __global__ void __launch_bounds__(kWeightedThreads)
     combine_weighted_backward_kernel(const __grid_constant__ WeightedParams P) {
   chain();
+  constexpr int kWarps = kWeightedThreads / 32;
   __shared__ Offsets o;
+  __shared__ float part[kBlock ? A2AV_MAX_TOPK : 1][kWarps];  // the warps' sums of an item
   using Q = Piece<T, N>;
   using V = typename Q::Raw;
   constexpr int kVectors = N == 1 ? 8 : 16 / N, kSlice = 32 * kVectors;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const long long nv = P.H / N, tokens = P.token_first[P.W];
-  const long long warps = (long long)gridDim.x * (kWeightedThreads / 32);
-  long long g = (long long)blockIdx.x * (kWeightedThreads / 32) + threadIdx.x / 32;
+  const long long by = kBlock ? gridDim.x : (long long)gridDim.x * kWarps;
+  long long g = kBlock ? blockIdx.x : (long long)blockIdx.x * kWarps + warp;
   Item item;
   if (g < tokens) item = fetch_item(P, g, lane);
   if (!build_offsets(P, o)) return;
   while (g < tokens) {
     const Item it = item;
-    g += warps;
+    g += by;
     if (g < tokens) item = fetch_item(P, g, lane);
     int p;
     long long at;
@@ -244,7 +250,8 @@ __global__ void __launch_bounds__(kWeightedThreads)
       T *d0 = from_lane(d_row, j), *d1 = from_lane(d_row, j1);
       const float w0 = __shfl_sync(kAll, it.w, j), w1 = __shfl_sync(kAll, it.w, j1);
       float dot0 = 0.0f, dot1 = 0.0f;
-      for (long long v0 = lane; v0 < nv; v0 += kSlice) {
+      for (long long v0 = lane + (kBlock ? warp * kSlice : 0); v0 < nv;
+           v0 += kBlock ? kWarps * kSlice : kSlice) {
         V d[kVectors], x[kVectors], y[kVectors];
         load_slice<T, N, kVectors>(d, dy, v0, nv);
         if (P.reads) {
@@ -285,33 +292,46 @@ __global__ void __launch_bounds__(kWeightedThreads)
           dot0 += __shfl_xor_sync(kAll, dot0, s);
           dot1 += __shfl_xor_sync(kAll, dot1, s);
         }
-        float* dw = P.d_weight[it.r] + it.t * P.k + j;
+        float* dw = kBlock ? &part[j][warp] : P.d_weight[it.r] + it.t * P.k + j;
         if (lane == 0) dw[0] = dot0;
-        if (lane == 1 && two) dw[1] = dot1;
+        if (lane == 1 && two) dw[kBlock ? kWarps : 1] = dot1;
       }
+    }
+    if (kBlock && P.reads) {
+      __syncthreads();
+      if (threadIdx.x < P.k) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) sum += part[threadIdx.x][i];
+        P.d_weight[it.r][it.t * P.k + threadIdx.x] = sum;
+      }
+      __syncthreads();
     }
   }
 }
 
 using WeightedKernel = void (*)(WeightedParams);
 
+enum WeightedForm { kForward, kBackward, kBackwardBlock };
+
 // `bytes`: of a vector, 16, 4 or one element, as every row and buffer allows.
 template <typename T, int N>
-WeightedKernel weighted_kernel_of(bool backward) {
-  return backward ? combine_weighted_backward_kernel<T, N> : combine_weighted_kernel<T, N>;
+WeightedKernel weighted_kernel_of(WeightedForm form) {
+  if (form == kForward) return combine_weighted_kernel<T, N>;
+  return form == kBackward ? combine_weighted_backward_kernel<T, N, false>
+                           : combine_weighted_backward_kernel<T, N, true>;
 }
 
 template <typename T>
-WeightedKernel weighted_kernel_of(int bytes, bool backward) {
-  if (bytes == 16) return weighted_kernel_of<T, 16 / sizeof(T)>(backward);
-  return bytes == 4 ? weighted_kernel_of<T, 4 / sizeof(T)>(backward)
-                    : weighted_kernel_of<T, 1>(backward);
+WeightedKernel weighted_kernel_of(int bytes, WeightedForm form) {
+  if (bytes == 16) return weighted_kernel_of<T, 16 / sizeof(T)>(form);
+  return bytes == 4 ? weighted_kernel_of<T, 4 / sizeof(T)>(form) : weighted_kernel_of<T, 1>(form);
 }
 
-WeightedKernel weighted_kernel_of(int dtype, int bytes, bool backward) {
-  if (dtype == A2AV_F32) return weighted_kernel_of<float>(bytes, backward);
-  if (dtype == A2AV_BF16) return weighted_kernel_of<__nv_bfloat16>(bytes, backward);
-  return weighted_kernel_of<__half>(bytes, backward);
+WeightedKernel weighted_kernel_of(int dtype, int bytes, WeightedForm form) {
+  if (dtype == A2AV_F32) return weighted_kernel_of<float>(bytes, form);
+  if (dtype == A2AV_BF16) return weighted_kernel_of<__nv_bfloat16>(bytes, form);
+  return weighted_kernel_of<__half>(bytes, form);
 }
 
 // Both directions: `peers` read, `d_peers` written (either may be NULL as the
@@ -373,14 +393,23 @@ int weighted_call(a2av_handle* h, int K, int k, int64_t H, int dtype, const void
   P.reads = peers != nullptr;
   P.writes = d_peers != nullptr;
   const int bytes = low % 16 == 0 ? 16 : low % 4 == 0 ? 4 : size;
-  const WeightedKernel kernel = weighted_kernel_of(dtype, bytes, backward);
+  // A block a token where that keeps more bytes in flight: rows of 8 KiB, a slice
+  // for each of its warps, until the tokens' warps fill the GPU several times over
+  // (14 KiB rows by twos, 128 tokens 13.0 -> 5.6 us, 4096: 64 -> 50; 8 KiB, 4096:
+  // 39 -> 33, but 16,384: 109 -> 114), shorter ones only with few tokens (4 KiB,
+  // 128: 6.4 -> 4.1; 4096: 16 -> 21).
+  const long long kib = (H * size + 1023) / 1024;
+  const bool by_block = backward && P.token_first[W] < h->sms * (kib >= 8 ? 64 : kib);
+  const WeightedKernel kernel =
+      weighted_kernel_of(dtype, bytes, !backward ? kForward : by_block ? kBackwardBlock : kBackward);
   int fit = 0;  // blocks an SM holds
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, kWeightedThreads, 0) != cudaSuccess)
     return A2AV_ERR_CUDA;
   const long long most = (long long)fit * h->sms, warps = kWeightedThreads / 32;
   const int slice = bytes == 16 ? 128 : 256;  // vectors of a forward warp's slice
   const long long slices = backward ? 1 : (H * size / bytes + slice - 1) / slice;
-  const long long blocks = (P.token_first[W] * slices + warps - 1) / warps;
+  const long long blocks =
+      by_block ? P.token_first[W] : (P.token_first[W] * slices + warps - 1) / warps;
   const unsigned grid = (unsigned)(blocks < most ? blocks : most);
   const cudaError_t e = launch_chained(kernel, dim3(grid), kWeightedThreads, 0,
                                        static_cast<cudaStream_t>(stream), h->pdl, P);
