@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kPlainThreads)
 }
 
 // ---------------------------------------------- activation's gradient --
-// dz from dy and the saved pre-activations: a warp takes a row, a vector of N
+// dz from dy and the saved pre-activations: a warp takes a row, or a part of one, a vector of N
 // elements a lane at a time.  Memory bound: with a gate 5 N elements of 2 bytes
 // are read and written a row (32,768 rows, N 2048, SiLU: 671 MB in 117 us, 5.7
 // TB/s).
@@ -150,15 +150,20 @@ __global__ void __launch_bounds__(256)
   using V = typename Q::Raw;
   const int nv = (int)(P.N / N), lane = threadIdx.x & 31;
   const int warps = gridDim.x * (blockDim.x / 32), all = g.peer_base[P.g.W];
+  const RowParts split(all, warps, nv);
   int p = 0;
-  for (int at = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; at < all; at += warps) {
+  for (int unit = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; unit < all * split.parts;
+       unit += warps) {
+    const int at = unit / split.parts;
+    int from, to;
+    split.run(unit - at * split.parts, nv, &from, &to);
     while (at >= g.peer_base[p + 1]) ++p;
     const long long row = at - g.peer_base[p];
     const V* dy = reinterpret_cast<const V*>(static_cast<const T*>(P.dy[p]) + row * P.N);
     const V* pre = reinterpret_cast<const V*>(static_cast<const T*>(P.pre_in[p]) + row * P.Z);
     V* dz = reinterpret_cast<V*>(static_cast<T*>(P.dz[p]) + row * P.Z);
 #pragma unroll 2
-    for (int v = lane; v < nv; v += 32) {
+    for (int v = from + lane; v < to; v += 32) {
       float d[N], z[N], u[N];
       Q::unpack(dy[v], d);
       Q::unpack(pre[v], z);

@@ -55,6 +55,20 @@ struct GroupTiles {
   long long first[kEntries + 1];
 };
 
+// How a row's vectors are shared out: one warp takes them all, or, where there
+// are fewer rows than warps, several take a run of them each (of 64 at least).
+struct RowParts {
+  int parts;
+  __device__ __forceinline__ RowParts(int rows, int warps, int vectors)
+      : parts(max(1, min(warps / max(rows, 1), (vectors + 63) / 64))) {}
+  // the run of `vectors` that part i has
+  __device__ __forceinline__ void run(int i, int vectors, int* from, int* to) const {
+    const int len = (vectors + 32 * parts - 1) / (32 * parts) * 32;
+    *from = min(i * len, vectors);
+    *to = min(*from + len, vectors);
+  }
+};
+
 struct GroupTile {
   int p, e;          // peer, local expert
   int rows;          // rows of the group

@@ -726,7 +726,13 @@ __global__ void __launch_bounds__(256) expert_tails_kernel(const __grid_constant
   const int lane = threadIdx.x & 31, W = P.g.W, K = P.g.K, E = W * K;
   const int zv = P.Z / 8, xv = P.D / 8;  // 16-byte vectors of a row
   const int warps = gridDim.x * (blockDim.x / 32);
-  for (int row = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; row < tt.first[E]; row += warps) {
+  const RowParts split(tt.first[E], warps, max(zv, xv));
+  for (int unit = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; unit < tt.first[E] * split.parts;
+       unit += warps) {
+    const int row = unit / split.parts, part = unit - row * split.parts;
+    int zi, z1, xi, x1;
+    split.run(part, zv, &zi, &z1);
+    split.run(part, xv, &xi, &x1);
     int lo = 0, hi = E;  // first[lo] <= row < first[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -750,9 +756,9 @@ __global__ void __launch_bounds__(256) expert_tails_kernel(const __grid_constant
     const uint4* z0 = static_cast<const uint4*>(P.dz[p]) + from * zv;
     const uint4* x0 = static_cast<const uint4*>(P.x[p]) + from * xv;
 #pragma unroll 4
-    for (int i = lane; i < zv; i += 32) z[i] = from < 0 ? make_uint4(0, 0, 0, 0) : z0[i];
+    for (int i = zi + lane; i < z1; i += 32) z[i] = from < 0 ? make_uint4(0, 0, 0, 0) : z0[i];
 #pragma unroll 4
-    for (int i = lane; i < xv; i += 32) x[i] = from < 0 ? make_uint4(0, 0, 0, 0) : x0[i];
+    for (int i = xi + lane; i < x1; i += 32) x[i] = from < 0 ? make_uint4(0, 0, 0, 0) : x0[i];
   }
 }
 
