@@ -387,7 +387,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps, L < 32 ? 4 : 1) route_kernel
   }
 }
 
-// A warp takes a token, a lane NJ experts.  Memory bound: the logits are read
+// A warp takes a token, a lane NJ experts: consecutive ones as vectors, or, where
+// rows are not aligned for those, every 32nd.  Memory bound: the logits are read
 // (softmax over all the experts) and their gradients written once, 65,536 tokens
 // of 256 experts, f32: 139 MB in 27 us, 0.75 of the copy rate.
 template <typename T, int NJ, bool kVec>
@@ -419,10 +420,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) d[j] = 0.0f;
     if (!bad) {
-      float* own = scatter[warp] + lane * NJ;
+      const float* own = scatter[warp] + (kVec ? lane * NJ : lane);
+      constexpr int kStep = kVec ? 1 : 32;
       if (dense) {
         float x[NJ];
-        load_logits<T, NJ, kVec>(row, E, lane, x);
+        if (kVec) {
+          load_logits<T, NJ, true>(row, E, lane, x);
+        } else {
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) x[j] = lane + 32 * j < E ? to_float(row[lane + 32 * j]) : -INFINITY;
+        }
         float m = x[0];
 #pragma unroll
         for (int j = 1; j < NJ; ++j) m = fmaxf(m, x[j]);
@@ -440,7 +447,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
         if (lane < k) scatter[warp][key] = g;
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) d[j] = x[j] * inv * (own[j] - dot);
+        for (int j = 0; j < NJ; ++j) d[j] = x[j] * inv * (own[j * kStep] - dot);
       } else {
         float onto;  // what the lane's choice gets
         if (softmax) {
@@ -462,10 +469,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
         if (lane < k) scatter[warp][key] = onto;
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) d[j] = own[j];
+        for (int j = 0; j < NJ; ++j) d[j] = own[j * kStep];
       }
       __syncwarp();
       if (lane < k) scatter[warp][key] = 0.0f;
+      __syncwarp();
     }
     T* out = static_cast<T*>(P.d_logits[r]) + (long long)t * E;
     if (kVec) {
@@ -483,7 +491,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
     } else {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const int e = lane * NJ + j;
+        const int e = lane + 32 * j;
         if (e < E) out[e] = from_float<T>(d[j]);
       }
     }
