@@ -297,7 +297,7 @@ def test_refusals():
 
 
 @pytest.mark.parametrize("tokens", [(1, 0, 3), (8, 9, 0), (64, 1, 33), (65, 64, 130), (0, 700, 2047)])
-@pytest.mark.parametrize("E,k", [(8, 2), (60, 3), (300, 8)])
+@pytest.mark.parametrize("E,k", [(8, 2), (60, 3), (61, 3), (255, 7), (300, 8)])
 def test_counts_of_uneven_ranks(tokens, E, k):
     """One block a rank or several; and ranks with fewer tokens than they were
     launched for, or none.  The counts are those of the keys, twice in a row into

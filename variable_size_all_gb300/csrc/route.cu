@@ -520,11 +520,9 @@ struct RouteShape {
 
 template <typename T, bool kVec>
 RouteKernel route_kernel_of(RouteShape f) {
-  if constexpr (kVec) {  // (many tokens)
-    if (f.lanes == 4) return route_kernel<T, 4, kManyNj, true>;
-    if (f.lanes == 8) return route_kernel<T, 8, kManyNj, true>;
-    if (f.lanes == 16) return route_kernel<T, 16, kManyNj, true>;
-  }
+  if (f.lanes == 4) return route_kernel<T, 4, kManyNj, kVec>;  // (many tokens)
+  if (f.lanes == 8) return route_kernel<T, 8, kManyNj, kVec>;
+  if (f.lanes == 16) return route_kernel<T, 16, kManyNj, kVec>;
   switch (f.nj) {
     case 1: return route_kernel<T, 32, 1, kVec>;
     case 2: return route_kernel<T, 32, 2, kVec>;
@@ -559,7 +557,8 @@ RouteKernel route_kernel_of(int dtype, RouteShape f, bool vec, bool backward) {
   return route_kernel_of<__half>(f, vec, backward);
 }
 
-// Tokens from which on several share a warp.
+// Tokens from which on several share a warp (also where rows take no vectors:
+// 65,536 tokens of 61 experts, bf16, 11.3 us against 25).
 constexpr long long kManyTokens = 2048;
 
 // The checks both calls share; fills what both need.
@@ -617,8 +616,7 @@ int route_params(a2av_handle* h, const a2av_route_t* c, const void* const* logit
   shape->lanes = 32;
   shape->nj = 1;
   while (shape->nj * 32 < c->experts) shape->nj *= 2;
-  if (d_logits == nullptr && all >= kManyTokens && c->experts <= 16 * kManyNj && aligned &&
-      (long long)c->experts * size % 16 == 0) {
+  if (d_logits == nullptr && all >= kManyTokens && c->experts <= 16 * kManyNj) {
     RouteShape many = {4, kManyNj};
     while (many.lanes * many.nj < c->experts) many.lanes *= 2;
     if (c->groups == 1 || group_lanes(many.nj) > 0) *shape = many;
