@@ -1,0 +1,175 @@
+"""The workspaces that calls use when they are given none: calls that may be in
+flight together (on two streams, from two threads, in a captured graph and
+beside it) never share one, and a larger call takes none away."""
+import threading
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+a2av = pytest.importorskip("variable_size_all_gb300")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    a2av.build()
+
+
+class _Seen:
+    """A module's functions; where the workspaces of the experts' gradients were."""
+
+    def __init__(self, module):
+        self._module, self.at = module, []
+
+    def __getattr__(self, name):
+        f = getattr(self._module, name)
+
+        def seen(*args):
+            result = f(*args)
+            if name == "expert_matmul_backward" and result is not None:
+                self.at.append(args[14].data_ptr())
+            return result
+        return seen
+
+
+class _Product:
+    """The gradients of a gated product: groups that are no multiples of 64 rows,
+    so that dz and the packed remainders are both in the workspace."""
+
+    def __init__(self, seed, rows=200, W=2, K=2, D=256, N=128):
+        gen = torch.Generator("cuda").manual_seed(seed)
+        new = lambda *shape: torch.randn(shape, device="cuda", generator=gen).bfloat16()
+        self.counts = torch.randint(rows // 2, rows, (W, W * K), generator=gen, device="cuda")
+        held = self.counts.view(W, W, K).sum((0, 2)).tolist()
+        self.x = [new(m, D) for m in held]
+        self.w = [new(K, 2 * N, D) for _ in range(W)]
+        self.dy, self.pre = [new(m, N) for m in held], [new(m, 2 * N) for m in held]
+        self.out = [[torch.empty_like(t) for t in ts] for ts in (self.x, self.w)]
+        self.out.append([torch.empty(K, 2 * N, device="cuda").bfloat16() for _ in range(W)])
+        self.shape = a2av.A2avExpert(K, D, N, a2av.BF16, 3, 1)
+        self.need = a2av.a2av_expert_matmul_workspace_bytes(W, self.shape, sum(held))
+
+    def call(self, eng, **options):
+        eng.expert_matmul_backward(self.x, self.counts, self.w, self.dy, *self.out, pre=self.pre,
+                                   activation="silu", gated=True, **options)
+
+    def results(self):
+        return [t.clone() for ts in self.out for t in ts]
+
+    def expected(self, eng):
+        """By itself, in a workspace of its own."""
+        torch.cuda.synchronize()
+        self.call(eng, workspace=torch.empty(self.need, dtype=torch.uint8, device="cuda"))
+        torch.cuda.synchronize()
+        expected = self.results()
+        for ts in self.out:
+            for t in ts:
+                t.zero_()
+        torch.cuda.synchronize()
+        return expected
+
+
+def _same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def _where(eng, product, **options):
+    """The workspace of a call: the first on a stream makes it, the second has it."""
+    eng._marshal = seen = _Seen(a2av._marshal)
+    product.call(eng, **options)
+    product.call(eng, **options)
+    torch.cuda.synchronize()
+    return seen.at[-1]
+
+
+def test_each_stream_and_each_thread_has_its_own():
+    product = _Product(0)
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    with a2av.A2av(2) as eng:
+        here = _where(eng, product)
+        there = _where(eng, product, stream=side)
+        with torch.cuda.stream(other):
+            third = _where(eng, product)
+        by_address = _where(eng, product, stream=other.cuda_stream)
+        found = []
+        thread = threading.Thread(target=lambda: found.append(_where(eng, product)))
+        thread.start()
+        thread.join()
+        assert len({here, there, third, *found}) == 4
+        assert by_address == third and _where(eng, product) == here
+        assert eng.status() == a2av.OK
+
+
+def test_two_streams_at_a_time():
+    """Calls on two streams, the second's growing meanwhile: as each by itself."""
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    sizes = (150, 400, 1500)
+    products = [[_Product(10 * i + j, rows) for i, rows in enumerate(sizes)] for j in range(2)]
+    with a2av.A2av(2) as eng:
+        expected = [[p.expected(eng) for p in ps] for ps in products]
+        for _ in range(3):
+            for step in range(len(sizes)):
+                for repeat in range(4):
+                    for s, ps in zip(streams, products):
+                        ps[step].call(eng, stream=s)
+        torch.cuda.synchronize()
+        assert eng.status() == a2av.OK
+        for ps, es in zip(products, expected):
+            for p, e in zip(ps, es):
+                assert _same(p.results(), e)
+
+
+def test_two_threads_on_one_stream():
+    products = [_Product(20 + j, 300) for j in range(2)]
+    with a2av.A2av(2) as eng:
+        expected = [p.expected(eng) for p in products]
+        start = threading.Barrier(2)
+
+        def work(p):
+            start.wait()
+            for _ in range(50):
+                p.call(eng)
+
+        threads = [threading.Thread(target=work, args=(p,)) for p in products]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        assert eng.status() == a2av.OK
+        for p, e in zip(products, expected):
+            assert _same(p.results(), e)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_a_captured_call_keeps_its_workspace(given):
+    """Captured, then a larger call and allocations in between: the replay writes
+    its own gradients and nothing of what was allocated since."""
+    small, large = _Product(30, 150), _Product(31, 900)
+    with a2av.A2av(2) as eng:
+        expected, more = small.expected(eng), large.expected(eng)
+        stream = torch.cuda.Stream()
+        for _ in range(2):
+            small.call(eng, stream=stream)  # (a kept workspace is there when the capture begins)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            small.call(eng, **(dict(stream=stream) if given else {}))
+        large.call(eng, stream=stream)
+        with torch.cuda.stream(stream):
+            since = [torch.full((small.need,), 7, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        for ts in small.out:
+            for t in ts:
+                t.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            graph.replay()
+            large.call(eng, stream=stream)  # (beside the replay, on the stream of the capture)
+        torch.cuda.synchronize()
+        assert eng.status() == a2av.OK
+        assert _same(small.results(), expected) and _same(large.results(), more)
+        assert all((t == 7).all() for t in since)

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 from ._build import LIBRARY, build
 
@@ -406,6 +407,14 @@ def _load_marshal():
         return _PlainMarshal
 
 
+class _Kept(threading.local):
+    """The default workspaces of an object's calls, one for each call and stream
+    in each thread, so that calls that may be in flight together share none."""
+
+    def __init__(self):
+        self.buffers = {}
+
+
 class BoundCall:
     """One library call whose arguments were marshalled once (``A2av.bind_run``,
     ``bind_run_multi``, ``bind_dispatch``).  Calling it enqueues the same
@@ -458,6 +467,7 @@ class A2av:
         self._codes = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
         self._int32, self._int64, self._float = torch.int32, torch.int64, torch.float32
         self._counts = ctypes.c_int64 * self.world_size
+        self._kept = _Kept()
         self._room = [ctypes.c_void_p * max(1, self.world_size * n) for n in range(9)]
         if path != PATH_AUTO:
             self._check(a2av_set_path(h, path), "a2av_set_path")
@@ -481,6 +491,35 @@ class A2av:
         if stream is not None or self._raw_stream is None:
             return _address(self._stream(stream))
         return ctypes.c_void_p(self._raw_stream(self._device) or None)
+
+    def _on(self, stream):
+        """``stream`` as torch's current one: what is allocated then is of its order."""
+        import torch
+        if not isinstance(stream, torch.cuda.Stream):
+            queue = self._stream(stream)
+            stream = torch.cuda.ExternalStream(queue) if queue else torch.cuda.default_stream()
+        return torch.cuda.stream(stream)
+
+    def _held(self, what):
+        """The workspace kept for this call on torch's current stream, or None."""
+        import torch
+        if torch.cuda.is_current_stream_capturing():
+            return None
+        return self._kept.buffers.get((what, self._stream(None)))
+
+    def _default_workspace(self, what, need):
+        """The default workspace of a call on torch's current stream: kept for the
+        calls that follow on it, which take their turns.  The allocator hands out
+        one that was too small in that stream's order only.  A call that is being
+        captured takes one from the graph's own memory, which lives as long as the
+        graph does and which no other call is given."""
+        import torch
+        held = self._held(what)
+        if held is None or held.numel() < need:
+            held = torch.empty(need, dtype=torch.uint8, device="cuda")
+            if not torch.cuda.is_current_stream_capturing():
+                self._kept.buffers[what, self._stream(None)] = held
+        return held
 
     def _buffers(self, tensors, what):
         """Pointer array for W buffers; True when one lives in pinned host memory."""
@@ -915,9 +954,14 @@ class A2av:
         a2av_expert_matmul_backward): any of ``d_rows``, ``d_weights`` and
         ``d_bias``, of the shapes of ``rows``, ``weights`` and the bias.
         ``pre`` is what the forward call wrote, needed with an activation or a
-        gate.  ``workspace`` defaults to a buffer the object keeps."""
-        import torch
-        kept = workspace if workspace is not None else getattr(self, "_expert_workspace", None)
+        gate.  ``workspace``: scratch that no other call in flight has; by default
+        the object keeps a buffer for each stream in each thread, and a call under
+        capture takes its own from the graph's memory."""
+        if workspace is None and stream is not None:
+            with self._on(stream):
+                return self.expert_matmul_backward(rows, counts, weights, d_outputs, d_rows, d_weights,
+                                                   d_bias, pre, activation, gated)
+        kept = workspace if workspace is not None else self._held("expert_matmul_backward")
         if self._whole("expert_matmul_backward", stream, rows, counts, weights, d_outputs, d_rows,
                        d_weights, d_bias, pre, _ACTIVATIONS.get(activation), gated, kept,
                        self._entries["expert_matmul_workspace_bytes"]):
@@ -932,10 +976,7 @@ class A2av:
         if activated and pre is None:
             raise ValueError("an activation's gradient needs pre")
         if workspace is None and need:
-            workspace = getattr(self, "_expert_workspace", None)
-            if workspace is None or workspace.numel() < need:
-                workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
-                self._expert_workspace = workspace
+            workspace = self._default_workspace("expert_matmul_backward", need)
         each, by_row = [(K, Z, D)] * W, [(m, D) for m in n]
         (x, w, z, dy, dx, dw, db), arrays = self._lists(
             (rows, dtype, by_row, "rows"), (weights, dtype, each, "weights"),
