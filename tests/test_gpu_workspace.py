@@ -173,3 +173,34 @@ def test_a_captured_call_keeps_its_workspace(given):
         assert eng.status() == a2av.OK
         assert _same(small.results(), expected) and _same(large.results(), more)
         assert all((t == 7).all() for t in since)
+
+
+def test_given_workspaces_are_checked():
+    """What is no contiguous memory of the device is refused, by the method as by
+    the compiled checks; of another type, its bytes count."""
+    product = _Product(40)
+    need = product.need
+    byte = lambda n, device="cuda": torch.zeros(n, dtype=torch.uint8, device=device)
+    with a2av.A2av(2) as eng:
+        expected = product.expected(eng)
+        for module in (a2av._marshal, a2av._PlainMarshal):
+            eng._marshal = module
+            for bad in (byte(need, "cpu"), byte(need, "cpu").pin_memory(), byte(1).expand(need),
+                        byte(2 * need)[::2], byte(need).cpu().numpy(), need):
+                with pytest.raises(ValueError):
+                    product.call(eng, workspace=bad)
+            for small in (byte(need - 1), byte(0), torch.zeros((need - 1) // 4, device="cuda")):
+                with pytest.raises(a2av.A2avError) as e:
+                    product.call(eng, workspace=small)
+                assert e.value.code == a2av.ERR_INVALID_ARG
+            with pytest.raises(a2av.A2avError):
+                product.call(eng, workspace=byte(need + 1)[1:])  # (not on 256 bytes)
+            torch.cuda.synchronize()
+            assert not any(t.any() for ts in product.out for t in ts)
+            for good in (byte(need), torch.zeros((need + 3) // 4, dtype=torch.int32, device="cuda")):
+                product.call(eng, workspace=good)
+                assert _same(product.results(), expected)
+                for ts in product.out:
+                    for t in ts:
+                        t.zero_()
+        assert eng.status() == a2av.OK

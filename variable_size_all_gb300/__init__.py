@@ -521,6 +521,14 @@ class A2av:
                 self._kept.buffers[what, self._stream(None)] = held
         return held
 
+    @staticmethod
+    def _scratch(workspace):
+        """Refuses a workspace whose numel() is not the memory behind its data_ptr()."""
+        import torch
+        if (not isinstance(workspace, torch.Tensor) or not workspace.is_cuda
+                or not workspace.is_contiguous()):
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+
     def _buffers(self, tensors, what):
         """Pointer array for W buffers; True when one lives in pinned host memory."""
         W = self.world_size
@@ -975,7 +983,9 @@ class A2av:
         activated = activation != "none" or bool(gated)
         if activated and pre is None:
             raise ValueError("an activation's gradient needs pre")
-        if workspace is None and need:
+        if workspace is not None:
+            self._scratch(workspace)
+        elif need:
             workspace = self._default_workspace("expert_matmul_backward", need)
         each, by_row = [(K, Z, D)] * W, [(m, D) for m in n]
         (x, w, z, dy, dx, dw, db), arrays = self._lists(
@@ -984,7 +994,8 @@ class A2av:
             (d_outputs, dtype, [(m, N) for m in n], "d_outputs"), (d_rows, dtype, by_row, "d_rows"),
             (d_weights, dtype, each, "d_weights"), (d_bias, dtype, [(K, Z)] * W, "d_bias"))
         args = [self.handle, ctypes.byref(shape), x, self._counts(*n), counts.data_ptr(), w, z, dy, dx,
-                dw, db, workspace.data_ptr() if need else None, workspace.numel() if need else 0,
+                dw, db, workspace.data_ptr() if need else None,
+                workspace.numel() * workspace.element_size() if need else 0,
                 self._queue(stream)]
         self._call("a2av_expert_matmul_backward", args, None, False)
 
