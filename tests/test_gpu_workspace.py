@@ -204,3 +204,105 @@ def test_given_workspaces_are_checked():
                     for t in ts:
                         t.zero_()
         assert eng.status() == a2av.OK
+
+
+class _Dispatch:
+    """A dispatch of several kernels and its return path, rows of 8 bytes to 2 KiB."""
+
+    def __init__(self, seed, tokens, width, W=4, K=4):
+        gen = torch.Generator("cuda").manual_seed(seed)
+        self.W, self.K, self.width, m = W, K, width, 2 * tokens
+        self.rows = [torch.randint(0, 256, (tokens, width), generator=gen, device="cuda").byte() for _ in range(W)]
+        self.src = [torch.arange(tokens, device="cuda").int().repeat_interleave(2) for _ in range(W)]
+        self.keys = [torch.randint(0, W * K, (m,), generator=gen, device="cuda").int() for _ in range(W)]
+        to = torch.stack([torch.bincount(k // K, minlength=W) for k in self.keys])
+        self.out = [torch.zeros(n, width, dtype=torch.uint8, device="cuda") for n in to.sum(0).tolist()]
+        self.pos = [torch.zeros(m, dtype=torch.int64, device="cuda") for _ in range(W)]
+        self.offsets = torch.zeros(W, 2, W, dtype=torch.int64, device="cuda")
+        self.splits = torch.zeros(W, W, dtype=torch.int64, device="cuda")
+        self.items = [torch.zeros(m, width, dtype=torch.uint8, device="cuda") for _ in range(W)]
+
+    def arguments(self):
+        return ((self.rows, self.src, self.keys, self.K, self.out, self.offsets, self.pos, self.width,
+                 self.splits),
+                (self.out, self.splits, self.keys, self.pos, self.K, self.items, self.width))
+
+    def call(self, eng, **options):
+        there, back = self.arguments()
+        eng.dispatch(*there, **options)
+        eng.combine_items(*back, **options)
+
+    def check(self):
+        for r in range(self.W):
+            assert torch.equal(self.items[r], self.rows[r].repeat_interleave(2, 0))
+
+
+@pytest.mark.parametrize("width", [8, 512, 2048])
+def test_dispatches_on_two_streams(width):
+    """Growing dispatches and their return paths on two streams at a time; bound
+    on one stream and called on both; and captured, with a larger one after."""
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    ds = [[_Dispatch(10 * i + j, n, width) for i, n in enumerate((300, 3000, 9000))] for j in range(2)]
+    torch.cuda.synchronize()
+    with a2av.A2av(4) as eng:
+        for _ in range(3):
+            for step in range(3):
+                for s, d in zip(streams, ds):
+                    d[step].call(eng, stream=s)
+        torch.cuda.synchronize()
+        assert eng.status() == a2av.OK
+        for d in ds[0] + ds[1]:
+            d.check()
+        # bound on the first stream; the second's calls go with the second's workspaces
+        bound = []
+        for d in (ds[0][1], ds[1][1]):
+            there, back = d.arguments()
+            bound.append((eng.bind_dispatch(*there, stream=streams[0]),
+                          eng.bind_combine_items(*back, stream=streams[0])))
+            for t in d.items:
+                t.zero_()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for s, calls in zip(streams, bound):
+                for call in calls:
+                    call(s)
+        torch.cuda.synchronize()
+        assert eng.status() == a2av.OK
+        ds[0][1].check()
+        ds[1][1].check()
+        # captured, then a larger one on the same stream and allocations in between
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=streams[0]):
+            ds[0][0].call(eng, stream=streams[0])
+        larger = _Dispatch(77, 20000, width)
+        for t in ds[0][0].items + larger.items:
+            t.zero_()
+        torch.cuda.synchronize()
+        larger.call(eng, stream=streams[0])
+        with torch.cuda.stream(streams[0]):
+            since = [torch.full((1 << 20,), 7, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        for _ in range(2):
+            graph.replay()
+            larger.call(eng, stream=streams[0])
+        torch.cuda.synchronize()
+        assert eng.status() == a2av.OK
+        ds[0][0].check()
+        larger.check()
+        assert all((t == 7).all() for t in since)
+
+
+def test_given_workspaces_of_a_dispatch_are_checked():
+    d = _Dispatch(5, 100, 64)
+    need = a2av.a2av_dispatch_workspace_bytes(4, 4, 200)
+    there, back = d.arguments()
+    with a2av.A2av(4) as eng:
+        for bad in (torch.zeros(need, dtype=torch.uint8), torch.zeros(1, dtype=torch.uint8, device="cuda").expand(need),
+                    need):
+            with pytest.raises(ValueError):
+                eng.dispatch(*there, workspace=bad)
+            with pytest.raises(ValueError):
+                eng.combine_items(*back, workspace=bad)
+        d.call(eng)
+        assert eng.status() == a2av.OK
+    d.check()

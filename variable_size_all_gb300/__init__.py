@@ -422,17 +422,27 @@ class BoundCall:
     the same buffers: the tensors must stay alive and keep their storage, while
     the device data they hold (splits, keys, rows) may change between calls.
     It skips the per-call Python checks and pointer gathering, which cost more
-    host time than a small exchange takes on the device."""
+    host time than a small exchange takes on the device.  Bound without a
+    workspace, it uses that of the stream's other calls: bind it with one of its
+    own if a graph that captures it is to be replayed beside them."""
 
-    def __init__(self, engine, fn, what, args, stream_index, keep):
+    def __init__(self, engine, fn, what, args, stream_index, keep, workspace=None):
+        # workspace: of a call that was given none, its place in args, its name and its size
         self._engine, self._fn, self._what = engine, fn, what
-        self._args, self._si, self._keep = tuple(args), stream_index, keep
+        self._args, self._si, self._keep, self._ws = tuple(args), stream_index, keep, workspace
 
     def __call__(self, stream=None):
         args = self._args
         if stream is not None:
             args = list(args)
-            args[self._si] = ctypes.c_void_p(A2av._stream(stream) or None)
+            queue = ctypes.c_void_p(A2av._stream(stream) or None)
+            if self._ws is not None and queue.value != args[self._si].value:
+                # (another stream than the workspace's: the one of that stream)
+                i, name, need = self._ws
+                with self._engine._on(stream):
+                    held = self._engine._default_workspace(name, need)
+                args[i], args[i + 1] = ctypes.c_void_p(held.data_ptr()), held.numel()
+            args[self._si] = queue
         rc = self._fn(*args)
         if rc != OK:
             raise A2avError(rc, self._what)
@@ -644,9 +654,15 @@ class A2av:
         ``row_bytes``); ``src_rows[r]`` / ``keys[r]``: int32 CUDA tensors, one
         entry per item; ``sorted_pos[r]``: int64 CUDA tensor receiving each
         item's position in key order; ``in_splits``: optional int64 [W, W]
-        receiving the split matrix.  ``workspace`` defaults to a buffer the
-        object keeps (torch allocation, sized by the largest item count)."""
+        receiving the split matrix.  ``workspace``: scratch that no other call in
+        flight has (sized by the largest item count); by default the object keeps
+        a buffer for each stream in each thread, and a call under capture takes
+        its own from the graph's memory."""
         import torch
+        if workspace is None and stream is not None:
+            with self._on(stream):
+                return self.dispatch(rows, src_rows, keys, keys_per_peer, outputs, out_splits_offsets,
+                                     sorted_pos, row_bytes, in_splits, _bind=_bind)
         W = self.world_size
         for name, ts, dt in (("src_rows", src_rows, torch.int32), ("keys", keys, torch.int32),
                              ("sorted_pos", sorted_pos, torch.int64)):
@@ -672,12 +688,12 @@ class A2av:
         need = a2av_dispatch_workspace_bytes(W, keys_per_peer, max(items))
         if need < 0:
             raise A2avError(ERR_UNSUPPORTED, "a2av_dispatch_workspace_bytes")
-        if workspace is None:
-            ws = getattr(self, "_workspace", None)
-            if ws is None or ws.numel() < need:
-                ws = torch.empty(need, dtype=torch.uint8, device="cuda")
-                self._workspace = ws
-            workspace = ws
+        own = None
+        if workspace is not None:
+            self._scratch(workspace)
+        else:
+            own = (12, "dispatch", need)
+            workspace = self._default_workspace("dispatch", need)
         n_rows = [0 if t is None else t.numel() // int(row_bytes) for t in rows]
         ptr = lambda ts: [0 if t is None or t.numel() == 0 else t.data_ptr() for t in ts]
         rows_arr, host_rows = self._buffers(rows, "rows")
@@ -694,7 +710,7 @@ class A2av:
         if _bind:
             keep = (rows, src_rows, keys, outputs, out_splits_offsets, sorted_pos, in_splits,
                     workspace)
-            return BoundCall(self, load().a2av_dispatch, "a2av_dispatch", args, 14, keep)
+            return BoundCall(self, load().a2av_dispatch, "a2av_dispatch", args, 14, keep, own)
         self._check(load().a2av_dispatch(*args), "a2av_dispatch")
 
     def bind_dispatch(self, rows, src_rows, keys, keys_per_peer: int, outputs,
@@ -716,8 +732,12 @@ class A2av:
         """The fused combine (see include/a2av.h, a2av_combine_items): every
         item's row from the peers' dispatch-layout buffers back to row i of
         ``item_out[r]``.  ``in_splits``, ``keys`` and ``sorted_pos`` as a
-        dispatch took or wrote them."""
+        dispatch took or wrote them.  ``workspace`` as in ``dispatch``."""
         import torch
+        if workspace is None and stream is not None:
+            with self._on(stream):
+                return self.combine_items(peers, in_splits, keys, sorted_pos, keys_per_peer, item_out,
+                                          row_bytes, _bind=_bind)
         W = self.world_size
         sp = self._matrix(in_splits, (W, W), "in_splits")
         for name, ts, dt in (("keys", keys, torch.int32), ("sorted_pos", sorted_pos, torch.int64)):
@@ -733,12 +753,12 @@ class A2av:
         if any((0 if t is None else t.numel()) < m * int(row_bytes)
                for t, m in zip(item_out, items)):
             raise ValueError("item_out[r] must hold one row per item of rank r")
-        if workspace is None:
-            ws = getattr(self, "_combine_workspace", None)
-            if ws is None:
-                ws = torch.empty(COMBINE_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
-                self._combine_workspace = ws
-            workspace = ws
+        own = None
+        if workspace is not None:
+            self._scratch(workspace)
+        else:
+            own = (9, "combine_items", COMBINE_WORKSPACE_BYTES)
+            workspace = self._default_workspace("combine_items", COMBINE_WORKSPACE_BYTES)
         peer_arr, host_p = self._buffers(peers, "peers")
         out_arr, host_o = self._buffers(item_out, "item_out")
         if host_p or host_o:
@@ -750,7 +770,7 @@ class A2av:
                 int(workspace.numel()), ctypes.c_void_p(self._stream(stream) or None)]
         if _bind:
             keep = (peers, in_splits, keys, sorted_pos, item_out, workspace)
-            return BoundCall(self, load().a2av_combine_items, "a2av_combine_items", args, 11, keep)
+            return BoundCall(self, load().a2av_combine_items, "a2av_combine_items", args, 11, keep, own)
         self._check(load().a2av_combine_items(*args), "a2av_combine_items")
 
     # ------------------------------------------- the MoE layer's operators --
