@@ -144,7 +144,8 @@ typedef struct {
  * group (r, e) has counts[r][p * K + e] rows, which follow the group before.
  * One rank with one expert is an ordinary linear layer.  Products are summed
  * in 32 bits; bias, activation and residual are applied in 32 bits and the
- * result is rounded once.  Rows of NaN stay within their own results.
+ * result is rounded once.  Rows of NaN stay within their own results.  An
+ * activation at an infinity, and its slope there, is the limit.
  *
  *  rows_ptrs          HOST array of W: peer p's x, [rows_per_peer[p]][D].  Read only.
  *  rows_per_peer      HOST int64 [W], up to 2^31 - 1 together: the rows each peer's buffers hold.

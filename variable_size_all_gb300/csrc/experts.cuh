@@ -232,14 +232,20 @@ __device__ __forceinline__ float reciprocal_fast(float x) {
 }
 constexpr float kLog2e = 1.44269504f;
 
+// Where exp(-z^2 / 2) and exp(-|z|) are 0 in 32 bits: beyond, a product with them
+// takes this in place of |z|, or it would be infinity times 0 where |z| is infinite
+// (a pre-activation out of 16 bits' range is saved as an infinity).  min and max
+// drop a NaN, so each result has a factor in which z has not been through them.
+constexpr float kFar = 16.0f, kFarExp = 128.0f;
+
 // The normal distribution's upper tail at |z|, from Abramowitz and Stegun's
 // rational approximation of the error function, 7.1.26 (1.5e-7 absolute), with
-// *density = exp(-z^2 / 2).  Kept as a tail, it costs no cancellation for
+// *density = exp(-z^2 / 2); x is min(|z|, kFar).  Kept as a tail, it costs no cancellation for
 // negative z, and a third of what the library's error function does, which made
 // the epilogue of a short contraction take longer than its products (4864 rows,
 // 2048 -> 7168: 100 us with erff, 86 with SiLU).
-__device__ __forceinline__ float normal_tail(float z, float* density) {
-  const float t = reciprocal_fast(fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.0f));
+__device__ __forceinline__ float normal_tail(float z, float x, float* density) {
+  const float t = reciprocal_fast(fmaf(0.3275911f * 0.70710678f, x, 1.0f));
   *density = exp2_fast(z * z * (-0.5f * kLog2e));
   float p = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
   p = fmaf(t, p, 0.5f * 1.421413741f);
@@ -253,10 +259,11 @@ __device__ __forceinline__ float act_fn(int a, float z) {
     case A2AV_ACT_RELU: return z < 0.0f ? 0.0f : z;  // (a NaN stays)
     case A2AV_ACT_GELU: {
       float density;
-      const float low = z * normal_tail(z, &density);
-      return z < 0.0f ? low : z - low;
+      const float x = fminf(fabsf(z), kFar);
+      return (z < 0.0f ? 0.0f : z) - x * normal_tail(z, x, &density);
     }
-    case A2AV_ACT_SILU: return z * reciprocal_fast(1.0f + exp2_fast(z * -kLog2e));
+    case A2AV_ACT_SILU:
+      return fmaxf(z, -kFarExp) * reciprocal_fast(1.0f + exp2_fast(z * -kLog2e));
     default: return z;
   }
 }
@@ -266,12 +273,14 @@ __device__ __forceinline__ float act_slope(int a, float z) {
     case A2AV_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
     case A2AV_ACT_GELU: {
       float density;
-      const float q = normal_tail(z, &density);
-      return fmaf(z * 0.39894228f, density, z < 0.0f ? q : 1.0f - q);
+      const float x = fminf(fabsf(z), kFar);
+      const float q = normal_tail(z, x, &density);  // the slope at -|z|:
+      const float low = fmaf(x * -0.39894228f, density, q);
+      return z < 0.0f ? low : 1.0f - low;
     }
     case A2AV_ACT_SILU: {
       const float s = reciprocal_fast(1.0f + exp2_fast(z * -kLog2e));
-      return s * fmaf(z, 1.0f - s, 1.0f);
+      return s * fmaf(fminf(fmaxf(z, -kFarExp), kFarExp), 1.0f - s, 1.0f);
     }
     default: return 1.0f;
   }
