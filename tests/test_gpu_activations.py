@@ -71,3 +71,28 @@ def test_infinities_and_nan(name, size, gated, dtype):
     assert np.array_equal(got[:size][known], slope[known], equal_nan=True)
     if gated:
         assert np.array_equal(got[size:], up, equal_nan=True)
+
+
+def _exact(name, x):
+    """(act, slope, the magnitude of the slope's terms) in 64 bits, without cancellation."""
+    phi = np.array([0.5 * math.erfc(-v / math.sqrt(2)) for v in x])
+    dens = np.exp(-x * x / 2) / math.sqrt(2 * math.pi)
+    if name == "gelu":
+        return x * phi, phi + x * dens, phi + np.abs(x) * dens
+    s, c = 1 / (1 + np.exp(-x)), 1 / (1 + np.exp(x))
+    return x * s, s * (1 + x * c), s * (1 + np.abs(x) * c)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("name", ["gelu", "silu"])
+def test_small_results_are_as_exact_as_large_ones(name, dtype):
+    """Relative error over the whole range: the rounding to the type, and 2^-16 for
+    the arithmetic before it.  (The exponential's argument, at most z^2 / 2 log2(e)
+    = 75 for the z below and rounded three times, is the most of that: 75 * 3 *
+    2^-24 * ln 2 = 2^-17.)"""
+    z = torch.cat([torch.linspace(-10.2, 10.2, 4096), torch.linspace(-1, 1, 512),
+                   torch.logspace(-6, 0, 256, 10.0), -torch.logspace(-6, 0, 256, 10.0)])
+    z = z.to(moe.DTYPES[dtype]).cuda()
+    act, slope, size = _exact(name, z.double().cpu().numpy())
+    moe.close(_forward(name, z), act, 2.0 ** -16 * np.abs(act), dtype, name)
+    moe.close(_slope(name, z), slope, 2.0 ** -16 * size, dtype, f"{name}'s slope")
