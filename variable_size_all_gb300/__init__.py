@@ -1019,16 +1019,23 @@ class A2av:
                 self._queue(stream)]
         self._call("a2av_expert_matmul_backward", args, None, False)
 
-    def _weighted_args(self, in_splits, keys, sorted_pos, keys_per_peer, token_rows, name, peers):
+    def _weighted_args(self, in_splits, keys, sorted_pos, keys_per_peer, token_rows, name, peers,
+                       by_choice):
         """What both directions of the weighted combine share: K, k, H, the type
         and its code, the rows of the ranks and of the peers' buffers (lists of
-        which are in ``peers``, as (tensors or None, name))."""
+        which are in ``peers``, as (tensors or None, name)).  k is the number of a
+        token's items; without any token, the width that keys or the lists
+        ``by_choice`` (weights) have."""
         self._matrix(in_splits, (self.world_size, self.world_size), "in_splits")
         n, H = self._tokens(token_rows, name)
         dtype, code = self._dtype(token_rows, name, (F32, BF16, F16))
         sizes = [self._marshal.sizes(ts) or [0 if t is None else t.numel() for t in ts]
                  for ts in (keys, sorted_pos)]
-        k = next((m // T for m, T in zip(sizes[0], n) if T), 1) or 1
+        k = next((m // T for m, T in zip(sizes[0], n) if T), None)
+        if k is None:
+            k = next((ts[0].shape[1] for ts in (keys, *by_choice)
+                      if ts is not None and ts[0] is not None and ts[0].dim() == 2), 1)
+        k = k or 1
         items = [T * k for T in n]
         for m, what in zip(sizes, ("keys", "sorted_pos")):
             if m != items:
@@ -1063,7 +1070,8 @@ class A2av:
                                      keys_per_peer, weights, outputs, residual):
             return
         K, k, H, dtype, code, n, held = self._weighted_args(
-            in_splits, keys, sorted_pos, keys_per_peer, outputs, "outputs", ((peers, "peers"),))
+            in_splits, keys, sorted_pos, keys_per_peer, outputs, "outputs", ((peers, "peers"),),
+            (weights,))
         shapes = [(m, H) for m in n]
         (x, ka, pa, w, r, y), arrays = self._lists(
             (peers, dtype, None, "peers"), (keys, self._int32, None, "keys"),
@@ -1094,7 +1102,7 @@ class A2av:
             return
         K, k, H, dtype, code, n, held = self._weighted_args(
             in_splits, keys, sorted_pos, keys_per_peer, d_outputs, "d_outputs",
-            ((peers, "peers"), (d_peers, "d_peers")))
+            ((peers, "peers"), (d_peers, "d_peers")), (weights, d_weights))
         shapes = [(m, k) for m in n]
         (x, ka, pa, w, dy, dx, dw), arrays = self._lists(
             (peers, dtype, None, "peers"), (keys, self._int32, None, "keys"),

@@ -224,6 +224,14 @@ bool type_of(PyObject* list, bool f32, at::ScalarType* type, int* code) {
   return *code != A2AV_F32 || (f32 && *type == at::kFloat);
 }
 
+// The second dimension of a list's first tensor; 0 where it has none.
+int64_t width_of(PyObject* list) {
+  PyObject** items = nullptr;
+  Py_ssize_t n = 0;
+  const at::Tensor* t = items_of(list, &items, &n) && n > 0 ? tensor_of(items[0]) : nullptr;
+  return t != nullptr && t->dim() == 2 ? t->size(1) : 0;
+}
+
 bool has_sizes(const at::Tensor& t, int64_t a, int64_t b) {
   return t.dim() == 2 && t.size(0) == a && t.size(1) == b;
 }
@@ -443,7 +451,7 @@ struct Weighted {
   bool has_weights, has_peers, has_d_peers;
 
   bool take_all(PyObject* p, PyObject* s, PyObject* ks, PyObject* ps, PyObject* per, PyObject* ws,
-                PyObject* rows, PyObject* dp) {
+                PyObject* rows, PyObject* dp, PyObject* dw) {
     H = 0;
     if (!type_of(rows, true, &type, &dtype) ||
         !take_any_rows(rows, c.W, type, token_rows, tokens, &H) ||
@@ -455,6 +463,9 @@ struct Weighted {
       return t.numel() == tokens[i] * (items < 0 ? 0 : items);
     };
     if (!take(ks, c.W, at::kInt, keys, fits)) return false;
+    // (no token on any rank: the width that the keys or the weights have)
+    for (PyObject* list : {ks, ws, dw})
+      if (items < 0 && width_of(list) > 0) items = width_of(list);
     if (items == 0 || items > INT_MAX) return false;
     k = items < 0 ? 1 : (int)items;
     if (!take(ps, c.W, at::kLong, pos, fits)) return false;
@@ -478,7 +489,8 @@ PyObject* combine_weighted(PyObject*, PyObject* const* args, Py_ssize_t n) {
       n, 12,
       [&] {
         return call_of(args, &m.c) && args[4] != Py_None &&
-               m.take_all(args[4], args[5], args[6], args[7], args[8], args[9], args[10], Py_None) &&
+               m.take_all(args[4], args[5], args[6], args[7], args[8], args[9], args[10], Py_None,
+                          Py_None) &&
                (args[11] == Py_None ||
                 take_rows(args[11], m.c.W, m.type, residual, m.tokens, m.H));
       },
@@ -500,7 +512,8 @@ PyObject* combine_weighted_backward(PyObject*, PyObject* const* args, Py_ssize_t
       n, 13,
       [&] {
         return call_of(args, &m.c) &&
-               m.take_all(args[4], args[5], args[6], args[7], args[8], args[9], args[10], args[11]) &&
+               m.take_all(args[4], args[5], args[6], args[7], args[8], args[9], args[10], args[11],
+                          args[12]) &&
                (args[12] == Py_None ||
                 take_rows(args[12], m.c.W, at::kFloat, d_weights, m.tokens, m.k));
       },
