@@ -71,7 +71,8 @@ typedef struct {
  *   groups > 1: the top_groups groups of the highest scores stay, c = -inf in the others
  *   key[j]    = the expert of the j-th largest c (ties: the lowest index)
  *   weight[j] = s[key[j]], renormalised (divided by sum_j s[key[j]]) if asked, * scale
- * The bias moves choices only, never weights.
+ * The bias moves choices only, never weights.  A token's keys and weights are the
+ * same, to the bit, whatever other tokens are routed with it.
  *
  * Special values: a NaN choice counts as -inf, so the k keys are always valid
  * and distinct.  A logit of -inf is an expert that is not available: its score

@@ -66,6 +66,37 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
+// The sum over a token's experts, NJ a lane: the binary tree of neighbours over
+// their numbers, which is the same however many lanes and experts a lane share it
+// out (what is past the last expert adds 0).  So a token gets the same scores in
+// a batch of any size.
+template <int L, int NJ>
+__device__ __forceinline__ float experts_sum(float (&v)[NJ]) {
+#pragma unroll
+  for (int n = NJ / 2; n > 0; n /= 2)
+#pragma unroll
+    for (int j = 0; j < n; ++j) v[j] = __fadd_rn(v[2 * j], v[2 * j + 1]);
+  float sum = v[0];
+#pragma unroll
+  for (int o = 1; o < L; o *= 2) sum = __fadd_rn(sum, __shfl_xor_sync(kAll, sum, o));
+  return sum;
+}
+
+// The same for 32 choices, choice lane + L s in v[s]: the tree that joins those 16
+// apart first, then 8, ...
+template <int L, int N>
+__device__ __forceinline__ float choices_sum(float (&v)[N]) {
+  static_assert(L * N == 32, "32 choices");
+#pragma unroll
+  for (int n = N / 2; n > 0; n /= 2)
+#pragma unroll
+    for (int s = 0; s < n; ++s) v[s] = __fadd_rn(v[s], v[s + n]);
+  float sum = v[0];
+#pragma unroll
+  for (int o = L / 2; o > 0; o /= 2) sum = __fadd_rn(sum, __shfl_xor_sync(kAll, sum, o));
+  return sum;
+}
+
 template <int L = 32>
 __device__ __forceinline__ float lanes_max(float v) {
 #pragma unroll
@@ -254,10 +285,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, L < 32 ? 4 : 1) route_kernel
 #pragma unroll
       for (int j = 1; j < NJ; ++j) m = fmaxf(m, c[j]);
       m = lanes_max<L>(m);
-      total = 0.0f;
+      float e[NJ];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) total += exp_below(c[j], m);
-      total = lanes_sum<L>(total);
+      for (int j = 0; j < NJ; ++j) e[j] = exp_below(c[j], m);
+      total = experts_sum<L>(e);
     }
     if (!softmax || !by_logit) {
 #pragma unroll
@@ -344,7 +375,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, L < 32 ? 4 : 1) route_kernel
     }
     __syncwarp();
     // weights, from the chosen logits alone where they are renormalised
-    float w[kTokens];
+    float w[kTokens], part[kTokens];
     float top = -INFINITY, sum = 0.0f;
 #pragma unroll
     for (int s = 0; s < kTokens; ++s) {
@@ -354,15 +385,17 @@ __global__ void __launch_bounds__(32 * kRouteWarps, L < 32 ? 4 : 1) route_kernel
     }
     if (softmax && P.renormalise) top = lanes_max<L>(top);
 #pragma unroll
-    for (int s = 0; s < kTokens; ++s)
+    for (int s = 0; s < kTokens; ++s) {
+      part[s] = 0.0f;
       if (sl + L * s < k) {
         w[s] = !softmax             ? sigmoid(w[s])
                : P.renormalise      ? exp_below(w[s], top)
                : m == -INFINITY     ? 0.0f
                                     : expf(w[s] - m) / total;
-        sum += w[s];
+        part[s] = w[s];
       }
-    if (P.renormalise) sum = lanes_sum<L>(sum);
+    }
+    if (P.renormalise) sum = choices_sum<L>(part);
 #pragma unroll
     for (int s = 0; s < kTokens; ++s) {
       const int i = sl + L * s;
