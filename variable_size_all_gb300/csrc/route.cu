@@ -497,7 +497,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
             const float dot = lanes_sum<32>(lane < k ? g * s : 0.0f);
             ds = sum == 0.0f ? 0.0f : (g - dot / sum) / sum;
           }
-          onto = ds * s * (1.0f - s);
+          // (1 - s as sigmoid(-x): of a score near 1 a difference would leave nothing)
+          onto = lane < k ? ds * s * sigmoid(-xs) : 0.0f;
         }
         if (lane < k) scatter[warp][key] = onto;
         __syncwarp();
