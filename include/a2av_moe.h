@@ -81,7 +81,7 @@ typedef struct {
  * through the arithmetic.
  *
  *  logits_ptrs        HOST array of W device pointers: rank r's [tokens_per_rank[r]][E].
- *  tokens_per_rank    HOST int64 [W], 0 .. 2^31 / k.
+ *  tokens_per_rank    HOST int64 [W], 0 .. (2^31 - 1) / k.
  *  bias_dev           DEVICE float [E] or NULL.
  *  key_ptrs           HOST array of W: int32 [tokens][k], written; a2av_dispatch's keys.
  *  weight_ptrs        HOST array of W: float [tokens][k], written.
@@ -90,7 +90,7 @@ typedef struct {
  *
  * Host errors: A2AV_ERR_INVALID_ARG for NULL or misaligned pointers of ranks that have
  * tokens and for values outside the ranges above; A2AV_ERR_UNSUPPORTED for more
- * experts, choices or groups than the limits, and for counts above 2^31.
+ * experts, choices or groups than the limits, and for more tokens.
  */
 int a2av_route(a2av_handle *h, const a2av_route_t *route, const void *const *logits_ptrs,
                const int64_t *tokens_per_rank, const float *bias_dev, int32_t *const *key_ptrs,

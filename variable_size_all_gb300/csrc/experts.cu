@@ -106,11 +106,11 @@ __global__ void __launch_bounds__(kPlainThreads)
     for (int r = 0; r < W; ++r) {
       int rows;
       const long long first = find_group(P.g, g, (p * W + r) * K + e, &rows);
-      for (int m0 = 0; m0 < rows; m0 += kDepth) {
+      for (unsigned m0 = 0; m0 < (unsigned)rows; m0 += kDepth) {  // (up to 2^31 - 1 rows)
         for (int i = tid; i < kTile * kDepth; i += kPlainThreads) {
           const int c = i % kTile, m = i / kTile;
           const long long row = first + m0 + m;
-          const bool in = m0 + m < rows;
+          const bool in = m0 + m < (unsigned)rows;
           zs[m][c] = in && z0 + c < P.Z ? to_float(dz[row * P.Z + z0 + c]) : 0.0f;
           xs[m][c] = in && d0 + c < P.D ? to_float(x[row * P.D + d0 + c]) : 0.0f;
         }
@@ -149,10 +149,11 @@ __global__ void __launch_bounds__(256)
   using Q = Piece<T, N>;
   using V = typename Q::Raw;
   const int nv = (int)(P.N / N), lane = threadIdx.x & 31;
-  const int warps = gridDim.x * (blockDim.x / 32), all = g.peer_base[P.g.W];
+  // (unsigned: up to 2^31 - 1 rows, and a stride past them)
+  const unsigned warps = gridDim.x * (blockDim.x / 32), all = g.peer_base[P.g.W];
   const RowParts split(all, warps, nv);
   int p = 0;
-  for (int unit = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; unit < all * split.parts;
+  for (unsigned unit = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; unit < all * split.parts;
        unit += warps) {
     const int at = unit / split.parts;
     int from, to;
@@ -215,15 +216,15 @@ __global__ void __launch_bounds__(kBiasThreads)
       if (z >= P.Z) continue;
       const T* from = static_cast<const T*>(P.dy[p]) + first * P.Z + z;
       constexpr int kAhead = 4;  // loads in flight
-      for (int m = team; m < rows; m += kAhead * kBiasRows) {
+      for (unsigned m = team; m < (unsigned)rows; m += kAhead * kBiasRows) {  // (up to 2^31 - 1)
         V v[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
-          if (m + u * kBiasRows < rows)
+          if (m + u * kBiasRows < (unsigned)rows)
             v[u] = *reinterpret_cast<const V*>(from + (long long)(m + u * kBiasRows) * P.Z);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
-          if (m + u * kBiasRows < rows) {
+          if (m + u * kBiasRows < (unsigned)rows) {
             float f[N];
             Q::unpack(v[u], f);
 #pragma unroll

@@ -121,6 +121,11 @@ __device__ __forceinline__ long long tile_of(unsigned i, unsigned pair, unsigned
 // read by this many pairs at about the same time.
 constexpr int kBand = 8;
 
+// Granules of a group of n rows (n up to 2^31 - 1).
+__device__ __forceinline__ int granules_of(int n) {
+  return (int)(((unsigned)n + kGranule - 1) / kGranule);
+}
+
 // Exclusive prefix sum of one value a thread over the block.
 __device__ __forceinline__ int block_prefix(int x, GroupTable& g) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -149,7 +154,7 @@ __device__ void build_tiles(const GroupParams& G, GroupTable& g, TileTable& tt, 
     for (int r = 0; r < G.W; ++r) {
       int rows;
       find_group(G, g, (p * G.W + r) * G.K + e, &rows);
-      granules += (rows + kGranule - 1) / kGranule;
+      granules += granules_of(rows);
     }
     return (granules + kTileGranules - 1) / kTileGranules;
   };
@@ -197,7 +202,7 @@ __device__ __forceinline__ void describe_tile(const GroupParams& G, const GroupT
   int rows = 0;
   long long first = 0;
   if (lane < G.W) first = find_group(G, g, (p * G.W + lane) * G.K + e, &rows);
-  const int granules = (rows + kGranule - 1) / kGranule;
+  const int granules = granules_of(rows);
   int inc = granules;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -216,9 +221,10 @@ __device__ __forceinline__ void describe_tile(const GroupParams& G, const GroupT
   int r = 0;
   for (int i = 0; i < G.W - 1; ++i)
     if (__shfl_sync(kAll, inc, i) <= mine) r = i + 1;
-  const int before = __shfl_sync(kAll, inc - granules, r) * kGranule;
-  const int n = __shfl_sync(kAll, rows, r) - (mine * kGranule - before);
-  const long long row = __shfl_sync(kAll, first, r) + (mine * kGranule - before);
+  // rows of the group before this granule
+  const int within = (int)((unsigned)(mine - __shfl_sync(kAll, inc - granules, r)) * kGranule);
+  const int n = __shfl_sync(kAll, rows, r) - within;
+  const long long row = __shfl_sync(kAll, first, r) + within;
   slot.row[lane] = (int)row;
   slot.n[lane] = lane < each && mine < total ? min(n, kGranule) : 0;
   if (lane == 0) {
@@ -393,7 +399,7 @@ __device__ __forceinline__ void plan_copies(Slot& slot, uint32_t rank) {
   for (int j = j0; j < j1;) {
     const int row = slot.row[j];
     int run = 1;
-    while (j + run < j1 && slot.row[j + run] == row + kGranule * run) ++run;
+    while (j + run < j1 && (unsigned)slot.row[j + run] == (unsigned)row + kGranule * run) ++run;
     int box = 31 - __clz(run);
     if (j + run == j1 && (1 << box) < run && j - j0 + (2 << box) <= kTileGranules / 2) ++box;
     c.row[n] = row;

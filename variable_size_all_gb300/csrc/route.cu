@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps, L < 32 ? 4 : 1) route_kernel
   const bool by_logit = P.score == A2AV_SCORE_SOFTMAX && P.bias == nullptr && P.group_top == 1;
   const bool softmax = P.score == A2AV_SCORE_SOFTMAX;
   const bool need_sum = softmax && (!by_logit || !P.renormalise);
-  const int n = P.tokens[r];
+  // (unsigned: a stride past 2^31 - 1 tokens fits)
+  const unsigned n = P.tokens[r];
   // the experts of this lane (the first `present` of its NJ; -inf where a group
   // that is dropped has one, NaN where there is none)
   const int present = E - sl * NJ;
@@ -272,10 +273,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, L < 32 ? 4 : 1) route_kernel
   Candidate* list = lists[warp * kTokens + sub];
   float* row_c = choices[warp * kTokens + sub];
   int* chosen = picks[warp * kTokens + sub];
-  for (int t0 = (blockIdx.x * kRouteWarps + warp) * kTokens; t0 < n;
+  for (unsigned t0 = (blockIdx.x * kRouteWarps + warp) * kTokens; t0 < n;
        t0 += gridDim.x * kRouteWarps * kTokens) {
     const bool live = t0 + sub < n;
-    const int t = live ? t0 + sub : n - 1;  // (lanes without a token repeat the last one)
+    const unsigned t = live ? t0 + sub : n - 1;  // (lanes without a token repeat the last one)
     const T* row = static_cast<const T*>(P.logits[r]) + (long long)t * E;
     float c[NJ];  // the logits, then the choices
     load_logits<T, NJ, kVec>(row, E, sl, c);
@@ -436,8 +437,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
   const int E = P.E, k = P.k;
   const bool softmax = P.score == A2AV_SCORE_SOFTMAX;
   const bool dense = softmax && !P.renormalise;
-  const int n = P.tokens[r];
-  for (int t = blockIdx.x * kRouteWarps + warp; t < n; t += gridDim.x * kRouteWarps) {
+  const unsigned n = P.tokens[r];  // (unsigned: as in the router)
+  for (unsigned t = blockIdx.x * kRouteWarps + warp; t < n; t += gridDim.x * kRouteWarps) {
     const T* row = static_cast<const T*>(P.logits[r]) + (long long)t * E;
     const long long i0 = (long long)t * k;
     int key = 0;
@@ -671,7 +672,7 @@ int route_params(a2av_handle* h, const a2av_route_t* c, const void* const* logit
 // against 55 us at 65,536 tokens over 256 experts).
 int route_blocks(const a2av_handle* h, int most, int lanes) {
   const int tokens = kRouteWarps * 32 / lanes;
-  const int all = (most + tokens - 1) / tokens;
+  const int all = (most - 1) / tokens + 1;  // (a rank without tokens: 1)
   const int fit = ((lanes < 32 ? 4 : 8) * h->sms + h->W - 1) / h->W;
   return all < 1 ? 1 : all < fit ? all : fit;
 }
