@@ -160,7 +160,9 @@ typedef struct {
  *                     (what the backward pass needs of an activation), or NULL.
  *
  * Device errors: A2AV_ERR_BAD_SPLITS when a count is negative or a peer's
- * groups have more rows than rows_per_peer: nothing is written.  Host errors:
+ * groups have more rows than rows_per_peer: nothing is written.  A2AV_ERR_TIMEOUT
+ * when a copy or a product has not come for about a second: results are not
+ * complete.  (A call's own length has no limit.)  Host errors:
  * A2AV_ERR_INVALID_ARG, A2AV_ERR_UNSUPPORTED (W * K or rows above the limits,
  * D, N or Z above 2^24), A2AV_ERR_CUDA.
  */
@@ -198,6 +200,7 @@ int64_t a2av_expert_matmul_workspace_bytes(int world_size, const a2av_expert_t *
  *  workspace          DEVICE scratch, 256-byte aligned, at least
  *                     a2av_expert_matmul_workspace_bytes(W, shape, sum of rows_per_peer),
  *                     not shared with a call in flight (NULL for no rows at all).
+ * Errors are those of the forward call.
  */
 int a2av_expert_matmul_backward(a2av_handle *h, const a2av_expert_t *shape,
                                 const void *const *rows_ptrs, const int64_t *rows_per_peer,

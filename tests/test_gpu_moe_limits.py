@@ -90,3 +90,28 @@ def test_experts_forward_and_rows_gradient(features):
         _check(y, lambda v: 2 * v.clamp_min(0))
     del x, y
     torch.cuda.empty_cache()
+
+
+def test_a_contraction_of_more_than_a_second():
+    """One expert's gradient over 2^30 rows and some: one tile, on one pair of CTAs,
+    whose other waits are limited.  Products of signs: the sums are whole numbers
+    that 32 bits hold exactly, so that the result is exact to its one rounding."""
+    rows, D, N = (1 << 30) + 1001, 8, 8
+    gen = torch.Generator("cuda").manual_seed(3)
+    signs = lambda n: torch.empty(rows, n, dtype=torch.bfloat16, device="cuda").random_(
+        0, 2, generator=gen).mul_(2).sub_(1)
+    x, dy = signs(D), signs(N)
+    w = torch.empty(1, N, D, dtype=torch.bfloat16, device="cuda")
+    d_w = torch.zeros_like(w)
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    with a2av.A2av(1) as eng:
+        counts = torch.tensor([[rows]], device="cuda")
+        begin.record()
+        eng.expert_matmul_backward([x], counts, [w], [dy], d_weights=[d_w])
+        end.record()
+        assert eng.status() == a2av.OK
+    assert begin.elapsed_time(end) > 1500, "not longer than a limited wait"
+    ref = torch.zeros(N, D, dtype=torch.float64, device="cuda")
+    for i in range(0, rows, 1 << 22):  # (sums of at most 2^22 signs: exact in 32 bits)
+        ref += (dy[i:i + (1 << 22)].float().T @ x[i:i + (1 << 22)].float()).double()
+    assert ref.abs().max() < 2 ** 24 and torch.equal(d_w[0], ref.bfloat16())

@@ -442,6 +442,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const uint32_t base = (smem_addr(dynamic) + 1023) & ~1023u;
+  const uint32_t ring = smem_addr(&b.empty[0]);
   constexpr int kTileF = kGated ? 128 : 256;  // features of the result per pair
   constexpr int kMyF = kTileF / 2;            // and per CTA
   pair_begin(b, warp, rank, 2);
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     // --------------------------------------------------- scheduler --
     for (long long t; (t = tile_of(i, pair, pairs)) < tiles; ++i) {
       const unsigned sl = i % kSlots;
-      ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_empty[sl]), ((i / kSlots) & 1) ^ 1));
+      ok = __all_sync(kAll, bar_wait_tile(smem_addr(&b.slot_empty[sl]), ((i / kSlots) & 1) ^ 1, ring));
       if (!ok) break;
       describe_tile(P.g, g, tt, t, tiles, nf, kTileF, slots[sl], lane);
       __syncwarp();
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     unsigned it = 0;
     for (; ok && tile_of(i, pair, pairs) < tiles; ++i) {
       const unsigned sl = i % kSlots;
-      ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
+      ok = __all_sync(kAll, bar_wait_tile(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1, ring));
       if (!ok) break;
       const Slot& slot = slots[sl];
       const Copies& copies = slot.copies;
@@ -527,8 +528,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     unsigned it = 0;
     for (; ok && tile_of(i, pair, pairs) < tiles; ++i) {
       const unsigned sl = i % kSlots, buf = i & 1;
-      ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1) &&
-                                bar_wait(smem_addr(&b.acc_empty[buf]), ((i >> 1) & 1) ^ 1));
+      ok = __all_sync(kAll, bar_wait_tile(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1, ring) &&
+                                bar_wait_tile(smem_addr(&b.acc_empty[buf]), ((i >> 1) & 1) ^ 1, ring));
       if (!ok) break;
       const uint32_t idesc = product(kBf16, kMn, false, kM, (slots[sl].granules + 1) / 2 * 2 * kGranule);
       __syncwarp();
@@ -570,7 +571,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     constexpr int kPieces = kGated ? 2 : 4;
     for (; ok && tile_of(i, pair, pairs) < tiles; ++i) {
       const unsigned sl = i % kSlots, buf = i & 1;
-      ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
+      ok = __all_sync(kAll, bar_wait_tile(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1, ring));
       if (!ok) break;
       const Slot& slot = slots[sl];
       const int p = slot.p, columns = slot.granules * kGranule;
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
       const T* res = static_cast<const T*>(P.residual[p]);
       uint4 held[kPieces];  // of the residual
       if (res != nullptr) load_rows<T, kPieces>(held, res, P.F, slot, c0 / kGranule, f, P.F, lane);
-      ok = __all_sync(kAll, bar_wait(smem_addr(&b.acc_full[buf]), (i >> 1) & 1));
+      ok = __all_sync(kAll, bar_wait_tile(smem_addr(&b.acc_full[buf]), (i >> 1) & 1, ring));
       if (!ok) break;
       fence_after_sync();
       if (c0 >= columns && lane == 0) bar_arrive_relaxed(empty0 + buf * 8);  // nothing to take
@@ -786,6 +787,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const uint32_t base = (smem_addr(dynamic) + 1023) & ~1023u;
+  const uint32_t ring = smem_addr(&b.empty[0]);
   pair_begin(b, warp, rank, 1);
   chain();
   const bool good = build_groups(P.g, g);
@@ -801,7 +803,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     // --------------------------------------------------- scheduler --
     for (unsigned t = pair; t < tiles; t += pairs, ++i) {
       const unsigned sl = i % kSlots;
-      ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_empty[sl]), ((i / kSlots) & 1) ^ 1));
+      ok = __all_sync(kAll, bar_wait_tile(smem_addr(&b.slot_empty[sl]), ((i / kSlots) & 1) ^ 1, ring));
       if (!ok) break;
       GradSlot& slot = slots[sl];
       const unsigned pe = t / (nz * nd), in = t - pe * (nz * nd);
@@ -837,7 +839,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     unsigned it = 0;
     for (unsigned t = pair; ok && t < tiles; t += pairs, ++i) {
       const unsigned sl = i % kSlots;
-      ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
+      ok = __all_sync(kAll, bar_wait_tile(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1, ring));
       if (!ok) break;
       const GradSlot& slot = slots[sl];
       const int p = slot.p;
@@ -880,7 +882,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     unsigned it = 0, n_tile = 0;
     for (unsigned t = pair; ok && t < tiles; t += pairs, ++i) {
       const unsigned sl = i % kSlots;
-      ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
+      ok = __all_sync(kAll, bar_wait_tile(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1, ring));
       if (!ok) break;
       const int blocks = slots[sl].blocks, last = slots[sl].last;
       const uint32_t idesc = product(kBf16, true, true, kM, columns_of(P.D - slots[sl].d));
@@ -889,7 +891,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
       if (blocks == 0) continue;
       const unsigned buf = n_tile & 1;
       const uint32_t d = tmem + buf * kN;
-      ok = __all_sync(kAll, bar_wait(smem_addr(&b.acc_empty[buf]), ((n_tile >> 1) & 1) ^ 1));
+      ok = __all_sync(kAll, bar_wait_tile(smem_addr(&b.acc_empty[buf]), ((n_tile >> 1) & 1) ^ 1, ring));
       if (!ok) break;
       fence_after_sync();
       ++n_tile;
@@ -926,7 +928,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     unsigned n_tile = 0;
     for (unsigned t = pair; ok && t < tiles; t += pairs, ++i) {
       const unsigned sl = i % kSlots;
-      ok = __all_sync(kAll, bar_wait(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1));
+      ok = __all_sync(kAll, bar_wait_tile(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1, ring));
       if (!ok) break;
       const int p = slots[sl].p, e = slots[sl].e, d0 = slots[sl].d;
       const int z0 = slots[sl].z + 128 * (int)rank + 32 * q;
@@ -936,7 +938,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
       const unsigned buf = n_tile & 1;
       const int columns = min(kN, P.D - d0);
       if (any) {
-        ok = __all_sync(kAll, bar_wait(smem_addr(&b.acc_full[buf]), (n_tile >> 1) & 1));
+        ok = __all_sync(kAll, bar_wait_tile(smem_addr(&b.acc_full[buf]), (n_tile >> 1) & 1, ring));
         if (!ok) break;
         fence_after_sync();
         ++n_tile;

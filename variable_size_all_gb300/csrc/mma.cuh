@@ -113,6 +113,27 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, unsigned parity) {
   return true;
 }
 
+// The same for what takes as long as a whole tile, which may be longer than that (a
+// weights' gradient over hundreds of millions of rows): false after about a second
+// in which `ring`, the barrier of one of the stages that the tile's operands go
+// through, has not turned over either.  It turns over as often as the tile's
+// contraction has blocks, so this wait ends too.
+__device__ __forceinline__ bool bar_wait_tile(uint32_t bar, unsigned parity, uint32_t ring) {
+  if (bar_try(bar, parity)) return true;
+  bool seen = bar_test(ring, 0);
+  long long start = clock64();
+  while (!bar_try(bar, parity)) {
+    const bool now = bar_test(ring, 0);
+    if (now != seen) {
+      seen = now;
+      start = clock64();
+    } else if (clock64() - start > kMmaWaitCycles) {
+      return false;
+    }
+  }
+  return true;
+}
+
 // ------------------------------------------------------------------ TMA --
 // One box of a tiled tensor to this CTA's shared memory; its bytes are counted
 // on `bar`, which may be in the other CTA of the pair.
