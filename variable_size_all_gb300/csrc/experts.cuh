@@ -266,7 +266,7 @@ __device__ __forceinline__ float act_fn(int a, float z) {
     case A2AV_ACT_GELU: {
       float density;
       const float x = fminf(fabsf(z), kFar);
-      return (z < 0.0f ? 0.0f : z) - x * normal_tail(z, x, &density);
+      return fmaf(-x, normal_tail(z, x, &density), fmaxf(z, 0.0f));
     }
     case A2AV_ACT_SILU:
       return fmaxf(z, -kFarExp) * reciprocal_fast(1.0f + exp2_fast(z * -kLog2e));
