@@ -66,31 +66,45 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
-// The sum over a token's experts, NJ a lane: the binary tree of neighbours over
-// their numbers, which is the same however many lanes and experts a lane share it
-// out (what is past the last expert adds 0).  So a token gets the same scores in
-// a batch of any size.
-template <int L, int NJ>
-__device__ __forceinline__ float experts_sum(float (&v)[NJ]) {
-#pragma unroll
-  for (int n = NJ / 2; n > 0; n /= 2)
-#pragma unroll
-    for (int j = 0; j < n; ++j) v[j] = __fadd_rn(v[2 * j], v[2 * j + 1]);
-  float sum = v[0];
+// exp(x - m) where m is the largest of the x's it belongs to; 0 where all are -inf.
+__device__ __forceinline__ float exp_below(float x, float m) {
+  return m == -INFINITY ? 0.0f : expf(x - m);
+}
+
+// The sum of exp(x - m) over a token's experts, NJ a lane: the binary tree of
+// neighbours over their numbers, which is the same however many lanes and experts
+// a lane share it out (what is past the last expert adds 0).  So a token gets the
+// same scores in a batch of any size.  lane_sum: of the lane's, depth first (an
+// array of them, summed level by level, cost a call that has no use for the sum
+// 2 % by its registers); experts_sum: of the lanes'.
+template <int kFrom, int kOf, int NJ>
+__device__ __forceinline__ float lane_sum(const float (&x)[NJ], float m) {
+  if constexpr (kOf == 1) {
+    return exp_below(x[kFrom], m);
+  } else {
+    const float first = lane_sum<kFrom, kOf / 2>(x, m);
+    return __fadd_rn(first, lane_sum<kFrom + kOf / 2, kOf / 2>(x, m));
+  }
+}
+
+template <int L>
+__device__ __forceinline__ float experts_sum(float sum) {
 #pragma unroll
   for (int o = 1; o < L; o *= 2) sum = __fadd_rn(sum, __shfl_xor_sync(kAll, sum, o));
   return sum;
 }
 
-// The same for 32 choices, choice lane + L s in v[s]: the tree that joins those 16
-// apart first, then 8, ...
+// The same for k of 32 choices, choice lane + L s in v[s]: the tree that joins those
+// 16 apart first, then 8, ... (levels that would add nothing but 0 are left out).
 template <int L, int N>
-__device__ __forceinline__ float choices_sum(float (&v)[N]) {
+__device__ __forceinline__ float choices_sum(float (&v)[N], int k) {
   static_assert(L * N == 32, "32 choices");
 #pragma unroll
   for (int n = N / 2; n > 0; n /= 2)
+    if (k > L * n) {
 #pragma unroll
-    for (int s = 0; s < n; ++s) v[s] = __fadd_rn(v[s], v[s + n]);
+      for (int s = 0; s < n; ++s) v[s] = __fadd_rn(v[s], v[s + n]);
+    }
   float sum = v[0];
 #pragma unroll
   for (int o = L / 2; o > 0; o /= 2) sum = __fadd_rn(sum, __shfl_xor_sync(kAll, sum, o));
@@ -118,11 +132,6 @@ __device__ __forceinline__ unsigned lanes_max(unsigned v) {
 // The accurate exponential and an IEEE division: choices are decided by these
 // scores, and equal logits must give equal ones on every path.
 __device__ __forceinline__ float sigmoid(float x) { return __frcp_rn(1.0f + expf(-x)); }
-
-// exp(x - m) where m is the largest of the x's it belongs to; 0 where all are -inf.
-__device__ __forceinline__ float exp_below(float x, float m) {
-  return m == -INFINITY ? 0.0f : expf(x - m);
-}
 
 // The lane's NJ logits (-inf past the last expert).
 template <typename T, int NJ, bool kVec>
@@ -286,10 +295,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, L < 32 ? 4 : 1) route_kernel
 #pragma unroll
       for (int j = 1; j < NJ; ++j) m = fmaxf(m, c[j]);
       m = lanes_max<L>(m);
-      float e[NJ];
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) e[j] = exp_below(c[j], m);
-      total = experts_sum<L>(e);
+      total = experts_sum<L>(lane_sum<0, NJ>(c, m));
     }
     if (!softmax || !by_logit) {
 #pragma unroll
@@ -396,7 +402,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, L < 32 ? 4 : 1) route_kernel
         part[s] = w[s];
       }
     }
-    if (P.renormalise) sum = choices_sum<L>(part);
+    if (P.renormalise) sum = choices_sum<L>(part, k);
 #pragma unroll
     for (int s = 0; s < kTokens; ++s) {
       const int i = sl + L * s;
