@@ -400,11 +400,13 @@ class _PlainMarshal:
 
 
 def _load_marshal():
+    """The compiled module, where there is one that was built for this torch."""
+    import torch
     try:
         from . import _marshal
-        return _marshal
     except ImportError:
         return _PlainMarshal
+    return _marshal if _marshal.torch_version == torch.__version__ else _PlainMarshal
 
 
 class _Kept(threading.local):

@@ -16,6 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "liba2av.so")
 MARSHAL_SOURCE = os.path.join(PKG, "csrc", "marshal.cpp")
 MARSHAL = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
+MARSHAL_TORCH = os.path.join(PKG, "_marshal.torch")  # the torch it was compiled against
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -38,29 +39,53 @@ def stale(output: str = LIBRARY) -> bool:
     return os.path.getmtime(output) < max(os.path.getmtime(d) for d in deps)
 
 
+def _marshal_is_current(torch) -> bool:
+    """Whether the compiled checks are of these sources and this torch, whose
+    tensors they read as its headers lay them out."""
+    try:
+        with open(MARSHAL_TORCH) as f:
+            made_for = f.read()
+        return made_for == torch.__version__ and os.path.getmtime(MARSHAL) >= max(
+            map(os.path.getmtime, (MARSHAL_SOURCE, os.path.join(INCLUDE, "a2av.h"),
+                                   os.path.join(INCLUDE, "a2av_moe.h"))))
+    except OSError:
+        return False
+
+
 def start_marshal(force: bool = False):
     """Begins to compile the binding's argument checks (csrc/marshal.cpp) against
     the installed torch; returns the process, or None when there is nothing to
-    do.  Without a compiler or the headers the binding does the checks itself."""
-    import torch
+    do.  Without torch, a compiler or the headers the binding does the checks itself."""
+    try:
+        import torch
+    except ImportError:
+        return None
     base = os.path.join(os.path.dirname(torch.__file__))
     include, python = os.path.join(base, "include"), sysconfig.get_paths()["include"]
-    if not force and os.path.exists(MARSHAL) and \
-            os.path.getmtime(MARSHAL) >= max(map(os.path.getmtime, (
-                MARSHAL_SOURCE, os.path.join(INCLUDE, "a2av.h"), os.path.join(INCLUDE, "a2av_moe.h")))):
+    if not force and _marshal_is_current(torch):
         return None
     if shutil.which("g++") is None or not os.path.exists(os.path.join(python, "Python.h")):
         return None
     return subprocess.Popen(
         ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w", "-I", INCLUDE, "-I", include, "-I",
          os.path.join(include, "torch", "csrc", "api", "include"), "-I", python,
-         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-o", MARSHAL + ".tmp",
+         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+         f'-DA2AV_TORCH="{torch.__version__}"', "-o", MARSHAL + ".tmp",
          MARSHAL_SOURCE, "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"])
 
 
 def finish_marshal(process) -> None:
-    if process is not None and process.wait() == 0:
+    """Puts the module in its place; where it did not compile, what was there is of
+    other sources or another torch, and goes."""
+    if process is None:
+        return
+    if process.wait() == 0:
+        import torch
         os.replace(MARSHAL + ".tmp", MARSHAL)
+        with open(MARSHAL_TORCH, "w") as f:
+            f.write(torch.__version__)
+    elif os.path.exists(MARSHAL):
+        os.remove(MARSHAL)
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
