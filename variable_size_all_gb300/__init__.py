@@ -441,8 +441,7 @@ class BoundCall:
             if self._ws is not None and queue.value != args[self._si].value:
                 # (another stream than the workspace's: the one of that stream)
                 i, name, need = self._ws
-                with self._engine._on(stream):
-                    held = self._engine._default_workspace(name, need)
+                held = self._engine._default_workspace(name, need, stream)
                 args[i], args[i + 1] = ctypes.c_void_p(held.data_ptr()), held.numel()
             args[self._si] = queue
         rc = self._fn(*args)
@@ -480,6 +479,8 @@ class A2av:
         self._int32, self._int64, self._float = torch.int32, torch.int64, torch.float32
         self._counts = ctypes.c_int64 * self.world_size
         self._kept = _Kept()
+        self._capture_status = ctypes.CDLL("libcuda.so.1").cuStreamIsCapturing
+        self._capture_status.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_int)]
         self._room = [ctypes.c_void_p * max(1, self.world_size * n) for n in range(9)]
         if path != PATH_AUTO:
             self._check(a2av_set_path(h, path), "a2av_set_path")
@@ -500,9 +501,13 @@ class A2av:
 
     def _queue(self, stream):
         """The cudaStream_t to enqueue on: ``stream``, or torch's current one."""
+        return _address(self._number(stream))
+
+    def _number(self, stream):
+        """``stream``, or torch's current one, as a number."""
         if stream is not None or self._raw_stream is None:
-            return _address(self._stream(stream))
-        return ctypes.c_void_p(self._raw_stream(self._device) or None)
+            return self._stream(stream)
+        return self._raw_stream(self._device)
 
     def _on(self, stream):
         """``stream`` as torch's current one: what is allocated then is of its order."""
@@ -512,25 +517,37 @@ class A2av:
             stream = torch.cuda.ExternalStream(queue) if queue else torch.cuda.default_stream()
         return torch.cuda.stream(stream)
 
-    def _held(self, what):
-        """The workspace kept for this call on torch's current stream, or None."""
+    def _capturing(self, stream, queue):
+        """Whether calls on ``stream``, whose number is ``queue``, go into a graph.
+        (The driver tells for any stream, but not in a thread that has made no CUDA
+        call yet; torch does for its current one.)"""
+        status = ctypes.c_int(0)
+        if self._capture_status(queue, ctypes.byref(status)) == 0:
+            return status.value != 0
         import torch
-        if torch.cuda.is_current_stream_capturing():
-            return None
-        return self._kept.buffers.get((what, self._stream(None)))
+        with self._on(torch.cuda.current_stream() if stream is None else stream):
+            return torch.cuda.is_current_stream_capturing()
 
-    def _default_workspace(self, what, need):
-        """The default workspace of a call on torch's current stream: kept for the
-        calls that follow on it, which take their turns.  The allocator hands out
-        one that was too small in that stream's order only.  A call that is being
-        captured takes one from the graph's own memory, which lives as long as the
-        graph does and which no other call is given."""
+    def _held(self, what, stream):
+        """The workspace kept for this call on ``stream``, or None."""
+        queue = self._number(stream)
+        return None if self._capturing(stream, queue) else self._kept.buffers.get((what, queue))
+
+    def _default_workspace(self, what, need, stream):
+        """The default workspace of a call on ``stream``: kept for the calls that
+        follow on it, which take their turns.  The allocator hands out one that was
+        too small in that stream's order only.  A call that is being captured takes
+        one from the graph's own memory, which lives as long as the graph does and
+        which no other call is given."""
+        held = self._held(what, stream)
+        if held is not None and held.numel() >= need:
+            return held
         import torch
-        held = self._held(what)
-        if held is None or held.numel() < need:
+        queue = self._number(stream)
+        with self._on(torch.cuda.current_stream() if stream is None else stream):
             held = torch.empty(need, dtype=torch.uint8, device="cuda")
-            if not torch.cuda.is_current_stream_capturing():
-                self._kept.buffers[what, self._stream(None)] = held
+        if not self._capturing(stream, queue):
+            self._kept.buffers[what, queue] = held
         return held
 
     @staticmethod
@@ -661,10 +678,6 @@ class A2av:
         a buffer for each stream in each thread, and a call under capture takes
         its own from the graph's memory."""
         import torch
-        if workspace is None and stream is not None:
-            with self._on(stream):
-                return self.dispatch(rows, src_rows, keys, keys_per_peer, outputs, out_splits_offsets,
-                                     sorted_pos, row_bytes, in_splits, _bind=_bind)
         W = self.world_size
         for name, ts, dt in (("src_rows", src_rows, torch.int32), ("keys", keys, torch.int32),
                              ("sorted_pos", sorted_pos, torch.int64)):
@@ -695,7 +708,7 @@ class A2av:
             self._scratch(workspace)
         else:
             own = (12, "dispatch", need)
-            workspace = self._default_workspace("dispatch", need)
+            workspace = self._default_workspace("dispatch", need, stream)
         n_rows = [0 if t is None else t.numel() // int(row_bytes) for t in rows]
         ptr = lambda ts: [0 if t is None or t.numel() == 0 else t.data_ptr() for t in ts]
         rows_arr, host_rows = self._buffers(rows, "rows")
@@ -708,7 +721,7 @@ class A2av:
                 _ptr_array(ptr(sorted_pos)),
                 ctypes.c_void_p(None if in_splits is None else in_splits.data_ptr()),
                 int(row_bytes), ctypes.c_void_p(workspace.data_ptr()), int(workspace.numel()),
-                ctypes.c_void_p(self._stream(stream) or None)]
+                self._queue(stream)]
         if _bind:
             keep = (rows, src_rows, keys, outputs, out_splits_offsets, sorted_pos, in_splits,
                     workspace)
@@ -736,10 +749,6 @@ class A2av:
         ``item_out[r]``.  ``in_splits``, ``keys`` and ``sorted_pos`` as a
         dispatch took or wrote them.  ``workspace`` as in ``dispatch``."""
         import torch
-        if workspace is None and stream is not None:
-            with self._on(stream):
-                return self.combine_items(peers, in_splits, keys, sorted_pos, keys_per_peer, item_out,
-                                          row_bytes, _bind=_bind)
         W = self.world_size
         sp = self._matrix(in_splits, (W, W), "in_splits")
         for name, ts, dt in (("keys", keys, torch.int32), ("sorted_pos", sorted_pos, torch.int64)):
@@ -760,7 +769,7 @@ class A2av:
             self._scratch(workspace)
         else:
             own = (9, "combine_items", COMBINE_WORKSPACE_BYTES)
-            workspace = self._default_workspace("combine_items", COMBINE_WORKSPACE_BYTES)
+            workspace = self._default_workspace("combine_items", COMBINE_WORKSPACE_BYTES, stream)
         peer_arr, host_p = self._buffers(peers, "peers")
         out_arr, host_o = self._buffers(item_out, "item_out")
         if host_p or host_o:
@@ -769,7 +778,7 @@ class A2av:
         args = [self.handle, int(keys_per_peer), _ptr_array(list(peer_arr)), sp,
                 _ptr_array(ptr(keys)), _ptr_array(ptr(sorted_pos)), _i64_array(items),
                 _ptr_array(list(out_arr)), int(row_bytes), ctypes.c_void_p(workspace.data_ptr()),
-                int(workspace.numel()), ctypes.c_void_p(self._stream(stream) or None)]
+                int(workspace.numel()), self._queue(stream)]
         if _bind:
             keep = (peers, in_splits, keys, sorted_pos, item_out, workspace)
             return BoundCall(self, load().a2av_combine_items, "a2av_combine_items", args, 11, keep, own)
@@ -833,12 +842,8 @@ class A2av:
         found something to look at: nothing has been enqueued then."""
         if self.handle is None:
             return False
-        if stream is not None or self._raw_stream is None:
-            stream = self._stream(stream)
-        else:
-            stream = self._raw_stream(self._device)
-        rc = getattr(self._marshal, what)(self._entries[what], self._address, stream, self.world_size,
-                                          *args)
+        rc = getattr(self._marshal, what)(self._entries[what], self._address, self._number(stream),
+                                          self.world_size, *args)
         if rc is None:
             return False
         if rc != OK:
@@ -987,11 +992,7 @@ class A2av:
         gate.  ``workspace``: scratch that no other call in flight has; by default
         the object keeps a buffer for each stream in each thread, and a call under
         capture takes its own from the graph's memory."""
-        if workspace is None and stream is not None:
-            with self._on(stream):
-                return self.expert_matmul_backward(rows, counts, weights, d_outputs, d_rows, d_weights,
-                                                   d_bias, pre, activation, gated)
-        kept = workspace if workspace is not None else self._held("expert_matmul_backward")
+        kept = workspace if workspace is not None else self._held("expert_matmul_backward", stream)
         if self._whole("expert_matmul_backward", stream, rows, counts, weights, d_outputs, d_rows,
                        d_weights, d_bias, pre, _ACTIVATIONS.get(activation), gated, kept,
                        self._entries["expert_matmul_workspace_bytes"]):
@@ -1008,7 +1009,7 @@ class A2av:
         if workspace is not None:
             self._scratch(workspace)
         elif need:
-            workspace = self._default_workspace("expert_matmul_backward", need)
+            workspace = self._default_workspace("expert_matmul_backward", need, stream)
         each, by_row = [(K, Z, D)] * W, [(m, D) for m in n]
         (x, w, z, dy, dx, dw, db), arrays = self._lists(
             (rows, dtype, by_row, "rows"), (weights, dtype, each, "weights"),
