@@ -188,7 +188,8 @@ int64_t a2av_expert_matmul_workspace_bytes(int world_size, const a2av_expert_t *
  *   d_rows = dz W_e      d_weights_e = dz_e^T x_e      d_bias_e = sum of dz_e's rows
  *
  * (the residual's gradient is dy itself).  dz is rounded to dtype, which the
- * tensor cores take, before the products; d_bias sums the rounded dz, in 32 bits.
+ * tensor cores take, before the products (in f16 one above 65504 is infinite);
+ * d_bias sums the rounded dz, in 32 bits.
  * An expert without rows gets gradients of 0.
  *
  *  rows_ptrs .. weight_ptrs   as in the forward call.

@@ -55,7 +55,13 @@ def _full_and_empty():
     return torch.randint(1, 500, (2, 40), generator=gen) * (torch.arange(40) % 2)
 
 
-COUNTS = {"one long": _one_long, "mixed": _mixed, "full and empty": _full_and_empty}
+def _many_groups():
+    """256 experts on eight ranks: four groups to an entry of a block's table, which walks them."""
+    gen = torch.Generator().manual_seed(4)
+    return torch.randint(0, 24, (8, 256), generator=gen) * (torch.rand((8, 256), generator=gen) < 0.8)
+
+
+COUNTS = {"one long": _one_long, "mixed": _mixed, "full and empty": _full_and_empty, "many groups": _many_groups}
 
 
 class _Case:
@@ -97,12 +103,13 @@ def _close(got, ref, bound, dtype, what):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("name,gated", [("silu", True), ("gelu", False), ("none", False), ("relu", True)])
-@pytest.mark.parametrize("kind,D,N", [("one long", 264, 2088), ("mixed", 200, 1032), ("full and empty", 520, 1288)])
+@pytest.mark.parametrize("kind,D,N", [("one long", 264, 2088), ("mixed", 200, 1032), ("full and empty", 520, 1288),
+                                      ("many groups", 136, 264)])
 def test_forward(kind, D, N, name, gated, dtype):
     c = _Case(kind, D, N, dtype, gated)
     tiles = int(c.row_tiles().sum()) * -(-N // (128 if gated else 256))
     assert tiles > 2 * _pairs()
-    if kind != "full and empty":
+    if kind in ("one long", "mixed"):
         assert c.row_tiles().max() > 8  # (more than a band)
     if kind == "mixed":
         assert {0, 1} <= set(c.row_tiles().tolist())
@@ -132,7 +139,8 @@ def test_forward(kind, D, N, name, gated, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("name,gated", [("silu", True), ("gelu", False), ("none", False)])
-@pytest.mark.parametrize("kind,D,N", [("one long", 2056, 1032), ("mixed", 1288, 520), ("full and empty", 1288, 264)])
+@pytest.mark.parametrize("kind,D,N", [("one long", 2056, 1032), ("mixed", 1288, 520), ("full and empty", 1288, 264),
+                                      ("many groups", 264, 136)])
 def test_backward(kind, D, N, name, gated, dtype):
     c = _Case(kind, D, N, dtype, gated, seed=1)
     nd = -(-D // 256)

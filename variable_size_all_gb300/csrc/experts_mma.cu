@@ -426,11 +426,14 @@ __device__ __forceinline__ void plan_copies(Slot& slot, uint32_t rank) {
 // 128 of the first half and their partners of the second, eight and eight in
 // turn (one copy of a five-dimensional view of the weights puts them so): a
 // thread of the epilogue finds both in its registers.
-// (Zipf-skewed rows over 64 experts: 16,384 rows, 2048 -> 7168, 436 to 490 us,
-// bound by the bytes in flight for the experts of few rows; 131,072 rows,
-// 7168 -> 2 x 2048 gated, 4.6 to 5.1 ms, 1.5 to 1.7 PFLOP/s under the power cap.
-// 5001 rows of one, 2048 -> 7168 with bias, GELU and residual: 121 us, 1.2
-// PFLOP/s: 560 tiles are 7.4 rounds of 76 pairs and so take 8.)
+// (Zipf-skewed rows over 64 experts: 16,384 rows, 2048 -> 7168, 475 to 490 us,
+// with the tensor pipe 56 % busy and the memory at 67 % of its nominal rate: tiles
+// bound by one and by the other share the time, and neither is saturated; 131,072
+// rows, 7168 -> 2 x 2048 gated, 4.96 to 5.15 ms, 1.5 PFLOP/s under the power cap, 3 %
+// more where z is saved.  5001 rows of one, f16, 2048 -> 7168: 105 us, 560 tiles
+// being 7.4 rounds of 76 pairs that take 8 (98 for 4864 rows, 7 rounds); bias adds
+// nothing, SiLU 2 us, GELU 9, the residual 10, 123 with all of them: the 32 blocks
+// of products of a tile are too few to hide its epilogue.)
 template <typename T, bool kMn, bool kGated>
 __global__ void __launch_bounds__(kMmaThreads, 1) __cluster_dims__(2, 1, 1)
     expert_mma_kernel(const __grid_constant__ MmaParams P) {

@@ -16,12 +16,16 @@
 // and finds the next costs some for every expert.  (Many equal choices can make
 // more candidates than there is room for; then those rounds are run.)
 //
-// Bound by instruction issue with many experts: 65,536 tokens of 256 experts
-// (f32, sigmoid, 4 of 8 groups, top 8) take 52 us against 10.5 for the memory,
-// 608 instructions a token, the issue slots 66 % busy; most are the exact
-// exponential and division of every score, which decide ties.  65,536 tokens of
-// 64 experts (bf16, top 2) take 10.7 us with the clearing of the counts, 4 tokens
-// on each of 8 ranks 3.5, one small launch.
+// Bound by steps that wait for one another: 65,536 tokens of 256 experts (f32,
+// sigmoid, 4 of 8 groups, top 8) take 52 us against 10.5 for the memory.  A token
+// takes 597 of a warp's instructions, which fill 65 % of the issue slots at 44 %
+// of the warps an SM holds; between two of them a warp waits 2.8 cycles for
+// shuffles and shared memory, 2.3 for the arithmetic before, 1.3 for loads.  (The
+// exact exponential and division of every score, which decide ties, are a tenth of
+// the instructions; without them it took as long.)  65,536 tokens of 64 experts
+// (bf16, top 2) take 10.7 us with the clearing of the counts, of a warp's waits
+// 3.6 for shuffles and shared memory, 2.2 and 1.9 for the others; 4 tokens on each
+// of 8 ranks 3.5, one small launch.
 #include "moe_device.cuh"
 
 namespace {
