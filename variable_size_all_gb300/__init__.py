@@ -27,6 +27,9 @@ __all__ = [
     "a2av_route", "a2av_route_backward", "a2av_expert_matmul", "a2av_expert_matmul_backward",
     "a2av_expert_matmul_workspace_bytes", "a2av_combine_weighted", "a2av_combine_weighted_backward",
     "A2avRoute", "A2avExpert", "F32", "BF16", "F16", "MAX_TOPK", "MAX_ROUTE_GROUPS",
+    "a2av_mx_row_bytes", "a2av_norm", "a2av_norm_workspace_bytes", "a2av_norm_backward",
+    "a2av_quantise", "a2av_dequantise", "a2av_expert_matmul_mx", "mx_row_bytes", "PLAIN", "MXFP8",
+    "MXFP4", "MAX_NORM_FEATURES", "MAX_MX_FEATURES",
 ]
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_BAD_SPLITS, ERR_TIMEOUT = 0, -1, -2, -3, -4, -5
@@ -38,6 +41,9 @@ MAX_EXCHANGES = 4
 COMBINE_WORKSPACE_BYTES = 256 + 16 * 32 * 32
 F32, BF16, F16 = 0, 1, 2
 MAX_TOPK, MAX_ROUTE_GROUPS = 32, 32
+PLAIN, MXFP8, MXFP4 = 0, 1, 2
+MAX_NORM_FEATURES, MAX_MX_FEATURES = 16384, 1 << 24
+_FORMATS = {None: PLAIN, "mxfp8": MXFP8, "mxfp4": MXFP4}
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 
@@ -121,7 +127,17 @@ def load():
                                           vp]
     lib.a2av_combine_weighted_backward.argtypes = [vp, ci, ci, i64, ci, vp, i64p, vp, vp, vp, vp,
                                                    i64p, vp, vp, vp, vp]
-    for f in ("a2av_create", "a2av_run", "a2av_combine", "a2av_status", "a2av_destroy", "a2av_set_path",
+    f32 = ctypes.c_float
+    lib.a2av_mx_row_bytes.argtypes = [i64, ci]
+    lib.a2av_mx_row_bytes.restype = i64
+    lib.a2av_norm.argtypes = [vp, i64, ci, ci, f32, vp, i64p, vp, vp, vp, vp, vp]
+    lib.a2av_norm_workspace_bytes.argtypes = [i64, i64]
+    lib.a2av_norm_workspace_bytes.restype = i64
+    lib.a2av_norm_backward.argtypes = [vp, i64, ci, f32, vp, i64p, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.a2av_quantise.argtypes = lib.a2av_dequantise.argtypes = [vp, i64, ci, ci, vp, i64p, vp, vp]
+    lib.a2av_expert_matmul_mx.argtypes = [vp, expert_p, ci, vp, i64p, vp, vp, vp, vp, vp, vp]
+    for f in ("a2av_norm", "a2av_norm_backward", "a2av_quantise", "a2av_dequantise",
+              "a2av_expert_matmul_mx", "a2av_create", "a2av_run", "a2av_combine", "a2av_status", "a2av_destroy", "a2av_set_path",
               "a2av_set_grid", "a2av_last_launch", "a2av_version", "a2av_run_noalloc",
               "a2av_run_multi", "a2av_route", "a2av_route_backward", "a2av_expert_matmul",
               "a2av_expert_matmul_backward", "a2av_combine_weighted",
@@ -353,7 +369,69 @@ def a2av_combine_weighted_backward(handle, keys_per_peer: int, topk: int, hidden
         _optional_ptrs(d_peer_ptrs), _optional_ptrs(d_weight_ptrs), _address(stream))
 
 
+def a2av_mx_row_bytes(features: int, format: int) -> int:
+    return load().a2av_mx_row_bytes(int(features), int(format))
+
+
+def a2av_norm(handle, features: int, dtype: int, format: int, eps: float, x_ptrs, tokens_per_rank,
+              weight: int, residual_ptrs, sum_ptrs, out_ptrs, stream: int = 0) -> int:
+    """Raw norm (include/a2av_mx.h): integer device addresses, lists (or None) per rank."""
+    return load().a2av_norm(handle, int(features), int(dtype), int(format), eps, _ptr_array(x_ptrs),
+                            _i64_array(tokens_per_rank), _address(weight),
+                            _optional_ptrs(residual_ptrs), _optional_ptrs(sum_ptrs),
+                            _ptr_array(out_ptrs), _address(stream))
+
+
+def a2av_norm_workspace_bytes(features: int, total_rows: int) -> int:
+    return load().a2av_norm_workspace_bytes(int(features), int(total_rows))
+
+
+def a2av_norm_backward(handle, features: int, dtype: int, eps: float, sum_ptrs, tokens_per_rank,
+                       weight: int, d_out_ptrs, d_sum_ptrs, d_x_ptrs, d_weight: int, workspace: int,
+                       workspace_bytes: int, stream: int = 0) -> int:
+    """Raw gradients of the norm."""
+    return load().a2av_norm_backward(
+        handle, int(features), int(dtype), eps, _ptr_array(sum_ptrs), _i64_array(tokens_per_rank),
+        _address(weight), _ptr_array(d_out_ptrs), _optional_ptrs(d_sum_ptrs), _ptr_array(d_x_ptrs),
+        _address(d_weight), _address(workspace), int(workspace_bytes), _address(stream))
+
+
+def a2av_quantise(handle, features: int, dtype: int, format: int, x_ptrs, rows_per_rank, packed_ptrs,
+                  stream: int = 0) -> int:
+    """Raw packing of rows."""
+    return load().a2av_quantise(handle, int(features), int(dtype), int(format), _ptr_array(x_ptrs),
+                                _i64_array(rows_per_rank), _ptr_array(packed_ptrs), _address(stream))
+
+
+def a2av_dequantise(handle, features: int, dtype: int, format: int, packed_ptrs, rows_per_rank,
+                    out_ptrs, stream: int = 0) -> int:
+    """Raw unpacking of rows."""
+    return load().a2av_dequantise(handle, int(features), int(dtype), int(format),
+                                  _ptr_array(packed_ptrs), _i64_array(rows_per_rank),
+                                  _ptr_array(out_ptrs), _address(stream))
+
+
+def a2av_expert_matmul_mx(handle, shape: A2avExpert, format: int, rows_ptrs, rows_per_peer,
+                          counts: int, weight_ptrs, bias_ptrs, residual_ptrs, out_ptrs,
+                          stream: int = 0) -> int:
+    """Raw experts' product of packed rows and weights."""
+    return load().a2av_expert_matmul_mx(
+        handle, ctypes.byref(shape), int(format), _ptr_array(rows_ptrs), _i64_array(rows_per_peer),
+        _address(counts), _ptr_array(weight_ptrs), _optional_ptrs(bias_ptrs),
+        _optional_ptrs(residual_ptrs), _ptr_array(out_ptrs), _address(stream))
+
+
 # --------------------------------------------------------- torch-facing --
+def mx_row_bytes(features: int, format: str) -> int:
+    """Bytes of a packed row ("mxfp8" or "mxfp4") of ``features`` values."""
+    if format is None or format not in _FORMATS:
+        raise ValueError("format must be one of " + str(sorted(f for f in _FORMATS if f)))
+    n = a2av_mx_row_bytes(features, _FORMATS[format])
+    if n < 0:
+        raise ValueError(f"features must be in 1..{MAX_MX_FEATURES}")
+    return n
+
+
 class _PlainMarshal:
     """``_marshal`` (csrc/marshal.cpp) without the compiled module."""
 
@@ -397,6 +475,7 @@ class _PlainMarshal:
 
     route_backward = expert_matmul = expert_matmul_backward = route
     combine_weighted = combine_weighted_backward = route
+    norm = norm_backward = quantise = dequantise = expert_matmul_mx = route
 
 
 def _load_marshal():
@@ -473,10 +552,13 @@ class A2av:
         self._entries = {what: ctypes.cast(getattr(load(), "a2av_" + what), ctypes.c_void_p).value
                          for what in ("route", "route_backward", "expert_matmul",
                                       "expert_matmul_backward", "expert_matmul_workspace_bytes",
-                                      "combine_weighted", "combine_weighted_backward")}
+                                      "combine_weighted", "combine_weighted_backward", "norm",
+                                      "norm_backward", "norm_workspace_bytes", "quantise",
+                                      "dequantise", "expert_matmul_mx", "mx_row_bytes")}
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._codes = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
         self._int32, self._int64, self._float = torch.int32, torch.int64, torch.float32
+        self._bytes = torch.uint8
         self._counts = ctypes.c_int64 * self.world_size
         self._kept = _Kept()
         self._capture_status = ctypes.CDLL("libcuda.so.1").cuStreamIsCapturing
@@ -1115,6 +1197,152 @@ class A2av:
         args = [self.handle, K, k, H, code, x, self._counts(*held), in_splits.data_ptr(), ka, pa, w,
                 self._counts(*n), dy, dx, dw, self._queue(stream)]
         self._call("a2av_combine_weighted_backward", args, None, False)
+
+    # ----------------------------------------- the norm and packed rows --
+    def _vector(self, t, n, name):
+        """The address of a float32 [n] tensor."""
+        import torch
+        if (not isinstance(t, torch.Tensor) or t.dtype != self._float or not t.is_cuda
+                or t.shape != (n,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous CUDA float32 [{n}] tensor")
+        return t.data_ptr()
+
+    def norm(self, x, weight, outputs, residual=None, sums=None, eps: float = 1e-6, format=None,
+             stream=None, _bind=False):
+        """Root-mean-square norm (see include/a2av_mx.h, a2av_norm): s = x + residual,
+        y = s / sqrt(mean(s^2) + eps) * weight.
+
+        ``x[r]`` and ``residual[r]`` (optional): rank r's [T, H] float32, bfloat16 or
+        float16 tensor; ``weight`` float32 [H].  Written: ``sums[r]`` (optional; may be
+        ``x[r]`` or ``residual[r]``) with s, and ``outputs[r]`` with y: [T, H] of the same
+        type, or, with ``format`` "mxfp8" or "mxfp4", packed rows, uint8
+        [T, mx_row_bytes(H, format)]."""
+        if not _bind and self._whole("norm", stream, x, weight, outputs, residual, sums, eps,
+                                     _FORMATS.get(format), self._entries["mx_row_bytes"]):
+            return
+        n, H = self._tokens(x, "x")
+        dtype, code = self._dtype(x, "x", (F32, BF16, F16))
+        width = H if format is None else mx_row_bytes(H, format)
+        w = self._vector(weight, H, "weight")
+        shapes = [(m, H) for m in n]
+        (xs, res, kept, y), arrays = self._lists(
+            (x, dtype, shapes, "x"), (residual, dtype, shapes, "residual"), (sums, dtype, shapes, "sums"),
+            (outputs, dtype if format is None else self._bytes, [(m, width) for m in n], "outputs"))
+        args = [self.handle, H, code, _FORMATS[format], eps, xs, self._counts(*n), w, res, kept, y,
+                self._queue(stream)]
+        return self._call("a2av_norm", args, (x, weight, outputs, residual, sums, arrays), _bind)
+
+    def bind_norm(self, x, weight, outputs, **options) -> BoundCall:
+        """``norm`` marshalled once (see BoundCall)."""
+        return self.norm(x, weight, outputs, **options, _bind=True)
+
+    def norm_backward(self, sums, weight, d_outputs, d_x, d_weight=None, d_sums=None,
+                      eps: float = 1e-6, workspace=None, stream=None):
+        """The gradients of ``norm`` (see include/a2av_mx.h, a2av_norm_backward):
+        ``d_x[r]`` [T, H], of x and of the residual, and ``d_weight`` float32 [H] (optional, over
+        all ranks), from the ``sums`` that the forward call kept (x, without a residual),
+        ``d_outputs[r]`` and, where s reaches further, ``d_sums[r]``.  ``d_x[r]`` may be
+        ``d_outputs[r]`` or ``d_sums[r]``.  ``workspace`` as in ``expert_matmul_backward``."""
+        kept = workspace if workspace is not None or d_weight is None else \
+            self._held("norm_backward", stream)
+        if self._whole("norm_backward", stream, sums, weight, d_outputs, d_x, d_weight, d_sums, eps,
+                       kept, self._entries["norm_workspace_bytes"]):
+            return
+        n, H = self._tokens(sums, "sums")
+        dtype, code = self._dtype(sums, "sums", (F32, BF16, F16))
+        w = self._vector(weight, H, "weight")
+        dw = None if d_weight is None else self._vector(d_weight, H, "d_weight")
+        need = 0
+        if d_weight is not None:
+            need = a2av_norm_workspace_bytes(H, sum(n))
+            if need < 0:
+                raise A2avError(ERR_UNSUPPORTED, "a2av_norm_workspace_bytes")
+        if workspace is not None:
+            self._scratch(workspace)
+        elif need:
+            workspace = self._default_workspace("norm_backward", need, stream)
+        shapes = [(m, H) for m in n]
+        (s, dy, ds, dx), arrays = self._lists(
+            (sums, dtype, shapes, "sums"), (d_outputs, dtype, shapes, "d_outputs"),
+            (d_sums, dtype, shapes, "d_sums"), (d_x, dtype, shapes, "d_x"))
+        args = [self.handle, H, code, eps, s, self._counts(*n), w, dy, ds, dx, dw,
+                workspace.data_ptr() if need else None,
+                workspace.numel() * workspace.element_size() if need else 0, self._queue(stream)]
+        self._call("a2av_norm_backward", args, None, False)
+
+    def _pack_args(self, what, plain, plain_name, packed, packed_name, format, stream, bind):
+        n, D = self._tokens(plain, plain_name)
+        dtype, code = self._dtype(plain, plain_name, (F32, BF16, F16))
+        width = mx_row_bytes(D, format)
+        (x, p), arrays = self._lists((plain, dtype, [(m, D) for m in n], plain_name),
+                                     (packed, self._bytes, [(m, width) for m in n], packed_name))
+        if what == "a2av_dequantise":
+            x, p = p, x
+        args = [self.handle, D, code, _FORMATS[format], x, self._counts(*n), p, self._queue(stream)]
+        return self._call(what, args, (plain, packed, arrays), bind)
+
+    def quantise(self, x, rows, format: str, stream=None, _bind=False):
+        """``x[r]`` [R, D] (float32, bfloat16 or float16) to packed rows ``rows[r]``, uint8
+        [R, mx_row_bytes(D, format)], ``format`` "mxfp8" or "mxfp4" (see
+        include/a2av_mx.h).  An expert's weights [K, Z, D] are K * Z rows."""
+        if not _bind and self._whole("quantise", stream, x, rows, _FORMATS.get(format),
+                                     self._entries["mx_row_bytes"]):
+            return
+        return self._pack_args("a2av_quantise", x, "x", rows, "rows", format, stream, _bind)
+
+    def bind_quantise(self, x, rows, format: str, stream=None) -> BoundCall:
+        """``quantise`` marshalled once (see BoundCall)."""
+        return self.quantise(x, rows, format, stream, _bind=True)
+
+    def dequantise(self, rows, outputs, format: str, stream=None, _bind=False):
+        """Packed rows back to ``outputs[r]`` [R, D]: code * scale, rounded once."""
+        if not _bind and self._whole("dequantise", stream, rows, outputs, _FORMATS.get(format),
+                                     self._entries["mx_row_bytes"]):
+            return
+        return self._pack_args("a2av_dequantise", outputs, "outputs", rows, "rows", format, stream, _bind)
+
+    def bind_dequantise(self, rows, outputs, format: str, stream=None) -> BoundCall:
+        """``dequantise`` marshalled once (see BoundCall)."""
+        return self.dequantise(rows, outputs, format, stream, _bind=True)
+
+    def expert_matmul_mx(self, rows, counts, weights, outputs, in_features: int, format: str,
+                         activation: str = "none", gated: bool = False, bias=None, residual=None,
+                         stream=None, _bind=False):
+        """``expert_matmul`` on packed rows and weights (see include/a2av_mx.h,
+        a2av_expert_matmul_mx): ``rows[p]`` uint8 [rows, B] and ``weights[p]`` uint8
+        [K, Z, B], B = mx_row_bytes(in_features, format), both of ``format`` "mxfp8" or
+        "mxfp4"; ``outputs[p]``, ``bias[p]`` and ``residual[p]`` bfloat16 or float16."""
+        if not _bind and self._whole("expert_matmul_mx", stream, rows, counts, weights, outputs,
+                                     in_features, _FORMATS.get(format), _ACTIVATIONS.get(activation),
+                                     gated, bias, residual, self._entries["mx_row_bytes"]):
+            return
+        if activation not in _ACTIVATIONS:
+            raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}")
+        W, D = self.world_size, int(in_features)
+        B = mx_row_bytes(D, format)
+        n, N = self._tokens(outputs, "outputs")
+        dtype, code = self._dtype(outputs, "outputs", (F16, BF16))
+        if len(weights) != W or any(w is None or w.dim() != 3 for w in weights):
+            raise ValueError(f"weights must be {W} tensors [experts, features, {B}]")
+        K, Z = weights[0].shape[0], 2 * N if gated else N
+        self._matrix(counts, (W, W * K), "counts")
+        shape = A2avExpert(K, D, N, code, _ACTIVATIONS[activation], int(bool(gated)))
+        by_row = [(m, N) for m in n]
+        (x, w, b, r, y), arrays = self._lists(
+            (rows, self._bytes, [(m, B) for m in n], "rows"),
+            (weights, self._bytes, [(K, Z, B)] * W, "weights"), (bias, dtype, [(K, Z)] * W, "bias"),
+            (residual, dtype, by_row, "residual"), (outputs, dtype, by_row, "outputs"))
+        args = [self.handle, ctypes.byref(shape), _FORMATS[format], x, self._counts(*n),
+                counts.data_ptr(), w, b, r, y, self._queue(stream)]
+        keep = (rows, counts, weights, outputs, bias, residual, arrays)
+        return self._call("a2av_expert_matmul_mx", args, keep, _bind)
+
+    def bind_expert_matmul_mx(self, rows, counts, weights, outputs, in_features: int, format: str,
+                              **options) -> BoundCall:
+        """``expert_matmul_mx`` marshalled once: new counts and rows are allowed
+        within the buffers' row counts (see BoundCall)."""
+        return self.expert_matmul_mx(rows, counts, weights, outputs, in_features, format, **options,
+                                     _bind=True)
 
     def status(self, stream=None) -> int:
         rc, v = a2av_status(self.handle, self._stream(stream))

@@ -9,10 +9,13 @@ import sysconfig
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", f) for f in ("a2av.cu", "dispatch.cu", "route.cu", "experts.cu",
-                                                  "experts_mma.cu", "weighted.cu")]
+                                                  "experts_mma.cu", "experts_mx.cu", "norm.cu",
+                                                  "weighted.cu")]
 HEADERS = [os.path.join(PKG, "csrc", f) for f in ("a2av_device.cuh", "a2av_handle.h",
-                                                  "moe_device.cuh", "experts.cuh", "mma.cuh")]
+                                                  "moe_device.cuh", "experts.cuh", "mma.cuh",
+                                                  "mx_device.cuh")]
 INCLUDE = os.path.join(ROOT, "include")
+INTERFACES = [os.path.join(INCLUDE, f) for f in ("a2av.h", "a2av_moe.h", "a2av_mx.h")]
 LIBRARY = os.path.join(PKG, "liba2av.so")
 MARSHAL_SOURCE = os.path.join(PKG, "csrc", "marshal.cpp")
 MARSHAL = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
@@ -35,7 +38,7 @@ def command(output: str = LIBRARY, extra=()) -> list:
 def stale(output: str = LIBRARY) -> bool:
     if not os.path.exists(output):
         return True
-    deps = SOURCES + HEADERS + [os.path.join(INCLUDE, f) for f in ("a2av.h", "a2av_moe.h")] + [__file__]
+    deps = SOURCES + HEADERS + INTERFACES + [__file__]
     return os.path.getmtime(output) < max(os.path.getmtime(d) for d in deps)
 
 
@@ -46,8 +49,7 @@ def _marshal_is_current(torch) -> bool:
         with open(MARSHAL_TORCH) as f:
             made_for = f.read()
         return made_for == torch.__version__ and os.path.getmtime(MARSHAL) >= max(
-            map(os.path.getmtime, (MARSHAL_SOURCE, os.path.join(INCLUDE, "a2av.h"),
-                                   os.path.join(INCLUDE, "a2av_moe.h"))))
+            map(os.path.getmtime, (MARSHAL_SOURCE, *INTERFACES)))
     except OSError:
         return False
 

@@ -263,22 +263,10 @@ int shape_ok(const a2av_expert_t* c, int W) {
   return A2AV_OK;
 }
 
-// Copies a list of W pointers (`need`: rows or experts of peer p want one).
-bool take(const void** to, const void* const* from, int W, const int64_t* rows, int size) {
-  for (int p = 0; p < W; ++p) {
-    to[p] = from != nullptr && (rows == nullptr || rows[p] > 0) ? from[p] : nullptr;
-    if (from != nullptr && (rows == nullptr || rows[p] > 0) && to[p] == nullptr) return false;
-    if (!aligned_to(to[p], size)) return false;
-  }
-  return true;
-}
+}  // namespace
 
-bool take(void** to, void* const* from, int W, const int64_t* rows, int size) {
-  return take(const_cast<const void**>(to), from, W, rows, size);
-}
-
-int expert_params(a2av_handle* h, const a2av_expert_t* c, const int64_t* rows_per_peer,
-                  const int64_t* counts, ExpertParams* P) {
+int a2av_expert_params(a2av_handle* h, const a2av_expert_t* c, const int64_t* rows_per_peer,
+                       const int64_t* counts, A2avExperts* P) {
   if (h == nullptr || rows_per_peer == nullptr || counts == nullptr || !aligned_to(counts, 8))
     return A2AV_ERR_INVALID_ARG;
   const int rc = shape_ok(c, h->W);
@@ -302,6 +290,8 @@ int expert_params(a2av_handle* h, const a2av_expert_t* c, const int64_t* rows_pe
   P->gated = c->gated != 0;
   return current_device(h);
 }
+
+namespace {
 
 template <typename T>
 cudaError_t launch_forward(a2av_handle* h, const ExpertParams& P, int dtype, cudaStream_t s) {
@@ -361,7 +351,7 @@ extern "C" int a2av_expert_matmul(a2av_handle* h, const a2av_expert_t* shape,
   if (rows_ptrs == nullptr || weight_ptrs == nullptr || out_ptrs == nullptr)
     return A2AV_ERR_INVALID_ARG;
   ExpertParams P;
-  const int rc = expert_params(h, shape, rows_per_peer, counts_dev, &P);
+  const int rc = a2av_expert_params(h, shape, rows_per_peer, counts_dev, &P);
   if (rc != A2AV_OK) return rc;
   const int W = h->W, size = dtype_bytes(shape->dtype);
   if (!take(P.x, rows_ptrs, W, rows_per_peer, size) || !take(P.w, weight_ptrs, W, nullptr, size) ||
@@ -399,7 +389,7 @@ extern "C" int a2av_expert_matmul_backward(
       (d_rows_ptrs == nullptr && d_weight_ptrs == nullptr && d_bias_ptrs == nullptr))
     return A2AV_ERR_INVALID_ARG;
   ExpertParams P;
-  const int rc = expert_params(h, shape, rows_per_peer, counts_dev, &P);
+  const int rc = a2av_expert_params(h, shape, rows_per_peer, counts_dev, &P);
   if (rc != A2AV_OK) return rc;
   const int W = h->W, size = dtype_bytes(shape->dtype);
   const bool dz_needed = shape->activation != A2AV_ACT_NONE || shape->gated;

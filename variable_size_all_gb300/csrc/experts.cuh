@@ -292,6 +292,21 @@ __device__ __forceinline__ float act_slope(int a, float z) {
   }
 }
 
+// ----------------------------------------------------------- host side --
+// Copies a list of W pointers (`need`: rows or experts of peer p want one).
+inline bool take(const void** to, const void* const* from, int W, const int64_t* rows, int size) {
+  for (int p = 0; p < W; ++p) {
+    to[p] = from != nullptr && (rows == nullptr || rows[p] > 0) ? from[p] : nullptr;
+    if (from != nullptr && (rows == nullptr || rows[p] > 0) && to[p] == nullptr) return false;
+    if (!aligned_to(to[p], size)) return false;
+  }
+  return true;
+}
+
+inline bool take(void** to, void* const* from, int W, const int64_t* rows, int size) {
+  return take(const_cast<const void**>(to), from, W, rows, size);
+}
+
 }  // namespace
 
 // experts_mma.cu: the same products on the tensor cores.  `direction` 0: out =
@@ -305,3 +320,8 @@ __attribute__((visibility("hidden"))) bool a2av_expert_mma(a2av_handle* h, const
 // Rows of the weights' gradient's packed remainders (see experts_mma.cu), at
 // most; and their place: Z elements each for dz, then D each for x.
 __attribute__((visibility("hidden"))) int64_t a2av_expert_tail_rows(int W, int K, int64_t rows);
+
+// experts.cu: a call's groups and shape, checked; the buffers are still to be taken.
+__attribute__((visibility("hidden"))) int a2av_expert_params(a2av_handle* h, const a2av_expert_t* c,
+                                                             const int64_t* rows_per_peer,
+                                                             const int64_t* counts, A2avExperts* P);

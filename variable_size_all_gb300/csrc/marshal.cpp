@@ -3,8 +3,9 @@
 // small tensors, and reading five attributes of each through Python took longer
 // (12 us of a combine's 27 on 8 ranks) than the kernel does.
 //
-// route, route_backward, expert_matmul, expert_matmul_backward, combine_weighted
-// and combine_weighted_backward(function, handle, stream, W, the method's arguments)
+// route, route_backward, expert_matmul, expert_matmul_backward, combine_weighted,
+// combine_weighted_backward, norm, norm_backward, quantise, dequantise and
+// expert_matmul_mx(function, handle, stream, W, the method's arguments)
 // -> the library's return value: the whole call, where every list has W good
 // tensors and every number is in its range.  None where one is not, or is
 // missing: nothing has been called, and the binding goes through its arguments
@@ -28,7 +29,7 @@
 #include <climits>
 #include <cstdint>
 
-#include "a2av_moe.h"
+#include "a2av_mx.h"
 
 namespace {
 
@@ -529,6 +530,171 @@ PyObject* combine_weighted_backward(PyObject*, PyObject* const* args, Py_ssize_t
       });
 }
 
+// A packed row's bytes by the library's own function, or -1.
+int64_t packed_bytes(PyObject* entry, int64_t features, int format) {
+  void* f = PyLong_Check(entry) ? PyLong_AsVoidPtr(entry) : nullptr;
+  return f == nullptr ? -1 : reinterpret_cast<decltype(&a2av_mx_row_bytes)>(f)(features, format);
+}
+
+// A float [n].
+bool vector_of(PyObject* o, int64_t n, float** out) {
+  const at::Tensor* t = tensor_of(o);
+  if (!is_good(t, at::kFloat) || t->dim() != 1 || t->size(0) != n) return false;
+  *out = static_cast<float*>(t->data_ptr());
+  return true;
+}
+
+// An optional list of [rows[i], width].
+bool take_optional(PyObject* list, int W, at::ScalarType type, void** out, const int64_t* rows,
+                   int64_t width) {
+  return list == Py_None || take_rows(list, W, type, out, rows, width);
+}
+
+// The lists that a norm's calls begin with.
+struct Normed {
+  Call c;
+  at::ScalarType type;
+  int dtype;
+  int64_t rows[kRanks], H;
+  void* x[kRanks];
+  float *weight, eps;
+
+  bool take_all(PyObject* list, PyObject* w, PyObject* e) {
+    H = 0;
+    eps = (float)PyFloat_AsDouble(e);
+    return type_of(list, true, &type, &dtype) && take_any_rows(list, c.W, type, x, rows, &H) &&
+           vector_of(w, H, &weight);
+  }
+};
+
+// (..., x, weight, outputs, residual, sums, eps, format, a2av_mx_row_bytes)
+PyObject* norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  Normed m;
+  int format = A2AV_PLAIN;
+  void *out[kRanks], *residual[kRanks], *sums[kRanks];
+  return whole(
+      n, 12,
+      [&] {
+        if (!call_of(args, &m.c) || !m.take_all(args[4], args[5], args[9]) || !int_of(args[10], &format) ||
+            !take_optional(args[7], m.c.W, m.type, residual, m.rows, m.H) ||
+            !take_optional(args[8], m.c.W, m.type, sums, m.rows, m.H))
+          return false;
+        if (format == A2AV_PLAIN) return take_rows(args[6], m.c.W, m.type, out, m.rows, m.H);
+        return take_rows(args[6], m.c.W, at::kByte, out, m.rows, packed_bytes(args[11], m.H, format));
+      },
+      [&] {
+        return reinterpret_cast<decltype(&a2av_norm)>(m.c.function)(
+            static_cast<a2av_handle*>(m.c.handle), m.H, m.dtype, format, m.eps, m.x, m.rows, m.weight,
+            args[7] == Py_None ? nullptr : residual, args[8] == Py_None ? nullptr : sums, out,
+            m.c.stream);
+      });
+}
+
+// (..., sums, weight, d_outputs, d_x, d_weight, d_sums, eps, workspace,
+// a2av_norm_workspace_bytes); None as well where the workspace is too small.
+PyObject* norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  Normed m;
+  void *dy[kRanks], *dx[kRanks], *ds[kRanks], *workspace = nullptr;
+  float* d_weight = nullptr;
+  int64_t bytes = 0;
+  return whole(
+      n, 13,
+      [&] {
+        if (!call_of(args, &m.c) || !m.take_all(args[4], args[5], args[10]) ||
+            !take_rows(args[6], m.c.W, m.type, dy, m.rows, m.H) ||
+            !take_rows(args[7], m.c.W, m.type, dx, m.rows, m.H) ||
+            !take_optional(args[9], m.c.W, m.type, ds, m.rows, m.H))
+          return false;
+        if (args[8] == Py_None) return true;
+        const at::Tensor* t = tensor_of(args[11]);
+        void* size_of = PyLong_Check(args[12]) ? PyLong_AsVoidPtr(args[12]) : nullptr;
+        if (!vector_of(args[8], m.H, &d_weight) || !is_good(t, at::kByte) || size_of == nullptr)
+          return false;
+        int64_t total = 0;
+        for (int p = 0; p < m.c.W; ++p) total += m.rows[p];
+        workspace = t->data_ptr();
+        bytes = t->numel();
+        const int64_t need =
+            reinterpret_cast<decltype(&a2av_norm_workspace_bytes)>(size_of)(m.H, total);
+        return need > 0 && bytes >= need;
+      },
+      [&] {
+        return reinterpret_cast<decltype(&a2av_norm_backward)>(m.c.function)(
+            static_cast<a2av_handle*>(m.c.handle), m.H, m.dtype, m.eps, m.x, m.rows, m.weight, dy,
+            args[9] == Py_None ? nullptr : ds, dx, d_weight, workspace, bytes, m.c.stream);
+      });
+}
+
+// (..., rows to read, rows to write, format, a2av_mx_row_bytes); `back`: from packed ones.
+PyObject* packing(PyObject* const* args, Py_ssize_t n, bool back) {
+  Call c;
+  at::ScalarType type;
+  int dtype, format;
+  int64_t rows[kRanks], D = 0;
+  void *plain[kRanks], *packed[kRanks];
+  return whole(
+      n, 8,
+      [&] {
+        return call_of(args, &c) && type_of(args[back ? 5 : 4], true, &type, &dtype) &&
+               take_any_rows(args[back ? 5 : 4], c.W, type, plain, rows, &D) &&
+               int_of(args[6], &format) &&
+               take_rows(args[back ? 4 : 5], c.W, at::kByte, packed, rows,
+                         packed_bytes(args[7], D, format));
+      },
+      [&] {
+        // (the two have one signature)
+        return reinterpret_cast<decltype(&a2av_quantise)>(c.function)(
+            static_cast<a2av_handle*>(c.handle), D, dtype, format, back ? packed : plain, rows,
+            back ? plain : packed, c.stream);
+      });
+}
+PyObject* quantise(PyObject*, PyObject* const* args, Py_ssize_t n) { return packing(args, n, false); }
+PyObject* dequantise(PyObject*, PyObject* const* args, Py_ssize_t n) { return packing(args, n, true); }
+
+// (..., rows, counts, weights, outputs, in_features, format, activation, gated, bias,
+// residual, a2av_mx_row_bytes)
+PyObject* expert_matmul_mx(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  Call c;
+  a2av_expert_t shape;
+  at::ScalarType type;
+  int format, D;
+  int64_t held[kRanks], K = 0, Z, N = 0, bytes;
+  const int64_t* counts;
+  void *rows[kRanks], *weights[kRanks], *out[kRanks], *bias[kRanks], *residual[kRanks];
+  return whole(
+      n, 15,
+      [&] {
+        if (!call_of(args, &c) || !type_of(args[7], false, &type, &shape.dtype) ||
+            !take_any_rows(args[7], c.W, type, out, held, &N) || !int_of(args[8], &D) ||
+            !int_of(args[9], &format) || !int_of(args[10], &shape.activation))
+          return false;
+        bytes = packed_bytes(args[14], D, format);
+        shape.gated = PyObject_IsTrue(args[11]) == 1;
+        Z = shape.gated ? 2 * N : N;
+        if (!take_rows(args[4], c.W, at::kByte, rows, held, bytes) ||
+            !take(args[6], c.W, at::kByte, weights, [&](const at::Tensor& t, int i) {
+              if (t.dim() != 3 || (i > 0 && t.size(0) != K)) return false;
+              K = t.size(0);
+              return t.size(1) == Z && t.size(2) == bytes;
+            }) ||
+            K > INT_MAX || !matrix_of(args[5], c.W, c.W * K, &counts) ||
+            !take_optional(args[13], c.W, type, residual, held, N))
+          return false;
+        shape.experts_per_peer = (int)K;
+        shape.in_features = D;
+        shape.out_features = N;
+        return args[12] == Py_None || take(args[12], c.W, type, bias, [&](const at::Tensor& t, int) {
+                 return has_sizes(t, K, Z);
+               });
+      },
+      [&] {
+        return reinterpret_cast<decltype(&a2av_expert_matmul_mx)>(c.function)(
+            static_cast<a2av_handle*>(c.handle), &shape, format, rows, held, counts, weights,
+            args[12] == Py_None ? nullptr : bias, args[13] == Py_None ? nullptr : residual, out,
+            c.stream);
+      });
+}
+
 #define A2AV_WHOLE(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, "A whole call."}
 
@@ -543,6 +709,11 @@ PyMethodDef methods[] = {
     A2AV_WHOLE(expert_matmul_backward),
     A2AV_WHOLE(combine_weighted),
     A2AV_WHOLE(combine_weighted_backward),
+    A2AV_WHOLE(norm),
+    A2AV_WHOLE(norm_backward),
+    A2AV_WHOLE(quantise),
+    A2AV_WHOLE(dequantise),
+    A2AV_WHOLE(expert_matmul_mx),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,

@@ -1,0 +1,635 @@
+// norm.cu -- the root-mean-square norm with the residual's addition (a2av_norm),
+// its gradients, and packed rows (a2av_quantise, a2av_dequantise); the interface is
+// in include/a2av_mx.h.
+//
+// All are bound by memory: each row is read once and written once.  A block (a
+// warp, for short rows) takes a row, keeps it in registers between the sum of
+// squares and the result, and goes on to another; the weight stays in registers.
+#include "mx_device.cuh"
+
+namespace {
+
+struct NormParams {
+  const void* x[kW];         // backward: s
+  const void* residual[kW];  // or NULL; backward: d_sums
+  void* sums[kW];            // or NULL
+  void* out[kW];             // y; backward: d_x
+  const void* d_out[kW];     // backward: dy
+  long long first[kW + 1];   // tokens before each rank's
+  const float* weight;
+  float* part;               // backward: [blocks][H], or NULL
+  MxRow row;                 // of packed results
+  int W, H;
+  float eps;
+};
+
+// Token t of all ranks' (rank-major): its rank; *t becomes its number there.
+__device__ __forceinline__ int rank_of(const long long* first, long long* t) {
+  int r = 0;
+  while (first[r + 1] <= *t) ++r;
+  *t -= first[r];
+  return r;
+}
+
+// Sums of kSums values over a warp, or over the block.
+template <bool kWarp, int kSums>
+__device__ __forceinline__ void row_sum(float (&x)[kSums], float (*shared)[kSums]) {
+#pragma unroll
+  for (int i = 0; i < kSums; ++i)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x[i] += __shfl_xor_sync(kAll, x[i], o);
+  if constexpr (!kWarp) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
+    __syncthreads();  // (the row before has been summed by all)
+    if (lane == 0)
+#pragma unroll
+      for (int i = 0; i < kSums; ++i) shared[warp][i] = x[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) {
+      x[i] = lane < warps ? shared[lane][i] : 0.0f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x[i] += __shfl_xor_sync(kAll, x[i], o);
+    }
+  }
+}
+
+// Vectors of N elements, U a thread: thread i of the row's has i, i + threads, ...
+template <typename T, int N, int U, int kFormat, bool kWarp>
+__global__ void __launch_bounds__(kWarp ? 256 : 1024)
+    norm_kernel(const __grid_constant__ NormParams P) {
+  chain();
+  using Q = Piece<T, N>;
+  using V = typename Q::Raw;
+  __shared__ float sums[32][1];
+  const int threads = kWarp ? 32 : blockDim.x, i0 = kWarp ? threadIdx.x % 32 : threadIdx.x;
+  const int nv = P.H / N;
+  // vectors of a packed row, zeros behind the row's own
+  const int np = kFormat == A2AV_PLAIN ? nv : (int)P.row.scales * (kMxBlock / N);
+  const int per = kWarp ? blockDim.x / 32 : 1;
+  const long long rows = P.first[P.W], by = (long long)gridDim.x * per;
+  float w[U][N];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int v = i0 + u * threads;
+      w[u][i] = v < nv ? P.weight[v * N + i] : 0.0f;
+    }
+  for (long long g = (long long)blockIdx.x * per + (kWarp ? threadIdx.x / 32 : 0); g < rows; g += by) {
+    long long t = g;
+    const int r = rank_of(P.first, &t);
+    const V* x = reinterpret_cast<const V*>(static_cast<const T*>(P.x[r]) + t * P.H);
+    const V* res = reinterpret_cast<const V*>(static_cast<const T*>(P.residual[r]) + t * P.H);
+    V* kept = reinterpret_cast<V*>(static_cast<T*>(P.sums[r]) + t * P.H);
+    const bool add = P.residual[r] != nullptr, keep = P.sums[r] != nullptr;
+    V s[U], a[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = i0 + u * threads;
+      if (v < nv) s[u] = x[v];
+      if (v < nv && add) a[u] = res[v];
+    }
+    float total[1] = {0.0f};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = i0 + u * threads;
+      if (v < nv) {
+        float f[N];
+        Q::unpack(s[u], f);
+        if (add) {
+          float b[N];
+          Q::unpack(a[u], b);
+#pragma unroll
+          for (int i = 0; i < N; ++i) f[i] += b[i];
+          s[u] = Q::pack(f);
+          Q::unpack(s[u], f);
+        }
+        if (keep) kept[v] = s[u];
+#pragma unroll
+        for (int i = 0; i < N; ++i) total[0] += f[i] * f[i];
+      }
+    }
+    row_sum<kWarp, 1>(total, sums);
+    const float scale = __frsqrt_rn(total[0] / P.H + P.eps);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = i0 + u * threads;
+      float f[N];
+      if (v < nv) {
+        Q::unpack(s[u], f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] *= scale * w[u][i];
+      }
+      if constexpr (kFormat == A2AV_PLAIN) {
+        if (v < nv) reinterpret_cast<V*>(static_cast<T*>(P.out[r]) + t * P.H)[v] = Q::pack(f);
+      } else {
+        if (v >= nv)
+#pragma unroll
+          for (int i = 0; i < N; ++i) f[i] = 0.0f;
+        unsigned char* to = static_cast<unsigned char*>(P.out[r]) + t * P.row.bytes;
+        if (u * threads < np) mx_store<kFormat, N>(to, P.row.values, v, f, v < np);
+      }
+    }
+    if constexpr (kFormat != A2AV_PLAIN) {
+      const int used = (int)(P.row.values + P.row.scales);
+      unsigned char* to = static_cast<unsigned char*>(P.out[r]) + t * P.row.bytes;
+      if (used + i0 < P.row.bytes) to[used + i0] = 0;  // (31 at most)
+    }
+  }
+}
+
+// d_x, and a block's part of the weight's gradient, kept in registers over its
+// rows.
+template <typename T, int N, int U, bool kWarp>
+__global__ void __launch_bounds__(kWarp ? 256 : 1024)
+    norm_backward_kernel(const __grid_constant__ NormParams P) {
+  chain();
+  using Q = Piece<T, N>;
+  using V = typename Q::Raw;
+  __shared__ float sums[32][2];
+  const int threads = kWarp ? 32 : blockDim.x, i0 = kWarp ? threadIdx.x % 32 : threadIdx.x;
+  const int nv = P.H / N, per = kWarp ? blockDim.x / 32 : 1;
+  const long long rows = P.first[P.W], by = (long long)gridDim.x * per;
+  float w[U][N], dw[U][N];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int v = i0 + u * threads;
+      w[u][i] = v < nv ? P.weight[v * N + i] : 0.0f;
+      dw[u][i] = 0.0f;
+    }
+  for (long long g = (long long)blockIdx.x * per + (kWarp ? threadIdx.x / 32 : 0); g < rows; g += by) {
+    long long t = g;
+    const int r = rank_of(P.first, &t);
+    const V* x = reinterpret_cast<const V*>(static_cast<const T*>(P.x[r]) + t * P.H);
+    const V* dy = reinterpret_cast<const V*>(static_cast<const T*>(P.d_out[r]) + t * P.H);
+    const V* ds = reinterpret_cast<const V*>(static_cast<const T*>(P.residual[r]) + t * P.H);
+    V* out = reinterpret_cast<V*>(static_cast<T*>(P.out[r]) + t * P.H);
+    const bool add = P.residual[r] != nullptr;
+    V s[U], d[U], a[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = i0 + u * threads;
+      if (v < nv) {
+        s[u] = x[v];
+        d[u] = dy[v];
+        if (add) a[u] = ds[v];
+      }
+    }
+    float total[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * threads < nv) {
+        float f[N], e[N];
+        Q::unpack(s[u], f);
+        Q::unpack(d[u], e);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          total[0] += f[i] * f[i];
+          total[1] += f[i] * (e[i] * w[u][i]);
+        }
+      }
+    row_sum<kWarp, 2>(total, sums);
+    const float scale = __frsqrt_rn(total[0] / P.H + P.eps);
+    const float along = scale * scale * (total[1] / P.H);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = i0 + u * threads;
+      if (v < nv) {
+        float f[N], e[N], y[N];
+        Q::unpack(s[u], f);
+        Q::unpack(d[u], e);
+        if (add) Q::unpack(a[u], y);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          dw[u][i] += e[i] * (f[i] * scale);
+          const float z = scale * (e[i] * w[u][i] - f[i] * along);
+          y[i] = add ? y[i] + z : z;
+        }
+        out[v] = Q::pack(y);
+      }
+    }
+  }
+  if (P.part == nullptr) return;
+  if constexpr (kWarp) {  // the block's warps one after the other
+    __shared__ float all[32 * U * N];
+    for (int k = 0; k < per; ++k) {
+      if (threadIdx.x / 32 == k)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            float* at = all + (i0 + u * 32) * N + i;
+            *at = k == 0 ? dw[u][i] : *at + dw[u][i];
+          }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < P.H; c += blockDim.x) P.part[(long long)blockIdx.x * P.H + c] = all[c];
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = i0 + u * threads;
+      if (v < nv)
+#pragma unroll
+        for (int i = 0; i < N; ++i) P.part[(long long)blockIdx.x * P.H + v * N + i] = dw[u][i];
+    }
+  }
+}
+
+// The blocks' parts of 32 columns, summed by 32 warps and joined.
+__global__ void __launch_bounds__(1024) norm_weight_kernel(const float* part, int blocks, int H,
+                                                           float* d_weight) {
+  chain();
+  __shared__ float sums[32][33];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+  float sum = 0.0f;
+  if (c < H)
+#pragma unroll 4
+    for (int b = warp; b < blocks; b += 32) sum += part[(long long)b * H + c];
+  sums[warp][lane] = sum;
+  __syncthreads();
+  if (warp == 0 && c < H) {
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum += sums[i][lane];
+    d_weight[c] = sum;
+  }
+}
+
+// ---------------------------------------------------------- packed rows --
+struct PackParams {
+  const void* from[kW];
+  void* to[kW];
+  long long first[kW + 1];  // rows before each rank's
+  long long D;
+  MxRow row;
+  int W;
+};
+
+constexpr int kPackThreads = 256;
+
+// A warp takes 32 U neighbouring vectors of a row.
+template <typename T, int N, int U, int kFormat>
+__global__ void __launch_bounds__(kPackThreads) quantise_kernel(const __grid_constant__ PackParams P) {
+  chain();
+  using Q = Piece<T, N>;
+  using V = typename Q::Raw;
+  const int lane = threadIdx.x % 32;
+  const long long nv = P.D / N, np = P.row.scales * (kMxBlock / N);
+  const long long slices = (np + 32 * U - 1) / (32 * U), units = P.first[P.W] * slices;
+  const long long warps = (long long)gridDim.x * (kPackThreads / 32);
+  for (long long g = (long long)blockIdx.x * (kPackThreads / 32) + threadIdx.x / 32; g < units; g += warps) {
+    long long t = g / slices;
+    const long long slice = g - t * slices, v0 = slice * (32 * U) + lane;
+    const int r = rank_of(P.first, &t);
+    const V* x = reinterpret_cast<const V*>(static_cast<const T*>(P.from[r]) + t * P.D);
+    unsigned char* to = static_cast<unsigned char*>(P.to[r]) + t * P.row.bytes;
+    V s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (v0 + 32 * u < nv) s[u] = x[v0 + 32 * u];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long v = v0 + 32 * u;
+      float f[N] = {};
+      if (v < nv) Q::unpack(s[u], f);
+      if (v - lane < np) mx_store<kFormat, N>(to, P.row.values, v, f, v < np);
+    }
+    const long long used = P.row.values + P.row.scales;
+    if (slice == slices - 1 && used + lane < P.row.bytes) to[used + lane] = 0;
+  }
+}
+
+template <typename T, int N, int U, int kFormat>
+__global__ void __launch_bounds__(kPackThreads) dequantise_kernel(const __grid_constant__ PackParams P) {
+  chain();
+  using Q = Piece<T, N>;
+  using V = typename Q::Raw;
+  constexpr int kBits = kFormat == A2AV_MXFP8 ? 8 : 4;
+  const int lane = threadIdx.x % 32;
+  const long long nv = P.D / N;
+  const long long slices = (nv + 32 * U - 1) / (32 * U), units = P.first[P.W] * slices;
+  const long long warps = (long long)gridDim.x * (kPackThreads / 32);
+  for (long long g = (long long)blockIdx.x * (kPackThreads / 32) + threadIdx.x / 32; g < units; g += warps) {
+    long long t = g / slices;
+    const long long v0 = (g - t * slices) * (32 * U) + lane;
+    const int r = rank_of(P.first, &t);
+    const unsigned char* from = static_cast<const unsigned char*>(P.from[r]) + t * P.row.bytes;
+    V* out = reinterpret_cast<V*>(static_cast<T*>(P.to[r]) + t * P.D);
+    unsigned w[U][N * kBits >= 32 ? N * kBits / 32 : 1], s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long v = v0 + 32 * u;
+      if (v < nv) {
+        s[u] = from[P.row.values + v * N / kMxBlock];
+        if constexpr (N == 1) {
+          w[u][0] = from[v * kBits / 8] >> (kBits == 4 ? v % 2 * 4 : 0);
+        } else if constexpr (N * kBits == 64) {
+          const uint2 c = reinterpret_cast<const uint2*>(from)[v];
+          w[u][0] = c.x;
+          w[u][1] = c.y;
+        } else if constexpr (N * kBits == 32) {
+          w[u][0] = reinterpret_cast<const unsigned*>(from)[v];
+        } else {
+          w[u][0] = reinterpret_cast<const unsigned short*>(from)[v];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long v = v0 + 32 * u;
+      if (v < nv) {
+        const float by = mx_scale_value(s[u]);
+        float f[N];
+        if constexpr (N == 1) {
+          f[0] = by * (kBits == 8 ? e4m3_values(w[u][0]) : e2m1_values(w[u][0])).x;
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; i += 2) {
+            const unsigned c = w[u][i * kBits / 32] >> (i * kBits % 32);
+            const float2 p = kBits == 8 ? e4m3_values(c) : e2m1_values(c);
+            f[i] = by * p.x;
+            f[i + 1] = by * p.y;
+          }
+        }
+        out[v] = Q::pack(f);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------ host side --
+// Copies a list of W pointers of ranks that have rows; the bits below their common
+// alignment go to *low.
+bool take_rows(const void** to, const void* const* from, int W, const int64_t* rows, int size,
+               uintptr_t* low) {
+  for (int r = 0; r < W; ++r) {
+    to[r] = rows[r] > 0 ? from[r] : nullptr;
+    if ((rows[r] > 0 && to[r] == nullptr) || !aligned_to(to[r], size)) return false;
+    *low |= (uintptr_t)to[r];
+  }
+  return true;
+}
+
+bool take_rows(void** to, void* const* from, int W, const int64_t* rows, int size, uintptr_t* low) {
+  return take_rows(const_cast<const void**>(to), from, W, rows, size, low);
+}
+
+// Rows before each rank's.
+int count_rows(const a2av_handle* h, const int64_t* rows, long long* first) {
+  for (int r = 0; r < h->W; ++r) {
+    if (rows[r] < 0) return A2AV_ERR_INVALID_ARG;
+    if (rows[r] > kMaxCount - first[r]) return A2AV_ERR_UNSUPPORTED;
+    first[r + 1] = first[r] + rows[r];
+  }
+  return A2AV_OK;
+}
+
+bool is_packed(int format) { return format == A2AV_MXFP8 || format == A2AV_MXFP4; }
+
+constexpr int kNormParts = 1024;  // most blocks that keep a part of the weight's gradient
+
+using NormKernel = void (*)(NormParams);
+
+// How a norm's rows are shared out: `vector` of 16 bytes' elements or one; a warp
+// a row where it can hold one.
+constexpr int kHeld = 4, kHeldScalar = 16;  // vectors a thread keeps
+
+struct NormForm {
+  bool vector, warp;
+  int threads;  // of a block
+};
+
+NormForm norm_form(int64_t H, int size, uintptr_t low, long long rows, int sms) {
+  NormForm f;
+  f.vector = low % 16 == 0 && H * size % 16 == 0;
+  const long long nv = f.vector ? H * size / 16 : H;
+  const int held = f.vector ? kHeld : kHeldScalar;
+  f.warp = nv <= 32 * held;
+  f.threads = 256;
+  if (!f.warp) {
+    long long threads = (nv + held - 1) / held;
+    f.threads = (int)((threads + 31) / 32 * 32);
+    // few rows: every thread of a block has one vector
+    if (rows < 2 * sms) f.threads = (int)((nv < 1024 ? nv : 1024) + 31) / 32 * 32;
+  }
+  return f;
+}
+
+template <typename T, int kFormat>
+NormKernel norm_kernel_of(const NormForm& f) {
+  constexpr int N = 16 / sizeof(T);
+  if (f.vector) return f.warp ? norm_kernel<T, N, kHeld, kFormat, true> : norm_kernel<T, N, kHeld, kFormat, false>;
+  return f.warp ? norm_kernel<T, 1, kHeldScalar, kFormat, true>
+                : norm_kernel<T, 1, kHeldScalar, kFormat, false>;
+}
+
+template <typename T>
+NormKernel norm_kernel_of(int format, const NormForm& f) {
+  if (format == A2AV_MXFP8) return norm_kernel_of<T, A2AV_MXFP8>(f);
+  return format == A2AV_MXFP4 ? norm_kernel_of<T, A2AV_MXFP4>(f) : norm_kernel_of<T, A2AV_PLAIN>(f);
+}
+
+template <typename T>
+NormKernel norm_backward_kernel_of(const NormForm& f) {
+  constexpr int N = 16 / sizeof(T);
+  if (f.vector) return f.warp ? norm_backward_kernel<T, N, kHeld, true> : norm_backward_kernel<T, N, kHeld, false>;
+  return f.warp ? norm_backward_kernel<T, 1, kHeldScalar, true>
+                : norm_backward_kernel<T, 1, kHeldScalar, false>;
+}
+
+// The blocks that share `rows` rows: as many as the GPU holds, and not more than
+// the rows need.
+cudaError_t blocks_of(const a2av_handle* h, const void* kernel, const NormForm& f, long long rows,
+                      unsigned* blocks) {
+  int fit = 0;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, f.threads, 0);
+  const long long most = (long long)fit * h->sms, per = f.warp ? f.threads / 32 : 1;
+  const long long want = (rows + per - 1) / per;
+  *blocks = (unsigned)(want < most ? want : most);
+  return e;
+}
+
+int norm_ok(const a2av_handle* h, int64_t features, int dtype, float eps, const void* x,
+            const int64_t* tokens, const float* weight, const void* out) {
+  if (h == nullptr || x == nullptr || tokens == nullptr || weight == nullptr || out == nullptr ||
+      features < 1 || dtype_bytes(dtype) == 0 || !(eps >= 0.0f) || eps > 3.4e38f || !aligned_to(weight, 4))
+    return A2AV_ERR_INVALID_ARG;
+  return features > A2AV_MAX_NORM_FEATURES ? A2AV_ERR_UNSUPPORTED : A2AV_OK;
+}
+
+using PackKernel = void (*)(PackParams);
+constexpr int kPackVectors = 4;
+
+template <typename T, int kFormat>
+PackKernel pack_kernel_of(bool vector, bool back) {
+  constexpr int N = 16 / sizeof(T);
+  if (back)
+    return vector ? dequantise_kernel<T, N, kPackVectors, kFormat> : dequantise_kernel<T, 1, 8, kFormat>;
+  return vector ? quantise_kernel<T, N, kPackVectors, kFormat> : quantise_kernel<T, 1, 8, kFormat>;
+}
+
+template <typename T>
+PackKernel pack_kernel_of(int format, bool vector, bool back) {
+  return format == A2AV_MXFP8 ? pack_kernel_of<T, A2AV_MXFP8>(vector, back)
+                              : pack_kernel_of<T, A2AV_MXFP4>(vector, back);
+}
+
+// Both directions; `plain` and `packed` are the buffers' lists.
+int pack_call(a2av_handle* h, int64_t features, int dtype, int format, const void* const* plain,
+              const int64_t* rows, const void* const* packed, bool back, void* stream) {
+  const int size = dtype_bytes(dtype);
+  if (h == nullptr || plain == nullptr || rows == nullptr || packed == nullptr || features < 1 ||
+      size == 0 || !is_packed(format))
+    return A2AV_ERR_INVALID_ARG;
+  if (features > A2AV_MAX_MX_FEATURES) return A2AV_ERR_UNSUPPORTED;
+  PackParams P;
+  std::memset(&P, 0, sizeof(P));
+  int rc = count_rows(h, rows, P.first);
+  if (rc != A2AV_OK) return rc;
+  uintptr_t low = (uintptr_t)(features * size), other = 0;
+  const void** from = P.from;
+  const void** to = const_cast<const void**>(P.to);
+  if (!take_rows(back ? to : from, plain, h->W, rows, size, &low) ||
+      !take_rows(back ? from : to, packed, h->W, rows, 16, &other))
+    return A2AV_ERR_INVALID_ARG;
+  rc = current_device(h);
+  if (rc != A2AV_OK) return rc;
+  if (P.first[h->W] == 0) return A2AV_OK;
+  P.W = h->W;
+  P.D = features;
+  P.row = mx_row(features, format);
+  const bool vector = low % 16 == 0;
+  const PackKernel kernel = dtype == A2AV_F32    ? pack_kernel_of<float>(format, vector, back)
+                            : dtype == A2AV_BF16 ? pack_kernel_of<__nv_bfloat16>(format, vector, back)
+                                                 : pack_kernel_of<__half>(format, vector, back);
+  int fit = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, kPackThreads, 0) != cudaSuccess)
+    return A2AV_ERR_CUDA;
+  const long long vectors = vector ? features * size / 16 : features, warps = kPackThreads / 32;
+  const long long slice = 32 * (vector ? kPackVectors : 8);
+  const long long slices = (vectors + slice - 1) / slice;
+  const long long want = (P.first[h->W] * slices + warps - 1) / warps, most = (long long)fit * h->sms;
+  const cudaError_t e = launch_chained(kernel, dim3((unsigned)(want < most ? want : most)), kPackThreads, 0,
+                                       static_cast<cudaStream_t>(stream), h->pdl, P);
+  return e != cudaSuccess || cudaGetLastError() != cudaSuccess ? A2AV_ERR_CUDA : A2AV_OK;
+}
+
+}  // namespace
+
+extern "C" int64_t a2av_mx_row_bytes(int64_t features, int format) {
+  if (features < 1 || features > A2AV_MAX_MX_FEATURES || !is_packed(format)) return -1;
+  return mx_row(features, format).bytes;
+}
+
+extern "C" int a2av_norm(a2av_handle* h, int64_t features, int dtype, int format, float eps,
+                         const void* const* x_ptrs, const int64_t* tokens_per_rank,
+                         const float* weight_dev, const void* const* residual_ptrs,
+                         void* const* sum_ptrs, void* const* out_ptrs, void* stream) {
+  int rc = norm_ok(h, features, dtype, eps, x_ptrs, tokens_per_rank, weight_dev, out_ptrs);
+  if (rc != A2AV_OK) return rc;
+  if (format != A2AV_PLAIN && !is_packed(format)) return A2AV_ERR_INVALID_ARG;
+  NormParams P;
+  std::memset(&P, 0, sizeof(P));
+  rc = count_rows(h, tokens_per_rank, P.first);
+  if (rc != A2AV_OK) return rc;
+  const int W = h->W, size = dtype_bytes(dtype);
+  uintptr_t low = 0, other = 0;
+  if (!take_rows(P.x, x_ptrs, W, tokens_per_rank, size, &low) ||
+      (residual_ptrs != nullptr && !take_rows(P.residual, residual_ptrs, W, tokens_per_rank, size, &low)) ||
+      (sum_ptrs != nullptr && !take_rows(P.sums, sum_ptrs, W, tokens_per_rank, size, &low)) ||
+      !take_rows(P.out, out_ptrs, W, tokens_per_rank, format == A2AV_PLAIN ? size : 16,
+                 format == A2AV_PLAIN ? &low : &other))
+    return A2AV_ERR_INVALID_ARG;
+  rc = current_device(h);
+  if (rc != A2AV_OK) return rc;
+  const long long rows = P.first[W];
+  if (rows == 0) return A2AV_OK;
+  P.weight = weight_dev;
+  if (format != A2AV_PLAIN) P.row = mx_row(features, format);
+  P.W = W;
+  P.H = (int)features;
+  P.eps = eps;
+  const NormForm f = norm_form(features, size, low, rows, h->sms);
+  const NormKernel kernel = dtype == A2AV_F32    ? norm_kernel_of<float>(format, f)
+                            : dtype == A2AV_BF16 ? norm_kernel_of<__nv_bfloat16>(format, f)
+                                                 : norm_kernel_of<__half>(format, f);
+  unsigned blocks;
+  if (blocks_of(h, reinterpret_cast<const void*>(kernel), f, rows, &blocks) != cudaSuccess)
+    return A2AV_ERR_CUDA;
+  const cudaError_t e = launch_chained(kernel, dim3(blocks), f.threads, 0,
+                                       static_cast<cudaStream_t>(stream), h->pdl, P);
+  return e != cudaSuccess || cudaGetLastError() != cudaSuccess ? A2AV_ERR_CUDA : A2AV_OK;
+}
+
+extern "C" int64_t a2av_norm_workspace_bytes(int64_t features, int64_t total_rows) {
+  if (features < 1 || features > A2AV_MAX_NORM_FEATURES || total_rows < 0 || total_rows > kMaxCount)
+    return -1;
+  return (total_rows < kNormParts ? total_rows : kNormParts) * features * 4;
+}
+
+extern "C" int a2av_norm_backward(a2av_handle* h, int64_t features, int dtype, float eps,
+                                  const void* const* sum_ptrs, const int64_t* tokens_per_rank,
+                                  const float* weight_dev, const void* const* d_out_ptrs,
+                                  const void* const* d_sum_ptrs, void* const* d_x_ptrs,
+                                  float* d_weight_dev, void* workspace, int64_t workspace_bytes,
+                                  void* stream) {
+  int rc = norm_ok(h, features, dtype, eps, sum_ptrs, tokens_per_rank, weight_dev, d_x_ptrs);
+  if (rc != A2AV_OK) return rc;
+  if (d_out_ptrs == nullptr || !aligned_to(d_weight_dev, 4)) return A2AV_ERR_INVALID_ARG;
+  NormParams P;
+  std::memset(&P, 0, sizeof(P));
+  rc = count_rows(h, tokens_per_rank, P.first);
+  if (rc != A2AV_OK) return rc;
+  const int W = h->W, size = dtype_bytes(dtype);
+  uintptr_t low = 0;
+  if (!take_rows(P.x, sum_ptrs, W, tokens_per_rank, size, &low) ||
+      !take_rows(P.d_out, d_out_ptrs, W, tokens_per_rank, size, &low) ||
+      (d_sum_ptrs != nullptr && !take_rows(P.residual, d_sum_ptrs, W, tokens_per_rank, size, &low)) ||
+      !take_rows(P.out, d_x_ptrs, W, tokens_per_rank, size, &low))
+    return A2AV_ERR_INVALID_ARG;
+  const long long rows = P.first[W];
+  if (d_weight_dev != nullptr) {
+    const int64_t need = a2av_norm_workspace_bytes(features, rows);
+    if (workspace_bytes < need || !aligned_to(workspace, 256) || (need > 0 && workspace == nullptr))
+      return A2AV_ERR_INVALID_ARG;
+    P.part = static_cast<float*>(workspace);
+  }
+  rc = current_device(h);
+  if (rc != A2AV_OK) return rc;
+  P.weight = weight_dev;
+  P.W = W;
+  P.H = (int)features;
+  P.eps = eps;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  unsigned blocks = 0;
+  if (rows > 0) {
+    const NormForm f = norm_form(features, size, low, rows, h->sms);
+    const NormKernel kernel = dtype == A2AV_F32    ? norm_backward_kernel_of<float>(f)
+                              : dtype == A2AV_BF16 ? norm_backward_kernel_of<__nv_bfloat16>(f)
+                                                   : norm_backward_kernel_of<__half>(f);
+    if (blocks_of(h, reinterpret_cast<const void*>(kernel), f, rows, &blocks) != cudaSuccess)
+      return A2AV_ERR_CUDA;
+    if (blocks > (unsigned)kNormParts) blocks = kNormParts;
+    e = launch_chained(kernel, dim3(blocks), f.threads, 0, s, h->pdl, P);
+  }
+  if (e == cudaSuccess && d_weight_dev != nullptr)
+    e = launch_chained(norm_weight_kernel, dim3((unsigned)((features + 31) / 32)), 1024, 0, s, h->pdl,
+                       (const float*)P.part, (int)blocks, (int)features, d_weight_dev);
+  return e != cudaSuccess || cudaGetLastError() != cudaSuccess ? A2AV_ERR_CUDA : A2AV_OK;
+}
+
+extern "C" int a2av_quantise(a2av_handle* h, int64_t features, int dtype, int format,
+                             const void* const* x_ptrs, const int64_t* rows_per_rank,
+                             void* const* packed_ptrs, void* stream) {
+  return pack_call(h, features, dtype, format, x_ptrs, rows_per_rank, packed_ptrs, false, stream);
+}
+
+extern "C" int a2av_dequantise(a2av_handle* h, int64_t features, int dtype, int format,
+                               const void* const* packed_ptrs, const int64_t* rows_per_rank,
+                               void* const* out_ptrs, void* stream) {
+  return pack_call(h, features, dtype, format, out_ptrs, rows_per_rank, packed_ptrs, true, stream);
+}
