@@ -12,7 +12,7 @@ SOURCES = [os.path.join(PKG, "csrc", f) for f in ("a2av.cu", "dispatch.cu", "rou
                                                   "experts_mma.cu", "experts_mx.cu", "norm.cu",
                                                   "weighted.cu")]
 HEADERS = [os.path.join(PKG, "csrc", f) for f in ("a2av_device.cuh", "a2av_handle.h",
-                                                  "moe_device.cuh", "experts.cuh", "mma.cuh",
+                                                  "moe_device.cuh", "experts.cuh", "experts_tile.cuh", "mma.cuh",
                                                   "mx_device.cuh")]
 INCLUDE = os.path.join(ROOT, "include")
 INTERFACES = [os.path.join(INCLUDE, f) for f in ("a2av.h", "a2av_moe.h", "a2av_mx.h")]

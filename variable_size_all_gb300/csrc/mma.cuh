@@ -78,6 +78,12 @@ __device__ __forceinline__ void bar_arrive_tx(uint32_t bar, unsigned bytes) {
                : "memory");
 }
 
+// The same with this thread's writes (and those of the threads it has synchronised
+// with) published, to shared memory alone where the thread has no others.
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // Whether a phase of a barrier of this CTA is complete (waits a little for it).
 __device__ __forceinline__ bool bar_try(uint32_t bar, unsigned parity) {
   unsigned done;
@@ -104,11 +110,43 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, unsigned parity) {
   return done != 0;
 }
 
+// Both for a phase that another CTA's bar_arrive_cluster completes.
+__device__ __forceinline__ bool bar_try_cluster(uint32_t bar, unsigned parity) {
+  unsigned done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool bar_test_cluster(uint32_t bar, unsigned parity) {
+  unsigned done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Waits for a phase of a barrier of this CTA; false after about a second.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, unsigned parity) {
   if (bar_try(bar, parity)) return true;
   const long long start = clock64();
   while (!bar_try(bar, parity))
+    if (clock64() - start > kMmaWaitCycles) return false;
+  return true;
+}
+
+__device__ __forceinline__ bool bar_wait_cluster(uint32_t bar, unsigned parity) {
+  if (bar_try_cluster(bar, parity)) return true;
+  const long long start = clock64();
+  while (!bar_try_cluster(bar, parity))
     if (clock64() - start > kMmaWaitCycles) return false;
   return true;
 }
@@ -155,6 +193,11 @@ __device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 
+// This thread's writes to shared memory, before what tensor cores and copies read of it.
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // -------------------------------------------------------------- tcgen05 --
 __device__ __forceinline__ void tmem_alloc(uint32_t to, unsigned columns) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to),
@@ -173,6 +216,39 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
       "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"((unsigned)add), "r"((unsigned)issue)
+      : "memory");
+}
+
+// Products of 8-bit (e4m3, 32 a step) or 4-bit operands (e2m1, 64) with a scale for
+// each 32 of either side, in TMEM at `a_scale` and `b_scale`: the scales of a step are
+// the bytes that idesc names of the words there.
+template <bool k4Bit>
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t a_scale, uint32_t b_scale, bool add, bool issue) {
+  if constexpr (k4Bit)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], "
+        "p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"((unsigned)add), "r"((unsigned)issue)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"((unsigned)add), "r"((unsigned)issue)
+        : "memory");
+}
+
+// 32 rows of 16 bytes of each CTA's shared memory (512 bytes in a row) to four
+// columns of its TMEM, row i to lane i of each of the four quarters of the lanes.
+// It is done before the products that the thread issues after it, and after those before.
+__device__ __forceinline__ void tmem_copy(uint32_t to, uint64_t from, bool issue) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(to),
+      "l"(from), "r"((unsigned)issue)
       : "memory");
 }
 
@@ -236,6 +312,30 @@ __device__ __forceinline__ uint32_t product(bool bf16, bool a_mn, bool b_mn, int
   d |= (uint32_t)(n >> 3) << 17;
   d |= (uint32_t)(m >> 4) << 24;
   return d;
+}
+
+// What tmem_copy reads: rows of 16 bytes, eight of them 128 bytes.
+__device__ __forceinline__ uint64_t scale_rows(uint32_t addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr & 0x3ffff) >> 4);
+  d |= (uint64_t)(128 >> 4) << 32;
+  d |= (uint64_t)1 << 46;  // descriptor version of this architecture; no swizzle
+  return d;
+}
+
+// Operands of mma_scaled, both K-major; scales are powers of two.  A step's scales
+// are at byte `id` of their words.
+__device__ __forceinline__ uint32_t product_scaled(bool four_bit, int m, int n) {
+  uint32_t d = 0;
+  d |= (four_bit ? 1u : 0u) << 7;   // A: e2m1 of its kind, or e4m3
+  d |= (four_bit ? 1u : 0u) << 10;  // B
+  d |= (uint32_t)(n >> 3) << 17;
+  d |= 1u << 23;                    // scales of eight bits of exponent
+  d |= (uint32_t)(m >> 4) << 24;
+  return d;
+}
+__device__ __forceinline__ uint32_t with_scales(uint32_t product, unsigned id) {
+  return product | id << 4 | id << 29;  // B's and A's
 }
 
 // 8 x 8 matrices of 16-bit elements between registers (lane l: row l / 4,
