@@ -25,7 +25,8 @@ constexpr int kAccColumns = 256;      // columns between the two tiles' sums
 constexpr int kScaleWarps = 3;        // 128 features, 128 rows and the other rows
 constexpr int kAtom = 512;            // bytes of 128 rows' words of scales
 constexpr int kMxThreads = 128 + 32 * (kEpilogueWarps + kScaleWarps);
-constexpr int kAhead = 3;             // 16-byte pieces of scales that a lane has in flight
+constexpr int kAhead = 3;             // 16-byte pieces of a row's scales in flight
+constexpr int kHeld = kAhead * 128 * 16;  // of a scale warp's rows
 
 // Words of scales that a stage has of each row.
 template <int kFormat>
@@ -34,7 +35,7 @@ template <int kFormat>
 constexpr int kScaleBytes = kScaleWords<kFormat> * kScaleWarps * kAtom;  // of a stage
 template <int kFormat>
 constexpr size_t kMxSmem = 1024 + (size_t)kMxStages * (kStageBytes + kScaleBytes<kFormat>) +
-                           kEpilogueWarps * kStaging;
+                           kEpilogueWarps * kStaging + kScaleWarps * kHeld;
 
 struct MxParams {
   CUtensorMap rows[kBoxes][kW];  // [rows][bytes of values] in boxes of 1, 2 .. 16 granules
@@ -193,13 +194,13 @@ __global__ void __launch_bounds__(kMxThreads, 1) __cluster_dims__(2, 1, 1)
       for (int kb = 0; kb < blocks; ++kb, ++it) {
         const unsigned s = it % kMxStages;
         if (!__all_sync(kAll, ready)) {
-          ok = __all_sync(kAll, bar_wait_cluster(smem_addr(&b.full[s]), (it / kMxStages) & 1));
+          ok = __all_sync(kAll, bar_wait(smem_addr(&b.full[s]), (it / kMxStages) & 1));
           if (!ok) break;
         }
         fence_after_sync();
         // (the next stage is looked at while this one's products are issued)
         const unsigned next = (it + 1) % kMxStages;
-        ready = bar_test_cluster(smem_addr(&b.full[next]), ((it + 1) / kMxStages) & 1);
+        ready = bar_test(smem_addr(&b.full[next]), ((it + 1) / kMxStages) & 1);
         // the stage's scales, in turn behind the one and the other tile's sums: a
         // column for every 32 rows, the features' words first
         const uint32_t sa = tmem + (it & 1) * kAccColumns + kMxColumns, sb = sa + 4 * kWords;
@@ -231,6 +232,8 @@ __global__ void __launch_bounds__(kMxThreads, 1) __cluster_dims__(2, 1, 1)
     // a lane has rows lane, 32 + lane, 64 + lane and 96 + lane of the warp's 128
     const int part = warp - 4 - kEpilogueWarps;
     const uint32_t full0 = map_to(smem_addr(&b.full[0]), 0);
+    const uint32_t held = scales + kMxStages * kScaleBytes<kFormat> + kEpilogueWarps * kStaging +
+                          part * kHeld + lane * 16;
     constexpr int kPer = 4 / kWords;  // stages that a piece lasts
     const int count = (int)P.at.scales, pieces = (count + 15) / 16;
     unsigned it = 0;
@@ -262,50 +265,58 @@ __global__ void __launch_bounds__(kMxThreads, 1) __cluster_dims__(2, 1, 1)
       }
       any = __any_sync(kAll, any);
       if (lane == 0) bar_arrive_here(smem_addr(&b.slot_empty[sl]));
-      uint4 v[kAhead][4];
-      const auto load = [&](uint4(&to)[4], int c) {
+      // pieces come through a ring of the lane's own, so that several are in flight
+      const auto fetch = [&](int c) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool here = from[k] != nullptr && c < pieces;
+          copy_async(held + (c % kAhead * 4 + k) * 512, here ? from[k] + c : static_cast<const uint4*>(P.w[p]),
+                     here ? 16 : 0);
+        }
+        copy_async_commit();
+      };
+      for (int c = 0; c < kAhead; ++c) fetch(c);
+      for (int c = 0; ok && c < pieces; ++c) {
+        copy_async_wait<kAhead - 1>();
+        uint4 v[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          to[k] = from[k] != nullptr && c < pieces ? __ldg(from[k] + c) : make_uint4(0, 0, 0, 0);
-      };
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w)
+                       : "r"(held + (c % kAhead * 4 + k) * 512)
+                       : "memory");
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) load(v[a], a);
-      for (int c0 = 0; ok && c0 < pieces; c0 += kAhead) {
+        for (int j = 0; j < kPer; ++j) {
+          if (!ok || c * kPer + j >= blocks) continue;
+          const unsigned s = it % kMxStages;
+          ok = __all_sync(kAll, bar_wait(smem_addr(&b.empty[s]), ((it / kMxStages) & 1) ^ 1));
+          if (!ok) continue;
+          if (any) {
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-          const int c = c0 + a;
+            for (int w = 0; w < kWords; ++w) {
+              const int word = j * kWords + w;
+              uint32_t x[4];
 #pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            if (!ok || c * kPer + j >= blocks) continue;
-            const unsigned s = it % kMxStages;
-            ok = __all_sync(kAll, bar_wait(smem_addr(&b.empty[s]), ((it / kMxStages) & 1) ^ 1));
-            if (!ok) continue;
-            if (any) {
-#pragma unroll
-              for (int w = 0; w < kWords; ++w) {
-                const int word = j * kWords + w;
-                uint32_t x[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  x[k] = word == 0 ? v[a][k].x : word == 1 ? v[a][k].y : word == 2 ? v[a][k].z : v[a][k].w;
-                // (what follows the scales is no scale: products with its zeros stay 0)
-                const int valid = count - 16 * c - 4 * word;
-                const uint32_t mask = valid >= 4 ? ~0u : valid <= 0 ? 0u : (1u << (8 * valid)) - 1;
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                 scales + s * kScaleBytes<kFormat> + (w * kScaleWarps + part) * kAtom + lane * 16),
-                             "r"(x[0] & mask), "r"(x[1] & mask), "r"(x[2] & mask), "r"(x[3] & mask)
-                             : "memory");
-              }
-              fence_async_shared();
+              for (int k = 0; k < 4; ++k)
+                x[k] = word == 0 ? v[k].x : word == 1 ? v[k].y : word == 2 ? v[k].z : v[k].w;
+              // (what follows the scales is no scale: products with its zeros stay 0)
+              const int valid = count - 16 * c - 4 * word;
+              const uint32_t mask = valid >= 4 ? ~0u : valid <= 0 ? 0u : (1u << (8 * valid)) - 1;
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               scales + s * kScaleBytes<kFormat> + (w * kScaleWarps + part) * kAtom + lane * 16),
+                           "r"(x[0] & mask), "r"(x[1] & mask), "r"(x[2] & mask), "r"(x[3] & mask)
+                           : "memory");
             }
-            __syncwarp();
-            if (lane == 0) bar_arrive_cluster(full0 + s * 8);
-            ++it;
+            fence_async_shared();
           }
-          if (c + kAhead < pieces) load(v[a], c + kAhead);
+          __syncwarp();
+          if (lane == 0) bar_arrive_filled(full0 + s * 8);
+          ++it;
         }
+        fetch(c + kAhead);
       }
     }
+    copy_async_wait<0>();
     if (!ok && lane == 0) note_error(P.g.status, A2AV_ERR_TIMEOUT);
   } else if (warp >= 4) {
     // ---------------------------------------------------- epilogue --

@@ -78,10 +78,11 @@ __device__ __forceinline__ void bar_arrive_tx(uint32_t bar, unsigned bytes) {
                : "memory");
 }
 
-// The same with this thread's writes (and those of the threads it has synchronised
-// with) published, to shared memory alone where the thread has no others.
-__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// The same for what threads of this CTA have written to its own shared memory, for
+// copies and tensor cores to read there (each after fence_async_shared): a release in
+// the CTA.  (One at the cluster's scope also waits for memory: 1.1 us for every stage.)
+__device__ __forceinline__ void bar_arrive_filled(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // Whether a phase of a barrier of this CTA is complete (waits a little for it).
@@ -110,43 +111,11 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, unsigned parity) {
   return done != 0;
 }
 
-// Both for a phase that another CTA's bar_arrive_cluster completes.
-__device__ __forceinline__ bool bar_try_cluster(uint32_t bar, unsigned parity) {
-  unsigned done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-__device__ __forceinline__ bool bar_test_cluster(uint32_t bar, unsigned parity) {
-  unsigned done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
 // Waits for a phase of a barrier of this CTA; false after about a second.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, unsigned parity) {
   if (bar_try(bar, parity)) return true;
   const long long start = clock64();
   while (!bar_try(bar, parity))
-    if (clock64() - start > kMmaWaitCycles) return false;
-  return true;
-}
-
-__device__ __forceinline__ bool bar_wait_cluster(uint32_t bar, unsigned parity) {
-  if (bar_try_cluster(bar, parity)) return true;
-  const long long start = clock64();
-  while (!bar_try_cluster(bar, parity))
     if (clock64() - start > kMmaWaitCycles) return false;
   return true;
 }
@@ -191,6 +160,17 @@ __device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap* map, 
       ".cta_group::2 [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(bar)
       : "memory");
+}
+
+// 16 bytes, or zeros for size 0, to this thread's place in shared memory; the copies
+// committed so far but the last kLeft groups of them are there.
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, int size) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(size) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
 // This thread's writes to shared memory, before what tensor cores and copies read of it.
