@@ -20,6 +20,7 @@ struct NormParams {
   float* part;               // backward: [blocks][H], or NULL
   MxRow row;                 // of packed results
   int W, H;
+  int ahead;                 // arrays whose rows are fetched ahead, 0: they are not
   float eps;
 };
 
@@ -31,7 +32,8 @@ __device__ __forceinline__ int rank_of(const long long* first, long long* t) {
   return r;
 }
 
-// Sums of kSums values over a warp, or over the block.
+// Sums of kSums values over a warp, or over the block: `shared` is not that of the
+// row before, whose sums others may still be reading.
 template <bool kWarp, int kSums>
 __device__ __forceinline__ void row_sum(float (&x)[kSums], float (*shared)[kSums]) {
 #pragma unroll
@@ -40,7 +42,6 @@ __device__ __forceinline__ void row_sum(float (&x)[kSums], float (*shared)[kSums
     for (int o = 16; o > 0; o >>= 1) x[i] += __shfl_xor_sync(kAll, x[i], o);
   if constexpr (!kWarp) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
-    __syncthreads();  // (the row before has been summed by all)
     if (lane == 0)
 #pragma unroll
       for (int i = 0; i < kSums; ++i) shared[warp][i] = x[i];
@@ -49,25 +50,93 @@ __device__ __forceinline__ void row_sum(float (&x)[kSums], float (*shared)[kSums
     for (int i = 0; i < kSums; ++i) {
       x[i] = lane < warps ? shared[lane][i] : 0.0f;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) x[i] += __shfl_xor_sync(kAll, x[i], o);
+      for (int o = 8; o > 0; o >>= 1) x[i] += __shfl_xor_sync(kAll, x[i], o);
+      x[i] = __shfl_sync(kAll, x[i], 0);
     }
   }
 }
 
-// Vectors of N elements, U a thread: thread i of the row's has i, i + threads, ...
-template <typename T, int N, int U, int kFormat, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 256 : 1024)
-    norm_kernel(const __grid_constant__ NormParams P) {
+// How a row lies on its threads: vectors of N elements, U a thread, thread i having
+// the vectors i, i + threads, ...
+constexpr int kHeldValues = 32;  // of a row in a thread
+template <typename T, bool kVector>
+constexpr int kVectorSize = kVector ? 16 / sizeof(T) : 1;
+
+// What a thread has of the next row of `arrays` arrays, on its way to a place of its
+// own in shared memory while it works on this one (rows of vectors): two rows of them,
+// U vectors a thread each.
+template <typename V, int U>
+struct Ahead {
+  V* place;
+  int arrays, stage;
+  __device__ __forceinline__ V* at(int stage, int row, int u) const {
+    return place + ((stage * arrays + row) * U + u) * blockDim.x;
+  }
+  __device__ __forceinline__ void fetch(int row, const V* from, int i0, int threads, int nv) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = i0 + u * threads;
+      if (v < nv) {
+        const unsigned to = (unsigned)__cvta_generic_to_shared(at(stage, row, u));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from + v) : "memory");
+      }
+    }
+  }
+  // All that was fetched before the last commit is there; the next goes to the other half.
+  __device__ __forceinline__ void commit_and_wait() {
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 1;" ::: "memory");
+    stage ^= 1;
+  }
+  __device__ __forceinline__ void commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    stage ^= 1;
+  }
+};
+
+// U vectors of a thread, as they were fetched (the last but one row) or from memory.
+template <typename V, int U>
+__device__ __forceinline__ void take_row(V (&to)[U], const Ahead<V, U>& ahead, bool fetched, int row,
+                                         const V* from, int i0, int threads, int nv) {
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int v = i0 + u * threads;
+    if (v < nv) to[u] = fetched ? *ahead.at(ahead.stage, row, u) : from[v];
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ const T* row_of(const void* p, long long t, int H) {
+  return static_cast<const T*>(p) + t * H;
+}
+
+template <typename T, bool kVector, int kFormat, bool kWarp, int kThreads>
+__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ NormParams P) {
   chain();
+  constexpr int N = kVectorSize<T, kVector>, U = kHeldValues / N;
   using Q = Piece<T, N>;
   using V = typename Q::Raw;
-  __shared__ float sums[32][1];
+  extern __shared__ uint4 room[];
+  __shared__ float sums[2][kThreads / 32][1];
   const int threads = kWarp ? 32 : blockDim.x, i0 = kWarp ? threadIdx.x % 32 : threadIdx.x;
   const int nv = P.H / N;
   // vectors of a packed row, zeros behind the row's own
   const int np = kFormat == A2AV_PLAIN ? nv : (int)P.row.scales * (kMxBlock / N);
   const int per = kWarp ? blockDim.x / 32 : 1;
   const long long rows = P.first[P.W], by = (long long)gridDim.x * per;
+  long long g = (long long)blockIdx.x * per + (kWarp ? threadIdx.x / 32 : 0);
+  Ahead<V, U> ahead{reinterpret_cast<V*>(room) + threadIdx.x, P.ahead, 0};
+  const bool fetched = kVector && P.ahead > 0;
+  const auto fetch = [&](long long g) {
+    if (g >= rows) return;
+    const int r = rank_of(P.first, &g);
+    ahead.fetch(0, reinterpret_cast<const V*>(row_of<T>(P.x[r], g, P.H)), i0, threads, nv);
+    if (P.residual[r] != nullptr)
+      ahead.fetch(1, reinterpret_cast<const V*>(row_of<T>(P.residual[r], g, P.H)), i0, threads, nv);
+  };
+  if (fetched) {
+    fetch(g);
+    ahead.commit();
+  }
   float w[U][N];
 #pragma unroll
   for (int u = 0; u < U; ++u)
@@ -76,20 +145,20 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024)
       const int v = i0 + u * threads;
       w[u][i] = v < nv ? P.weight[v * N + i] : 0.0f;
     }
-  for (long long g = (long long)blockIdx.x * per + (kWarp ? threadIdx.x / 32 : 0); g < rows; g += by) {
+  for (int parity = 0; g < rows; g += by, parity ^= 1) {
     long long t = g;
     const int r = rank_of(P.first, &t);
-    const V* x = reinterpret_cast<const V*>(static_cast<const T*>(P.x[r]) + t * P.H);
-    const V* res = reinterpret_cast<const V*>(static_cast<const T*>(P.residual[r]) + t * P.H);
     V* kept = reinterpret_cast<V*>(static_cast<T*>(P.sums[r]) + t * P.H);
     const bool add = P.residual[r] != nullptr, keep = P.sums[r] != nullptr;
-    V s[U], a[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int v = i0 + u * threads;
-      if (v < nv) s[u] = x[v];
-      if (v < nv && add) a[u] = res[v];
+    if (fetched) {
+      fetch(g + by);
+      ahead.commit_and_wait();
     }
+    V s[U], a[U];
+    take_row(s, ahead, fetched, 0, reinterpret_cast<const V*>(row_of<T>(P.x[r], t, P.H)), i0, threads, nv);
+    if (add)
+      take_row(a, ahead, fetched, 1, reinterpret_cast<const V*>(row_of<T>(P.residual[r], t, P.H)), i0,
+               threads, nv);
     float total[1] = {0.0f};
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -110,7 +179,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024)
         for (int i = 0; i < N; ++i) total[0] += f[i] * f[i];
       }
     }
-    row_sum<kWarp, 1>(total, sums);
+    row_sum<kWarp, 1>(total, sums[parity]);
     const float scale = __frsqrt_rn(total[0] / P.H + P.eps);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -141,16 +210,32 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024)
 
 // d_x, and a block's part of the weight's gradient, kept in registers over its
 // rows.
-template <typename T, int N, int U, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 256 : 1024)
-    norm_backward_kernel(const __grid_constant__ NormParams P) {
+template <typename T, bool kVector, bool kWarp, int kThreads>
+__global__ void __launch_bounds__(kThreads) norm_backward_kernel(const __grid_constant__ NormParams P) {
   chain();
+  constexpr int N = kVectorSize<T, kVector>, U = kHeldValues / N;
   using Q = Piece<T, N>;
   using V = typename Q::Raw;
-  __shared__ float sums[32][2];
+  extern __shared__ uint4 room[];
+  __shared__ float sums[2][kThreads / 32][2];
   const int threads = kWarp ? 32 : blockDim.x, i0 = kWarp ? threadIdx.x % 32 : threadIdx.x;
   const int nv = P.H / N, per = kWarp ? blockDim.x / 32 : 1;
   const long long rows = P.first[P.W], by = (long long)gridDim.x * per;
+  long long g = (long long)blockIdx.x * per + (kWarp ? threadIdx.x / 32 : 0);
+  Ahead<V, U> ahead{reinterpret_cast<V*>(room) + threadIdx.x, P.ahead, 0};
+  const bool fetched = kVector && P.ahead > 0;
+  const auto fetch = [&](long long g) {
+    if (g >= rows) return;
+    const int r = rank_of(P.first, &g);
+    ahead.fetch(0, reinterpret_cast<const V*>(row_of<T>(P.x[r], g, P.H)), i0, threads, nv);
+    ahead.fetch(1, reinterpret_cast<const V*>(row_of<T>(P.d_out[r], g, P.H)), i0, threads, nv);
+    if (P.residual[r] != nullptr)
+      ahead.fetch(2, reinterpret_cast<const V*>(row_of<T>(P.residual[r], g, P.H)), i0, threads, nv);
+  };
+  if (fetched) {
+    fetch(g);
+    ahead.commit();
+  }
   float w[U][N], dw[U][N];
 #pragma unroll
   for (int u = 0; u < U; ++u)
@@ -160,24 +245,22 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024)
       w[u][i] = v < nv ? P.weight[v * N + i] : 0.0f;
       dw[u][i] = 0.0f;
     }
-  for (long long g = (long long)blockIdx.x * per + (kWarp ? threadIdx.x / 32 : 0); g < rows; g += by) {
+  for (int parity = 0; g < rows; g += by, parity ^= 1) {
     long long t = g;
     const int r = rank_of(P.first, &t);
-    const V* x = reinterpret_cast<const V*>(static_cast<const T*>(P.x[r]) + t * P.H);
-    const V* dy = reinterpret_cast<const V*>(static_cast<const T*>(P.d_out[r]) + t * P.H);
-    const V* ds = reinterpret_cast<const V*>(static_cast<const T*>(P.residual[r]) + t * P.H);
     V* out = reinterpret_cast<V*>(static_cast<T*>(P.out[r]) + t * P.H);
     const bool add = P.residual[r] != nullptr;
-    V s[U], d[U], a[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int v = i0 + u * threads;
-      if (v < nv) {
-        s[u] = x[v];
-        d[u] = dy[v];
-        if (add) a[u] = ds[v];
-      }
+    if (fetched) {
+      fetch(g + by);
+      ahead.commit_and_wait();
     }
+    V s[U], d[U], a[U];
+    take_row(s, ahead, fetched, 0, reinterpret_cast<const V*>(row_of<T>(P.x[r], t, P.H)), i0, threads, nv);
+    take_row(d, ahead, fetched, 1, reinterpret_cast<const V*>(row_of<T>(P.d_out[r], t, P.H)), i0, threads,
+             nv);
+    if (add)
+      take_row(a, ahead, fetched, 2, reinterpret_cast<const V*>(row_of<T>(P.residual[r], t, P.H)), i0,
+               threads, nv);
     float total[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -191,7 +274,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024)
           total[1] += f[i] * (e[i] * w[u][i]);
         }
       }
-    row_sum<kWarp, 2>(total, sums);
+    row_sum<kWarp, 2>(total, sums[parity]);
     const float scale = __frsqrt_rn(total[0] / P.H + P.eps);
     const float along = scale * scale * (total[1] / P.H);
 #pragma unroll
@@ -214,7 +297,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024)
   }
   if (P.part == nullptr) return;
   if constexpr (kWarp) {  // the block's warps one after the other
-    __shared__ float all[32 * U * N];
+    __shared__ float all[32 * kHeldValues];
     for (int k = 0; k < per; ++k) {
       if (threadIdx.x / 32 == k)
 #pragma unroll
@@ -393,63 +476,82 @@ constexpr int kNormParts = 1024;  // most blocks that keep a part of the weight'
 
 using NormKernel = void (*)(NormParams);
 
-// How a norm's rows are shared out: `vector` of 16 bytes' elements or one; a warp
-// a row where it can hold one.
-constexpr int kHeld = 4, kHeldScalar = 16;  // vectors a thread keeps
-
+// How a norm's rows are shared out: in vectors of 16 bytes or element by element; a
+// warp a row where it can hold one, else a block of up to 256 or 512 threads.
 struct NormForm {
-  bool vector, warp;
+  bool vector, warp, wide;
   int threads;  // of a block
 };
 
 NormForm norm_form(int64_t H, int size, uintptr_t low, long long rows, int sms) {
   NormForm f;
   f.vector = low % 16 == 0 && H * size % 16 == 0;
-  const long long nv = f.vector ? H * size / 16 : H;
-  const int held = f.vector ? kHeld : kHeldScalar;
+  const int n = f.vector ? 16 / size : 1, held = kHeldValues / n;
+  const int nv = (int)H / n;
   f.warp = nv <= 32 * held;
+  f.wide = false;
   f.threads = 256;
   if (!f.warp) {
-    long long threads = (nv + held - 1) / held;
-    f.threads = (int)((threads + 31) / 32 * 32);
-    // few rows: every thread of a block has one vector
-    if (rows < 2 * sms) f.threads = (int)((nv < 1024 ? nv : 1024) + 31) / 32 * 32;
+    int each = held;
+    // few rows: more threads a row, with less to do each
+    while (rows < 2 * sms && each > 1 && (nv + each / 2 - 1) / (each / 2) <= 512) each /= 2;
+    f.threads = ((nv + each - 1) / each + 31) / 32 * 32;
+    f.wide = f.threads > 256;
   }
   return f;
 }
 
-template <typename T, int kFormat>
+template <typename T, bool kVector, int kFormat>
 NormKernel norm_kernel_of(const NormForm& f) {
-  constexpr int N = 16 / sizeof(T);
-  if (f.vector) return f.warp ? norm_kernel<T, N, kHeld, kFormat, true> : norm_kernel<T, N, kHeld, kFormat, false>;
-  return f.warp ? norm_kernel<T, 1, kHeldScalar, kFormat, true>
-                : norm_kernel<T, 1, kHeldScalar, kFormat, false>;
+  if (f.warp) return norm_kernel<T, kVector, kFormat, true, 256>;
+  return f.wide ? norm_kernel<T, kVector, kFormat, false, 512> : norm_kernel<T, kVector, kFormat, false, 256>;
 }
 
 template <typename T>
 NormKernel norm_kernel_of(int format, const NormForm& f) {
-  if (format == A2AV_MXFP8) return norm_kernel_of<T, A2AV_MXFP8>(f);
-  return format == A2AV_MXFP4 ? norm_kernel_of<T, A2AV_MXFP4>(f) : norm_kernel_of<T, A2AV_PLAIN>(f);
+  if (format == A2AV_MXFP8)
+    return f.vector ? norm_kernel_of<T, true, A2AV_MXFP8>(f) : norm_kernel_of<T, false, A2AV_MXFP8>(f);
+  if (format == A2AV_MXFP4)
+    return f.vector ? norm_kernel_of<T, true, A2AV_MXFP4>(f) : norm_kernel_of<T, false, A2AV_MXFP4>(f);
+  return f.vector ? norm_kernel_of<T, true, A2AV_PLAIN>(f) : norm_kernel_of<T, false, A2AV_PLAIN>(f);
+}
+
+template <typename T, bool kVector>
+NormKernel norm_backward_kernel_of(const NormForm& f) {
+  if (f.warp) return norm_backward_kernel<T, kVector, true, 256>;
+  return f.wide ? norm_backward_kernel<T, kVector, false, 512> : norm_backward_kernel<T, kVector, false, 256>;
 }
 
 template <typename T>
 NormKernel norm_backward_kernel_of(const NormForm& f) {
-  constexpr int N = 16 / sizeof(T);
-  if (f.vector) return f.warp ? norm_backward_kernel<T, N, kHeld, true> : norm_backward_kernel<T, N, kHeld, false>;
-  return f.warp ? norm_backward_kernel<T, 1, kHeldScalar, true>
-                : norm_backward_kernel<T, 1, kHeldScalar, false>;
+  return f.vector ? norm_backward_kernel_of<T, true>(f) : norm_backward_kernel_of<T, false>(f);
 }
 
-// The blocks that share `rows` rows: as many as the GPU holds, and not more than
-// the rows need.
-cudaError_t blocks_of(const a2av_handle* h, const void* kernel, const NormForm& f, long long rows,
-                      unsigned* blocks) {
+constexpr size_t kMostRoom = 200 << 10;  // shared memory that a block fetches rows to
+
+// Launches a kernel whose rows have `arrays` arrays to read.  The blocks are as many
+// as the GPU holds, and not more than the rows need or `limit`; where they take
+// several rows each, they fetch them ahead.
+cudaError_t launch_norm(const a2av_handle* h, NormKernel kernel, const NormForm& f, int size, int arrays,
+                        long long rows, long long limit, NormParams& P, cudaStream_t s, unsigned* blocks) {
+  const void* k = reinterpret_cast<const void*>(kernel);
+  const long long per = f.warp ? f.threads / 32 : 1, want = (rows + per - 1) / per;
   int fit = 0;
-  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, f.threads, 0);
-  const long long most = (long long)fit * h->sms, per = f.warp ? f.threads / 32 : 1;
-  const long long want = (rows + per - 1) / per;
+  size_t room = 0;
+  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, k, f.threads, 0);
+  if (e != cudaSuccess) return e;
+  const size_t two_rows = (size_t)2 * arrays * f.threads * kHeldValues * size;
+  if (f.vector && want > (long long)fit * h->sms && two_rows <= kMostRoom) {
+    P.ahead = arrays;
+    room = two_rows;
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)room);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, k, f.threads, room);
+    if (e != cudaSuccess) return e;
+  }
+  long long most = (long long)fit * h->sms;
+  if (most > limit) most = limit;
   *blocks = (unsigned)(want < most ? want : most);
-  return e;
+  return launch_chained(kernel, dim3(*blocks), f.threads, room, s, h->pdl, P);
 }
 
 int norm_ok(const a2av_handle* h, int64_t features, int dtype, float eps, const void* x,
@@ -557,10 +659,8 @@ extern "C" int a2av_norm(a2av_handle* h, int64_t features, int dtype, int format
                             : dtype == A2AV_BF16 ? norm_kernel_of<__nv_bfloat16>(format, f)
                                                  : norm_kernel_of<__half>(format, f);
   unsigned blocks;
-  if (blocks_of(h, reinterpret_cast<const void*>(kernel), f, rows, &blocks) != cudaSuccess)
-    return A2AV_ERR_CUDA;
-  const cudaError_t e = launch_chained(kernel, dim3(blocks), f.threads, 0,
-                                       static_cast<cudaStream_t>(stream), h->pdl, P);
+  const cudaError_t e = launch_norm(h, kernel, f, size, residual_ptrs != nullptr ? 2 : 1, rows, rows, P,
+                                    static_cast<cudaStream_t>(stream), &blocks);
   return e != cudaSuccess || cudaGetLastError() != cudaSuccess ? A2AV_ERR_CUDA : A2AV_OK;
 }
 
@@ -611,10 +711,7 @@ extern "C" int a2av_norm_backward(a2av_handle* h, int64_t features, int dtype, f
     const NormKernel kernel = dtype == A2AV_F32    ? norm_backward_kernel_of<float>(f)
                               : dtype == A2AV_BF16 ? norm_backward_kernel_of<__nv_bfloat16>(f)
                                                    : norm_backward_kernel_of<__half>(f);
-    if (blocks_of(h, reinterpret_cast<const void*>(kernel), f, rows, &blocks) != cudaSuccess)
-      return A2AV_ERR_CUDA;
-    if (blocks > (unsigned)kNormParts) blocks = kNormParts;
-    e = launch_chained(kernel, dim3(blocks), f.threads, 0, s, h->pdl, P);
+    e = launch_norm(h, kernel, f, size, d_sum_ptrs != nullptr ? 3 : 2, rows, kNormParts, P, s, &blocks);
   }
   if (e == cudaSuccess && d_weight_dev != nullptr)
     e = launch_chained(norm_weight_kernel, dim3((unsigned)((features + 31) / 32)), 1024, 0, s, h->pdl,
