@@ -5,18 +5,20 @@
 #include "a2av_mx.h"
 #include "moe_device.cuh"
 
+#include <type_traits>
+
 namespace {
 
 constexpr int kMxBlock = 32;  // values a scale
 
 // Where the parts of a packed row lie.
 struct MxRow {
-  long long values, scales, bytes;  // bytes of the values, of the scales, of the row
+  int values, scales, bytes;  // bytes of the values, of the scales, of the row
 };
 
 __host__ __device__ __forceinline__ MxRow mx_row(long long features, int format) {
   MxRow r;
-  r.scales = (features + kMxBlock - 1) / kMxBlock;
+  r.scales = (int)((features + kMxBlock - 1) / kMxBlock);
   r.values = r.scales * (format == A2AV_MXFP8 ? kMxBlock : kMxBlock / 2);
   r.bytes = (r.values + r.scales + 31) / 32 * 32;
   return r;
@@ -34,7 +36,7 @@ __device__ __forceinline__ unsigned mx_scale(unsigned bits) {
 }
 
 // 1 / scale (s < 255: at most 253), a power of two.
-__device__ __forceinline__ float mx_inverse(unsigned s) { return __uint_as_float((254u - s) << 23); }
+__device__ __forceinline__ float mx_inverse(unsigned s) { return __uint_as_float((254u - s) << 23); }  // (255: of no use)
 
 // 2^(s - 127), NaN for 255 (2^-127 has no exponent of its own in 32 bits).
 __device__ __forceinline__ float mx_scale_value(unsigned s) {
@@ -86,6 +88,102 @@ __device__ __forceinline__ float2 e2m1_values(unsigned pair) {
   return unpack2(r, __half());
 }
 
+// N values as pairs, or the one of N = 1: products of pairs are one instruction on
+// this architecture.
+template <int N>
+constexpr int kPairs = N == 1 ? 1 : N / 2;
+template <int N>
+using PairOf = std::conditional_t<N == 1, float, float2>;
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
+        "l"(reinterpret_cast<const unsigned long long&>(c)));
+  return r;
+}
+__device__ __forceinline__ float mul2(float a, float b) { return a * b; }
+__device__ __forceinline__ float add2(float a, float b) { return a + b; }
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+template <typename P>
+__device__ __forceinline__ P both(float x) {
+  if constexpr (__is_same(P, float))
+    return x;
+  else
+    return make_float2(x, x);
+}
+__device__ __forceinline__ float sum_of(float x) { return x; }
+__device__ __forceinline__ float sum_of(float2 x) { return x.x + x.y; }
+// Value i of some pairs.
+template <int M>
+__device__ __forceinline__ float value_of(const float (&f)[M], int i) { return f[i]; }
+template <int M>
+__device__ __forceinline__ float value_of(const float2 (&f)[M], int i) { return i % 2 == 0 ? f[i / 2].x : f[i / 2].y; }
+
+// N elements of a row between memory's words and pairs.
+template <typename T, int N>
+struct Pairs {
+  using Raw = typename Piece<T, N>::Raw;
+  static __device__ __forceinline__ void unpack(const Raw& r, PairOf<N> (&f)[kPairs<N>]) {
+    if constexpr (N == 1) {
+      f[0] = to_float(r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if constexpr (sizeof(T) == 4)
+          f[i] = make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+        else if constexpr (__is_same(T, __nv_bfloat16))
+          f[i] = make_float2(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xffff0000u));
+        else
+          f[i] = unpack2(r.w[i], T());
+      }
+    }
+  }
+  static __device__ __forceinline__ Raw pack(const PairOf<N> (&f)[kPairs<N>]) {
+    if constexpr (N == 1) {
+      return from_float<T>(f[0]);
+    } else {
+      Raw r;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if constexpr (sizeof(T) == 4) {
+          r.w[2 * i] = __float_as_uint(f[i].x);
+          r.w[2 * i + 1] = __float_as_uint(f[i].y);
+        } else {
+          r.w[i] = pack2(f[i].x, f[i].y, T());
+        }
+      }
+      return r;
+    }
+  }
+};
+
+// The largest magnitude of some values, NaN where one is NaN.
+__device__ __forceinline__ float largest(const float (&f)[1]) { return fabsf(f[0]); }
+template <int M>
+__device__ __forceinline__ float largest(const float2 (&f)[M]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < M; ++i)
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(fabsf(f[i].x)), "f"(fabsf(f[i].y)));
+  return m;
+}
+
 // The codes of N neighbouring values (already divided by their scale), the first
 // lowest.
 template <int kFormat, int N>
@@ -94,24 +192,39 @@ struct MxCodes {
   static constexpr int kWords = N * kBits >= 32 ? N * kBits / 32 : 1;
   unsigned w[kWords];
 
-  __device__ __forceinline__ void encode(const float (&f)[N]) {
+  __device__ __forceinline__ void encode(const PairOf<N> (&f)[kPairs<N>]) {
     if constexpr (N == 1) {
       w[0] = kFormat == A2AV_MXFP8 ? e4m3_pair(f[0], 0.0f) & 0xffu : e2m1_pair(f[0], 0.0f) & 0xfu;
+    } else if constexpr (kFormat == A2AV_MXFP8) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+        asm("{\n\t.reg .b16 l, h;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+            "mov.b32 %0, {l, h};\n\t}"
+            : "=r"(w[i])
+            : "f"(f[2 * i].x), "f"(f[2 * i].y), "f"(f[2 * i + 1].x), "f"(f[2 * i + 1].y));
     } else {
+      static_assert(N == 4 || N == 8, "vectors of 16 bytes");
+      unsigned part[N / 4];
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) w[i] = 0;
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const unsigned p = kFormat == A2AV_MXFP8 ? e4m3_pair(f[2 * i], f[2 * i + 1])
-                                                 : e2m1_pair(f[2 * i], f[2 * i + 1]);
-        w[2 * i * kBits / 32] |= p << (2 * i * kBits % 32);
+      for (int i = 0; i < N / 4; ++i) {
+        unsigned short r;
+        asm("{\n\t.reg .b8 a, b;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+            "mov.b16 %0, {a, b};\n\t}"
+            : "=h"(r)
+            : "f"(f[2 * i].x), "f"(f[2 * i].y), "f"(f[2 * i + 1].x), "f"(f[2 * i + 1].y));
+        part[i] = r;
       }
+      w[0] = N == 8 ? part[0] | part[N / 4 - 1] << 16 : part[0];
     }
   }
 
   // To the values' place of a row, v being the number of these N in it.  With N = 1
   // (by a whole warp) two lanes share a byte of 4-bit codes.
-  __device__ __forceinline__ void store(unsigned char* row, long long v) const {
+  __device__ __forceinline__ void store(unsigned char* row, int v) const {
     if constexpr (N == 1 && kFormat == A2AV_MXFP8) {
       row[v] = (unsigned char)w[0];
     } else if constexpr (N == 1) {
@@ -129,21 +242,21 @@ struct MxCodes {
 };
 
 // N values of a row, the number v of such, to codes and (by the block's first
-// lane) their scale: by whole warps, 32 / N neighbouring lanes a block; `write`
-// says whether the lane's block is in the row (values past the row's end are 0).
+// lane) their scale: by whole warps, 32 / N neighbouring lanes a block; `top` has
+// the bits of the lane's largest magnitude, and `write` says whether the lane's block
+// is in the row (values past the row's end are 0).
 template <int kFormat, int N>
-__device__ __forceinline__ void mx_store(unsigned char* row, long long scales_at, long long v,
-                                         float (&f)[N], bool write) {
+__device__ __forceinline__ void mx_store(unsigned char* row, int scales_at, int v, PairOf<N> (&f)[kPairs<N>],
+                                         unsigned top, bool write) {
   constexpr int kLanes = kMxBlock / N;
-  unsigned top = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
   const unsigned s = mx_scale<kFormat>(lanes_max<kLanes>(top));
-  const float by = mx_inverse(s);
+  const PairOf<N> by = both<PairOf<N>>(mx_inverse(s));
 #pragma unroll
-  for (int i = 0; i < N; ++i) f[i] = s == 255u ? 0.0f : f[i] * by;
+  for (int i = 0; i < kPairs<N>; ++i) f[i] = mul2(f[i], by);
   MxCodes<kFormat, N> c;
   c.encode(f);
+#pragma unroll
+  for (int i = 0; i < c.kWords; ++i) c.w[i] = s == 255u ? 0u : c.w[i];
   if (write) {  // (N = 1: the whole warp or none of it)
     c.store(row, v);
     if (threadIdx.x % kLanes == 0) row[scales_at + v / kLanes] = (unsigned char)s;

@@ -21,15 +21,12 @@ struct NormParams {
   MxRow row;                 // of packed results
   int W, H;
   int ahead;                 // arrays whose rows are fetched ahead, 0: they are not
-  float eps;
+  float eps, per_feature;    // 1 / H
 };
 
-// Token t of all ranks' (rank-major): its rank; *t becomes its number there.
-__device__ __forceinline__ int rank_of(const long long* first, long long* t) {
-  int r = 0;
-  while (first[r + 1] <= *t) ++r;
-  *t -= first[r];
-  return r;
+// Token t of all ranks' (rank-major), in rank r or a later one.
+__device__ __forceinline__ void find_rank(const long long* first, long long t, int* r) {
+  while (first[*r + 1] <= t) ++*r;
 }
 
 // Sums of kSums values over a warp, or over the block: `shared` is not that of the
@@ -104,106 +101,119 @@ __device__ __forceinline__ void take_row(V (&to)[U], const Ahead<V, U>& ahead, b
   }
 }
 
-template <typename T>
-__device__ __forceinline__ const T* row_of(const void* p, long long t, int H) {
-  return static_cast<const T*>(p) + t * H;
+template <typename V, typename T>
+__device__ __forceinline__ const V* row_of(const void* p, long long t, int H) {
+  return reinterpret_cast<const V*>(static_cast<const T*>(p) + t * H);
+}
+template <typename V, typename T>
+__device__ __forceinline__ V* row_of(void* p, long long t, int H) {
+  return reinterpret_cast<V*>(static_cast<T*>(p) + t * H);
+}
+
+// The weight's N values of vector v, zeros past the row.
+template <int N>
+__device__ __forceinline__ void take_weight(PairOf<N> (&w)[kPairs<N>], const float* weight, int v, int nv) {
+#pragma unroll
+  for (int i = 0; i < kPairs<N>; ++i) {
+    if constexpr (N == 1)
+      w[i] = v < nv ? weight[v] : 0.0f;
+    else
+      w[i] = v < nv ? make_float2(weight[v * N + 2 * i], weight[v * N + 2 * i + 1]) : make_float2(0.0f, 0.0f);
+  }
 }
 
 template <typename T, bool kVector, int kFormat, bool kWarp, int kThreads>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ NormParams P) {
+__global__ void __launch_bounds__(kThreads, 512 / kThreads)
+    norm_kernel(const __grid_constant__ NormParams P) {
   chain();
-  constexpr int N = kVectorSize<T, kVector>, U = kHeldValues / N;
-  using Q = Piece<T, N>;
+  constexpr int N = kVectorSize<T, kVector>, U = kHeldValues / N, M = kPairs<N>;
+  using Q = Pairs<T, N>;
   using V = typename Q::Raw;
+  using F = PairOf<N>;
   extern __shared__ uint4 room[];
   __shared__ float sums[2][kThreads / 32][1];
   const int threads = kWarp ? 32 : blockDim.x, i0 = kWarp ? threadIdx.x % 32 : threadIdx.x;
   const int nv = P.H / N;
   // vectors of a packed row, zeros behind the row's own
-  const int np = kFormat == A2AV_PLAIN ? nv : (int)P.row.scales * (kMxBlock / N);
+  const int np = kFormat == A2AV_PLAIN ? nv : P.row.scales * (kMxBlock / N);
   const int per = kWarp ? blockDim.x / 32 : 1;
   const long long rows = P.first[P.W], by = (long long)gridDim.x * per;
   long long g = (long long)blockIdx.x * per + (kWarp ? threadIdx.x / 32 : 0);
   Ahead<V, U> ahead{reinterpret_cast<V*>(room) + threadIdx.x, P.ahead, 0};
   const bool fetched = kVector && P.ahead > 0;
+  int next = 0, r = 0;  // ranks of the row that is fetched and of this one
   const auto fetch = [&](long long g) {
     if (g >= rows) return;
-    const int r = rank_of(P.first, &g);
-    ahead.fetch(0, reinterpret_cast<const V*>(row_of<T>(P.x[r], g, P.H)), i0, threads, nv);
-    if (P.residual[r] != nullptr)
-      ahead.fetch(1, reinterpret_cast<const V*>(row_of<T>(P.residual[r], g, P.H)), i0, threads, nv);
+    find_rank(P.first, g, &next);
+    const long long t = g - P.first[next];
+    ahead.fetch(0, row_of<V, T>(P.x[next], t, P.H), i0, threads, nv);
+    if (P.residual[next] != nullptr) ahead.fetch(1, row_of<V, T>(P.residual[next], t, P.H), i0, threads, nv);
   };
   if (fetched) {
     fetch(g);
     ahead.commit();
   }
-  float w[U][N];
+  F w[U][M];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int v = i0 + u * threads;
-      w[u][i] = v < nv ? P.weight[v * N + i] : 0.0f;
-    }
+  for (int u = 0; u < U; ++u) take_weight<N>(w[u], P.weight, i0 + u * threads, nv);
   for (int parity = 0; g < rows; g += by, parity ^= 1) {
-    long long t = g;
-    const int r = rank_of(P.first, &t);
-    V* kept = reinterpret_cast<V*>(static_cast<T*>(P.sums[r]) + t * P.H);
+    find_rank(P.first, g, &r);
+    const long long t = g - P.first[r];
+    V* kept = row_of<V, T>(P.sums[r], t, P.H);
     const bool add = P.residual[r] != nullptr, keep = P.sums[r] != nullptr;
     if (fetched) {
       fetch(g + by);
       ahead.commit_and_wait();
     }
     V s[U], a[U];
-    take_row(s, ahead, fetched, 0, reinterpret_cast<const V*>(row_of<T>(P.x[r], t, P.H)), i0, threads, nv);
-    if (add)
-      take_row(a, ahead, fetched, 1, reinterpret_cast<const V*>(row_of<T>(P.residual[r], t, P.H)), i0,
-               threads, nv);
-    float total[1] = {0.0f};
+    take_row(s, ahead, fetched, 0, row_of<V, T>(P.x[r], t, P.H), i0, threads, nv);
+    if (add) take_row(a, ahead, fetched, 1, row_of<V, T>(P.residual[r], t, P.H), i0, threads, nv);
+    F total2 = both<F>(0.0f);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int v = i0 + u * threads;
       if (v < nv) {
-        float f[N];
+        F f[M];
         Q::unpack(s[u], f);
         if (add) {
-          float b[N];
+          F b[M];
           Q::unpack(a[u], b);
 #pragma unroll
-          for (int i = 0; i < N; ++i) f[i] += b[i];
+          for (int i = 0; i < M; ++i) f[i] = add2(f[i], b[i]);
           s[u] = Q::pack(f);
           Q::unpack(s[u], f);
         }
         if (keep) kept[v] = s[u];
 #pragma unroll
-        for (int i = 0; i < N; ++i) total[0] += f[i] * f[i];
+        for (int i = 0; i < M; ++i) total2 = fma2(f[i], f[i], total2);
       }
     }
+    float total[1] = {sum_of(total2)};
     row_sum<kWarp, 1>(total, sums[parity]);
-    const float scale = __frsqrt_rn(total[0] / P.H + P.eps);
+    const F scale = both<F>(rsqrtf(fmaf(total[0], P.per_feature, P.eps)));
+    unsigned char* packed = static_cast<unsigned char*>(P.out[r]) + t * P.row.bytes;
+    V* out = row_of<V, T>(P.out[r], t, P.H);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int v = i0 + u * threads;
-      float f[N];
+      F f[M];
       if (v < nv) {
         Q::unpack(s[u], f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) f[i] *= scale * w[u][i];
+        for (int i = 0; i < M; ++i) f[i] = mul2(mul2(f[i], scale), w[u][i]);
       }
       if constexpr (kFormat == A2AV_PLAIN) {
-        if (v < nv) reinterpret_cast<V*>(static_cast<T*>(P.out[r]) + t * P.H)[v] = Q::pack(f);
-      } else {
+        if (v < nv) out[v] = Q::pack(f);
+      } else if (u * threads < np) {
         if (v >= nv)
 #pragma unroll
-          for (int i = 0; i < N; ++i) f[i] = 0.0f;
-        unsigned char* to = static_cast<unsigned char*>(P.out[r]) + t * P.row.bytes;
-        if (u * threads < np) mx_store<kFormat, N>(to, P.row.values, v, f, v < np);
+          for (int i = 0; i < M; ++i) f[i] = both<F>(0.0f);
+        mx_store<kFormat, N>(packed, P.row.values, v, f, __float_as_uint(largest(f)), v < np);
       }
     }
     if constexpr (kFormat != A2AV_PLAIN) {
-      const int used = (int)(P.row.values + P.row.scales);
-      unsigned char* to = static_cast<unsigned char*>(P.out[r]) + t * P.row.bytes;
-      if (used + i0 < P.row.bytes) to[used + i0] = 0;  // (31 at most)
+      const int used = P.row.values + P.row.scales;
+      if (used + i0 < P.row.bytes) packed[used + i0] = 0;  // (31 at most)
     }
   }
 }
@@ -211,11 +221,13 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
 // d_x, and a block's part of the weight's gradient, kept in registers over its
 // rows.
 template <typename T, bool kVector, bool kWarp, int kThreads>
-__global__ void __launch_bounds__(kThreads) norm_backward_kernel(const __grid_constant__ NormParams P) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 1 : 512 / kThreads)
+    norm_backward_kernel(const __grid_constant__ NormParams P) {
   chain();
-  constexpr int N = kVectorSize<T, kVector>, U = kHeldValues / N;
-  using Q = Piece<T, N>;
+  constexpr int N = kVectorSize<T, kVector>, U = kHeldValues / N, M = kPairs<N>;
+  using Q = Pairs<T, N>;
   using V = typename Q::Raw;
+  using F = PairOf<N>;
   extern __shared__ uint4 room[];
   __shared__ float sums[2][kThreads / 32][2];
   const int threads = kWarp ? 32 : blockDim.x, i0 = kWarp ? threadIdx.x % 32 : threadIdx.x;
@@ -224,78 +236,77 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const __grid_co
   long long g = (long long)blockIdx.x * per + (kWarp ? threadIdx.x / 32 : 0);
   Ahead<V, U> ahead{reinterpret_cast<V*>(room) + threadIdx.x, P.ahead, 0};
   const bool fetched = kVector && P.ahead > 0;
+  int next = 0, r = 0;  // ranks of the row that is fetched and of this one
   const auto fetch = [&](long long g) {
     if (g >= rows) return;
-    const int r = rank_of(P.first, &g);
-    ahead.fetch(0, reinterpret_cast<const V*>(row_of<T>(P.x[r], g, P.H)), i0, threads, nv);
-    ahead.fetch(1, reinterpret_cast<const V*>(row_of<T>(P.d_out[r], g, P.H)), i0, threads, nv);
-    if (P.residual[r] != nullptr)
-      ahead.fetch(2, reinterpret_cast<const V*>(row_of<T>(P.residual[r], g, P.H)), i0, threads, nv);
+    find_rank(P.first, g, &next);
+    const long long t = g - P.first[next];
+    ahead.fetch(0, row_of<V, T>(P.x[next], t, P.H), i0, threads, nv);
+    ahead.fetch(1, row_of<V, T>(P.d_out[next], t, P.H), i0, threads, nv);
+    if (P.residual[next] != nullptr) ahead.fetch(2, row_of<V, T>(P.residual[next], t, P.H), i0, threads, nv);
   };
   if (fetched) {
     fetch(g);
     ahead.commit();
   }
-  float w[U][N], dw[U][N];
+  F w[U][M], dw[U][M];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
+  for (int u = 0; u < U; ++u) {
+    take_weight<N>(w[u], P.weight, i0 + u * threads, nv);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int v = i0 + u * threads;
-      w[u][i] = v < nv ? P.weight[v * N + i] : 0.0f;
-      dw[u][i] = 0.0f;
-    }
+    for (int i = 0; i < M; ++i) dw[u][i] = both<F>(0.0f);
+  }
   for (int parity = 0; g < rows; g += by, parity ^= 1) {
-    long long t = g;
-    const int r = rank_of(P.first, &t);
-    V* out = reinterpret_cast<V*>(static_cast<T*>(P.out[r]) + t * P.H);
+    find_rank(P.first, g, &r);
+    const long long t = g - P.first[r];
+    V* out = row_of<V, T>(P.out[r], t, P.H);
     const bool add = P.residual[r] != nullptr;
     if (fetched) {
       fetch(g + by);
       ahead.commit_and_wait();
     }
     V s[U], d[U], a[U];
-    take_row(s, ahead, fetched, 0, reinterpret_cast<const V*>(row_of<T>(P.x[r], t, P.H)), i0, threads, nv);
-    take_row(d, ahead, fetched, 1, reinterpret_cast<const V*>(row_of<T>(P.d_out[r], t, P.H)), i0, threads,
-             nv);
-    if (add)
-      take_row(a, ahead, fetched, 2, reinterpret_cast<const V*>(row_of<T>(P.residual[r], t, P.H)), i0,
-               threads, nv);
-    float total[2] = {0.0f, 0.0f};
+    take_row(s, ahead, fetched, 0, row_of<V, T>(P.x[r], t, P.H), i0, threads, nv);
+    take_row(d, ahead, fetched, 1, row_of<V, T>(P.d_out[r], t, P.H), i0, threads, nv);
+    if (add && !fetched) take_row(a, ahead, false, 2, row_of<V, T>(P.residual[r], t, P.H), i0, threads, nv);
+    F squares = both<F>(0.0f), products = both<F>(0.0f);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (i0 + u * threads < nv) {
-        float f[N], e[N];
+        F f[M], e[M];
         Q::unpack(s[u], f);
         Q::unpack(d[u], e);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          total[0] += f[i] * f[i];
-          total[1] += f[i] * (e[i] * w[u][i]);
+        for (int i = 0; i < M; ++i) {
+          squares = fma2(f[i], f[i], squares);
+          products = fma2(f[i], mul2(e[i], w[u][i]), products);
         }
       }
+    float total[2] = {sum_of(squares), sum_of(products)};
     row_sum<kWarp, 2>(total, sums[parity]);
-    const float scale = __frsqrt_rn(total[0] / P.H + P.eps);
-    const float along = scale * scale * (total[1] / P.H);
+    const float one = rsqrtf(fmaf(total[0], P.per_feature, P.eps));
+    const F scale = both<F>(one), along = both<F>(-one * one * (total[1] * P.per_feature));
+    if (add && fetched) take_row(a, ahead, true, 2, row_of<V, T>(P.residual[r], t, P.H), i0, threads, nv);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int v = i0 + u * threads;
       if (v < nv) {
-        float f[N], e[N], y[N];
+        F f[M], e[M], y[M];
         Q::unpack(s[u], f);
         Q::unpack(d[u], e);
         if (add) Q::unpack(a[u], y);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          dw[u][i] += e[i] * (f[i] * scale);
-          const float z = scale * (e[i] * w[u][i] - f[i] * along);
-          y[i] = add ? y[i] + z : z;
+        for (int i = 0; i < M; ++i) {
+          dw[u][i] = fma2(e[i], mul2(f[i], scale), dw[u][i]);
+          const F z = fma2(f[i], along, mul2(e[i], w[u][i]));
+          y[i] = add ? fma2(z, scale, y[i]) : mul2(z, scale);
         }
         out[v] = Q::pack(y);
       }
     }
   }
   if (P.part == nullptr) return;
+  float* part = P.part + (long long)blockIdx.x * P.H;
   if constexpr (kWarp) {  // the block's warps one after the other
     __shared__ float all[32 * kHeldValues];
     for (int k = 0; k < per; ++k) {
@@ -305,18 +316,19 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const __grid_co
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             float* at = all + (i0 + u * 32) * N + i;
-            *at = k == 0 ? dw[u][i] : *at + dw[u][i];
+            const float x = value_of(dw[u], i);
+            *at = k == 0 ? x : *at + x;
           }
       __syncthreads();
     }
-    for (int c = threadIdx.x; c < P.H; c += blockDim.x) P.part[(long long)blockIdx.x * P.H + c] = all[c];
+    for (int c = threadIdx.x; c < P.H; c += blockDim.x) part[c] = all[c];
   } else {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int v = i0 + u * threads;
       if (v < nv)
 #pragma unroll
-        for (int i = 0; i < N; ++i) P.part[(long long)blockIdx.x * P.H + v * N + i] = dw[u][i];
+        for (int i = 0; i < N; ++i) part[v * N + i] = value_of(dw[u], i);
     }
   }
 }
@@ -346,27 +358,71 @@ struct PackParams {
   const void* from[kW];
   void* to[kW];
   long long first[kW + 1];  // rows before each rank's
-  long long D;
   MxRow row;
-  int W;
+  int D, W;
 };
 
 constexpr int kPackThreads = 256;
+
+// The rows' slices, shared out among all warps; a warp's next is found without a
+// division.
+struct Slice {
+  long long t;  // row
+  int slice;
+};
+struct Slices {
+  long long rows, t_on;
+  int slices, slice_on;
+  __device__ __forceinline__ Slices(long long rows, int slices) : rows(rows), slices(slices) {
+    const long long warps = (long long)gridDim.x * (kPackThreads / 32);
+    t_on = warps / slices;
+    slice_on = (int)(warps - t_on * slices);
+  }
+  __device__ __forceinline__ Slice first() const {
+    const long long g = (long long)blockIdx.x * (kPackThreads / 32) + threadIdx.x / 32;
+    return {g / slices, (int)(g % slices)};
+  }
+  __device__ __forceinline__ void next(Slice* at) const {
+    at->t += t_on;
+    at->slice += slice_on;
+    if (at->slice >= slices) {
+      at->slice -= slices;
+      ++at->t;
+    }
+  }
+};
+
+// The bits, in 32, of the largest magnitude of a vector: of pairs of 16 bits by
+// one instruction each.
+template <typename T, int N>
+__device__ __forceinline__ unsigned top_bits(const typename Pairs<T, N>::Raw& r, const PairOf<N> (&f)[kPairs<N>]) {
+  if constexpr (N > 1 && sizeof(T) == 2) {
+    using T2 = std::conditional_t<__is_same(T, __half), __half2, __nv_bfloat162>;
+    T2 m = __habs2(reinterpret_cast<const T2&>(r.w[0]));
+#pragma unroll
+    for (int i = 1; i < N / 2; ++i) m = __hmax2_nan(m, __habs2(reinterpret_cast<const T2&>(r.w[i])));
+    return __float_as_uint(to_float(__hmax_nan(m.x, m.y))) & 0x7fffffffu;
+  } else {
+    return __float_as_uint(largest(f));
+  }
+}
 
 // A warp takes 32 U neighbouring vectors of a row.
 template <typename T, int N, int U, int kFormat>
 __global__ void __launch_bounds__(kPackThreads) quantise_kernel(const __grid_constant__ PackParams P) {
   chain();
-  using Q = Piece<T, N>;
+  using Q = Pairs<T, N>;
   using V = typename Q::Raw;
+  using F = PairOf<N>;
+  constexpr int M = kPairs<N>;
   const int lane = threadIdx.x % 32;
-  const long long nv = P.D / N, np = P.row.scales * (kMxBlock / N);
-  const long long slices = (np + 32 * U - 1) / (32 * U), units = P.first[P.W] * slices;
-  const long long warps = (long long)gridDim.x * (kPackThreads / 32);
-  for (long long g = (long long)blockIdx.x * (kPackThreads / 32) + threadIdx.x / 32; g < units; g += warps) {
-    long long t = g / slices;
-    const long long slice = g - t * slices, v0 = slice * (32 * U) + lane;
-    const int r = rank_of(P.first, &t);
+  const int nv = P.D / N, np = P.row.scales * (kMxBlock / N);
+  const Slices cut(P.first[P.W], (np + 32 * U - 1) / (32 * U));
+  int r = 0;
+  for (Slice at = cut.first(); at.t < cut.rows; cut.next(&at)) {
+    find_rank(P.first, at.t, &r);
+    const long long t = at.t - P.first[r];
+    const int v0 = at.slice * (32 * U) + lane;
     const V* x = reinterpret_cast<const V*>(static_cast<const T*>(P.from[r]) + t * P.D);
     unsigned char* to = static_cast<unsigned char*>(P.to[r]) + t * P.row.bytes;
     V s[U];
@@ -375,40 +431,47 @@ __global__ void __launch_bounds__(kPackThreads) quantise_kernel(const __grid_con
       if (v0 + 32 * u < nv) s[u] = x[v0 + 32 * u];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const long long v = v0 + 32 * u;
-      float f[N] = {};
-      if (v < nv) Q::unpack(s[u], f);
-      if (v - lane < np) mx_store<kFormat, N>(to, P.row.values, v, f, v < np);
+      const int v = v0 + 32 * u;
+      F f[M];
+      unsigned top = 0;
+#pragma unroll
+      for (int i = 0; i < M; ++i) f[i] = both<F>(0.0f);
+      if (v < nv) {
+        Q::unpack(s[u], f);
+        top = top_bits<T, N>(s[u], f);
+      }
+      if (v - lane < np) mx_store<kFormat, N>(to, P.row.values, v, f, top, v < np);
     }
-    const long long used = P.row.values + P.row.scales;
-    if (slice == slices - 1 && used + lane < P.row.bytes) to[used + lane] = 0;
+    const int used = P.row.values + P.row.scales;
+    if (at.slice == cut.slices - 1 && used + lane < P.row.bytes) to[used + lane] = 0;
   }
 }
 
 template <typename T, int N, int U, int kFormat>
 __global__ void __launch_bounds__(kPackThreads) dequantise_kernel(const __grid_constant__ PackParams P) {
   chain();
-  using Q = Piece<T, N>;
+  using Q = Pairs<T, N>;
   using V = typename Q::Raw;
-  constexpr int kBits = kFormat == A2AV_MXFP8 ? 8 : 4;
+  using F = PairOf<N>;
+  constexpr int kBits = kFormat == A2AV_MXFP8 ? 8 : 4, M = kPairs<N>;
   const int lane = threadIdx.x % 32;
-  const long long nv = P.D / N;
-  const long long slices = (nv + 32 * U - 1) / (32 * U), units = P.first[P.W] * slices;
-  const long long warps = (long long)gridDim.x * (kPackThreads / 32);
-  for (long long g = (long long)blockIdx.x * (kPackThreads / 32) + threadIdx.x / 32; g < units; g += warps) {
-    long long t = g / slices;
-    const long long v0 = (g - t * slices) * (32 * U) + lane;
-    const int r = rank_of(P.first, &t);
+  const int nv = P.D / N;
+  const Slices cut(P.first[P.W], (nv + 32 * U - 1) / (32 * U));
+  int r = 0;
+  for (Slice at = cut.first(); at.t < cut.rows; cut.next(&at)) {
+    find_rank(P.first, at.t, &r);
+    const long long t = at.t - P.first[r];
+    const int v0 = at.slice * (32 * U) + lane;
     const unsigned char* from = static_cast<const unsigned char*>(P.from[r]) + t * P.row.bytes;
     V* out = reinterpret_cast<V*>(static_cast<T*>(P.to[r]) + t * P.D);
     unsigned w[U][N * kBits >= 32 ? N * kBits / 32 : 1], s[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const long long v = v0 + 32 * u;
+      const int v = v0 + 32 * u;
       if (v < nv) {
-        s[u] = from[P.row.values + v * N / kMxBlock];
+        s[u] = from[P.row.values + v / (kMxBlock / N)];
         if constexpr (N == 1) {
-          w[u][0] = from[v * kBits / 8] >> (kBits == 4 ? v % 2 * 4 : 0);
+          w[u][0] = kBits == 8 ? from[v] : from[v / 2] >> (v % 2 * 4);
         } else if constexpr (N * kBits == 64) {
           const uint2 c = reinterpret_cast<const uint2*>(from)[v];
           w[u][0] = c.x;
@@ -422,20 +485,18 @@ __global__ void __launch_bounds__(kPackThreads) dequantise_kernel(const __grid_c
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const long long v = v0 + 32 * u;
+      const int v = v0 + 32 * u;
       if (v < nv) {
-        const float by = mx_scale_value(s[u]);
-        float f[N];
-        if constexpr (N == 1) {
-          f[0] = by * (kBits == 8 ? e4m3_values(w[u][0]) : e2m1_values(w[u][0])).x;
-        } else {
+        const F by = both<F>(mx_scale_value(s[u]));
+        F f[M];
 #pragma unroll
-          for (int i = 0; i < N; i += 2) {
-            const unsigned c = w[u][i * kBits / 32] >> (i * kBits % 32);
-            const float2 p = kBits == 8 ? e4m3_values(c) : e2m1_values(c);
-            f[i] = by * p.x;
-            f[i + 1] = by * p.y;
-          }
+        for (int i = 0; i < M; ++i) {
+          const unsigned c = w[u][2 * i * kBits / 32] >> (2 * i * kBits % 32);
+          const float2 p = kBits == 8 ? e4m3_values(c) : e2m1_values(c);
+          if constexpr (N == 1)
+            f[i] = p.x * by;
+          else
+            f[i] = mul2(p, by);
         }
         out[v] = Q::pack(f);
       }
@@ -601,7 +662,7 @@ int pack_call(a2av_handle* h, int64_t features, int dtype, int format, const voi
   if (rc != A2AV_OK) return rc;
   if (P.first[h->W] == 0) return A2AV_OK;
   P.W = h->W;
-  P.D = features;
+  P.D = (int)features;
   P.row = mx_row(features, format);
   const bool vector = low % 16 == 0;
   const PackKernel kernel = dtype == A2AV_F32    ? pack_kernel_of<float>(format, vector, back)
@@ -654,6 +715,7 @@ extern "C" int a2av_norm(a2av_handle* h, int64_t features, int dtype, int format
   P.W = W;
   P.H = (int)features;
   P.eps = eps;
+  P.per_feature = 1.0f / (float)features;
   const NormForm f = norm_form(features, size, low, rows, h->sms);
   const NormKernel kernel = dtype == A2AV_F32    ? norm_kernel_of<float>(format, f)
                             : dtype == A2AV_BF16 ? norm_kernel_of<__nv_bfloat16>(format, f)
@@ -703,6 +765,7 @@ extern "C" int a2av_norm_backward(a2av_handle* h, int64_t features, int dtype, f
   P.W = W;
   P.H = (int)features;
   P.eps = eps;
+  P.per_feature = 1.0f / (float)features;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   unsigned blocks = 0;
