@@ -5,6 +5,7 @@
 // All are bound by memory: each row is read once and written once.  A block (a
 // warp, for short rows) takes a row, keeps it in registers between the sum of
 // squares and the result, and goes on to another; the weight stays in registers.
+#include "mma.cuh"
 #include "mx_device.cuh"
 
 namespace {
@@ -19,8 +20,8 @@ struct NormParams {
   const float* weight;
   float* part;               // backward: [blocks][H], or NULL
   MxRow row;                 // of packed results
+  int* status;
   int W, H;
-  int ahead;                 // arrays whose rows are fetched ahead, 0: they are not
   float eps, per_feature;    // 1 / H
 };
 
@@ -47,83 +48,110 @@ __device__ __forceinline__ void row_sum(float (&x)[kSums], float (*shared)[kSums
     for (int i = 0; i < kSums; ++i) {
       x[i] = lane < warps ? shared[lane][i] : 0.0f;
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) x[i] += __shfl_xor_sync(kAll, x[i], o);
-      x[i] = __shfl_sync(kAll, x[i], 0);
+      for (int o = 16; o > 0; o >>= 1) x[i] += __shfl_xor_sync(kAll, x[i], o);
     }
   }
 }
 
 // How a row lies on its threads: vectors of N elements, U a thread, thread i having
 // the vectors i, i + threads, ...
-constexpr int kHeldValues = 32;  // of a row in a thread
+constexpr int kHeldValues = 32;    // of a row in a thread
+// (the backward pass keeps the weight's gradient of its values as well)
+__host__ __device__ constexpr int held_backward(bool vector, int size) { return vector && size == 2 ? 32 : 16; }
 template <typename T, bool kVector>
 constexpr int kVectorSize = kVector ? 16 / sizeof(T) : 1;
 
-// What a thread has of the next row of `arrays` arrays, on its way to a place of its
-// own in shared memory while it works on this one (rows of vectors): two rows of them,
-// U vectors a thread each.
-template <typename V, int U>
+// Rows on their way to shared memory, by bulk copies, while others are worked on: two
+// rows of `arrays` arrays of `bytes` each, for the block or for each of its warps.
 struct Ahead {
-  V* place;
-  int arrays, stage;
-  __device__ __forceinline__ V* at(int stage, int row, int u) const {
-    return place + ((stage * arrays + row) * U + u) * blockDim.x;
+  uint32_t place, bar;  // of the stage that is read next
+  uint32_t step;        // bytes of a stage
+  int turn, parity;
+  bool lost;            // a copy has not come
+
+  __device__ __forceinline__ uint32_t at(int stage) const { return place + (stage ? step : 0); }
+  // By the thread that copies; a list of `count` arrays.
+  __device__ __forceinline__ void expect(int stage, unsigned total) const {
+    bar_arrive_tx(bar + 8 * stage, total);
   }
-  __device__ __forceinline__ void fetch(int row, const V* from, int i0, int threads, int nv) const {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int v = i0 + u * threads;
-      if (v < nv) {
-        const unsigned to = (unsigned)__cvta_generic_to_shared(at(stage, row, u));
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from + v) : "memory");
-      }
-    }
+  __device__ __forceinline__ void fetch(int stage, int array, const void* from, unsigned bytes) const {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            at(stage) + array * bytes),
+        "l"(from), "r"(bytes), "r"(bar + 8 * stage)
+        : "memory");
   }
-  // All that was fetched before the last commit is there; the next goes to the other half.
-  __device__ __forceinline__ void commit_and_wait() {
-    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 1;" ::: "memory");
-    stage ^= 1;
+  __device__ __forceinline__ void wait() {
+    if (!lost) lost = !bar_wait(bar + 8 * turn, parity);
   }
-  __device__ __forceinline__ void commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    stage ^= 1;
+  __device__ __forceinline__ void next() {
+    parity ^= turn;
+    turn ^= 1;
   }
 };
 
-// U vectors of a thread, as they were fetched (the last but one row) or from memory.
-template <typename V, int U>
-__device__ __forceinline__ void take_row(V (&to)[U], const Ahead<V, U>& ahead, bool fetched, int row,
-                                         const V* from, int i0, int threads, int nv) {
+// A copy has not come: this is recorded, and what is in flight waited for, with a limit,
+// before the block may leave.
+__device__ __noinline__ void give_up(const Ahead& ahead, int* status) {
+  note_error(status, A2AV_ERR_TIMEOUT);
+  bar_wait(ahead.bar + 8 * ahead.turn, ahead.parity);
+  bar_wait(ahead.bar + 8 * (ahead.turn ^ 1), ahead.parity ^ ahead.turn);
+}
+
+// U vectors of a thread: from shared memory (`row`: the array's bytes there), or from
+// memory (`from`: the thread's first).
+template <bool kAhead, typename V, int U>
+__device__ __forceinline__ void take_row(V (&to)[U], uint32_t row, const V* from, int i0,
+                                         int threads, int nv) {
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int v = i0 + u * threads;
-    if (v < nv) to[u] = fetched ? *ahead.at(ahead.stage, row, u) : from[v];
-  }
-}
-
-template <typename V, typename T>
-__device__ __forceinline__ const V* row_of(const void* p, long long t, int H) {
-  return reinterpret_cast<const V*>(static_cast<const T*>(p) + t * H);
-}
-template <typename V, typename T>
-__device__ __forceinline__ V* row_of(void* p, long long t, int H) {
-  return reinterpret_cast<V*>(static_cast<T*>(p) + t * H);
-}
-
-// The weight's N values of vector v, zeros past the row.
-template <int N>
-__device__ __forceinline__ void take_weight(PairOf<N> (&w)[kPairs<N>], const float* weight, int v, int nv) {
-#pragma unroll
-  for (int i = 0; i < kPairs<N>; ++i) {
-    if constexpr (N == 1)
-      w[i] = v < nv ? weight[v] : 0.0f;
+    if (i0 + u * threads >= nv) continue;
+    if constexpr (kAhead)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(to[u].w[0]), "=r"(to[u].w[1]), "=r"(to[u].w[2]), "=r"(to[u].w[3])
+                   : "r"(row + 16 * (i0 + u * threads))
+                   : "memory");
     else
-      w[i] = v < nv ? make_float2(weight[v * N + 2 * i], weight[v * N + 2 * i + 1]) : make_float2(0.0f, 0.0f);
+      to[u] = from[u * threads];
   }
 }
 
-template <typename T, bool kVector, int kFormat, bool kWarp, int kThreads>
-__global__ void __launch_bounds__(kThreads, 512 / kThreads)
+// A token's place: its rank and its first element in the rank's buffers.
+struct Token {
+  int r;
+  long long at;
+};
+template <typename V, typename T>
+__device__ __forceinline__ const V* row_of(const void* const* list, const Token& t, int vector = 0) {
+  return reinterpret_cast<const V*>(static_cast<const T*>(list[t.r]) + t.at) + vector;
+}
+template <typename V, typename T>
+__device__ __forceinline__ V* row_of(void* const* list, const Token& t, int vector = 0) {
+  return reinterpret_cast<V*>(static_cast<T*>(list[t.r]) + t.at) + vector;
+}
+// Token g of all ranks', g being no smaller than the last one.
+__device__ __forceinline__ void find_token(const NormParams& P, long long g, Token* t) {
+  find_rank(P.first, g, &t->r);
+  t->at = (g - P.first[t->r]) * P.H;
+}
+
+// The weight's N values of vector v.  They are read again for every row, from L1: in
+// registers they would cost the block that an SM has beside this one.
+template <int N>
+__device__ __forceinline__ void take_weight(PairOf<N> (&w)[kPairs<N>], const float* weight, int v) {
+  if constexpr (N == 1) {
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(w[0]) : "l"(weight + v));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; i += 2)
+      asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(w[i].x), "=f"(w[i].y), "=f"(w[i + 1].x), "=f"(w[i + 1].y)
+                   : "l"(weight + v * N + 2 * i));
+  }
+}
+
+template <typename T, bool kVector, int kFormat, bool kWarp, int kThreads, bool kAhead>
+__global__ void __maxnreg__(sizeof(T) == 4 || !kVector ? 128 : 96)
     norm_kernel(const __grid_constant__ NormParams P) {
   chain();
   constexpr int N = kVectorSize<T, kVector>, U = kHeldValues / N, M = kPairs<N>;
@@ -132,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads)
   using F = PairOf<N>;
   extern __shared__ uint4 room[];
   __shared__ float sums[2][kThreads / 32][1];
+  __shared__ unsigned long long bars[kWarp ? 2 * kThreads / 32 : 2];
   const int threads = kWarp ? 32 : blockDim.x, i0 = kWarp ? threadIdx.x % 32 : threadIdx.x;
   const int nv = P.H / N;
   // vectors of a packed row, zeros behind the row's own
@@ -139,35 +168,47 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads)
   const int per = kWarp ? blockDim.x / 32 : 1;
   const long long rows = P.first[P.W], by = (long long)gridDim.x * per;
   long long g = (long long)blockIdx.x * per + (kWarp ? threadIdx.x / 32 : 0);
-  Ahead<V, U> ahead{reinterpret_cast<V*>(room) + threadIdx.x, P.ahead, 0};
-  const bool fetched = kVector && P.ahead > 0;
-  int next = 0, r = 0;  // ranks of the row that is fetched and of this one
-  const auto fetch = [&](long long g) {
-    if (g >= rows) return;
-    find_rank(P.first, g, &next);
-    const long long t = g - P.first[next];
-    ahead.fetch(0, row_of<V, T>(P.x[next], t, P.H), i0, threads, nv);
-    if (P.residual[next] != nullptr) ahead.fetch(1, row_of<V, T>(P.residual[next], t, P.H), i0, threads, nv);
+  Ahead ahead;
+  // (the thread that copies: the block's or the warp's first)
+  const unsigned bytes = (unsigned)P.H * sizeof(T);
+  const auto fetch = [&](int stage, const Token& t) {
+    const bool more = P.residual[t.r] != nullptr;
+    ahead.expect(stage, (more ? 2 : 1) * bytes);
+    ahead.fetch(stage, 0, row_of<V, T>(P.x, t), bytes);
+    if (more) ahead.fetch(stage, 1, row_of<V, T>(P.residual, t), bytes);
   };
-  if (fetched) {
-    fetch(g);
-    ahead.commit();
+  Token coming = {0, 0};
+  if constexpr (kAhead) {
+    const int own = kWarp ? threadIdx.x / 32 : 0;
+    ahead.step = 2 * bytes;
+    ahead.place = smem_addr(room) + own * 2 * ahead.step;
+    ahead.bar = smem_addr(&bars[2 * own]);
+    ahead.turn = ahead.parity = 0;
+    ahead.lost = false;
+    if (i0 == 0) {
+      bar_init(ahead.bar, 1);
+      bar_init(ahead.bar + 8, 1);
+      bar_init_done();
+      for (int i = 0; i < 2 && g + i * by < rows; ++i) {
+        find_token(P, g + i * by, &coming);
+        fetch(i, coming);
+      }
+    }
+    __syncthreads();
   }
-  F w[U][M];
-#pragma unroll
-  for (int u = 0; u < U; ++u) take_weight<N>(w[u], P.weight, i0 + u * threads, nv);
+  Token t = {0, 0};
   for (int parity = 0; g < rows; g += by, parity ^= 1) {
-    find_rank(P.first, g, &r);
-    const long long t = g - P.first[r];
-    V* kept = row_of<V, T>(P.sums[r], t, P.H);
-    const bool add = P.residual[r] != nullptr, keep = P.sums[r] != nullptr;
-    if (fetched) {
-      fetch(g + by);
-      ahead.commit_and_wait();
+    find_token(P, g, &t);
+    V* kept = row_of<V, T>(P.sums, t, i0);
+    const bool add = P.residual[t.r] != nullptr, keep = P.sums[t.r] != nullptr;
+    uint32_t here = 0;
+    if constexpr (kAhead) {
+      ahead.wait();
+      here = ahead.at(ahead.turn);
     }
     V s[U], a[U];
-    take_row(s, ahead, fetched, 0, row_of<V, T>(P.x[r], t, P.H), i0, threads, nv);
-    if (add) take_row(a, ahead, fetched, 1, row_of<V, T>(P.residual[r], t, P.H), i0, threads, nv);
+    take_row<kAhead>(s, here, row_of<V, T>(P.x, t, i0), i0, threads, nv);
+    if (add) take_row<kAhead>(a, here + bytes, row_of<V, T>(P.residual, t, i0), i0, threads, nv);
     F total2 = both<F>(0.0f);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -183,27 +224,42 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads)
           s[u] = Q::pack(f);
           Q::unpack(s[u], f);
         }
-        if (keep) kept[v] = s[u];
+        if (keep) kept[u * threads] = s[u];
 #pragma unroll
         for (int i = 0; i < M; ++i) total2 = fma2(f[i], f[i], total2);
       }
     }
     float total[1] = {sum_of(total2)};
     row_sum<kWarp, 1>(total, sums[parity]);
+    // (all threads have taken their part of the row: its place is free)
+    if constexpr (kAhead) {
+      if (kWarp) __syncwarp();
+      if (i0 == 0 && g + 2 * by < rows && !ahead.lost) {
+        find_token(P, g + 2 * by, &coming);
+        fetch(ahead.turn, coming);
+      }
+      ahead.next();
+    }
     const F scale = both<F>(rsqrtf(fmaf(total[0], P.per_feature, P.eps)));
-    unsigned char* packed = static_cast<unsigned char*>(P.out[r]) + t * P.row.bytes;
-    V* out = row_of<V, T>(P.out[r], t, P.H);
+    unsigned char* packed = nullptr;
+    V* out = nullptr;
+    if constexpr (kFormat == A2AV_PLAIN)
+      out = row_of<V, T>(P.out, t, i0);
+    else
+      packed = static_cast<unsigned char*>(P.out[t.r]) + (g - P.first[t.r]) * P.row.bytes;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int v = i0 + u * threads;
       F f[M];
       if (v < nv) {
+        F w[M];
+        take_weight<N>(w, P.weight, v);
         Q::unpack(s[u], f);
 #pragma unroll
-        for (int i = 0; i < M; ++i) f[i] = mul2(mul2(f[i], scale), w[u][i]);
+        for (int i = 0; i < M; ++i) f[i] = mul2(mul2(f[i], scale), w[i]);
       }
       if constexpr (kFormat == A2AV_PLAIN) {
-        if (v < nv) out[v] = Q::pack(f);
+        if (v < nv) out[u * threads] = Q::pack(f);
       } else if (u * threads < np) {
         if (v >= nv)
 #pragma unroll
@@ -216,99 +272,127 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads)
       if (used + i0 < P.row.bytes) packed[used + i0] = 0;  // (31 at most)
     }
   }
+  if constexpr (kAhead)
+    if (ahead.lost) give_up(ahead, P.status);
 }
 
 // d_x, and a block's part of the weight's gradient, kept in registers over its
 // rows.
-template <typename T, bool kVector, bool kWarp, int kThreads>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 1 : 512 / kThreads)
+template <typename T, bool kVector, bool kWarp, int kThreads, bool kAhead>
+__global__ void __maxnreg__(kThreads > 512 ? 64 : kThreads > 256 || sizeof(T) == 4 ? 128 : 144)
     norm_backward_kernel(const __grid_constant__ NormParams P) {
   chain();
-  constexpr int N = kVectorSize<T, kVector>, U = kHeldValues / N, M = kPairs<N>;
+  constexpr int N = kVectorSize<T, kVector>, U = held_backward(kVector, sizeof(T)) / N, M = kPairs<N>;
   using Q = Pairs<T, N>;
   using V = typename Q::Raw;
   using F = PairOf<N>;
   extern __shared__ uint4 room[];
   __shared__ float sums[2][kThreads / 32][2];
+  __shared__ unsigned long long bars[kWarp ? 2 * kThreads / 32 : 2];
   const int threads = kWarp ? 32 : blockDim.x, i0 = kWarp ? threadIdx.x % 32 : threadIdx.x;
   const int nv = P.H / N, per = kWarp ? blockDim.x / 32 : 1;
   const long long rows = P.first[P.W], by = (long long)gridDim.x * per;
   long long g = (long long)blockIdx.x * per + (kWarp ? threadIdx.x / 32 : 0);
-  Ahead<V, U> ahead{reinterpret_cast<V*>(room) + threadIdx.x, P.ahead, 0};
-  const bool fetched = kVector && P.ahead > 0;
-  int next = 0, r = 0;  // ranks of the row that is fetched and of this one
-  const auto fetch = [&](long long g) {
-    if (g >= rows) return;
-    find_rank(P.first, g, &next);
-    const long long t = g - P.first[next];
-    ahead.fetch(0, row_of<V, T>(P.x[next], t, P.H), i0, threads, nv);
-    ahead.fetch(1, row_of<V, T>(P.d_out[next], t, P.H), i0, threads, nv);
-    if (P.residual[next] != nullptr) ahead.fetch(2, row_of<V, T>(P.residual[next], t, P.H), i0, threads, nv);
+  Ahead ahead;
+  // (the thread that copies: the block's or the warp's first)
+  const unsigned bytes = (unsigned)P.H * sizeof(T);
+  const auto fetch = [&](int stage, const Token& t) {
+    const bool more = P.residual[t.r] != nullptr;
+    ahead.expect(stage, (more ? 3 : 2) * bytes);
+    ahead.fetch(stage, 0, row_of<V, T>(P.x, t), bytes);
+    ahead.fetch(stage, 1, row_of<V, T>(P.d_out, t), bytes);
+    if (more) ahead.fetch(stage, 2, row_of<V, T>(P.residual, t), bytes);
   };
-  if (fetched) {
-    fetch(g);
-    ahead.commit();
+  Token coming = {0, 0};
+  if constexpr (kAhead) {
+    const int own = kWarp ? threadIdx.x / 32 : 0;
+    ahead.step = 3 * bytes;
+    ahead.place = smem_addr(room) + own * 2 * ahead.step;
+    ahead.bar = smem_addr(&bars[2 * own]);
+    ahead.turn = ahead.parity = 0;
+    ahead.lost = false;
+    if (i0 == 0) {
+      bar_init(ahead.bar, 1);
+      bar_init(ahead.bar + 8, 1);
+      bar_init_done();
+      for (int i = 0; i < 2 && g + i * by < rows; ++i) {
+        find_token(P, g + i * by, &coming);
+        fetch(i, coming);
+      }
+    }
+    __syncthreads();
   }
-  F w[U][M], dw[U][M];
+  Token t = {0, 0};
+  F dw[U][M];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    take_weight<N>(w[u], P.weight, i0 + u * threads, nv);
+  for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int i = 0; i < M; ++i) dw[u][i] = both<F>(0.0f);
-  }
   for (int parity = 0; g < rows; g += by, parity ^= 1) {
-    find_rank(P.first, g, &r);
-    const long long t = g - P.first[r];
-    V* out = row_of<V, T>(P.out[r], t, P.H);
-    const bool add = P.residual[r] != nullptr;
-    if (fetched) {
-      fetch(g + by);
-      ahead.commit_and_wait();
+    find_token(P, g, &t);
+    V* out = row_of<V, T>(P.out, t, i0);
+    const bool add = P.residual[t.r] != nullptr;
+    uint32_t here = 0;
+    if constexpr (kAhead) {
+      ahead.wait();
+      here = ahead.at(ahead.turn);
     }
     V s[U], d[U], a[U];
-    take_row(s, ahead, fetched, 0, row_of<V, T>(P.x[r], t, P.H), i0, threads, nv);
-    take_row(d, ahead, fetched, 1, row_of<V, T>(P.d_out[r], t, P.H), i0, threads, nv);
-    if (add && !fetched) take_row(a, ahead, false, 2, row_of<V, T>(P.residual[r], t, P.H), i0, threads, nv);
+    take_row<kAhead>(s, here, row_of<V, T>(P.x, t, i0), i0, threads, nv);
+    take_row<kAhead>(d, here + bytes, row_of<V, T>(P.d_out, t, i0), i0, threads, nv);
+    if (add) take_row<kAhead>(a, here + 2 * bytes, row_of<V, T>(P.residual, t, i0), i0, threads, nv);
     F squares = both<F>(0.0f), products = both<F>(0.0f);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (i0 + u * threads < nv) {
-        F f[M], e[M];
+        F f[M], e[M], w[M];
+        take_weight<N>(w, P.weight, i0 + u * threads);
         Q::unpack(s[u], f);
         Q::unpack(d[u], e);
 #pragma unroll
         for (int i = 0; i < M; ++i) {
           squares = fma2(f[i], f[i], squares);
-          products = fma2(f[i], mul2(e[i], w[u][i]), products);
+          products = fma2(f[i], mul2(e[i], w[i]), products);
         }
       }
     float total[2] = {sum_of(squares), sum_of(products)};
     row_sum<kWarp, 2>(total, sums[parity]);
+    // (all threads have taken their part of the row: its place is free)
+    if constexpr (kAhead) {
+      if (kWarp) __syncwarp();
+      if (i0 == 0 && g + 2 * by < rows && !ahead.lost) {
+        find_token(P, g + 2 * by, &coming);
+        fetch(ahead.turn, coming);
+      }
+      ahead.next();
+    }
     const float one = rsqrtf(fmaf(total[0], P.per_feature, P.eps));
     const F scale = both<F>(one), along = both<F>(-one * one * (total[1] * P.per_feature));
-    if (add && fetched) take_row(a, ahead, true, 2, row_of<V, T>(P.residual[r], t, P.H), i0, threads, nv);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int v = i0 + u * threads;
       if (v < nv) {
-        F f[M], e[M], y[M];
+        F f[M], e[M], y[M], w[M];
+        take_weight<N>(w, P.weight, v);
         Q::unpack(s[u], f);
         Q::unpack(d[u], e);
         if (add) Q::unpack(a[u], y);
 #pragma unroll
         for (int i = 0; i < M; ++i) {
           dw[u][i] = fma2(e[i], mul2(f[i], scale), dw[u][i]);
-          const F z = fma2(f[i], along, mul2(e[i], w[u][i]));
+          const F z = fma2(f[i], along, mul2(e[i], w[i]));
           y[i] = add ? fma2(z, scale, y[i]) : mul2(z, scale);
         }
-        out[v] = Q::pack(y);
+        out[u * threads] = Q::pack(y);
       }
     }
   }
+  if constexpr (kAhead)
+    if (ahead.lost) give_up(ahead, P.status);
   if (P.part == nullptr) return;
   float* part = P.part + (long long)blockIdx.x * P.H;
   if constexpr (kWarp) {  // the block's warps one after the other
-    __shared__ float all[32 * kHeldValues];
+    __shared__ float all[32 * U * N];
     for (int k = 0; k < per; ++k) {
       if (threadIdx.x / 32 == k)
 #pragma unroll
@@ -537,76 +621,101 @@ constexpr int kNormParts = 1024;  // most blocks that keep a part of the weight'
 
 using NormKernel = void (*)(NormParams);
 
-// How a norm's rows are shared out: in vectors of 16 bytes or element by element; a
-// warp a row where it can hold one, else a block of up to 256 or 512 threads.
+// How a norm's rows are shared out, `held` values a thread: in vectors of 16 bytes or
+// element by element; a warp a row where it can hold one, else a block of up to 256,
+// 512 or 1024 threads.
 struct NormForm {
-  bool vector, warp, wide;
-  int threads;  // of a block
+  bool vector, warp, ahead;
+  int threads, most;  // of a block, and what its kernel is made for
 };
 
-NormForm norm_form(int64_t H, int size, uintptr_t low, long long rows, int sms) {
+NormForm norm_form(int64_t H, int size, uintptr_t low, long long rows, int sms, bool backward) {
   NormForm f;
   f.vector = low % 16 == 0 && H * size % 16 == 0;
-  const int n = f.vector ? 16 / size : 1, held = kHeldValues / n;
-  const int nv = (int)H / n;
+  int held = backward ? held_backward(f.vector, size) : kHeldValues;
+  const int n = f.vector ? 16 / size : 1, nv = (int)H / n;
+  held /= n;
   f.warp = nv <= 32 * held;
-  f.wide = false;
   f.threads = 256;
   if (!f.warp) {
-    int each = held;
     // few rows: more threads a row, with less to do each
-    while (rows < 2 * sms && each > 1 && (nv + each / 2 - 1) / (each / 2) <= 512) each /= 2;
-    f.threads = ((nv + each - 1) / each + 31) / 32 * 32;
-    f.wide = f.threads > 256;
+    while (rows < 2 * sms && held > 1 && (nv + held / 2 - 1) / (held / 2) <= 512) held /= 2;
+    f.threads = ((nv + held - 1) / held + 31) / 32 * 32;
   }
+  f.ahead = false;
+  f.most = f.threads <= 256 ? 256 : f.threads <= 512 ? 512 : 1024;
   return f;
 }
 
-template <typename T, bool kVector, int kFormat>
+template <typename T, int kFormat>
 NormKernel norm_kernel_of(const NormForm& f) {
-  if (f.warp) return norm_kernel<T, kVector, kFormat, true, 256>;
-  return f.wide ? norm_kernel<T, kVector, kFormat, false, 512> : norm_kernel<T, kVector, kFormat, false, 256>;
+  if (f.vector && f.ahead) {
+    if (f.warp) return norm_kernel<T, true, kFormat, true, 256, true>;
+    return f.most == 256 ? norm_kernel<T, true, kFormat, false, 256, true>
+                         : norm_kernel<T, true, kFormat, false, 512, true>;
+  }
+  if (f.vector) {
+    if (f.warp) return norm_kernel<T, true, kFormat, true, 256, false>;
+    return norm_kernel<T, true, kFormat, false, 512, false>;
+  }
+  return f.warp ? norm_kernel<T, false, kFormat, true, 256, false> : norm_kernel<T, false, kFormat, false, 512, false>;
 }
 
 template <typename T>
 NormKernel norm_kernel_of(int format, const NormForm& f) {
-  if (format == A2AV_MXFP8)
-    return f.vector ? norm_kernel_of<T, true, A2AV_MXFP8>(f) : norm_kernel_of<T, false, A2AV_MXFP8>(f);
-  if (format == A2AV_MXFP4)
-    return f.vector ? norm_kernel_of<T, true, A2AV_MXFP4>(f) : norm_kernel_of<T, false, A2AV_MXFP4>(f);
-  return f.vector ? norm_kernel_of<T, true, A2AV_PLAIN>(f) : norm_kernel_of<T, false, A2AV_PLAIN>(f);
-}
-
-template <typename T, bool kVector>
-NormKernel norm_backward_kernel_of(const NormForm& f) {
-  if (f.warp) return norm_backward_kernel<T, kVector, true, 256>;
-  return f.wide ? norm_backward_kernel<T, kVector, false, 512> : norm_backward_kernel<T, kVector, false, 256>;
+  if (format == A2AV_MXFP8) return norm_kernel_of<T, A2AV_MXFP8>(f);
+  return format == A2AV_MXFP4 ? norm_kernel_of<T, A2AV_MXFP4>(f) : norm_kernel_of<T, A2AV_PLAIN>(f);
 }
 
 template <typename T>
 NormKernel norm_backward_kernel_of(const NormForm& f) {
-  return f.vector ? norm_backward_kernel_of<T, true>(f) : norm_backward_kernel_of<T, false>(f);
+  if (f.vector && f.ahead) {
+    if (f.warp) return norm_backward_kernel<T, true, true, 256, true>;
+    return f.most == 256 ? norm_backward_kernel<T, true, false, 256, true>
+                         : norm_backward_kernel<T, true, false, 512, true>;
+  }
+  if (f.vector) {
+    if (f.warp) return norm_backward_kernel<T, true, true, 256, false>;
+    if constexpr (sizeof(T) == 4)  // (16 bits: 16,384 features are 512 threads')
+      if (f.most > 512) return norm_backward_kernel<T, true, false, 1024, false>;
+    return norm_backward_kernel<T, true, false, 512, false>;
+  }
+  if (f.warp) return norm_backward_kernel<T, false, true, 256, false>;
+  return f.most <= 512 ? norm_backward_kernel<T, false, false, 512, false>
+                       : norm_backward_kernel<T, false, false, 1024, false>;
+}
+
+NormKernel norm_kernel_of(int dtype, int format, const NormForm& f) {
+  if (dtype == A2AV_F32) return norm_kernel_of<float>(format, f);
+  return dtype == A2AV_BF16 ? norm_kernel_of<__nv_bfloat16>(format, f) : norm_kernel_of<__half>(format, f);
+}
+
+NormKernel norm_backward_kernel_of(int dtype, const NormForm& f) {
+  if (dtype == A2AV_F32) return norm_backward_kernel_of<float>(f);
+  return dtype == A2AV_BF16 ? norm_backward_kernel_of<__nv_bfloat16>(f) : norm_backward_kernel_of<__half>(f);
 }
 
 constexpr size_t kMostRoom = 200 << 10;  // shared memory that a block fetches rows to
 
-// Launches a kernel whose rows have `arrays` arrays to read.  The blocks are as many
-// as the GPU holds, and not more than the rows need or `limit`; where they take
-// several rows each, they fetch them ahead.
-cudaError_t launch_norm(const a2av_handle* h, NormKernel kernel, const NormForm& f, int size, int arrays,
-                        long long rows, long long limit, NormParams& P, cudaStream_t s, unsigned* blocks) {
-  const void* k = reinterpret_cast<const void*>(kernel);
+// Launches the kernel that kernel_of(form) is, whose rows take `row_bytes` of all arrays
+// together.  The blocks are as many as the GPU holds, and not more than the rows need
+// or `limit`; where they take several rows each, they fetch them ahead.
+template <typename K>
+cudaError_t launch_norm(const a2av_handle* h, K kernel_of, NormForm f, int row_bytes, long long rows,
+                        long long limit, const NormParams& P, cudaStream_t s, unsigned* blocks) {
   const long long per = f.warp ? f.threads / 32 : 1, want = (rows + per - 1) / per;
+  NormKernel kernel = kernel_of(f);
   int fit = 0;
   size_t room = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, k, f.threads, 0);
+  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, f.threads, 0);
   if (e != cudaSuccess) return e;
-  const size_t two_rows = (size_t)2 * arrays * f.threads * kHeldValues * size;
-  if (f.vector && want > (long long)fit * h->sms && two_rows <= kMostRoom) {
-    P.ahead = arrays;
+  const size_t two_rows = (size_t)2 * per * row_bytes;
+  if (f.vector && f.most <= 512 && want > (long long)fit * h->sms && two_rows <= kMostRoom) {
+    f.ahead = true;
+    kernel = kernel_of(f);
     room = two_rows;
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)room);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, k, f.threads, room);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)room);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, f.threads, room);
     if (e != cudaSuccess) return e;
   }
   long long most = (long long)fit * h->sms;
@@ -699,7 +808,7 @@ extern "C" int a2av_norm(a2av_handle* h, int64_t features, int dtype, int format
   rc = count_rows(h, tokens_per_rank, P.first);
   if (rc != A2AV_OK) return rc;
   const int W = h->W, size = dtype_bytes(dtype);
-  uintptr_t low = 0, other = 0;
+  uintptr_t low = (uintptr_t)weight_dev, other = 0;
   if (!take_rows(P.x, x_ptrs, W, tokens_per_rank, size, &low) ||
       (residual_ptrs != nullptr && !take_rows(P.residual, residual_ptrs, W, tokens_per_rank, size, &low)) ||
       (sum_ptrs != nullptr && !take_rows(P.sums, sum_ptrs, W, tokens_per_rank, size, &low)) ||
@@ -715,13 +824,12 @@ extern "C" int a2av_norm(a2av_handle* h, int64_t features, int dtype, int format
   P.W = W;
   P.H = (int)features;
   P.eps = eps;
+  P.status = h->d_status;
   P.per_feature = 1.0f / (float)features;
-  const NormForm f = norm_form(features, size, low, rows, h->sms);
-  const NormKernel kernel = dtype == A2AV_F32    ? norm_kernel_of<float>(format, f)
-                            : dtype == A2AV_BF16 ? norm_kernel_of<__nv_bfloat16>(format, f)
-                                                 : norm_kernel_of<__half>(format, f);
+  const NormForm f = norm_form(features, size, low, rows, h->sms, false);
   unsigned blocks;
-  const cudaError_t e = launch_norm(h, kernel, f, size, residual_ptrs != nullptr ? 2 : 1, rows, rows, P,
+  const cudaError_t e = launch_norm(h, [&](const NormForm& g) { return norm_kernel_of(dtype, format, g); }, f,
+                                    2 * (int)features * size, rows, rows, P,
                                     static_cast<cudaStream_t>(stream), &blocks);
   return e != cudaSuccess || cudaGetLastError() != cudaSuccess ? A2AV_ERR_CUDA : A2AV_OK;
 }
@@ -746,7 +854,7 @@ extern "C" int a2av_norm_backward(a2av_handle* h, int64_t features, int dtype, f
   rc = count_rows(h, tokens_per_rank, P.first);
   if (rc != A2AV_OK) return rc;
   const int W = h->W, size = dtype_bytes(dtype);
-  uintptr_t low = 0;
+  uintptr_t low = (uintptr_t)weight_dev;
   if (!take_rows(P.x, sum_ptrs, W, tokens_per_rank, size, &low) ||
       !take_rows(P.d_out, d_out_ptrs, W, tokens_per_rank, size, &low) ||
       (d_sum_ptrs != nullptr && !take_rows(P.residual, d_sum_ptrs, W, tokens_per_rank, size, &low)) ||
@@ -765,16 +873,15 @@ extern "C" int a2av_norm_backward(a2av_handle* h, int64_t features, int dtype, f
   P.W = W;
   P.H = (int)features;
   P.eps = eps;
+  P.status = h->d_status;
   P.per_feature = 1.0f / (float)features;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   unsigned blocks = 0;
   if (rows > 0) {
-    const NormForm f = norm_form(features, size, low, rows, h->sms);
-    const NormKernel kernel = dtype == A2AV_F32    ? norm_backward_kernel_of<float>(f)
-                              : dtype == A2AV_BF16 ? norm_backward_kernel_of<__nv_bfloat16>(f)
-                                                   : norm_backward_kernel_of<__half>(f);
-    e = launch_norm(h, kernel, f, size, d_sum_ptrs != nullptr ? 3 : 2, rows, kNormParts, P, s, &blocks);
+    const NormForm f = norm_form(features, size, low, rows, h->sms, true);
+    e = launch_norm(h, [&](const NormForm& g) { return norm_backward_kernel_of(dtype, g); }, f,
+                    3 * (int)features * size, rows, kNormParts, P, s, &blocks);
   }
   if (e == cudaSuccess && d_weight_dev != nullptr)
     e = launch_chained(norm_weight_kernel, dim3((unsigned)((features + 31) / 32)), 1024, 0, s, h->pdl,
