@@ -25,7 +25,7 @@ constexpr int kAccColumns = 256;      // columns between the two tiles' sums
 constexpr int kScaleWarps = 3;        // 128 features, 128 rows and the other rows
 constexpr int kAtom = 512;            // bytes of 128 rows' words of scales
 constexpr int kMxThreads = 128 + 32 * (kEpilogueWarps + kScaleWarps);
-constexpr int kAhead = 3;             // 16-byte pieces of a row's scales in flight
+constexpr int kAhead = 3;             // 16-byte pieces of a row's scales in flight, at most
 constexpr int kHeld = kAhead * 128 * 16;  // of a scale warp's rows
 
 // Words of scales that a stage has of each row.
@@ -229,61 +229,84 @@ __global__ void __launch_bounds__(kMxThreads, 1) __cluster_dims__(2, 1, 1)
     if (!ok && lane == 0) note_error(P.g.status, A2AV_ERR_TIMEOUT);
   } else if (warp >= 4 + kEpilogueWarps) {
     // ------------------------------------------------------ scales --
-    // a lane has rows lane, 32 + lane, 64 + lane and 96 + lane of the warp's 128
+    // a lane has rows lane, 32 + lane, 64 + lane and 96 + lane of the warp's 128;
+    // pieces of 16 bytes of their scales come through a ring of the lane's own, the
+    // next tile's behind this one's (no further: a slot three tiles on is described
+    // when this tile is done)
     const int part = warp - 4 - kEpilogueWarps;
     const uint32_t full0 = map_to(smem_addr(&b.full[0]), 0);
     const uint32_t held = scales + kMxStages * kScaleBytes<kFormat> + kEpilogueWarps * kStaging +
                           part * kHeld + lane * 16;
     constexpr int kPer = 4 / kWords;  // stages that a piece lasts
-    const int count = (int)P.at.scales, pieces = (count + 15) / 16;
-    unsigned it = 0;
-    for (; ok && tile_of(i, pair, pairs) < tiles; ++i) {
-      const unsigned sl = i % kSlots;
-      ok = __all_sync(kAll, bar_wait_tile(smem_addr(&b.slot_full[sl]), (i / kSlots) & 1, ring));
-      if (!ok) break;
-      const Slot& slot = slots[sl];
-      const int p = slot.p;
-      const uint4* from[4];  // NULL: no such row
-      bool any = false;
+    const int count = P.at.scales, pieces = (count + 15) / 16, lead = min(pieces, kAhead);
+    const uint4* from[4];   // of the tile that is fetched; NULL: no such row
+    unsigned fi = 0, it = 0, any = 0;  // that tile, stages, tiles with rows (a bit each)
+    int fc = 0;             // the piece that is fetched next
+    bool more = tile_of(0, pair, pairs) < tiles;
+    uint32_t into = held, out_of = held;  // places in the ring
+    const auto next_place = [&](uint32_t at) { return at == held + (kAhead - 1) * 2048 ? held : at + 2048; };
+    const auto fetch = [&] {
+      if (more) {
+        if (fc == 0) {
+          const unsigned sl = fi % kSlots;
+          ok = __all_sync(kAll, bar_wait_tile(smem_addr(&b.slot_full[sl]), (fi / kSlots) & 1, ring));
+          const Slot& slot = slots[sl];
+          bool some = false;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = lane + 32 * k;
-        const unsigned char* row = nullptr;
-        if (part == 0) {
-          const int f = slot.f + kMyF * rank + (kGated ? r / 16 * 8 + r % 8 : r);
-          const long long z = f + (kGated && r / 8 % 2 ? P.F : 0);
-          if (f < P.F)
-            row = static_cast<const unsigned char*>(P.w[p]) + ((long long)slot.e * P.Z + z) * P.at.bytes;
-        } else {
-          const int n = (part - 1) * 128 + r, gr = n / kGranule;
-          if (n % kGranule < slot.n[gr])
-            row = static_cast<const unsigned char*>(P.x[p]) +
-                  ((long long)slot.row[gr] + n % kGranule) * P.at.bytes;
+          for (int k = 0; k < 4; ++k) {
+            const int r = lane + 32 * k;
+            const unsigned char* row = nullptr;
+            if (!ok) {
+            } else if (part == 0) {
+              const int f = slot.f + kMyF * rank + (kGated ? r / 16 * 8 + r % 8 : r);
+              const long long z = f + (kGated && r / 8 % 2 ? P.F : 0);
+              if (f < P.F)
+                row = static_cast<const unsigned char*>(P.w[slot.p]) +
+                      ((long long)slot.e * P.Z + z) * P.at.bytes;
+            } else {
+              const int m = (part - 1) * 128 + r, gr = m / kGranule;
+              if (m % kGranule < slot.n[gr])
+                row = static_cast<const unsigned char*>(P.x[slot.p]) +
+                      ((long long)slot.row[gr] + m % kGranule) * P.at.bytes;
+            }
+            from[k] = row == nullptr ? nullptr : reinterpret_cast<const uint4*>(row + P.at.values);
+            some = some || row != nullptr;
+          }
+          const unsigned bit = 1u << (fi & 31);
+          any = __any_sync(kAll, some) ? any | bit : any & ~bit;
+          if (ok && lane == 0) bar_arrive_here(smem_addr(&b.slot_empty[sl]));
         }
-        from[k] = row == nullptr ? nullptr : reinterpret_cast<const uint4*>(row + P.at.values);
-        any = any || row != nullptr;
-      }
-      any = __any_sync(kAll, any);
-      if (lane == 0) bar_arrive_here(smem_addr(&b.slot_empty[sl]));
-      // pieces come through a ring of the lane's own, so that several are in flight
-      const auto fetch = [&](int c) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const bool here = from[k] != nullptr && c < pieces;
-          copy_async(held + (c % kAhead * 4 + k) * 512, here ? from[k] + c : static_cast<const uint4*>(P.w[p]),
+          // (zeros: any address does)
+          const bool here = ok && from[k] != nullptr;
+          copy_async(into + k * 512, here ? from[k] + fc : static_cast<const void*>(P.g.counts),
                      here ? 16 : 0);
         }
-        copy_async_commit();
-      };
-      for (int c = 0; c < kAhead; ++c) fetch(c);
+        into = next_place(into);
+        if (++fc == pieces) {
+          fc = 0;
+          ++fi;
+          more = ok && tile_of(fi, pair, pairs) < tiles;
+        }
+      }
+      copy_async_commit();
+    };
+    for (int c = 0; c < lead; ++c) fetch();
+    for (; ok && tile_of(i, pair, pairs) < tiles; ++i) {
       for (int c = 0; ok && c < pieces; ++c) {
-        copy_async_wait<kAhead - 1>();
+        if (lead == 3)
+          copy_async_wait<2>();
+        else if (lead == 2)
+          copy_async_wait<1>();
+        else
+          copy_async_wait<0>();
         uint4 v[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w)
-                       : "r"(held + (c % kAhead * 4 + k) * 512)
+                       : "r"(out_of + k * 512)
                        : "memory");
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
@@ -291,7 +314,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) __cluster_dims__(2, 1, 1)
           const unsigned s = it % kMxStages;
           ok = __all_sync(kAll, bar_wait(smem_addr(&b.empty[s]), ((it / kMxStages) & 1) ^ 1));
           if (!ok) continue;
-          if (any) {
+          if (any >> (i & 31) & 1) {
 #pragma unroll
             for (int w = 0; w < kWords; ++w) {
               const int word = j * kWords + w;
@@ -313,7 +336,8 @@ __global__ void __launch_bounds__(kMxThreads, 1) __cluster_dims__(2, 1, 1)
           if (lane == 0) bar_arrive_filled(full0 + s * 8);
           ++it;
         }
-        fetch(c + kAhead);
+        out_of = next_place(out_of);
+        if (ok) fetch();
       }
     }
     copy_async_wait<0>();
