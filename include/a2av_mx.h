@@ -6,10 +6,11 @@
  *
  * A serving layer on W ranks (a2av_moe.h has the other calls):
  *
- *   a2av_norm              h += x; y = norm(h), written as packed rows
+ *   a2av_norm              h += x; y = norm(h), written as packed rows (and plain, for the router)
  *   a2av_route, a2av_dispatch   row_bytes = a2av_mx_row_bytes(features, format)
  *   a2av_expert_matmul_mx  packed rows times packed weights, in 32 bits
  *   a2av_quantise          the inner activations packed again, for the next product
+ *   a2av_combine_weighted  a token's rows summed, onto h
  *
  * A packed row of D values, Dp being D rounded up to 32:
  *
@@ -74,14 +75,17 @@ int64_t a2av_mx_row_bytes(int64_t features, int format);
  *  sum_ptrs           HOST array of W: s is written here, or NULL.  May be x_ptrs or
  *                     residual_ptrs.
  *  out_ptrs           HOST array of W: y, [tokens][H] or [tokens][a2av_mx_row_bytes(H)].
+ *  plain_ptrs         HOST array of W: y rounded to dtype as well (for a router's product),
+ *                     with a packed format, or NULL.
  *
- * Host errors: A2AV_ERR_INVALID_ARG, A2AV_ERR_UNSUPPORTED (features or tokens above the
- * limits), A2AV_ERR_CUDA.
+ * Device error: A2AV_ERR_TIMEOUT when a copy has not come for about a second: results
+ * are not complete.  Host errors: A2AV_ERR_INVALID_ARG, A2AV_ERR_UNSUPPORTED (features or
+ * tokens above the limits), A2AV_ERR_CUDA.
  */
 int a2av_norm(a2av_handle *h, int64_t features, int dtype, int format, float eps,
               const void *const *x_ptrs, const int64_t *tokens_per_rank, const float *weight_dev,
               const void *const *residual_ptrs, void *const *sum_ptrs, void *const *out_ptrs,
-              void *stream);
+              void *const *plain_ptrs, void *stream);
 
 /* a2av_norm_workspace_bytes -- device workspace of a2av_norm_backward with a weight's
  * gradient for `total_rows` tokens together; -1 for what it would reject. */

@@ -131,6 +131,22 @@ def test_packed_output_is_the_plain_ones(fmt):
         assert torch.equal(again[0], packed[0])
 
 
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_both_outputs(fmt):
+    """With a packed result, the plain one as well: each what a call by itself gives."""
+    for dtype, tokens, H, offset in (("bf16", [9, 0, 2], 1024, 0), ("f32", [3], 100, 0), ("f16", [700], 1504, 1),
+                                     ("bf16", [900], 7168, 0)):
+        x, res, w = _rows(tokens, H, dtype, 40, offset), _rows(tokens, H, dtype, 41, offset), _weight(H)
+        want, packed = _forward(x, w, dtype, res), _forward(x, w, dtype, res, fmt=fmt)
+        out, plain = [torch.zeros_like(t) for t in packed], [torch.zeros_like(t) for t in x]
+        with a2av.A2av(len(x)) as eng:
+            eng.norm(x, w, out, residual=res, eps=EPS, format=fmt, plain=plain)
+            assert eng.status() == a2av.OK
+            with pytest.raises(ValueError):
+                eng.norm(x, w, plain, residual=res, plain=plain)
+        assert all(torch.equal(a, b) for a, b in zip(out + plain, packed + want))
+
+
 def test_special_rows():
     """Rows of zeros, of NaN and infinities, and rows whose squares pass 32 bits, by themselves."""
     H = 256

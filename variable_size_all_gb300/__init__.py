@@ -130,7 +130,7 @@ def load():
     f32 = ctypes.c_float
     lib.a2av_mx_row_bytes.argtypes = [i64, ci]
     lib.a2av_mx_row_bytes.restype = i64
-    lib.a2av_norm.argtypes = [vp, i64, ci, ci, f32, vp, i64p, vp, vp, vp, vp, vp]
+    lib.a2av_norm.argtypes = [vp, i64, ci, ci, f32, vp, i64p, vp, vp, vp, vp, vp, vp]
     lib.a2av_norm_workspace_bytes.argtypes = [i64, i64]
     lib.a2av_norm_workspace_bytes.restype = i64
     lib.a2av_norm_backward.argtypes = [vp, i64, ci, f32, vp, i64p, vp, vp, vp, vp, vp, vp, i64, vp]
@@ -374,12 +374,13 @@ def a2av_mx_row_bytes(features: int, format: int) -> int:
 
 
 def a2av_norm(handle, features: int, dtype: int, format: int, eps: float, x_ptrs, tokens_per_rank,
-              weight: int, residual_ptrs, sum_ptrs, out_ptrs, stream: int = 0) -> int:
+              weight: int, residual_ptrs, sum_ptrs, out_ptrs, plain_ptrs=None,
+              stream: int = 0) -> int:
     """Raw norm (include/a2av_mx.h): integer device addresses, lists (or None) per rank."""
     return load().a2av_norm(handle, int(features), int(dtype), int(format), eps, _ptr_array(x_ptrs),
                             _i64_array(tokens_per_rank), _address(weight),
                             _optional_ptrs(residual_ptrs), _optional_ptrs(sum_ptrs),
-                            _ptr_array(out_ptrs), _address(stream))
+                            _ptr_array(out_ptrs), _optional_ptrs(plain_ptrs), _address(stream))
 
 
 def a2av_norm_workspace_bytes(features: int, total_rows: int) -> int:
@@ -1208,7 +1209,7 @@ class A2av:
         return t.data_ptr()
 
     def norm(self, x, weight, outputs, residual=None, sums=None, eps: float = 1e-6, format=None,
-             stream=None, _bind=False):
+             plain=None, stream=None, _bind=False):
         """Root-mean-square norm (see include/a2av_mx.h, a2av_norm): s = x + residual,
         y = s / sqrt(mean(s^2) + eps) * weight.
 
@@ -1216,21 +1217,24 @@ class A2av:
         float16 tensor; ``weight`` float32 [H].  Written: ``sums[r]`` (optional; may be
         ``x[r]`` or ``residual[r]``) with s, and ``outputs[r]`` with y: [T, H] of the same
         type, or, with ``format`` "mxfp8" or "mxfp4", packed rows, uint8
-        [T, mx_row_bytes(H, format)]."""
+        [T, mx_row_bytes(H, format)]; ``plain[r]`` (optional, then) gets y in the rows' type too."""
         if not _bind and self._whole("norm", stream, x, weight, outputs, residual, sums, eps,
-                                     _FORMATS.get(format), self._entries["mx_row_bytes"]):
+                                     _FORMATS.get(format), plain, self._entries["mx_row_bytes"]):
             return
         n, H = self._tokens(x, "x")
         dtype, code = self._dtype(x, "x", (F32, BF16, F16))
         width = H if format is None else mx_row_bytes(H, format)
+        if format is None and plain is not None:
+            raise ValueError("plain goes with a packed format")
         w = self._vector(weight, H, "weight")
         shapes = [(m, H) for m in n]
-        (xs, res, kept, y), arrays = self._lists(
+        (xs, res, kept, y, too), arrays = self._lists(
             (x, dtype, shapes, "x"), (residual, dtype, shapes, "residual"), (sums, dtype, shapes, "sums"),
-            (outputs, dtype if format is None else self._bytes, [(m, width) for m in n], "outputs"))
+            (outputs, dtype if format is None else self._bytes, [(m, width) for m in n], "outputs"),
+            (plain, dtype, shapes, "plain"))
         args = [self.handle, H, code, _FORMATS[format], eps, xs, self._counts(*n), w, res, kept, y,
-                self._queue(stream)]
-        return self._call("a2av_norm", args, (x, weight, outputs, residual, sums, arrays), _bind)
+                too, self._queue(stream)]
+        return self._call("a2av_norm", args, (x, weight, outputs, residual, sums, plain, arrays), _bind)
 
     def bind_norm(self, x, weight, outputs, **options) -> BoundCall:
         """``norm`` marshalled once (see BoundCall)."""

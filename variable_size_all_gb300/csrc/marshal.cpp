@@ -567,26 +567,28 @@ struct Normed {
   }
 };
 
-// (..., x, weight, outputs, residual, sums, eps, format, a2av_mx_row_bytes)
+// (..., x, weight, outputs, residual, sums, eps, format, plain, a2av_mx_row_bytes)
 PyObject* norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Normed m;
   int format = A2AV_PLAIN;
-  void *out[kRanks], *residual[kRanks], *sums[kRanks];
+  void *out[kRanks], *residual[kRanks], *sums[kRanks], *plain[kRanks];
   return whole(
-      n, 12,
+      n, 13,
       [&] {
         if (!call_of(args, &m.c) || !m.take_all(args[4], args[5], args[9]) || !int_of(args[10], &format) ||
             !take_optional(args[7], m.c.W, m.type, residual, m.rows, m.H) ||
             !take_optional(args[8], m.c.W, m.type, sums, m.rows, m.H))
           return false;
-        if (format == A2AV_PLAIN) return take_rows(args[6], m.c.W, m.type, out, m.rows, m.H);
-        return take_rows(args[6], m.c.W, at::kByte, out, m.rows, packed_bytes(args[11], m.H, format));
+        if (format == A2AV_PLAIN)
+          return args[11] == Py_None && take_rows(args[6], m.c.W, m.type, out, m.rows, m.H);
+        return take_rows(args[6], m.c.W, at::kByte, out, m.rows, packed_bytes(args[12], m.H, format)) &&
+               take_optional(args[11], m.c.W, m.type, plain, m.rows, m.H);
       },
       [&] {
         return reinterpret_cast<decltype(&a2av_norm)>(m.c.function)(
             static_cast<a2av_handle*>(m.c.handle), m.H, m.dtype, format, m.eps, m.x, m.rows, m.weight,
             args[7] == Py_None ? nullptr : residual, args[8] == Py_None ? nullptr : sums, out,
-            m.c.stream);
+            args[11] == Py_None ? nullptr : plain, m.c.stream);
       });
 }
 

@@ -15,6 +15,7 @@ struct NormParams {
   const void* residual[kW];  // or NULL; backward: d_sums
   void* sums[kW];            // or NULL
   void* out[kW];             // y; backward: d_x
+  void* plain[kW];           // y in the rows' type as well, or NULL
   const void* d_out[kW];     // backward: dy
   long long first[kW + 1];   // tokens before each rank's
   const float* weight;
@@ -242,10 +243,9 @@ __global__ void __maxnreg__(sizeof(T) == 4 || !kVector ? 128 : 96)
     }
     const F scale = both<F>(rsqrtf(fmaf(total[0], P.per_feature, P.eps)));
     unsigned char* packed = nullptr;
-    V* out = nullptr;
-    if constexpr (kFormat == A2AV_PLAIN)
-      out = row_of<V, T>(P.out, t, i0);
-    else
+    V* out = row_of<V, T>(kFormat == A2AV_PLAIN ? P.out : P.plain, t, i0);
+    const bool plain = kFormat == A2AV_PLAIN || P.plain[t.r] != nullptr;
+    if constexpr (kFormat != A2AV_PLAIN)
       packed = static_cast<unsigned char*>(P.out[t.r]) + (g - P.first[t.r]) * P.row.bytes;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -258,13 +258,13 @@ __global__ void __maxnreg__(sizeof(T) == 4 || !kVector ? 128 : 96)
 #pragma unroll
         for (int i = 0; i < M; ++i) f[i] = mul2(mul2(f[i], scale), w[i]);
       }
-      if constexpr (kFormat == A2AV_PLAIN) {
-        if (v < nv) out[u * threads] = Q::pack(f);
-      } else if (u * threads < np) {
+      if (plain && v < nv) out[u * threads] = Q::pack(f);
+      if (kFormat != A2AV_PLAIN && u * threads < np) {
         if (v >= nv)
 #pragma unroll
           for (int i = 0; i < M; ++i) f[i] = both<F>(0.0f);
-        mx_store<kFormat, N>(packed, P.row.values, v, f, __float_as_uint(largest(f)), v < np);
+        if constexpr (kFormat != A2AV_PLAIN)
+          mx_store<kFormat, N>(packed, P.row.values, v, f, __float_as_uint(largest(f)), v < np);
       }
     }
     if constexpr (kFormat != A2AV_PLAIN) {
@@ -799,10 +799,12 @@ extern "C" int64_t a2av_mx_row_bytes(int64_t features, int format) {
 extern "C" int a2av_norm(a2av_handle* h, int64_t features, int dtype, int format, float eps,
                          const void* const* x_ptrs, const int64_t* tokens_per_rank,
                          const float* weight_dev, const void* const* residual_ptrs,
-                         void* const* sum_ptrs, void* const* out_ptrs, void* stream) {
+                         void* const* sum_ptrs, void* const* out_ptrs, void* const* plain_ptrs,
+                         void* stream) {
   int rc = norm_ok(h, features, dtype, eps, x_ptrs, tokens_per_rank, weight_dev, out_ptrs);
   if (rc != A2AV_OK) return rc;
-  if (format != A2AV_PLAIN && !is_packed(format)) return A2AV_ERR_INVALID_ARG;
+  if ((format != A2AV_PLAIN && !is_packed(format)) || (format == A2AV_PLAIN && plain_ptrs != nullptr))
+    return A2AV_ERR_INVALID_ARG;
   NormParams P;
   std::memset(&P, 0, sizeof(P));
   rc = count_rows(h, tokens_per_rank, P.first);
@@ -813,7 +815,8 @@ extern "C" int a2av_norm(a2av_handle* h, int64_t features, int dtype, int format
       (residual_ptrs != nullptr && !take_rows(P.residual, residual_ptrs, W, tokens_per_rank, size, &low)) ||
       (sum_ptrs != nullptr && !take_rows(P.sums, sum_ptrs, W, tokens_per_rank, size, &low)) ||
       !take_rows(P.out, out_ptrs, W, tokens_per_rank, format == A2AV_PLAIN ? size : 16,
-                 format == A2AV_PLAIN ? &low : &other))
+                 format == A2AV_PLAIN ? &low : &other) ||
+      (plain_ptrs != nullptr && !take_rows(P.plain, plain_ptrs, W, tokens_per_rank, size, &low)))
     return A2AV_ERR_INVALID_ARG;
   rc = current_device(h);
   if (rc != A2AV_OK) return rc;
