@@ -120,6 +120,8 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 __device__ __forceinline__ float mul2(float a, float b) { return a * b; }
 __device__ __forceinline__ float add2(float a, float b) { return a + b; }
 __device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float minus(float x) { return -x; }
+__device__ __forceinline__ float2 minus(float2 x) { return make_float2(-x.x, -x.y); }
 template <typename P>
 __device__ __forceinline__ P both(float x) {
   if constexpr (__is_same(P, float))

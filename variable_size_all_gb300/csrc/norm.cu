@@ -151,6 +151,20 @@ __device__ __forceinline__ void take_weight(PairOf<N> (&w)[kPairs<N>], const flo
   }
 }
 
+// 1 / sqrt(x) as a sum of two, to some 2^-45: what the first is off, from its square.
+// (The norm's codes go by which side of a border a value is on: with the last bits of
+// the scale and of both products right, the 8-bit results differ from those of 64 bits as
+// rarely as an f32 value's rounding makes them.)
+struct Scale {
+  float high, low;
+};
+__device__ __forceinline__ Scale inverse_root(float x) {
+  const float r = rsqrtf(x), t = x * r;
+  const float off = fmaf(-t, r, 1.0f) - fmaf(x, r, -t) * r;
+  const float low = 0.5f * r * off;
+  return {r, isfinite(low) ? low : 0.0f};  // (x of 0 or infinity)
+}
+
 template <typename T, bool kVector, int kFormat, bool kWarp, int kThreads, bool kAhead>
 __global__ void __maxnreg__(sizeof(T) == 4 || !kVector ? 128 : 96)
     norm_kernel(const __grid_constant__ NormParams P) {
@@ -241,7 +255,8 @@ __global__ void __maxnreg__(sizeof(T) == 4 || !kVector ? 128 : 96)
       }
       ahead.next();
     }
-    const F scale = both<F>(rsqrtf(fmaf(total[0], P.per_feature, P.eps)));
+    const Scale root = inverse_root(fmaf(total[0], P.per_feature, P.eps));
+    const F high = both<F>(root.high), low = both<F>(root.low);
     unsigned char* packed = nullptr;
     V* out = row_of<V, T>(kFormat == A2AV_PLAIN ? P.out : P.plain, t, i0);
     const bool plain = kFormat == A2AV_PLAIN || P.plain[t.r] != nullptr;
@@ -256,7 +271,10 @@ __global__ void __maxnreg__(sizeof(T) == 4 || !kVector ? 128 : 96)
         take_weight<N>(w, P.weight, v);
         Q::unpack(s[u], f);
 #pragma unroll
-        for (int i = 0; i < M; ++i) f[i] = mul2(mul2(f[i], scale), w[i]);
+        for (int i = 0; i < M; ++i) {
+          const F a = mul2(f[i], high), rest = fma2(f[i], low, fma2(f[i], high, minus(a)));
+          f[i] = fma2(a, w[i], mul2(rest, w[i]));
+        }
       }
       if (plain && v < nv) out[u * threads] = Q::pack(f);
       if (kFormat != A2AV_PLAIN && u * threads < np) {
@@ -279,7 +297,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 || !kVector ? 128 : 96)
 // d_x, and a block's part of the weight's gradient, kept in registers over its
 // rows.
 template <typename T, bool kVector, bool kWarp, int kThreads, bool kAhead>
-__global__ void __maxnreg__(kThreads > 512 ? 64 : kThreads > 256 || sizeof(T) == 4 ? 128 : 144)
+__global__ void __maxnreg__(kThreads > 512 ? 64 : 128)
     norm_backward_kernel(const __grid_constant__ NormParams P) {
   chain();
   constexpr int N = kVectorSize<T, kVector>, U = held_backward(kVector, sizeof(T)) / N, M = kPairs<N>;
