@@ -46,29 +46,9 @@ __device__ __forceinline__ float mx_scale_value(unsigned s) {
 // The largest of a value over the lanes that differ in the low kLanes - 1 bits.
 template <int kLanes>
 __device__ __forceinline__ unsigned lanes_max(unsigned x) {
-  if constexpr (kLanes == 32) {
-    return __reduce_max_sync(kAll, x);
-  } else {
 #pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) x = max(x, __shfl_xor_sync(kAll, x, o));
-    return x;
-  }
-}
-
-__device__ __forceinline__ unsigned e4m3_pair(float lo, float hi) {
-  unsigned short r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ unsigned e2m1_pair(float lo, float hi) {
-  unsigned short r;
-  asm("{\n\t.reg .b8 b;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
-      "mov.b16 %0, {b, b};\n\t}"
-      : "=h"(r)
-      : "f"(hi), "f"(lo));
-  return r & 0xffu;
+  for (int o = 1; o < kLanes; o <<= 1) x = max(x, __shfl_xor_sync(kAll, x, o));
+  return x;
 }
 
 // Two codes (in the low bits) as the values they stand for.
@@ -88,13 +68,7 @@ __device__ __forceinline__ float2 e2m1_values(unsigned pair) {
   return unpack2(r, __half());
 }
 
-// N values as pairs, or the one of N = 1: products of pairs are one instruction on
-// this architecture.
-template <int N>
-constexpr int kPairs = N == 1 ? 1 : N / 2;
-template <int N>
-using PairOf = std::conditional_t<N == 1, float, float2>;
-
+// Values are held in pairs: products of pairs are one instruction on this architecture.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 r;
   asm("mul.rn.f32x2 %0, %1, %2;"
@@ -117,66 +91,129 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         "l"(reinterpret_cast<const unsigned long long&>(c)));
   return r;
 }
-__device__ __forceinline__ float mul2(float a, float b) { return a * b; }
-__device__ __forceinline__ float add2(float a, float b) { return a + b; }
-__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
-__device__ __forceinline__ float minus(float x) { return -x; }
 __device__ __forceinline__ float2 minus(float2 x) { return make_float2(-x.x, -x.y); }
-template <typename P>
-__device__ __forceinline__ P both(float x) {
-  if constexpr (__is_same(P, float))
-    return x;
-  else
-    return make_float2(x, x);
-}
-__device__ __forceinline__ float sum_of(float x) { return x; }
-__device__ __forceinline__ float sum_of(float2 x) { return x.x + x.y; }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 // Value i of some pairs.
-template <int M>
-__device__ __forceinline__ float value_of(const float (&f)[M], int i) { return f[i]; }
 template <int M>
 __device__ __forceinline__ float value_of(const float2 (&f)[M], int i) { return i % 2 == 0 ? f[i / 2].x : f[i / 2].y; }
 
-// N elements of a row between memory's words and pairs.
-template <typename T, int N>
+// A vector of 16 bytes, N elements of a row, between memory's words and pairs.
+template <typename T>
 struct Pairs {
+  static constexpr int N = 16 / sizeof(T);
   using Raw = typename Piece<T, N>::Raw;
-  static __device__ __forceinline__ void unpack(const Raw& r, PairOf<N> (&f)[kPairs<N>]) {
-    if constexpr (N == 1) {
-      f[0] = to_float(r);
-    } else {
+  static __device__ __forceinline__ void unpack(const Raw& r, float2 (&f)[N / 2]) {
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        if constexpr (sizeof(T) == 4)
-          f[i] = make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
-        else if constexpr (__is_same(T, __nv_bfloat16))
-          f[i] = make_float2(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xffff0000u));
-        else
-          f[i] = unpack2(r.w[i], T());
-      }
+    for (int i = 0; i < N / 2; ++i) {
+      if constexpr (sizeof(T) == 4)
+        f[i] = make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+      else if constexpr (__is_same(T, __nv_bfloat16))
+        f[i] = make_float2(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xffff0000u));
+      else
+        f[i] = unpack2(r.w[i], T());
     }
   }
-  static __device__ __forceinline__ Raw pack(const PairOf<N> (&f)[kPairs<N>]) {
-    if constexpr (N == 1) {
-      return from_float<T>(f[0]);
-    } else {
-      Raw r;
+  static __device__ __forceinline__ Raw pack(const float2 (&f)[N / 2]) {
+    Raw r;
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        if constexpr (sizeof(T) == 4) {
-          r.w[2 * i] = __float_as_uint(f[i].x);
-          r.w[2 * i + 1] = __float_as_uint(f[i].y);
-        } else {
-          r.w[i] = pack2(f[i].x, f[i].y, T());
-        }
+    for (int i = 0; i < N / 2; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        r.w[2 * i] = __float_as_uint(f[i].x);
+        r.w[2 * i + 1] = __float_as_uint(f[i].y);
+      } else {
+        r.w[i] = pack2(f[i].x, f[i].y, T());
       }
-      return r;
     }
+    return r;
+  }
+};
+
+// Rows that take no vectors (of any alignment).  A warp moves what are 32 vectors
+// elsewhere element by element, neighbouring lanes on neighbouring elements: lane l has the
+// elements 32 k + l of them.  That serves where a value does not depend on its
+// neighbours; for codes (whose blocks would have an element a lane: two to three times as
+// long) they go through 512 bytes of the warp's own to the lanes that have them as vectors.
+template <typename T>
+struct Loose {
+  static constexpr int N = 16 / sizeof(T);
+  using Raw = typename Pairs<T>::Raw;
+  using Bits = std::conditional_t<sizeof(T) == 4, unsigned, unsigned short>;
+
+  static __device__ __forceinline__ int element(int first, int k) { return first * N + 32 * k + threadIdx.x % 32; }
+
+  // Of the 32 vectors from `first` on of a row of n elements, U times, `step` vectors further
+  // each: the lane's elements, zeros past the row.
+  template <int U>
+  static __device__ __forceinline__ void load(Raw (&to)[U], const void* row, int first, int step, int n) {
+    Bits e[U][N];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int i = element(first + u * step, k);
+        e[u][k] = i < n ? static_cast<const Bits*>(row)[i] : Bits(0);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4)
+          to[u].w[j] = e[u][j];
+        else
+          to[u].w[j] = e[u][2 * j] | (unsigned)e[u][2 * j + 1] << 16;
+      }
+  }
+  static __device__ __forceinline__ Bits of(const Raw& r, int k) {
+    if constexpr (sizeof(T) == 4)
+      return r.w[k];
+    else
+      return (Bits)(r.w[k / 2] >> (k % 2 * 16));
+  }
+  template <int U>
+  static __device__ __forceinline__ void store(void* row, const Raw (&from)[U], int first, int step, int n) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int i = element(first + u * step, k);
+        if (i < n) static_cast<Bits*>(row)[i] = of(from[u], k);
+      }
+  }
+
+  // From the lanes that have the elements to those that have the vectors, and back.
+  template <int U>
+  static __device__ __forceinline__ void spread(Raw (&x)[U], uint4 (*place)[32]) {
+    const int lane = threadIdx.x % 32;
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < N; ++k) reinterpret_cast<Bits*>(place[u])[32 * k + lane] = of(x[u], k);
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < U; ++u) reinterpret_cast<uint4&>(x[u]) = place[u][lane];
+  }
+  template <int U>
+  static __device__ __forceinline__ void gather(Raw (&x)[U], uint4 (*place)[32]) {
+    const int lane = threadIdx.x % 32;
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < U; ++u) place[u][lane] = reinterpret_cast<const uint4&>(x[u]);
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4)
+          x[u].w[j] = reinterpret_cast<const Bits*>(place[u])[32 * j + lane];
+        else
+          x[u].w[j] = reinterpret_cast<const Bits*>(place[u])[64 * j + lane] |
+                      (unsigned)reinterpret_cast<const Bits*>(place[u])[64 * j + 32 + lane] << 16;
+      }
   }
 };
 
 // The largest magnitude of some values, NaN where one is NaN.
-__device__ __forceinline__ float largest(const float (&f)[1]) { return fabsf(f[0]); }
 template <int M>
 __device__ __forceinline__ float largest(const float2 (&f)[M]) {
   float m = 0.0f;
@@ -194,10 +231,8 @@ struct MxCodes {
   static constexpr int kWords = N * kBits >= 32 ? N * kBits / 32 : 1;
   unsigned w[kWords];
 
-  __device__ __forceinline__ void encode(const PairOf<N> (&f)[kPairs<N>]) {
-    if constexpr (N == 1) {
-      w[0] = kFormat == A2AV_MXFP8 ? e4m3_pair(f[0], 0.0f) & 0xffu : e2m1_pair(f[0], 0.0f) & 0xfu;
-    } else if constexpr (kFormat == A2AV_MXFP8) {
+  __device__ __forceinline__ void encode(const float2 (&f)[N / 2]) {
+    if constexpr (kFormat == A2AV_MXFP8) {
 #pragma unroll
       for (int i = 0; i < kWords; ++i)
         asm("{\n\t.reg .b16 l, h;\n\t"
@@ -208,7 +243,7 @@ struct MxCodes {
             : "f"(f[2 * i].x), "f"(f[2 * i].y), "f"(f[2 * i + 1].x), "f"(f[2 * i + 1].y));
     } else {
       static_assert(N == 4 || N == 8, "vectors of 16 bytes");
-      unsigned part[N / 4];
+      unsigned part[N / 4];  // (four .b8 in one mov.b32 came out wrong)
 #pragma unroll
       for (int i = 0; i < N / 4; ++i) {
         unsigned short r;
@@ -224,15 +259,9 @@ struct MxCodes {
     }
   }
 
-  // To the values' place of a row, v being the number of these N in it.  With N = 1
-  // (by a whole warp) two lanes share a byte of 4-bit codes.
+  // To the values' place of a row, v being the number of these N in it.
   __device__ __forceinline__ void store(unsigned char* row, int v) const {
-    if constexpr (N == 1 && kFormat == A2AV_MXFP8) {
-      row[v] = (unsigned char)w[0];
-    } else if constexpr (N == 1) {
-      const unsigned next = __shfl_down_sync(kAll, w[0], 1);
-      if (v % 2 == 0) row[v / 2] = (unsigned char)(w[0] | next << 4);
-    } else if constexpr (N * kBits == 64) {
+    if constexpr (N * kBits == 64) {
       reinterpret_cast<uint2*>(row)[v] = make_uint2(w[0], w[1]);
     } else if constexpr (N * kBits == 32) {
       reinterpret_cast<unsigned*>(row)[v] = w[0];
@@ -248,18 +277,18 @@ struct MxCodes {
 // the bits of the lane's largest magnitude, and `write` says whether the lane's block
 // is in the row (values past the row's end are 0).
 template <int kFormat, int N>
-__device__ __forceinline__ void mx_store(unsigned char* row, int scales_at, int v, PairOf<N> (&f)[kPairs<N>],
+__device__ __forceinline__ void mx_store(unsigned char* row, int scales_at, int v, float2 (&f)[N / 2],
                                          unsigned top, bool write) {
   constexpr int kLanes = kMxBlock / N;
   const unsigned s = mx_scale<kFormat>(lanes_max<kLanes>(top));
-  const PairOf<N> by = both<PairOf<N>>(mx_inverse(s));
+  const float2 by = both(mx_inverse(s));
 #pragma unroll
-  for (int i = 0; i < kPairs<N>; ++i) f[i] = mul2(f[i], by);
+  for (int i = 0; i < N / 2; ++i) f[i] = mul2(f[i], by);
   MxCodes<kFormat, N> c;
   c.encode(f);
 #pragma unroll
   for (int i = 0; i < c.kWords; ++i) c.w[i] = s == 255u ? 0u : c.w[i];
-  if (write) {  // (N = 1: the whole warp or none of it)
+  if (write) {
     c.store(row, v);
     if (threadIdx.x % kLanes == 0) row[scales_at + v / kLanes] = (unsigned char)s;
   }

@@ -24,6 +24,7 @@ struct NormParams {
   int* status;
   int W, H;
   float eps, per_feature;    // 1 / H
+  int weight_aligned;        // to 16 bytes
 };
 
 // Token t of all ranks' (rank-major), in rank r or a later one.
@@ -54,13 +55,14 @@ __device__ __forceinline__ void row_sum(float (&x)[kSums], float (*shared)[kSums
   }
 }
 
-// How a row lies on its threads: vectors of N elements, U a thread, thread i having
-// the vectors i, i + threads, ...
-constexpr int kHeldValues = 32;    // of a row in a thread
-// (the backward pass keeps the weight's gradient of its values as well)
-__host__ __device__ constexpr int held_backward(bool vector, int size) { return vector && size == 2 ? 32 : 16; }
-template <typename T, bool kVector>
-constexpr int kVectorSize = kVector ? 16 / sizeof(T) : 1;
+// How a row lies on its threads: in vectors of 16 bytes, thread i having the vectors
+// i, i + threads, ..., of these many values in all.  (The backward pass keeps the weight's
+// gradient of its values as well, and rows that take no vectors their elements on the way.)
+template <bool kAligned>
+constexpr int kHeld = kAligned ? 32 : 16;
+__host__ __device__ constexpr int held_backward(bool aligned, int size, int64_t H) {
+  return aligned ? (size == 2 ? 32 : 16) : H <= 8192 ? 8 : 16;  // (1024 threads have 8192 or 16,384)
+}
 
 // Rows on their way to shared memory, by bulk copies, while others are worked on: two
 // rows of `arrays` arrays of `bytes` each, for the block or for each of its warps.
@@ -99,22 +101,50 @@ __device__ __noinline__ void give_up(const Ahead& ahead, int* status) {
   bar_wait(ahead.bar + 8 * (ahead.turn ^ 1), ahead.parity ^ ahead.turn);
 }
 
-// U vectors of a thread: from shared memory (`row`: the array's bytes there), or from
-// memory (`from`: the thread's first).
-template <bool kAhead, typename V, int U>
-__device__ __forceinline__ void take_row(V (&to)[U], uint32_t row, const V* from, int i0,
-                                         int threads, int nv) {
+// A thread's U vectors of a row: from shared memory, where it has been fetched to `here`,
+// from memory, or (kAligned false) the elements that it has instead.
+template <typename T, bool kAhead, bool kAligned, int U, typename V>
+__device__ __forceinline__ void take_row(V (&to)[U], uint32_t here, const T* row, int i0, int threads, int H) {
+  if constexpr (!kAligned) {
+    Loose<T>::load(to, row, i0 - threadIdx.x % 32, threads, H);
+  } else {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (i0 + u * threads >= nv) continue;
-    if constexpr (kAhead)
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(to[u].w[0]), "=r"(to[u].w[1]), "=r"(to[u].w[2]), "=r"(to[u].w[3])
-                   : "r"(row + 16 * (i0 + u * threads))
-                   : "memory");
-    else
-      to[u] = from[u * threads];
+    for (int u = 0; u < U; ++u) {
+      const int v = i0 + u * threads;
+      if (v * Pairs<T>::N >= H) continue;
+      if constexpr (kAhead)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(to[u].w[0]), "=r"(to[u].w[1]), "=r"(to[u].w[2]), "=r"(to[u].w[3])
+                     : "r"(here + 16 * v)
+                     : "memory");
+      else
+        to[u] = reinterpret_cast<const V*>(row)[v];
+    }
   }
+}
+
+// And back to memory.
+template <typename T, bool kAligned, int U, typename V>
+__device__ __forceinline__ void give_row(T* row, const V (&from)[U], int i0, int threads, int H) {
+  if constexpr (!kAligned) {
+    Loose<T>::store(row, from, i0 - threadIdx.x % 32, threads, H);
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = i0 + u * threads;
+      if (v * Pairs<T>::N < H) reinterpret_cast<V*>(row)[v] = from[u];
+    }
+  }
+}
+
+// Whether a thread has anything of a row in vector v, and the column of its value i there.
+template <typename T, bool kVectors>
+__device__ __forceinline__ bool has_part(int v, int H) {
+  return (kVectors ? v : v - (int)(threadIdx.x % 32)) * Pairs<T>::N < H;
+}
+template <typename T, bool kVectors>
+__device__ __forceinline__ int column_of(int v, int i) {
+  return kVectors ? v * Pairs<T>::N + i : Loose<T>::element(v - threadIdx.x % 32, i);
 }
 
 // A token's place: its rank and its first element in the rank's buffers.
@@ -122,13 +152,13 @@ struct Token {
   int r;
   long long at;
 };
-template <typename V, typename T>
-__device__ __forceinline__ const V* row_of(const void* const* list, const Token& t, int vector = 0) {
-  return reinterpret_cast<const V*>(static_cast<const T*>(list[t.r]) + t.at) + vector;
+template <typename T>
+__device__ __forceinline__ const T* row_of(const void* const* list, const Token& t) {
+  return static_cast<const T*>(list[t.r]) + t.at;
 }
-template <typename V, typename T>
-__device__ __forceinline__ V* row_of(void* const* list, const Token& t, int vector = 0) {
-  return reinterpret_cast<V*>(static_cast<T*>(list[t.r]) + t.at) + vector;
+template <typename T>
+__device__ __forceinline__ T* row_of(void* const* list, const Token& t) {
+  return static_cast<T*>(list[t.r]) + t.at;
 }
 // Token g of all ranks', g being no smaller than the last one.
 __device__ __forceinline__ void find_token(const NormParams& P, long long g, Token* t) {
@@ -136,18 +166,25 @@ __device__ __forceinline__ void find_token(const NormParams& P, long long g, Tok
   t->at = (g - P.first[t->r]) * P.H;
 }
 
-// The weight's N values of vector v.  They are read again for every row, from L1: in
-// registers they would cost the block that an SM has beside this one.
-template <int N>
-__device__ __forceinline__ void take_weight(PairOf<N> (&w)[kPairs<N>], const float* weight, int v) {
-  if constexpr (N == 1) {
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(w[0]) : "l"(weight + v));
-  } else {
+// The weight's values of vector v, zeros past the row.  They are read again for every
+// row, from L1: in registers they would cost the block that an SM has beside this one.
+template <typename T, bool kAligned, bool kVectors>
+__device__ __forceinline__ void take_weight(float2 (&w)[Pairs<T>::N / 2], const NormParams& P, int v) {
+  constexpr int N = Pairs<T>::N;
+  const float* from = P.weight + v * N;
+  if (kAligned || (kVectors && P.weight_aligned && v * N + N <= P.H)) {
 #pragma unroll
     for (int i = 0; i < N / 2; i += 2)
       asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
                    : "=f"(w[i].x), "=f"(w[i].y), "=f"(w[i + 1].x), "=f"(w[i + 1].y)
-                   : "l"(weight + v * N + 2 * i));
+                   : "l"(from + 2 * i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const int a = column_of<T, kVectors>(v, 2 * i), b = column_of<T, kVectors>(v, 2 * i + 1);
+      w[i].x = a < P.H ? P.weight[a] : 0.0f;
+      w[i].y = b < P.H ? P.weight[b] : 0.0f;
+    }
   }
 }
 
@@ -165,19 +202,23 @@ __device__ __forceinline__ Scale inverse_root(float x) {
   return {r, isfinite(low) ? low : 0.0f};  // (x of 0 or infinity)
 }
 
-template <typename T, bool kVector, int kFormat, bool kWarp, int kThreads, bool kAhead>
-__global__ void __maxnreg__(sizeof(T) == 4 || !kVector ? 128 : 96)
+template <typename T, bool kAligned, int kFormat, bool kWarp, int kThreads, bool kAhead>
+__global__ void __maxnreg__(kThreads > 512 ? 64 : !kAligned ? 72 : sizeof(T) == 4 ? 128 : kAhead && !kWarp ? 80 : 96)
     norm_kernel(const __grid_constant__ NormParams P) {
   chain();
-  constexpr int N = kVectorSize<T, kVector>, U = kHeldValues / N, M = kPairs<N>;
-  using Q = Pairs<T, N>;
+  using Q = Pairs<T>;
   using V = typename Q::Raw;
-  using F = PairOf<N>;
+  using F = float2;
+  constexpr int N = Q::N, U = kHeld<kAligned> / N, M = N / 2;
   extern __shared__ uint4 room[];
   __shared__ float sums[2][kThreads / 32][1];
   __shared__ unsigned long long bars[kWarp ? 2 * kThreads / 32 : 2];
+  // (rows that take no vectors have them for codes alone)
+  constexpr bool kVectors = kAligned || kFormat != A2AV_PLAIN, kSpread = kVectors && !kAligned;
+  __shared__ uint4 places[kSpread ? kThreads / 32 : 1][kSpread ? U : 1][32];
+  uint4(*place)[32] = places[kSpread ? threadIdx.x / 32 : 0];
   const int threads = kWarp ? 32 : blockDim.x, i0 = kWarp ? threadIdx.x % 32 : threadIdx.x;
-  const int nv = P.H / N;
+  const int nv = (P.H + N - 1) / N;
   // vectors of a packed row, zeros behind the row's own
   const int np = kFormat == A2AV_PLAIN ? nv : P.row.scales * (kMxBlock / N);
   const int per = kWarp ? blockDim.x / 32 : 1;
@@ -189,8 +230,8 @@ __global__ void __maxnreg__(sizeof(T) == 4 || !kVector ? 128 : 96)
   const auto fetch = [&](int stage, const Token& t) {
     const bool more = P.residual[t.r] != nullptr;
     ahead.expect(stage, (more ? 2 : 1) * bytes);
-    ahead.fetch(stage, 0, row_of<V, T>(P.x, t), bytes);
-    if (more) ahead.fetch(stage, 1, row_of<V, T>(P.residual, t), bytes);
+    ahead.fetch(stage, 0, row_of<T>(P.x, t), bytes);
+    if (more) ahead.fetch(stage, 1, row_of<T>(P.residual, t), bytes);
   };
   Token coming = {0, 0};
   if constexpr (kAhead) {
@@ -214,7 +255,7 @@ __global__ void __maxnreg__(sizeof(T) == 4 || !kVector ? 128 : 96)
   Token t = {0, 0};
   for (int parity = 0; g < rows; g += by, parity ^= 1) {
     find_token(P, g, &t);
-    V* kept = row_of<V, T>(P.sums, t, i0);
+    T* kept = row_of<T>(P.sums, t);
     const bool add = P.residual[t.r] != nullptr, keep = P.sums[t.r] != nullptr;
     uint32_t here = 0;
     if constexpr (kAhead) {
@@ -222,13 +263,12 @@ __global__ void __maxnreg__(sizeof(T) == 4 || !kVector ? 128 : 96)
       here = ahead.at(ahead.turn);
     }
     V s[U], a[U];
-    take_row<kAhead>(s, here, row_of<V, T>(P.x, t, i0), i0, threads, nv);
-    if (add) take_row<kAhead>(a, here + bytes, row_of<V, T>(P.residual, t, i0), i0, threads, nv);
-    F total2 = both<F>(0.0f);
+    take_row<T, kAhead, kAligned>(s, here, row_of<T>(P.x, t), i0, threads, P.H);
+    if (add) take_row<T, kAhead, kAligned>(a, here + bytes, row_of<T>(P.residual, t), i0, threads, P.H);
+    F total2 = both(0.0f);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int v = i0 + u * threads;
-      if (v < nv) {
+      if (has_part<T, kAligned>(i0 + u * threads, P.H)) {
         F f[M];
         Q::unpack(s[u], f);
         if (add) {
@@ -239,12 +279,13 @@ __global__ void __maxnreg__(sizeof(T) == 4 || !kVector ? 128 : 96)
           s[u] = Q::pack(f);
           Q::unpack(s[u], f);
         }
-        if (keep) kept[u * threads] = s[u];
 #pragma unroll
         for (int i = 0; i < M; ++i) total2 = fma2(f[i], f[i], total2);
       }
     }
-    float total[1] = {sum_of(total2)};
+    if (keep) give_row<T, kAligned>(kept, s, i0, threads, P.H);
+    if constexpr (kSpread) Loose<T>::spread(s, place);
+    float total[1] = {total2.x + total2.y};
     row_sum<kWarp, 1>(total, sums[parity]);
     // (all threads have taken their part of the row: its place is free)
     if constexpr (kAhead) {
@@ -256,9 +297,9 @@ __global__ void __maxnreg__(sizeof(T) == 4 || !kVector ? 128 : 96)
       ahead.next();
     }
     const Scale root = inverse_root(fmaf(total[0], P.per_feature, P.eps));
-    const F high = both<F>(root.high), low = both<F>(root.low);
+    const F high = both(root.high), low = both(root.low);
     unsigned char* packed = nullptr;
-    V* out = row_of<V, T>(kFormat == A2AV_PLAIN ? P.out : P.plain, t, i0);
+    T* out = row_of<T>(kFormat == A2AV_PLAIN ? P.out : P.plain, t);
     const bool plain = kFormat == A2AV_PLAIN || P.plain[t.r] != nullptr;
     if constexpr (kFormat != A2AV_PLAIN)
       packed = static_cast<unsigned char*>(P.out[t.r]) + (g - P.first[t.r]) * P.row.bytes;
@@ -266,9 +307,11 @@ __global__ void __maxnreg__(sizeof(T) == 4 || !kVector ? 128 : 96)
     for (int u = 0; u < U; ++u) {
       const int v = i0 + u * threads;
       F f[M];
-      if (v < nv) {
+#pragma unroll
+      for (int i = 0; i < M; ++i) f[i] = both(0.0f);
+      if (has_part<T, kVectors>(v, P.H)) {
         F w[M];
-        take_weight<N>(w, P.weight, v);
+        take_weight<T, kAligned, kVectors>(w, P, v);
         Q::unpack(s[u], f);
 #pragma unroll
         for (int i = 0; i < M; ++i) {
@@ -276,14 +319,15 @@ __global__ void __maxnreg__(sizeof(T) == 4 || !kVector ? 128 : 96)
           f[i] = fma2(a, w[i], mul2(rest, w[i]));
         }
       }
-      if (plain && v < nv) out[u * threads] = Q::pack(f);
+      s[u] = Q::pack(f);
       if (kFormat != A2AV_PLAIN && u * threads < np) {
-        if (v >= nv)
-#pragma unroll
-          for (int i = 0; i < M; ++i) f[i] = both<F>(0.0f);
         if constexpr (kFormat != A2AV_PLAIN)
           mx_store<kFormat, N>(packed, P.row.values, v, f, __float_as_uint(largest(f)), v < np);
       }
+    }
+    if (plain) {
+      if constexpr (kSpread) Loose<T>::gather(s, place);
+      give_row<T, kAligned>(out, s, i0, threads, P.H);
     }
     if constexpr (kFormat != A2AV_PLAIN) {
       const int used = P.row.values + P.row.scales;
@@ -296,19 +340,19 @@ __global__ void __maxnreg__(sizeof(T) == 4 || !kVector ? 128 : 96)
 
 // d_x, and a block's part of the weight's gradient, kept in registers over its
 // rows.
-template <typename T, bool kVector, bool kWarp, int kThreads, bool kAhead>
+template <typename T, bool kAligned, int kValues, bool kWarp, int kThreads, bool kAhead>
 __global__ void __maxnreg__(kThreads > 512 ? 64 : 128)
     norm_backward_kernel(const __grid_constant__ NormParams P) {
   chain();
-  constexpr int N = kVectorSize<T, kVector>, U = held_backward(kVector, sizeof(T)) / N, M = kPairs<N>;
-  using Q = Pairs<T, N>;
+  using Q = Pairs<T>;
   using V = typename Q::Raw;
-  using F = PairOf<N>;
+  using F = float2;
+  constexpr int N = Q::N, U = kValues / N, M = N / 2;
   extern __shared__ uint4 room[];
   __shared__ float sums[2][kThreads / 32][2];
   __shared__ unsigned long long bars[kWarp ? 2 * kThreads / 32 : 2];
   const int threads = kWarp ? 32 : blockDim.x, i0 = kWarp ? threadIdx.x % 32 : threadIdx.x;
-  const int nv = P.H / N, per = kWarp ? blockDim.x / 32 : 1;
+  const int per = kWarp ? blockDim.x / 32 : 1;
   const long long rows = P.first[P.W], by = (long long)gridDim.x * per;
   long long g = (long long)blockIdx.x * per + (kWarp ? threadIdx.x / 32 : 0);
   Ahead ahead;
@@ -317,9 +361,9 @@ __global__ void __maxnreg__(kThreads > 512 ? 64 : 128)
   const auto fetch = [&](int stage, const Token& t) {
     const bool more = P.residual[t.r] != nullptr;
     ahead.expect(stage, (more ? 3 : 2) * bytes);
-    ahead.fetch(stage, 0, row_of<V, T>(P.x, t), bytes);
-    ahead.fetch(stage, 1, row_of<V, T>(P.d_out, t), bytes);
-    if (more) ahead.fetch(stage, 2, row_of<V, T>(P.residual, t), bytes);
+    ahead.fetch(stage, 0, row_of<T>(P.x, t), bytes);
+    ahead.fetch(stage, 1, row_of<T>(P.d_out, t), bytes);
+    if (more) ahead.fetch(stage, 2, row_of<T>(P.residual, t), bytes);
   };
   Token coming = {0, 0};
   if constexpr (kAhead) {
@@ -345,10 +389,10 @@ __global__ void __maxnreg__(kThreads > 512 ? 64 : 128)
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int i = 0; i < M; ++i) dw[u][i] = both<F>(0.0f);
+    for (int i = 0; i < M; ++i) dw[u][i] = both(0.0f);
   for (int parity = 0; g < rows; g += by, parity ^= 1) {
     find_token(P, g, &t);
-    V* out = row_of<V, T>(P.out, t, i0);
+    T* out = row_of<T>(P.out, t);
     const bool add = P.residual[t.r] != nullptr;
     uint32_t here = 0;
     if constexpr (kAhead) {
@@ -356,15 +400,15 @@ __global__ void __maxnreg__(kThreads > 512 ? 64 : 128)
       here = ahead.at(ahead.turn);
     }
     V s[U], d[U], a[U];
-    take_row<kAhead>(s, here, row_of<V, T>(P.x, t, i0), i0, threads, nv);
-    take_row<kAhead>(d, here + bytes, row_of<V, T>(P.d_out, t, i0), i0, threads, nv);
-    if (add) take_row<kAhead>(a, here + 2 * bytes, row_of<V, T>(P.residual, t, i0), i0, threads, nv);
-    F squares = both<F>(0.0f), products = both<F>(0.0f);
+    take_row<T, kAhead, kAligned>(s, here, row_of<T>(P.x, t), i0, threads, P.H);
+    take_row<T, kAhead, kAligned>(d, here + bytes, row_of<T>(P.d_out, t), i0, threads, P.H);
+    if (add) take_row<T, kAhead, kAligned>(a, here + 2 * bytes, row_of<T>(P.residual, t), i0, threads, P.H);
+    F squares = both(0.0f), products = both(0.0f);
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (i0 + u * threads < nv) {
+      if (has_part<T, kAligned>(i0 + u * threads, P.H)) {
         F f[M], e[M], w[M];
-        take_weight<N>(w, P.weight, i0 + u * threads);
+        take_weight<T, kAligned, kAligned>(w, P, i0 + u * threads);
         Q::unpack(s[u], f);
         Q::unpack(d[u], e);
 #pragma unroll
@@ -373,7 +417,7 @@ __global__ void __maxnreg__(kThreads > 512 ? 64 : 128)
           products = fma2(f[i], mul2(e[i], w[i]), products);
         }
       }
-    float total[2] = {sum_of(squares), sum_of(products)};
+    float total[2] = {squares.x + squares.y, products.x + products.y};
     row_sum<kWarp, 2>(total, sums[parity]);
     // (all threads have taken their part of the row: its place is free)
     if constexpr (kAhead) {
@@ -385,13 +429,13 @@ __global__ void __maxnreg__(kThreads > 512 ? 64 : 128)
       ahead.next();
     }
     const float one = rsqrtf(fmaf(total[0], P.per_feature, P.eps));
-    const F scale = both<F>(one), along = both<F>(-one * one * (total[1] * P.per_feature));
+    const F scale = both(one), along = both(-one * one * (total[1] * P.per_feature));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int v = i0 + u * threads;
-      if (v < nv) {
-        F f[M], e[M], y[M], w[M];
-        take_weight<N>(w, P.weight, v);
+      F f[M], e[M], y[M], w[M];
+      if (has_part<T, kAligned>(v, P.H)) {
+        take_weight<T, kAligned, kAligned>(w, P, v);
         Q::unpack(s[u], f);
         Q::unpack(d[u], e);
         if (add) Q::unpack(a[u], y);
@@ -401,9 +445,10 @@ __global__ void __maxnreg__(kThreads > 512 ? 64 : 128)
           const F z = fma2(f[i], along, mul2(e[i], w[i]));
           y[i] = add ? fma2(z, scale, y[i]) : mul2(z, scale);
         }
-        out[u * threads] = Q::pack(y);
       }
+      a[u] = Q::pack(y);
     }
+    give_row<T, kAligned>(out, a, i0, threads, P.H);
   }
   if constexpr (kAhead)
     if (ahead.lost) give_up(ahead, P.status);
@@ -417,7 +462,7 @@ __global__ void __maxnreg__(kThreads > 512 ? 64 : 128)
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            float* at = all + (i0 + u * 32) * N + i;
+            float* at = all + column_of<T, kAligned>(i0 + u * 32, i);
             const float x = value_of(dw[u], i);
             *at = k == 0 ? x : *at + x;
           }
@@ -426,12 +471,12 @@ __global__ void __maxnreg__(kThreads > 512 ? 64 : 128)
     for (int c = threadIdx.x; c < P.H; c += blockDim.x) part[c] = all[c];
   } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int v = i0 + u * threads;
-      if (v < nv)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < N; ++i) part[v * N + i] = value_of(dw[u], i);
-    }
+      for (int i = 0; i < N; ++i) {
+        const int c = column_of<T, kAligned>(i0 + u * threads, i);
+        if (c < P.H) part[c] = value_of(dw[u], i);
+      }
   }
 }
 
@@ -496,51 +541,57 @@ struct Slices {
 
 // The bits, in 32, of the largest magnitude of a vector: of pairs of 16 bits by
 // one instruction each.
-template <typename T, int N>
-__device__ __forceinline__ unsigned top_bits(const typename Pairs<T, N>::Raw& r, const PairOf<N> (&f)[kPairs<N>]) {
-  if constexpr (N > 1 && sizeof(T) == 2) {
+template <typename T>
+__device__ __forceinline__ unsigned top_bits(const typename Pairs<T>::Raw& r, const float2 (&f)[Pairs<T>::N / 2]) {
+  if constexpr (sizeof(T) == 2) {
     using T2 = std::conditional_t<__is_same(T, __half), __half2, __nv_bfloat162>;
     T2 m = __habs2(reinterpret_cast<const T2&>(r.w[0]));
 #pragma unroll
-    for (int i = 1; i < N / 2; ++i) m = __hmax2_nan(m, __habs2(reinterpret_cast<const T2&>(r.w[i])));
+    for (int i = 1; i < Pairs<T>::N / 2; ++i) m = __hmax2_nan(m, __habs2(reinterpret_cast<const T2&>(r.w[i])));
     return __float_as_uint(to_float(__hmax_nan(m.x, m.y))) & 0x7fffffffu;
   } else {
     return __float_as_uint(largest(f));
   }
 }
 
-// A warp takes 32 U neighbouring vectors of a row.
-template <typename T, int N, int U, int kFormat>
+constexpr int kPackVectors = 4;  // of a lane at a time
+
+// A warp takes 32 x kPackVectors neighbouring vectors of a row.
+template <typename T, bool kAligned, int kFormat>
 __global__ void __launch_bounds__(kPackThreads) quantise_kernel(const __grid_constant__ PackParams P) {
   chain();
-  using Q = Pairs<T, N>;
-  using V = typename Q::Raw;
-  using F = PairOf<N>;
-  constexpr int M = kPairs<N>;
+  using Q = Pairs<T>;
+  constexpr int N = Q::N, U = kPackVectors;
+  __shared__ uint4 places[kAligned ? 1 : kPackThreads / 32][kAligned ? 1 : U][32];
   const int lane = threadIdx.x % 32;
-  const int nv = P.D / N, np = P.row.scales * (kMxBlock / N);
+  const int nv = (P.D + N - 1) / N, np = P.row.scales * (kMxBlock / N);
   const Slices cut(P.first[P.W], (np + 32 * U - 1) / (32 * U));
   int r = 0;
   for (Slice at = cut.first(); at.t < cut.rows; cut.next(&at)) {
     find_rank(P.first, at.t, &r);
     const long long t = at.t - P.first[r];
     const int v0 = at.slice * (32 * U) + lane;
-    const V* x = reinterpret_cast<const V*>(static_cast<const T*>(P.from[r]) + t * P.D);
+    const T* x = static_cast<const T*>(P.from[r]) + t * P.D;
     unsigned char* to = static_cast<unsigned char*>(P.to[r]) + t * P.row.bytes;
-    V s[U];
+    typename Q::Raw s[U];
+    if constexpr (kAligned) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (v0 + 32 * u < nv) s[u] = x[v0 + 32 * u];
+      for (int u = 0; u < U; ++u)
+        if (v0 + 32 * u < nv) s[u] = reinterpret_cast<const typename Q::Raw*>(x)[v0 + 32 * u];
+    } else {
+      Loose<T>::load(s, x, v0 - lane, 32, P.D);
+      Loose<T>::spread(s, places[threadIdx.x / 32]);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int v = v0 + 32 * u;
-      F f[M];
+      float2 f[N / 2];
       unsigned top = 0;
 #pragma unroll
-      for (int i = 0; i < M; ++i) f[i] = both<F>(0.0f);
+      for (int i = 0; i < N / 2; ++i) f[i] = both(0.0f);
       if (v < nv) {
         Q::unpack(s[u], f);
-        top = top_bits<T, N>(s[u], f);
+        top = top_bits<T>(s[u], f);
       }
       if (v - lane < np) mx_store<kFormat, N>(to, P.row.values, v, f, top, v < np);
     }
@@ -549,15 +600,14 @@ __global__ void __launch_bounds__(kPackThreads) quantise_kernel(const __grid_con
   }
 }
 
-template <typename T, int N, int U, int kFormat>
+template <typename T, bool kAligned, int kFormat>
 __global__ void __launch_bounds__(kPackThreads) dequantise_kernel(const __grid_constant__ PackParams P) {
   chain();
-  using Q = Pairs<T, N>;
-  using V = typename Q::Raw;
-  using F = PairOf<N>;
-  constexpr int kBits = kFormat == A2AV_MXFP8 ? 8 : 4, M = kPairs<N>;
+  using Q = Pairs<T>;
+  constexpr int N = Q::N, U = kPackVectors, kBits = kFormat == A2AV_MXFP8 ? 8 : 4;
+  __shared__ uint4 places[kAligned ? 1 : kPackThreads / 32][kAligned ? 1 : U][32];
   const int lane = threadIdx.x % 32;
-  const int nv = P.D / N;
+  const int nv = (P.D + N - 1) / N;
   const Slices cut(P.first[P.W], (nv + 32 * U - 1) / (32 * U));
   int r = 0;
   for (Slice at = cut.first(); at.t < cut.rows; cut.next(&at)) {
@@ -565,16 +615,17 @@ __global__ void __launch_bounds__(kPackThreads) dequantise_kernel(const __grid_c
     const long long t = at.t - P.first[r];
     const int v0 = at.slice * (32 * U) + lane;
     const unsigned char* from = static_cast<const unsigned char*>(P.from[r]) + t * P.row.bytes;
-    V* out = reinterpret_cast<V*>(static_cast<T*>(P.to[r]) + t * P.D);
+    T* out = static_cast<T*>(P.to[r]) + t * P.D;
     unsigned w[U][N * kBits >= 32 ? N * kBits / 32 : 1], s[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int v = v0 + 32 * u;
+      s[u] = 0;
+#pragma unroll
+      for (unsigned& x : w[u]) x = 0;
       if (v < nv) {
         s[u] = from[P.row.values + v / (kMxBlock / N)];
-        if constexpr (N == 1) {
-          w[u][0] = kBits == 8 ? from[v] : from[v / 2] >> (v % 2 * 4);
-        } else if constexpr (N * kBits == 64) {
+        if constexpr (N * kBits == 64) {
           const uint2 c = reinterpret_cast<const uint2*>(from)[v];
           w[u][0] = c.x;
           w[u][1] = c.y;
@@ -585,24 +636,20 @@ __global__ void __launch_bounds__(kPackThreads) dequantise_kernel(const __grid_c
         }
       }
     }
+    typename Q::Raw values[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int v = v0 + 32 * u;
-      if (v < nv) {
-        const F by = both<F>(mx_scale_value(s[u]));
-        F f[M];
+      const float2 by = both(mx_scale_value(s[u]));
+      float2 f[N / 2];
 #pragma unroll
-        for (int i = 0; i < M; ++i) {
-          const unsigned c = w[u][2 * i * kBits / 32] >> (2 * i * kBits % 32);
-          const float2 p = kBits == 8 ? e4m3_values(c) : e2m1_values(c);
-          if constexpr (N == 1)
-            f[i] = p.x * by;
-          else
-            f[i] = mul2(p, by);
-        }
-        out[v] = Q::pack(f);
+      for (int i = 0; i < N / 2; ++i) {
+        const unsigned c = w[u][2 * i * kBits / 32] >> (2 * i * kBits % 32);
+        f[i] = mul2(kBits == 8 ? e4m3_values(c) : e2m1_values(c), by);
       }
+      values[u] = Q::pack(f);
     }
+    if constexpr (!kAligned) Loose<T>::gather(values, places[threadIdx.x / 32]);
+    give_row<T, kAligned>(out, values, v0, 32, P.D);
   }
 }
 
@@ -639,19 +686,21 @@ constexpr int kNormParts = 1024;  // most blocks that keep a part of the weight'
 
 using NormKernel = void (*)(NormParams);
 
-// How a norm's rows are shared out, `held` values a thread: in vectors of 16 bytes or
-// element by element; a warp a row where it can hold one, else a block of up to 256,
-// 512 or 1024 threads.
+// How a norm's rows are shared out: a warp a row where it can
+// hold one, else a block of up to 256, 512 or 1024 threads.
 struct NormForm {
-  bool vector, warp, ahead;
+  bool aligned, warp, ahead;
   int threads, most;  // of a block, and what its kernel is made for
+  int held;           // values a thread has room for
 };
 
 NormForm norm_form(int64_t H, int size, uintptr_t low, long long rows, int sms, bool backward) {
   NormForm f;
-  f.vector = low % 16 == 0 && H * size % 16 == 0;
-  int held = backward ? held_backward(f.vector, size) : kHeldValues;
-  const int n = f.vector ? 16 / size : 1, nv = (int)H / n;
+  f.aligned = low % 16 == 0 && H * size % 16 == 0;
+  f.ahead = false;
+  const int n = 16 / size, nv = ((int)H + n - 1) / n;
+  int held = backward ? held_backward(f.aligned, size, H) : f.aligned ? kHeld<true> : kHeld<false>;
+  f.held = held;
   held /= n;
   f.warp = nv <= 32 * held;
   f.threads = 256;
@@ -660,22 +709,20 @@ NormForm norm_form(int64_t H, int size, uintptr_t low, long long rows, int sms, 
     while (rows < 2 * sms && held > 1 && (nv + held / 2 - 1) / (held / 2) <= 512) held /= 2;
     f.threads = ((nv + held - 1) / held + 31) / 32 * 32;
   }
-  f.ahead = false;
   f.most = f.threads <= 256 ? 256 : f.threads <= 512 ? 512 : 1024;
   return f;
 }
 
 template <typename T, int kFormat>
 NormKernel norm_kernel_of(const NormForm& f) {
-  if (f.vector && f.ahead) {
+  if (f.ahead) {
     if (f.warp) return norm_kernel<T, true, kFormat, true, 256, true>;
     return f.most == 256 ? norm_kernel<T, true, kFormat, false, 256, true>
                          : norm_kernel<T, true, kFormat, false, 512, true>;
   }
-  if (f.vector) {
-    if (f.warp) return norm_kernel<T, true, kFormat, true, 256, false>;
-    return norm_kernel<T, true, kFormat, false, 512, false>;
-  }
+  if (f.aligned)
+    return f.warp ? norm_kernel<T, true, kFormat, true, 256, false> : norm_kernel<T, true, kFormat, false, 512, false>;
+  if (f.most > 512) return norm_kernel<T, false, kFormat, false, 1024, false>;
   return f.warp ? norm_kernel<T, false, kFormat, true, 256, false> : norm_kernel<T, false, kFormat, false, 512, false>;
 }
 
@@ -687,20 +734,22 @@ NormKernel norm_kernel_of(int format, const NormForm& f) {
 
 template <typename T>
 NormKernel norm_backward_kernel_of(const NormForm& f) {
-  if (f.vector && f.ahead) {
-    if (f.warp) return norm_backward_kernel<T, true, true, 256, true>;
-    return f.most == 256 ? norm_backward_kernel<T, true, false, 256, true>
-                         : norm_backward_kernel<T, true, false, 512, true>;
+  constexpr int kOwn = held_backward(true, sizeof(T), 0);
+  if (f.ahead) {
+    if (f.warp) return norm_backward_kernel<T, true, kOwn, true, 256, true>;
+    return f.most == 256 ? norm_backward_kernel<T, true, kOwn, false, 256, true>
+                         : norm_backward_kernel<T, true, kOwn, false, 512, true>;
   }
-  if (f.vector) {
-    if (f.warp) return norm_backward_kernel<T, true, true, 256, false>;
-    if constexpr (sizeof(T) == 4)  // (16 bits: 16,384 features are 512 threads')
-      if (f.most > 512) return norm_backward_kernel<T, true, false, 1024, false>;
-    return norm_backward_kernel<T, true, false, 512, false>;
+  if (f.aligned) {
+    if constexpr (sizeof(T) == 4)  // (of 16 bits 512 threads hold any row)
+      if (f.most > 512) return norm_backward_kernel<T, true, kOwn, false, 1024, false>;
+    return f.warp ? norm_backward_kernel<T, true, kOwn, true, 256, false>
+                  : norm_backward_kernel<T, true, kOwn, false, 512, false>;
   }
-  if (f.warp) return norm_backward_kernel<T, false, true, 256, false>;
-  return f.most <= 512 ? norm_backward_kernel<T, false, false, 512, false>
-                       : norm_backward_kernel<T, false, false, 1024, false>;
+  if (f.held == 16) return norm_backward_kernel<T, false, 16, false, 1024, false>;
+  if (f.most > 512) return norm_backward_kernel<T, false, 8, false, 1024, false>;
+  return f.warp ? norm_backward_kernel<T, false, 8, true, 256, false>
+                : norm_backward_kernel<T, false, 8, false, 512, false>;
 }
 
 NormKernel norm_kernel_of(int dtype, int format, const NormForm& f) {
@@ -728,7 +777,7 @@ cudaError_t launch_norm(const a2av_handle* h, K kernel_of, NormForm f, int row_b
   cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, f.threads, 0);
   if (e != cudaSuccess) return e;
   const size_t two_rows = (size_t)2 * per * row_bytes;
-  if (f.vector && f.most <= 512 && want > (long long)fit * h->sms && two_rows <= kMostRoom) {
+  if (f.aligned && f.most <= 512 && want > (long long)fit * h->sms && two_rows <= kMostRoom) {
     f.ahead = true;
     kernel = kernel_of(f);
     room = two_rows;
@@ -751,20 +800,17 @@ int norm_ok(const a2av_handle* h, int64_t features, int dtype, float eps, const 
 }
 
 using PackKernel = void (*)(PackParams);
-constexpr int kPackVectors = 4;
 
 template <typename T, int kFormat>
-PackKernel pack_kernel_of(bool vector, bool back) {
-  constexpr int N = 16 / sizeof(T);
-  if (back)
-    return vector ? dequantise_kernel<T, N, kPackVectors, kFormat> : dequantise_kernel<T, 1, 8, kFormat>;
-  return vector ? quantise_kernel<T, N, kPackVectors, kFormat> : quantise_kernel<T, 1, 8, kFormat>;
+PackKernel pack_kernel_of(bool aligned, bool back) {
+  if (back) return aligned ? dequantise_kernel<T, true, kFormat> : dequantise_kernel<T, false, kFormat>;
+  return aligned ? quantise_kernel<T, true, kFormat> : quantise_kernel<T, false, kFormat>;
 }
 
 template <typename T>
-PackKernel pack_kernel_of(int format, bool vector, bool back) {
-  return format == A2AV_MXFP8 ? pack_kernel_of<T, A2AV_MXFP8>(vector, back)
-                              : pack_kernel_of<T, A2AV_MXFP4>(vector, back);
+PackKernel pack_kernel_of(int format, bool aligned, bool back) {
+  return format == A2AV_MXFP8 ? pack_kernel_of<T, A2AV_MXFP8>(aligned, back)
+                              : pack_kernel_of<T, A2AV_MXFP4>(aligned, back);
 }
 
 // Both directions; `plain` and `packed` are the buffers' lists.
@@ -791,15 +837,15 @@ int pack_call(a2av_handle* h, int64_t features, int dtype, int format, const voi
   P.W = h->W;
   P.D = (int)features;
   P.row = mx_row(features, format);
-  const bool vector = low % 16 == 0;
-  const PackKernel kernel = dtype == A2AV_F32    ? pack_kernel_of<float>(format, vector, back)
-                            : dtype == A2AV_BF16 ? pack_kernel_of<__nv_bfloat16>(format, vector, back)
-                                                 : pack_kernel_of<__half>(format, vector, back);
+  const bool aligned = low % 16 == 0;
+  const PackKernel kernel = dtype == A2AV_F32    ? pack_kernel_of<float>(format, aligned, back)
+                            : dtype == A2AV_BF16 ? pack_kernel_of<__nv_bfloat16>(format, aligned, back)
+                                                 : pack_kernel_of<__half>(format, aligned, back);
   int fit = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, kPackThreads, 0) != cudaSuccess)
     return A2AV_ERR_CUDA;
-  const long long vectors = vector ? features * size / 16 : features, warps = kPackThreads / 32;
-  const long long slice = 32 * (vector ? kPackVectors : 8);
+  const long long vectors = (features * size + 15) / 16, warps = kPackThreads / 32;
+  const long long slice = 32 * kPackVectors;
   const long long slices = (vectors + slice - 1) / slice;
   const long long want = (P.first[h->W] * slices + warps - 1) / warps, most = (long long)fit * h->sms;
   const cudaError_t e = launch_chained(kernel, dim3((unsigned)(want < most ? want : most)), kPackThreads, 0,
@@ -841,6 +887,7 @@ extern "C" int a2av_norm(a2av_handle* h, int64_t features, int dtype, int format
   const long long rows = P.first[W];
   if (rows == 0) return A2AV_OK;
   P.weight = weight_dev;
+  P.weight_aligned = aligned_to(weight_dev, 16);
   if (format != A2AV_PLAIN) P.row = mx_row(features, format);
   P.W = W;
   P.H = (int)features;
@@ -891,6 +938,7 @@ extern "C" int a2av_norm_backward(a2av_handle* h, int64_t features, int dtype, f
   rc = current_device(h);
   if (rc != A2AV_OK) return rc;
   P.weight = weight_dev;
+  P.weight_aligned = aligned_to(weight_dev, 16);
   P.W = W;
   P.H = (int)features;
   P.eps = eps;
