@@ -53,18 +53,25 @@ struct MxParams {
   int pairwise;  // gated weights come in one copy (their halves are whole eights)
 };
 
-// write_rows, or element by element where the rows take no vectors.
+// write_rows, or element by element where the rows take no vectors: a lane has one
+// column of the staged rows, eight of them at a time.
 template <typename T, int kPieces>
 __device__ __forceinline__ void write_any(bool vector, uint32_t stage, T* to, const Slot& slot, int j,
                                           int f, int F, int lane) {
   if (vector) return write_rows<T, kPieces, kPieces>(stage, to, F, slot, j, f, F, 0, lane);
-  constexpr int kValues = 8 * kPieces;  // of a staged row
-  for (int i = lane; i < 32 * kValues; i += 32) {
-    const int row = i / kValues, c = i % kValues, gr = j + row / kGranule, in = row % kGranule;
-    if (in < slot.n[gr] && f + c < F) {
+  constexpr int kValues = 8 * kPieces, kPer = 32 / kValues;  // columns, rows at a time
+  const int c = lane % kValues;
+  if (f + c >= F) return;
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g) {
+    const int gr = j + g, n = slot.n[gr];
+    unsigned short* at = reinterpret_cast<unsigned short*>(to) + (long long)slot.row[gr] * F + f + c;
+#pragma unroll
+    for (int i = 0; i < kGranule / kPer; ++i) {
+      const int in = lane / kValues + kPer * i;
       unsigned short v;
-      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(stage + row * kPitch + c * 2));
-      reinterpret_cast<unsigned short*>(to)[(long long)(slot.row[gr] + in) * F + f + c] = v;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(stage + (kGranule * g + in) * kPitch + c * 2));
+      if (in < n) at[(long long)in * F] = v;
     }
   }
 }
@@ -73,14 +80,20 @@ __device__ __forceinline__ void write_any(bool vector, uint32_t stage, T* to, co
 template <typename T, int kPieces>
 __device__ __forceinline__ void keep_elements(uint32_t stage, const T* from, const Slot& slot, int j, int f,
                                               int F, int lane) {
-  constexpr int kValues = 8 * kPieces;
-  for (int i = lane; i < 32 * kValues; i += 32) {
-    const int row = i / kValues, c = i % kValues, gr = j + row / kGranule, in = row % kGranule;
-    unsigned short v = 0;
-    if (in < slot.n[gr] && f + c < F)
-      v = reinterpret_cast<const unsigned short*>(from)[(long long)(slot.row[gr] + in) * F + f + c];
-    asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + row * kPitch + c * 2), "h"(v) : "memory");
+  constexpr int kValues = 8 * kPieces, kPer = 32 / kValues, kRows = 32 / kPer;
+  const int c = lane % kValues;
+  unsigned short v[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int row = lane / kValues + kPer * i, gr = j + row / kGranule, in = row % kGranule;
+    v[i] = 0;
+    if (f + c < F && in < slot.n[gr])
+      v[i] = reinterpret_cast<const unsigned short*>(from)[(long long)(slot.row[gr] + in) * F + f + c];
   }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + (lane / kValues + kPer * i) * kPitch + c * 2), "h"(v[i])
+                 : "memory");
 }
 
 template <typename T, int kFormat, bool kGated>
