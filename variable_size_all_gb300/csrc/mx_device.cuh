@@ -272,15 +272,27 @@ struct MxCodes {
   }
 };
 
+// Values that are what they are: none lies above its bits.
+struct Exact {
+  __device__ __forceinline__ bool operator()(unsigned) const { return false; }
+};
+
 // N values of a row, the number v of such, to codes and (by the block's first
 // lane) their scale: by whole warps, 32 / N neighbouring lanes a block; `top` has
 // the bits of the lane's largest magnitude, and `write` says whether the lane's block
-// is in the row (values past the row's end are 0).
-template <int kFormat, int N>
+// is in the row (values past the row's end are 0).  above(bits): whether one of the lane's
+// values of that magnitude was rounded down to it, asked where it is the largest that a scale
+// takes (one block in some 10^7 would otherwise get the scale below).
+template <int kFormat, int N, typename Above>
 __device__ __forceinline__ void mx_store(unsigned char* row, int scales_at, int v, float2 (&f)[N / 2],
-                                         unsigned top, bool write) {
+                                         unsigned top, bool write, Above above) {
   constexpr int kLanes = kMxBlock / N;
-  const unsigned s = mx_scale<kFormat>(lanes_max<kLanes>(top));
+  const unsigned bits = lanes_max<kLanes>(top);
+  unsigned s = mx_scale<kFormat>(bits);
+  if constexpr (!std::is_same_v<Above, Exact>) {
+    const bool full = (bits & 0x7fffffu) == (kFormat == A2AV_MXFP8 ? 0x600000u : 0x400000u);
+    if (__any_sync(kAll, full)) s += lanes_max<kLanes>(full && s > 0 && s < 255u && above(bits) ? 1u : 0u);
+  }
   const float2 by = both(mx_inverse(s));
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) f[i] = mul2(f[i], by);

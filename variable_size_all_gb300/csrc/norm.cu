@@ -23,7 +23,7 @@ struct NormParams {
   MxRow row;                 // of packed results
   int* status;
   int W, H;
-  float eps, per_feature;    // 1 / H
+  float eps, per_feature, per_feature_low;  // 1 / H, and what its rounding left
   int weight_aligned;        // to 16 bytes
 };
 
@@ -188,18 +188,57 @@ __device__ __forceinline__ void take_weight(float2 (&w)[Pairs<T>::N / 2], const 
   }
 }
 
-// 1 / sqrt(x) as a sum of two, to some 2^-45: what the first is off, from its square.
-// (The norm's codes go by which side of a border a value is on: with the last bits of
-// the scale and of both products right, the 8-bit results differ from those of 64 bits as
-// rarely as an f32 value's rounding makes them.)
-struct Scale {
+// A value as a sum of two floats.  (The norm's codes, and their blocks' scales, go by
+// which side of a border a value is on.  With what the last sums, the mean, the root and
+// the two products after it round off kept, a result is the exact one's rounding to 32
+// bits in all but the rarest rows, and its codes are those of the definition in 64 bits.)
+struct Two {
   float high, low;
 };
-__device__ __forceinline__ Scale inverse_root(float x) {
-  const float r = rsqrtf(x), t = x * r;
-  const float off = fmaf(-t, r, 1.0f) - fmaf(x, r, -t) * r;
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ Two add_two(Two a, Two b) {
+  const Two s = two_sum(a.high, b.high);
+  const float low = s.low + (a.low + b.low), high = s.high + low;
+  return isfinite(s.high) ? Two{high, low - (high - s.high)} : Two{s.high, 0.0f};
+}
+__device__ __forceinline__ Two lanes_sum(Two x, const int from) {
+#pragma unroll
+  for (int o = from; o > 0; o >>= 1)
+    x = add_two(x, {__shfl_xor_sync(kAll, x.high, o), __shfl_xor_sync(kAll, x.low, o)});
+  return x;
+}
+
+// The sum of x over a warp, or over the block (`shared` as in row_sum).  The first steps are
+// between as many partial sums that their roundings average out.
+template <bool kWarp, int kThreads>
+__device__ __forceinline__ Two precise_sum(float2 x, Two* shared) {
+  Two t = add_two({x.x, 0.0f}, {x.y, 0.0f});
+  if constexpr (kWarp) return lanes_sum(t, 16);
+  float s = t.high;
+#pragma unroll
+  for (int o = 16; o > 2; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+  t = lanes_sum({s, 0.0f}, 2);
+  // (every lane ends up with it: they take the warps' sums in turn, several times over)
+  constexpr int kMost = kThreads / 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
+  if (lane == 0) shared[warp] = t;
+  __syncthreads();
+  t = lane % kMost < warps ? shared[lane % kMost] : Two{0.0f, 0.0f};
+  return lanes_sum(t, kMost / 2);
+}
+
+// 1 / sqrt(mean + eps): what the first float is off, from its square.
+__device__ __forceinline__ Two inverse_root(const NormParams& P, Two sum) {
+  const float p = sum.high * P.per_feature;
+  const float rest = fmaf(sum.high, P.per_feature, -p) + (sum.low * P.per_feature + sum.high * P.per_feature_low);
+  const Two x = two_sum(p, P.eps);
+  const float r = rsqrtf(x.high), t = x.high * r;
+  const float off = fmaf(-t, r, 1.0f) - fmaf(x.high, r, -t) * r - (x.low + rest) * r * r;
   const float low = 0.5f * r * off;
-  return {r, isfinite(low) ? low : 0.0f};  // (x of 0 or infinity)
+  return {r, isfinite(low) ? low : 0.0f};  // (a mean of 0 or infinity)
 }
 
 template <typename T, bool kAligned, int kFormat, bool kWarp, int kThreads, bool kAhead>
@@ -211,7 +250,7 @@ __global__ void __maxnreg__(kThreads > 512 ? 64 : !kAligned ? 72 : sizeof(T) == 
   using F = float2;
   constexpr int N = Q::N, U = kHeld<kAligned> / N, M = N / 2;
   extern __shared__ uint4 room[];
-  __shared__ float sums[2][kThreads / 32][1];
+  __shared__ Two sums[2][kThreads / 32];
   __shared__ unsigned long long bars[kWarp ? 2 * kThreads / 32 : 2];
   // (rows that take no vectors have them for codes alone)
   constexpr bool kVectors = kAligned || kFormat != A2AV_PLAIN, kSpread = kVectors && !kAligned;
@@ -285,8 +324,7 @@ __global__ void __maxnreg__(kThreads > 512 ? 64 : !kAligned ? 72 : sizeof(T) == 
     }
     if (keep) give_row<T, kAligned>(kept, s, i0, threads, P.H);
     if constexpr (kSpread) Loose<T>::spread(s, place);
-    float total[1] = {total2.x + total2.y};
-    row_sum<kWarp, 1>(total, sums[parity]);
+    const Two total = precise_sum<kWarp, kThreads>(total2, sums[parity]);
     // (all threads have taken their part of the row: its place is free)
     if constexpr (kAhead) {
       if (kWarp) __syncwarp();
@@ -296,7 +334,7 @@ __global__ void __maxnreg__(kThreads > 512 ? 64 : !kAligned ? 72 : sizeof(T) == 
       }
       ahead.next();
     }
-    const Scale root = inverse_root(fmaf(total[0], P.per_feature, P.eps));
+    const Two root = inverse_root(P, total);
     const F high = both(root.high), low = both(root.low);
     unsigned char* packed = nullptr;
     T* out = row_of<T>(kFormat == A2AV_PLAIN ? P.out : P.plain, t);
@@ -319,15 +357,32 @@ __global__ void __maxnreg__(kThreads > 512 ? 64 : !kAligned ? 72 : sizeof(T) == 
           f[i] = fma2(a, w[i], mul2(rest, w[i]));
         }
       }
-      s[u] = Q::pack(f);
-      if (kFormat != A2AV_PLAIN && u * threads < np) {
-        if constexpr (kFormat != A2AV_PLAIN)
-          mx_store<kFormat, N>(packed, P.row.values, v, f, __float_as_uint(largest(f)), v < np);
+      if (plain) {
+        V y[1] = {Q::pack(f)};
+        if constexpr (kSpread) Loose<T>::gather(y, place);
+        give_row<T, kAligned>(out, y, v, 0, P.H);
       }
-    }
-    if (plain) {
-      if constexpr (kSpread) Loose<T>::gather(s, place);
-      give_row<T, kAligned>(out, s, i0, threads, P.H);
+      if constexpr (kFormat != A2AV_PLAIN) {
+        // whether one of the values of these bits is larger than them, rounded down
+        const auto above = [&](unsigned bits) {
+          bool any = false;
+          if (has_part<T, kVectors>(v, P.H)) {
+            F w[M], x[M];
+            take_weight<T, kAligned, kVectors>(w, P, v);
+            Q::unpack(s[u], x);
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+              const F a = mul2(x[i], high), rest = fma2(x[i], low, fma2(x[i], high, minus(a)));
+              const F c = mul2(rest, w[i]), y = fma2(a, w[i], c), off = add2(fma2(a, w[i], minus(y)), c);
+              any = any || (__float_as_uint(fabsf(y.x)) == bits && (y.x > 0.0f ? off.x : -off.x) > 0.0f) ||
+                    (__float_as_uint(fabsf(y.y)) == bits && (y.y > 0.0f ? off.y : -off.y) > 0.0f);
+            }
+          }
+          return any;
+        };
+        if (u * threads < np)
+          mx_store<kFormat, N>(packed, P.row.values, v, f, __float_as_uint(largest(f)), v < np, above);
+      }
     }
     if constexpr (kFormat != A2AV_PLAIN) {
       const int used = P.row.values + P.row.scales;
@@ -593,7 +648,7 @@ __global__ void __launch_bounds__(kPackThreads) quantise_kernel(const __grid_con
         Q::unpack(s[u], f);
         top = top_bits<T>(s[u], f);
       }
-      if (v - lane < np) mx_store<kFormat, N>(to, P.row.values, v, f, top, v < np);
+      if (v - lane < np) mx_store<kFormat, N>(to, P.row.values, v, f, top, v < np, Exact());
     }
     const int used = P.row.values + P.row.scales;
     if (at.slice == cut.slices - 1 && used + lane < P.row.bytes) to[used + lane] = 0;
@@ -893,7 +948,8 @@ extern "C" int a2av_norm(a2av_handle* h, int64_t features, int dtype, int format
   P.H = (int)features;
   P.eps = eps;
   P.status = h->d_status;
-  P.per_feature = 1.0f / (float)features;
+  P.per_feature = (float)(1.0 / (double)features);
+  P.per_feature_low = (float)(1.0 / (double)features - (double)P.per_feature);
   const NormForm f = norm_form(features, size, low, rows, h->sms, false);
   unsigned blocks;
   const cudaError_t e = launch_norm(h, [&](const NormForm& g) { return norm_kernel_of(dtype, format, g); }, f,
@@ -943,7 +999,8 @@ extern "C" int a2av_norm_backward(a2av_handle* h, int64_t features, int dtype, f
   P.H = (int)features;
   P.eps = eps;
   P.status = h->d_status;
-  P.per_feature = 1.0f / (float)features;
+  P.per_feature = (float)(1.0 / (double)features);
+  P.per_feature_low = (float)(1.0 / (double)features - (double)P.per_feature);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   unsigned blocks = 0;
