@@ -54,8 +54,6 @@ class PackedMoeBlock:
         self.received = new(C, self.row, dtype=torch.uint8)
         self.inner, self.answer = new(C, N), new(C, H)
         self.inner_packed = new(C, self.inner_row, dtype=torch.uint8)
-        for t in self.inner:
-            t.zero_()  # (rows past the received ones are packed as well)
 
     def pack(self, features, width):
         """Random weights [K, features, width] of each rank, packed expert by expert."""
@@ -79,7 +77,7 @@ class PackedMoeBlock:
                    self.offsets, self.pos, self.row, in_splits=self.splits)
         e.expert_matmul_mx(self.received, self.counts, self.up, self.inner, self.H, self.format,
                            activation="silu", gated=True)
-        e.quantise(self.inner, self.inner_packed, self.format)
+        e.quantise(self.inner, self.inner_packed, self.format, in_splits=self.splits)
         e.expert_matmul_mx(self.inner_packed, self.counts, self.down, self.answer, self.N, self.format)
         e.combine_weighted(self.answer, self.splits, self.keys, self.pos, K, self.weights, h, residual=h)
         return h

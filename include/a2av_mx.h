@@ -118,17 +118,23 @@ int a2av_norm_backward(a2av_handle *h, int64_t features, int dtype, float eps,
  * a2av_quantise -- rows of `features` values of dtype to packed rows of `format`, and
  * a2av_dequantise -- back: code * scale, rounded once to dtype.
  *
- *  rows_per_rank      HOST int64 [W], up to 2^31 - 1 together.  Weights [K][Z][D] are K * Z rows.
+ *  rows_per_rank      HOST int64 [W], up to 2^31 - 1 together: the rows that the buffers hold.
+ *                     Weights [K][Z][D] are K * Z rows.
+ *  in_splits_dev      DEVICE int64 [W][W], S as a2av_dispatch writes it, or NULL.  With it
+ *                     rank p's rows are those that it has received, the first sum_r S[r][p]
+ *                     (read on the device); rows past them are neither read nor written.
  *  x_ptrs / out_ptrs  HOST arrays of W: [rows][features].
  *  packed_ptrs        HOST array of W: [rows][a2av_mx_row_bytes(features, format)].
- * Errors are those of a2av_norm.
+ *
+ * Device error: A2AV_ERR_BAD_SPLITS when an entry of S is negative or a rank has received more
+ * rows than its buffers hold: nothing is written.  Host errors are those of a2av_norm.
  */
 int a2av_quantise(a2av_handle *h, int64_t features, int dtype, int format,
-                  const void *const *x_ptrs, const int64_t *rows_per_rank, void *const *packed_ptrs,
-                  void *stream);
+                  const void *const *x_ptrs, const int64_t *rows_per_rank,
+                  const int64_t *in_splits_dev, void *const *packed_ptrs, void *stream);
 int a2av_dequantise(a2av_handle *h, int64_t features, int dtype, int format,
                     const void *const *packed_ptrs, const int64_t *rows_per_rank,
-                    void *const *out_ptrs, void *stream);
+                    const int64_t *in_splits_dev, void *const *out_ptrs, void *stream);
 
 /*
  * a2av_expert_matmul_mx -- a2av_expert_matmul on packed rows and weights of one

@@ -136,6 +136,46 @@ def test_every_byte_of_a_packed_row_means_what_it_says():
     assert back[:2].isnan().all() and back[2] == 1
 
 
+@pytest.mark.parametrize("D", [64, 101])
+def test_received_rows_alone(D):
+    """With a dispatch's splits: rows past the received ones are left as they were, also where the
+    counts change between a graph's replays; splits that do not fit write nothing."""
+    W, held = 3, (40, 7, 0)
+    x = [_place(_values(n, D, 7 + p), torch.bfloat16) for p, n in enumerate(held)]
+    whole = _quantise(x, "mxfp8")
+    back = _dequantise(whole, D, torch.bfloat16, "mxfp8")
+    splits = torch.tensor([[5, 0, 0], [0, 7, 0], [21, 0, 0]], device="cuda")
+    rows, out = [torch.full_like(t, 9) for t in whole], [torch.full_like(t, 9) for t in x]
+    with a2av.A2av(W) as eng:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            eng.quantise(x, rows, "mxfp8", in_splits=splits)
+            eng.dequantise(rows, out, "mxfp8", in_splits=splits)
+        for S in ([[5, 0, 0], [0, 7, 0], [21, 0, 0]], [[0, 0, 0], [0, 0, 0], [0, 0, 0]],
+                  [[40, 1, 0], [0, 2, 0], [0, 3, 0]]):
+            splits.copy_(torch.tensor(S))
+            for t in rows + out:
+                t.fill_(9)
+            graph.replay()
+            assert eng.status() == a2av.OK
+            for p in range(W):
+                n = sum(S[r][p] for r in range(W))
+                assert torch.equal(rows[p][:n], whole[p][:n]) and (rows[p][n:] == 9).all()
+                assert torch.equal(out[p][:n], back[p][:n]) and (out[p][n:] == 9).all()
+        for S in ([[41, 0, 0]] + [[0] * 3] * 2, [[-1, 0, 0], [5, 0, 0], [0] * 3], [[0, 0, 1]] + [[0] * 3] * 2,
+                  [[2 ** 62, 0, 0], [2 ** 62, 0, 0], [2 ** 62, 0, 0]]):
+            splits.copy_(torch.tensor(S))
+            for t in rows + out:
+                t.fill_(9)
+            eng.quantise(x, rows, "mxfp8", in_splits=splits)
+            assert eng.status() == a2av.ERR_BAD_SPLITS
+            eng.dequantise(whole, out, "mxfp8", in_splits=splits)
+            assert eng.status() == a2av.ERR_BAD_SPLITS
+            assert all((t == 9).all() for t in rows + out)
+        with pytest.raises(ValueError):
+            eng.quantise(x, rows, "mxfp8", in_splits=splits.int())
+
+
 def test_graph_and_streams():
     x = [_place(_values(50, 512, 5), torch.bfloat16), _place(_values(7, 512, 6), torch.bfloat16)]
     want = _quantise(x, "mxfp4")

@@ -134,7 +134,7 @@ def load():
     lib.a2av_norm_workspace_bytes.argtypes = [i64, i64]
     lib.a2av_norm_workspace_bytes.restype = i64
     lib.a2av_norm_backward.argtypes = [vp, i64, ci, f32, vp, i64p, vp, vp, vp, vp, vp, vp, i64, vp]
-    lib.a2av_quantise.argtypes = lib.a2av_dequantise.argtypes = [vp, i64, ci, ci, vp, i64p, vp, vp]
+    lib.a2av_quantise.argtypes = lib.a2av_dequantise.argtypes = [vp, i64, ci, ci, vp, i64p, vp, vp, vp]
     lib.a2av_expert_matmul_mx.argtypes = [vp, expert_p, ci, vp, i64p, vp, vp, vp, vp, vp, vp]
     for f in ("a2av_norm", "a2av_norm_backward", "a2av_quantise", "a2av_dequantise",
               "a2av_expert_matmul_mx", "a2av_create", "a2av_run", "a2av_combine", "a2av_status", "a2av_destroy", "a2av_set_path",
@@ -398,18 +398,19 @@ def a2av_norm_backward(handle, features: int, dtype: int, eps: float, sum_ptrs, 
 
 
 def a2av_quantise(handle, features: int, dtype: int, format: int, x_ptrs, rows_per_rank, packed_ptrs,
-                  stream: int = 0) -> int:
+                  in_splits_dev: int = 0, stream: int = 0) -> int:
     """Raw packing of rows."""
     return load().a2av_quantise(handle, int(features), int(dtype), int(format), _ptr_array(x_ptrs),
-                                _i64_array(rows_per_rank), _ptr_array(packed_ptrs), _address(stream))
+                                _i64_array(rows_per_rank), _address(in_splits_dev),
+                                _ptr_array(packed_ptrs), _address(stream))
 
 
 def a2av_dequantise(handle, features: int, dtype: int, format: int, packed_ptrs, rows_per_rank,
-                    out_ptrs, stream: int = 0) -> int:
+                    out_ptrs, in_splits_dev: int = 0, stream: int = 0) -> int:
     """Raw unpacking of rows."""
     return load().a2av_dequantise(handle, int(features), int(dtype), int(format),
                                   _ptr_array(packed_ptrs), _i64_array(rows_per_rank),
-                                  _ptr_array(out_ptrs), _address(stream))
+                                  _address(in_splits_dev), _ptr_array(out_ptrs), _address(stream))
 
 
 def a2av_expert_matmul_mx(handle, shape: A2avExpert, format: int, rows_ptrs, rows_per_peer,
@@ -1274,40 +1275,46 @@ class A2av:
                 workspace.numel() * workspace.element_size() if need else 0, self._queue(stream)]
         self._call("a2av_norm_backward", args, None, False)
 
-    def _pack_args(self, what, plain, plain_name, packed, packed_name, format, stream, bind):
+    def _pack_args(self, what, plain, plain_name, packed, packed_name, format, in_splits, stream, bind):
         n, D = self._tokens(plain, plain_name)
         dtype, code = self._dtype(plain, plain_name, (F32, BF16, F16))
         width = mx_row_bytes(D, format)
+        if in_splits is not None:
+            self._matrix(in_splits, (self.world_size, self.world_size), "in_splits")
         (x, p), arrays = self._lists((plain, dtype, [(m, D) for m in n], plain_name),
                                      (packed, self._bytes, [(m, width) for m in n], packed_name))
         if what == "a2av_dequantise":
             x, p = p, x
-        args = [self.handle, D, code, _FORMATS[format], x, self._counts(*n), p, self._queue(stream)]
-        return self._call(what, args, (plain, packed, arrays), bind)
+        args = [self.handle, D, code, _FORMATS[format], x, self._counts(*n),
+                None if in_splits is None else in_splits.data_ptr(), p, self._queue(stream)]
+        return self._call(what, args, (plain, packed, in_splits, arrays), bind)
 
-    def quantise(self, x, rows, format: str, stream=None, _bind=False):
+    def quantise(self, x, rows, format: str, in_splits=None, stream=None, _bind=False):
         """``x[r]`` [R, D] (float32, bfloat16 or float16) to packed rows ``rows[r]``, uint8
         [R, mx_row_bytes(D, format)], ``format`` "mxfp8" or "mxfp4" (see
-        include/a2av_mx.h).  An expert's weights [K, Z, D] are K * Z rows."""
-        if not _bind and self._whole("quantise", stream, x, rows, _FORMATS.get(format),
+        include/a2av_mx.h).  An expert's weights [K, Z, D] are K * Z rows.  With a dispatch's
+        ``in_splits``, int64 [W, W], only the rows that rank r has received are read and written."""
+        if not _bind and self._whole("quantise", stream, x, rows, _FORMATS.get(format), in_splits,
                                      self._entries["mx_row_bytes"]):
             return
-        return self._pack_args("a2av_quantise", x, "x", rows, "rows", format, stream, _bind)
+        return self._pack_args("a2av_quantise", x, "x", rows, "rows", format, in_splits, stream, _bind)
 
-    def bind_quantise(self, x, rows, format: str, stream=None) -> BoundCall:
+    def bind_quantise(self, x, rows, format: str, **options) -> BoundCall:
         """``quantise`` marshalled once (see BoundCall)."""
-        return self.quantise(x, rows, format, stream, _bind=True)
+        return self.quantise(x, rows, format, **options, _bind=True)
 
-    def dequantise(self, rows, outputs, format: str, stream=None, _bind=False):
-        """Packed rows back to ``outputs[r]`` [R, D]: code * scale, rounded once."""
+    def dequantise(self, rows, outputs, format: str, in_splits=None, stream=None, _bind=False):
+        """Packed rows back to ``outputs[r]`` [R, D]: code * scale, rounded once.  ``in_splits``
+        as in ``quantise``."""
         if not _bind and self._whole("dequantise", stream, rows, outputs, _FORMATS.get(format),
-                                     self._entries["mx_row_bytes"]):
+                                     in_splits, self._entries["mx_row_bytes"]):
             return
-        return self._pack_args("a2av_dequantise", outputs, "outputs", rows, "rows", format, stream, _bind)
+        return self._pack_args("a2av_dequantise", outputs, "outputs", rows, "rows", format, in_splits,
+                               stream, _bind)
 
-    def bind_dequantise(self, rows, outputs, format: str, stream=None) -> BoundCall:
+    def bind_dequantise(self, rows, outputs, format: str, **options) -> BoundCall:
         """``dequantise`` marshalled once (see BoundCall)."""
-        return self.dequantise(rows, outputs, format, stream, _bind=True)
+        return self.dequantise(rows, outputs, format, **options, _bind=True)
 
     def expert_matmul_mx(self, rows, counts, weights, outputs, in_features: int, format: str,
                          activation: str = "none", gated: bool = False, bias=None, residual=None,

@@ -627,26 +627,27 @@ PyObject* norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
       });
 }
 
-// (..., rows to read, rows to write, format, a2av_mx_row_bytes); `back`: from packed ones.
+// (..., rows to read, rows to write, format, in_splits, a2av_mx_row_bytes); `back`: from packed ones.
 PyObject* packing(PyObject* const* args, Py_ssize_t n, bool back) {
   Call c;
   at::ScalarType type;
   int dtype, format;
   int64_t rows[kRanks], D = 0;
   void *plain[kRanks], *packed[kRanks];
+  const int64_t* splits = nullptr;
   return whole(
-      n, 8,
+      n, 9,
       [&] {
         return call_of(args, &c) && type_of(args[back ? 5 : 4], true, &type, &dtype) &&
                take_any_rows(args[back ? 5 : 4], c.W, type, plain, rows, &D) &&
-               int_of(args[6], &format) &&
+               int_of(args[6], &format) && (args[7] == Py_None || matrix_of(args[7], c.W, c.W, &splits)) &&
                take_rows(args[back ? 4 : 5], c.W, at::kByte, packed, rows,
-                         packed_bytes(args[7], D, format));
+                         packed_bytes(args[8], D, format));
       },
       [&] {
         // (the two have one signature)
         return reinterpret_cast<decltype(&a2av_quantise)>(c.function)(
-            static_cast<a2av_handle*>(c.handle), D, dtype, format, back ? packed : plain, rows,
+            static_cast<a2av_handle*>(c.handle), D, dtype, format, back ? packed : plain, rows, splits,
             back ? plain : packed, c.stream);
       });
 }

@@ -559,10 +559,41 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float* part, in
 struct PackParams {
   const void* from[kW];
   void* to[kW];
-  long long first[kW + 1];  // rows before each rank's
+  long long first[kW + 1];  // rows before each rank's, as many as the buffers hold
+  const long long* splits;  // S [W][W]: the rows that are there; or NULL, all of them
+  int* status;
   MxRow row;
   int D, W;
 };
+
+// Rows before each rank's that are worked on, by the whole block; false (in every
+// thread) and the status word set where S is not valid.
+__device__ __forceinline__ bool count_received(const PackParams& P, long long (&first)[kW + 1]) {
+  __shared__ int bad;
+  const int tid = threadIdx.x, W = P.W;
+  __shared__ long long rows[kW];
+  if (tid == 0) bad = 0;
+  __syncthreads();
+  if (tid < W) {
+    long long n = 0;
+    const long long most = P.first[tid + 1] - P.first[tid];
+    for (int r = 0; r < W; ++r) {
+      const long long s = __ldcg(P.splits + r * W + tid);
+      if (s < 0 || s > most - n) bad = 1;
+      n = s < 0 || s > most - n ? n : n + s;
+    }
+    rows[tid] = n;
+  }
+  __syncthreads();
+  if (tid <= W) {
+    long long at = 0;
+    for (int p = 0; p < tid; ++p) at += rows[p];
+    first[tid] = at;
+  }
+  __syncthreads();
+  if (bad && blockIdx.x == 0 && tid == 0) note_error(P.status, A2AV_ERR_BAD_SPLITS);
+  return !bad;
+}
 
 constexpr int kPackThreads = 256;
 
@@ -609,10 +640,19 @@ __device__ __forceinline__ unsigned top_bits(const typename Pairs<T>::Raw& r, co
   }
 }
 
+// (either stays in its own kind of memory)
+template <bool kReceived>
+__device__ __forceinline__ const auto& firsts(const PackParams& P, const long long (&received)[kReceived ? kW + 1 : 1]) {
+  if constexpr (kReceived)
+    return received;
+  else
+    return P.first;
+}
+
 constexpr int kPackVectors = 4;  // of a lane at a time
 
 // A warp takes 32 x kPackVectors neighbouring vectors of a row.
-template <typename T, bool kAligned, int kFormat>
+template <typename T, bool kAligned, int kFormat, bool kReceived>
 __global__ void __launch_bounds__(kPackThreads) quantise_kernel(const __grid_constant__ PackParams P) {
   chain();
   using Q = Pairs<T>;
@@ -620,11 +660,15 @@ __global__ void __launch_bounds__(kPackThreads) quantise_kernel(const __grid_con
   __shared__ uint4 places[kAligned ? 1 : kPackThreads / 32][kAligned ? 1 : U][32];
   const int lane = threadIdx.x % 32;
   const int nv = (P.D + N - 1) / N, np = P.row.scales * (kMxBlock / N);
-  const Slices cut(P.first[P.W], (np + 32 * U - 1) / (32 * U));
+  __shared__ long long received[kReceived ? kW + 1 : 1];
+  if constexpr (kReceived)
+    if (!count_received(P, received)) return;
+  const auto& first = firsts<kReceived>(P, received);
+  const Slices cut(first[P.W], (np + 32 * U - 1) / (32 * U));
   int r = 0;
   for (Slice at = cut.first(); at.t < cut.rows; cut.next(&at)) {
-    find_rank(P.first, at.t, &r);
-    const long long t = at.t - P.first[r];
+    find_rank(first, at.t, &r);
+    const long long t = at.t - first[r];
     const int v0 = at.slice * (32 * U) + lane;
     const T* x = static_cast<const T*>(P.from[r]) + t * P.D;
     unsigned char* to = static_cast<unsigned char*>(P.to[r]) + t * P.row.bytes;
@@ -655,7 +699,7 @@ __global__ void __launch_bounds__(kPackThreads) quantise_kernel(const __grid_con
   }
 }
 
-template <typename T, bool kAligned, int kFormat>
+template <typename T, bool kAligned, int kFormat, bool kReceived>
 __global__ void __launch_bounds__(kPackThreads) dequantise_kernel(const __grid_constant__ PackParams P) {
   chain();
   using Q = Pairs<T>;
@@ -663,11 +707,15 @@ __global__ void __launch_bounds__(kPackThreads) dequantise_kernel(const __grid_c
   __shared__ uint4 places[kAligned ? 1 : kPackThreads / 32][kAligned ? 1 : U][32];
   const int lane = threadIdx.x % 32;
   const int nv = (P.D + N - 1) / N;
-  const Slices cut(P.first[P.W], (nv + 32 * U - 1) / (32 * U));
+  __shared__ long long received[kReceived ? kW + 1 : 1];
+  if constexpr (kReceived)
+    if (!count_received(P, received)) return;
+  const auto& first = firsts<kReceived>(P, received);
+  const Slices cut(first[P.W], (nv + 32 * U - 1) / (32 * U));
   int r = 0;
   for (Slice at = cut.first(); at.t < cut.rows; cut.next(&at)) {
-    find_rank(P.first, at.t, &r);
-    const long long t = at.t - P.first[r];
+    find_rank(first, at.t, &r);
+    const long long t = at.t - first[r];
     const int v0 = at.slice * (32 * U) + lane;
     const unsigned char* from = static_cast<const unsigned char*>(P.from[r]) + t * P.row.bytes;
     T* out = static_cast<T*>(P.to[r]) + t * P.D;
@@ -856,24 +904,30 @@ int norm_ok(const a2av_handle* h, int64_t features, int dtype, float eps, const 
 
 using PackKernel = void (*)(PackParams);
 
-template <typename T, int kFormat>
-PackKernel pack_kernel_of(bool aligned, bool back) {
-  if (back) return aligned ? dequantise_kernel<T, true, kFormat> : dequantise_kernel<T, false, kFormat>;
-  return aligned ? quantise_kernel<T, true, kFormat> : quantise_kernel<T, false, kFormat>;
+struct PackForm {
+  bool aligned, back, received;
+};
+
+template <typename T, int kFormat, bool kReceived>
+PackKernel pack_kernel_of(const PackForm& f) {
+  if (f.back)
+    return f.aligned ? dequantise_kernel<T, true, kFormat, kReceived> : dequantise_kernel<T, false, kFormat, kReceived>;
+  return f.aligned ? quantise_kernel<T, true, kFormat, kReceived> : quantise_kernel<T, false, kFormat, kReceived>;
 }
 
 template <typename T>
-PackKernel pack_kernel_of(int format, bool aligned, bool back) {
-  return format == A2AV_MXFP8 ? pack_kernel_of<T, A2AV_MXFP8>(aligned, back)
-                              : pack_kernel_of<T, A2AV_MXFP4>(aligned, back);
+PackKernel pack_kernel_of(int format, const PackForm& f) {
+  if (format == A2AV_MXFP8)
+    return f.received ? pack_kernel_of<T, A2AV_MXFP8, true>(f) : pack_kernel_of<T, A2AV_MXFP8, false>(f);
+  return f.received ? pack_kernel_of<T, A2AV_MXFP4, true>(f) : pack_kernel_of<T, A2AV_MXFP4, false>(f);
 }
 
 // Both directions; `plain` and `packed` are the buffers' lists.
 int pack_call(a2av_handle* h, int64_t features, int dtype, int format, const void* const* plain,
-              const int64_t* rows, const void* const* packed, bool back, void* stream) {
+              const int64_t* rows, const int64_t* splits, const void* const* packed, bool back, void* stream) {
   const int size = dtype_bytes(dtype);
   if (h == nullptr || plain == nullptr || rows == nullptr || packed == nullptr || features < 1 ||
-      size == 0 || !is_packed(format))
+      size == 0 || !is_packed(format) || !aligned_to(splits, 8))
     return A2AV_ERR_INVALID_ARG;
   if (features > A2AV_MAX_MX_FEATURES) return A2AV_ERR_UNSUPPORTED;
   PackParams P;
@@ -891,11 +945,13 @@ int pack_call(a2av_handle* h, int64_t features, int dtype, int format, const voi
   if (P.first[h->W] == 0) return A2AV_OK;
   P.W = h->W;
   P.D = (int)features;
+  P.splits = reinterpret_cast<const long long*>(splits);
+  P.status = h->d_status;
   P.row = mx_row(features, format);
-  const bool aligned = low % 16 == 0;
-  const PackKernel kernel = dtype == A2AV_F32    ? pack_kernel_of<float>(format, aligned, back)
-                            : dtype == A2AV_BF16 ? pack_kernel_of<__nv_bfloat16>(format, aligned, back)
-                                                 : pack_kernel_of<__half>(format, aligned, back);
+  const PackForm form = {low % 16 == 0, back, splits != nullptr};
+  const PackKernel kernel = dtype == A2AV_F32    ? pack_kernel_of<float>(format, form)
+                            : dtype == A2AV_BF16 ? pack_kernel_of<__nv_bfloat16>(format, form)
+                                                 : pack_kernel_of<__half>(format, form);
   int fit = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, kPackThreads, 0) != cudaSuccess)
     return A2AV_ERR_CUDA;
@@ -1017,12 +1073,12 @@ extern "C" int a2av_norm_backward(a2av_handle* h, int64_t features, int dtype, f
 
 extern "C" int a2av_quantise(a2av_handle* h, int64_t features, int dtype, int format,
                              const void* const* x_ptrs, const int64_t* rows_per_rank,
-                             void* const* packed_ptrs, void* stream) {
-  return pack_call(h, features, dtype, format, x_ptrs, rows_per_rank, packed_ptrs, false, stream);
+                             const int64_t* in_splits_dev, void* const* packed_ptrs, void* stream) {
+  return pack_call(h, features, dtype, format, x_ptrs, rows_per_rank, in_splits_dev, packed_ptrs, false, stream);
 }
 
 extern "C" int a2av_dequantise(a2av_handle* h, int64_t features, int dtype, int format,
                                const void* const* packed_ptrs, const int64_t* rows_per_rank,
-                               void* const* out_ptrs, void* stream) {
-  return pack_call(h, features, dtype, format, out_ptrs, rows_per_rank, packed_ptrs, true, stream);
+                               const int64_t* in_splits_dev, void* const* out_ptrs, void* stream) {
+  return pack_call(h, features, dtype, format, out_ptrs, rows_per_rank, in_splits_dev, packed_ptrs, true, stream);
 }
