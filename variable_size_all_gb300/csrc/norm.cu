@@ -2,9 +2,21 @@
 // its gradients, and packed rows (a2av_quantise, a2av_dequantise); the interface is
 // in include/a2av_mx.h.
 //
-// All are bound by memory: each row is read once and written once.  A block (a
-// warp, for short rows) takes a row, keeps it in registers between the sum of
-// squares and the result, and goes on to another; the weight stays in registers.
+// All are bound by memory: what a row has is read once and written once.  Of 65,536
+// rows of 7168 in bf16, at a copy rate of 6.68 TB/s: the norm with a residual, 8-bit results
+// 535 us (93 %); its gradients, 616 to 640 us (88 to 91 %); rows to 8 bits 214 us (99 %), 131,072
+// of them back 467 us (91 %); 458,752 rows of 2048 to 4 bits and back 785 us (91 %).
+//
+// The norm: a block (a warp, for short rows) takes a row, holds it in registers
+// between its sums and its results, and goes on.  What decides is how much is in flight
+// meanwhile: bulk copies bring the block's next two rows to shared memory (rows read when
+// they are needed took 627 and 1441 us instead, cp.async by each thread 523 and 841, with two
+// registers of addresses for each array in every thread), and the weight is read from L1
+// for each row, because 32 registers less are a block more on an SM.  (A spill costs far more
+// than a block: its loads miss the little L1 that the rows leave, 1730 us.)
+//
+// Instructions count as well: values are multiplied in pairs, magnitudes of 16-bit rows
+// compared in pairs, ranks and slices followed without divisions.
 #include "mma.cuh"
 #include "mx_device.cuh"
 
@@ -56,8 +68,10 @@ __device__ __forceinline__ void row_sum(float (&x)[kSums], float (*shared)[kSums
 }
 
 // How a row lies on its threads: in vectors of 16 bytes, thread i having the vectors
-// i, i + threads, ..., of these many values in all.  (The backward pass keeps the weight's
-// gradient of its values as well, and rows that take no vectors their elements on the way.)
+// i, i + threads, ..., of these many values in all.  The backward pass keeps the weight's
+// gradient of its values as well; rows that take no vectors are not fetched ahead, and want
+// more threads instead (16,384 rows of 7161, bf16: the norm 226 us with 16 values a thread,
+// 270 with 32; the gradients of 32,768 rows of 1001 80 us with 8, 92 with 16).
 template <bool kAligned>
 constexpr int kHeld = kAligned ? 32 : 16;
 __host__ __device__ constexpr int held_backward(bool aligned, int size, int64_t H) {
@@ -535,7 +549,8 @@ __global__ void __maxnreg__(kThreads > 512 ? 64 : 128)
   }
 }
 
-// The blocks' parts of 32 columns, summed by 32 warps and joined.
+// The blocks' parts of 32 columns, summed by 32 warps and joined (304 parts of 7168: 7 us
+// of the 620).  The order is that of the blocks, which go by the sizes alone.
 __global__ void __launch_bounds__(1024) norm_weight_kernel(const float* part, int blocks, int H,
                                                            float* d_weight) {
   chain();
