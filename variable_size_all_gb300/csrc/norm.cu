@@ -4,7 +4,7 @@
 //
 // All are bound by memory: what a row has is read once and written once.  Of 65,536
 // rows of 7168 in bf16, at a copy rate of 6.68 TB/s: the norm with a residual, 8-bit results
-// 535 us (93 %); its gradients, 616 to 640 us (88 to 91 %); rows to 8 bits 214 us (99 %), 131,072
+// 529 to 543 us (91 to 93 %); its gradients, 616 to 640 us (88 to 91 %); rows to 8 bits 214 us (99 %), 131,072
 // of them back 467 us (91 %); 458,752 rows of 2048 to 4 bits and back 785 us (91 %).
 //
 // The norm: a block (a warp, for short rows) takes a row, holds it in registers
@@ -204,8 +204,10 @@ __device__ __forceinline__ void take_weight(float2 (&w)[Pairs<T>::N / 2], const 
 
 // A value as a sum of two floats.  (The norm's codes, and their blocks' scales, go by
 // which side of a border a value is on.  With what the last sums, the mean, the root and
-// the two products after it round off kept, a result is the exact one's rounding to 32
-// bits in all but the rarest rows, and its codes are those of the definition in 64 bits.)
+// the two products after it round off kept, a result is mostly the exact one's rounding to
+// 32 bits.  Of 7.05e9 values, 15 draws, 608 codes and 3 scales are not those of that
+// rounding, against 1698 and 12 with 32 bits alone, for 8 of 543 us.  Codes rounded from
+// 64 bits at once differ in 3371 against 3427: there the rounding to 32 bits decides.)
 struct Two {
   float high, low;
 };
@@ -225,23 +227,20 @@ __device__ __forceinline__ Two lanes_sum(Two x, const int from) {
   return x;
 }
 
-// The sum of x over a warp, or over the block (`shared` as in row_sum).  The first steps are
-// between as many partial sums that their roundings average out.
+// The sum of x over a warp, or over the block (`shared` as in row_sum).  A block's first
+// steps are between so many partial sums that their roundings average out.
 template <bool kWarp, int kThreads>
 __device__ __forceinline__ Two precise_sum(float2 x, Two* shared) {
-  Two t = add_two({x.x, 0.0f}, {x.y, 0.0f});
-  if constexpr (kWarp) return lanes_sum(t, 16);
-  float s = t.high;
+  if constexpr (kWarp) return lanes_sum(add_two({x.x, 0.0f}, {x.y, 0.0f}), 16);
+  float s = x.x + x.y;
 #pragma unroll
-  for (int o = 16; o > 2; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-  t = lanes_sum({s, 0.0f}, 2);
-  // (every lane ends up with it: they take the warps' sums in turn, several times over)
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+  // (every lane ends up with the sum: they take the warps' in turn, several times over)
   constexpr int kMost = kThreads / 32;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
-  if (lane == 0) shared[warp] = t;
+  if (lane == 0) shared[warp] = {s, 0.0f};
   __syncthreads();
-  t = lane % kMost < warps ? shared[lane % kMost] : Two{0.0f, 0.0f};
-  return lanes_sum(t, kMost / 2);
+  return lanes_sum(lane % kMost < warps ? shared[lane % kMost] : Two{0.0f, 0.0f}, kMost / 2);
 }
 
 // 1 / sqrt(mean + eps): what the first float is off, from its square.
@@ -332,8 +331,10 @@ __global__ void __maxnreg__(kThreads > 512 ? 64 : !kAligned ? 72 : sizeof(T) == 
           s[u] = Q::pack(f);
           Q::unpack(s[u], f);
         }
+        F squares = mul2(f[0], f[0]);
 #pragma unroll
-        for (int i = 0; i < M; ++i) total2 = fma2(f[i], f[i], total2);
+        for (int i = 1; i < M; ++i) squares = fma2(f[i], f[i], squares);
+        total2 = add2(total2, squares);
       }
     }
     if (keep) give_row<T, kAligned>(kept, s, i0, threads, P.H);
