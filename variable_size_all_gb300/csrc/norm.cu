@@ -4,7 +4,7 @@
 //
 // All are bound by memory: what a row has is read once and written once.  Of 65,536
 // rows of 7168 in bf16, at a copy rate of 6.68 TB/s: the norm with a residual, 8-bit results
-// 529 to 543 us (91 to 93 %); its gradients, 616 to 640 us (88 to 91 %); rows to 8 bits 214 us (99 %), 131,072
+// 528 to 543 us (91 to 93 %); its gradients, 616 to 640 us (88 to 91 %); rows to 8 bits 214 us (99 %), 131,072
 // of them back 467 us (91 %); 458,752 rows of 2048 to 4 bits and back 785 us (91 %).
 //
 // The norm: a block (a warp, for short rows) takes a row, holds it in registers
