@@ -1,6 +1,8 @@
 """The norm and its gradients over batches of more rows than a GPU holds at once,
 where rows are fetched ahead: by warps (up to 1024 features) and by blocks of 256 and
-512 threads, across ranks of any number of rows."""
+512 threads, across ranks of any number of rows; and called by two threads at once."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -159,3 +161,48 @@ def test_backward(case, more):
         into = a if which == "dy" else b
         again = _backward(s, w, a, b, into)
         assert torch.equal(again, dw) and all(torch.equal(p, q) for p, q in zip(into, dx))
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_two_threads(backward):
+    """A handle and a stream each, rows of different width for the same kernel."""
+    # 2048 and 8192 features of bf16: blocks of up to 256 threads (512: the gradients alike)
+    widths, failed, results = (2048, 8192), [], {}
+    data = {H: (_rows([4000], H, "bf16", 8), _weight(H), _rows([4000], H, "bf16", 10)) for H in widths}
+    want = {}
+    for H, (x, w, dy) in data.items():
+        out = [torch.empty_like(x[0])]
+        with a2av.A2av(1) as eng:
+            if backward:
+                eng.norm_backward(x, w, dy, out, eps=EPS)
+            else:
+                eng.norm(x, w, out, eps=EPS)
+            assert eng.status() == a2av.OK
+        want[H] = out[0]
+    start = threading.Barrier(2)
+
+    def work(H):
+        x, w, dy = data[H]
+        out = [torch.zeros_like(x[0])]
+        stream = torch.cuda.Stream()
+        try:
+            with a2av.A2av(1) as eng:
+                torch.cuda.synchronize()
+                start.wait(60)
+                for _ in range(1000):
+                    if backward:
+                        eng.norm_backward(x, w, dy, out, eps=EPS, stream=stream)
+                    else:
+                        eng.norm(x, w, out, eps=EPS, stream=stream)
+                assert eng.status(stream) == a2av.OK
+            results[H] = out[0]
+        except Exception as e:
+            failed.append((H, e))
+
+    threads = [threading.Thread(target=work, args=(H,)) for H in widths]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    assert all(torch.equal(results[H], want[H]) for H in widths)

@@ -900,7 +900,9 @@ cudaError_t launch_norm(const a2av_handle* h, K kernel_of, NormForm f, int row_b
     f.ahead = true;
     kernel = kernel_of(f);
     room = two_rows;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)room);
+    // (the most that any call asks for, and never less: the limit is the kernel's, which
+    // another thread may be about to launch with wider rows)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostRoom);
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, f.threads, room);
     if (e != cudaSuccess) return e;
   }
