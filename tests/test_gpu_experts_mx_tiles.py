@@ -33,3 +33,15 @@ def test_several_tiles_a_pair(fmt, gated, D):
     for _ in range(3):
         again = products._run(c, name, True, False)
         assert all(torch.equal(a, b) for a, b in zip(again, out))
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_counts_of_any_alignment(fmt):
+    """Counts eight bytes off sixteen, with tiles that have fewer rows and features than places."""
+    c = products._case(2, 3, 96, 40, 9, "bf16", fmt, False, seed=12, slack=2)
+    want = products._run(c, "relu", True, False)
+    counts = torch.empty(c["d_counts"].numel() + 1, dtype=torch.int64, device="cuda")[1:].view(c["d_counts"].shape)
+    counts.copy_(c["d_counts"])
+    assert counts.data_ptr() % 16 == 8
+    c["d_counts"] = counts
+    assert all(torch.equal(a, b) for a, b in zip(products._run(c, "relu", True, False), want))

@@ -303,10 +303,10 @@ __global__ void __launch_bounds__(kMxThreads, 1) __cluster_dims__(2, 1, 1)
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          // (zeros: any address does)
+          // (zeros: nothing is read, but the address has to be one of 16 bytes all the same,
+          // which weights are)
           const bool here = ok && from[k] != nullptr;
-          copy_async(into + k * 512, here ? from[k] + fc : static_cast<const void*>(P.g.counts),
-                     here ? 16 : 0);
+          copy_async(into + k * 512, here ? from[k] + fc : P.w[0], here ? 16 : 0);
         }
         into = next_place(into);
         if (++fc == pieces) {
