@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) __cluster_dims__(2, 1, 1)
   __shared__ TileTable tt;
   __shared__ Slot slots[kSlots];
   __shared__ Bars<kMxStages> b;
+  __shared__ unsigned long long filled[kMxStages];  // of the second CTA: its stage has its scales
   constexpr int kWords = kScaleWords<kFormat>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -124,7 +125,9 @@ __global__ void __launch_bounds__(kMxThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t ring = smem_addr(&b.empty[0]);
   constexpr int kTileF = kGated ? 128 : 256;  // features of the result per pair
   constexpr int kMyF = kTileF / 2;            // and per CTA
-  pair_begin(b, warp, 2 + 2 * kScaleWarps, kEpilogueWarps + kScaleWarps + 2 + (rank == 0 ? 1 : 0));
+  if (threadIdx.x == 0)
+    for (int s = 0; s < kMxStages; ++s) bar_init(smem_addr(&filled[s]), kScaleWarps);
+  pair_begin(b, warp, 2 + kScaleWarps + 1, kEpilogueWarps + kScaleWarps + 2 + (rank == 0 ? 1 : 0));
   chain();
   const int nf = (P.F + kTileF - 1) / kTileF;
   const bool good = build_groups(P.g, g);
@@ -219,13 +222,14 @@ __global__ void __launch_bounds__(kMxThreads, 1) __cluster_dims__(2, 1, 1)
       for (int kb = 0; kb < blocks; ++kb, ++it) {
         const unsigned s = it % kMxStages;
         if (!__all_sync(kAll, ready)) {
-          ok = __all_sync(kAll, bar_wait(smem_addr(&b.full[s]), (it / kMxStages) & 1));
+          ok = __all_sync(kAll, bar_wait_filled(smem_addr(&b.full[s]), (it / kMxStages) & 1));
           if (!ok) break;
         }
+        take_filled();  // (both CTAs' scales)
         fence_after_sync();
         // (the next stage is looked at while this one's products are issued)
         const unsigned next = (it + 1) % kMxStages;
-        ready = bar_test(smem_addr(&b.full[next]), ((it + 1) / kMxStages) & 1);
+        ready = bar_test_filled(smem_addr(&b.full[next]), ((it + 1) / kMxStages) & 1);
         // the stage's scales, in turn behind the one and the other tile's sums: a
         // column for every 32 rows, the features' words first
         const uint32_t sa = tmem + (it & 1) * kAccColumns + kMxColumns, sb = sa + 4 * kWords;
@@ -252,6 +256,20 @@ __global__ void __launch_bounds__(kMxThreads, 1) __cluster_dims__(2, 1, 1)
       if (ok) mma_commit(smem_addr(&b.acc_full[buf]), issuer);
     }
     if (!ok && lane == 0) note_error(P.g.status, A2AV_ERR_TIMEOUT);
+  } else if (warp == 1) {
+    // ------------------------------------ the second CTA's scales --
+    // passed on to the first CTA, whose products read them (by the scale warps themselves
+    // 131,072 rows of 4 bits take 1535 us, by this one 1502; without its fence 1490)
+    const uint32_t full0 = map_to(smem_addr(&b.full[0]), 0);
+    unsigned it = 0;
+    for (; ok && tile_of(i, pair, pairs) < tiles; ++i)
+      for (int kb = 0; kb < blocks; ++kb, ++it) {
+        const unsigned s = it % kMxStages;
+        ok = __all_sync(kAll, bar_wait(smem_addr(&filled[s]), (it / kMxStages) & 1));
+        if (!ok) break;
+        if (lane == 0) bar_pass_filled(full0 + s * 8);
+      }
+    if (!ok && lane == 0) note_error(P.g.status, A2AV_ERR_TIMEOUT);
   } else if (warp >= 4 + kEpilogueWarps) {
     // ------------------------------------------------------ scales --
     // a lane has rows lane, 32 + lane, 64 + lane and 96 + lane of the warp's 128;
@@ -259,7 +277,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) __cluster_dims__(2, 1, 1)
     // next tile's behind this one's (no further: a slot three tiles on is described
     // when this tile is done)
     const int part = warp - 4 - kEpilogueWarps;
-    const uint32_t full0 = map_to(smem_addr(&b.full[0]), 0);
+    const uint32_t into_bar = map_to(smem_addr(rank == 0 ? &b.full[0] : &filled[0]), rank);
     const uint32_t held = scales + kMxStages * kScaleBytes<kFormat> + kEpilogueWarps * kStaging +
                           part * kHeld + lane * 16;
     constexpr int kPer = 4 / kWords;  // stages that a piece lasts
@@ -358,7 +376,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) __cluster_dims__(2, 1, 1)
             fence_async_shared();
           }
           __syncwarp();
-          if (lane == 0) bar_arrive_filled(full0 + s * 8);
+          if (lane == 0) bar_arrive_filled(into_bar + s * 8);
           ++it;
         }
         out_of = next_place(out_of);

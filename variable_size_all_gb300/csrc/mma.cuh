@@ -78,11 +78,25 @@ __device__ __forceinline__ void bar_arrive_tx(uint32_t bar, unsigned bytes) {
                : "memory");
 }
 
-// The same for what threads of this CTA have written to its own shared memory, for
-// copies and tensor cores to read there (each after fence_async_shared): a release in
-// the CTA.  (One at the cluster's scope also waits for memory: 1.1 us for every stage.)
+// On a barrier of this CTA (a cluster address all the same), for what threads of this CTA
+// have written to its shared memory, for copies and tensor cores to read there (each
+// after fence_async_shared): a release in the CTA.
 __device__ __forceinline__ void bar_arrive_filled(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The same for the other CTA: on a barrier there, by a thread that has waited for this
+// CTA's, and taken by bar_wait_filled or bar_test_filled, then take_filled.  A release
+// at the cluster's scope, of shared memory alone: one of all memory also waits for what is on
+// its way there (1.1 us for every stage of the experts' products).
+__device__ __forceinline__ void bar_pass_filled(uint32_t bar) {
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void take_filled() {
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 
 // Whether a phase of a barrier of this CTA is complete (waits a little for it).
@@ -116,6 +130,37 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, unsigned parity) {
   if (bar_try(bar, parity)) return true;
   const long long start = clock64();
   while (!bar_try(bar, parity))
+    if (clock64() - start > kMmaWaitCycles) return false;
+  return true;
+}
+
+// The same at the cluster's scope, take_filled being what orders anything behind them.
+__device__ __forceinline__ bool bar_try_filled(uint32_t bar, unsigned parity) {
+  unsigned done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool bar_test_filled(uint32_t bar, unsigned parity) {
+  unsigned done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool bar_wait_filled(uint32_t bar, unsigned parity) {
+  if (bar_try_filled(bar, parity)) return true;
+  const long long start = clock64();
+  while (!bar_try_filled(bar, parity))
     if (clock64() - start > kMmaWaitCycles) return false;
   return true;
 }
