@@ -98,6 +98,10 @@ int64_t a2av_norm_workspace_bytes(int64_t features, int64_t total_rows);
  *   d_x = r * (g - s r^2 mean(g s)) + d_sums        (of x, and of the residual as well)
  *   d_weight = sum over all tokens of dy * s * r    (in 32 bits, in a fixed order)
  *
+ * A row of infinite length (see a2av_norm) has r = 0: its d_x is d_sums, NaN where s is not finite.
+ * Products g s are summed in 32 bits too: a row where that sum alone passes 2^128 gets
+ * infinities or NaN.
+ *
  *  sum_ptrs           s as the forward call kept it (x, without a residual).
  *  d_out_ptrs         HOST array of W: dy [tokens][H], of dtype.
  *  d_sum_ptrs         HOST array of W: what reaches s from elsewhere, or NULL (0).

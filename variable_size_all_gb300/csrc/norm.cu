@@ -499,7 +499,8 @@ __global__ void __maxnreg__(kThreads > 512 ? 64 : 128)
       ahead.next();
     }
     const float one = rsqrtf(fmaf(total[0], P.per_feature, P.eps));
-    const F scale = both(one), along = both(-one * one * (total[1] * P.per_feature));
+    // (1 / length^2 may not fit where the product does; of an infinite length nothing is left)
+    const F scale = both(one), along = both(one == 0.0f ? 0.0f : -one * (one * (total[1] * P.per_feature)));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int v = i0 + u * threads;
