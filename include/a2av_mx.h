@@ -63,6 +63,8 @@ int64_t a2av_mx_row_bytes(int64_t features, int format);
  * s, which is all that the backward pass needs.  A row of NaN or infinities
  * stays within its own results; squares are summed in 32 bits, so that a row whose
  * squares' sum passes 2^128 counts as one of infinite length (y = 0 where s is finite).
+ * Squares below 2^-126 keep fewer bits the smaller they are, and where all of a row's are 0
+ * (values below 2^-75) and eps is 0 as well, y is NaN.  Both are for eps to prevent.
  *
  *  features           H, 1 .. A2AV_MAX_NORM_FEATURES.
  *  dtype              a2av_dtype_t of x, residual, sums (and of y, with A2AV_PLAIN).

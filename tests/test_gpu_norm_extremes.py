@@ -1,5 +1,5 @@
-"""The norm and its gradients at the ends of their ranges: rows whose squares leave
-32 bits on either side."""
+"""The norm and its gradients at the ends of their ranges: infinite weights, rows
+whose squares leave 32 bits on either side."""
 import numpy as np
 import pytest
 import torch
@@ -42,6 +42,34 @@ def _norm_backward(s, w, dy, eps, ds=None):
 
 # a warp a row, a block a row, rows of no vectors, many rows (fetched ahead)
 SHAPES = [(5, 256), (3, 2048), (3, 1001), (1, 33), (5000, 512), (900, 7168)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_weights_without_end(shape, dtype):
+    """An infinite or NaN weight: the product's infinity (NaN for 0), in its own column;
+    its block of a packed row is NaN, the others are what they were."""
+    T, H = shape
+    rng = np.random.default_rng(H)
+    values = rng.standard_normal((T, H))
+    values[0, 3] = 0.0
+    x, w = _place(values, dtype), torch.from_numpy(1 + 0.3 * rng.standard_normal(H)).float().cuda()
+    odd = torch.tensor([0, 3, 5, H - 1], device="cuda")
+    bad = w.clone()
+    bad[odd] = torch.tensor([np.inf, np.inf, np.nan, -np.inf], device="cuda")
+    rest = torch.ones(H, dtype=torch.bool, device="cuda")
+    rest[odd] = False
+    clean, out = _norm(x, w, 1e-5), _norm(x, bad, 1e-5)
+    assert torch.equal(out[:, rest], clean[:, rest])
+    ref = mx.norm(moe.f64(x), moe.f64(bad), 1e-5)[:, odd.cpu().numpy()]
+    assert np.array_equal(moe.f64(out[:, odd]), ref, equal_nan=True)
+    for fmt in ("mxfp8", "mxfp4"):
+        plain = torch.empty_like(x)
+        a, b = _norm(x, w, 1e-5, fmt), _norm(x, bad, 1e-5, fmt, plain)
+        assert torch.equal(plain.nan_to_num(9), out.nan_to_num(9))
+        v, u = mx.unpack(a.cpu().numpy(), H, fmt)[0], mx.unpack(b.cpu().numpy(), H, fmt)[0]
+        lost = np.isin(np.arange(H) // 32, odd.cpu().numpy() // 32)
+        assert np.isnan(u[:, lost]).all() and np.array_equal(u[:, ~lost], v[:, ~lost])
 
 
 @pytest.mark.parametrize("more", [False, True])
@@ -94,3 +122,10 @@ def test_short_rows_without_eps(shape, dtype):
     moe.close(dx, d, 4 * mx.norm_error(H) * size, dtype, "d_x")
     moe.close(dw, terms.sum(0), (4 * mx.norm_error(H) + (T + 8) * 2.0 ** -24) * np.abs(terms).sum(0), "f32",
               "d_weight")
+
+
+def test_no_length_at_all():
+    """eps = 0 and rows whose squares are 0 in 32 bits."""
+    s = torch.zeros(3, 64, device="cuda")
+    s[1], s[2, 0] = 1e-30, -1e-30
+    assert _norm(s, torch.ones(64, device="cuda"), 0.0).isnan().all()

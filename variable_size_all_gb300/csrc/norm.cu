@@ -227,6 +227,15 @@ __device__ __forceinline__ Two lanes_sum(Two x, const int from) {
   return x;
 }
 
+// The weight that what a value's rounding left is multiplied by: an infinite one's largest
+// finite neighbour, so that the value's own product decides.
+__device__ __forceinline__ float2 finite(float2 w) {
+  float2 r;
+  asm("min.xorsign.abs.f32 %0, %1, 0f7F7FFFFF;" : "=f"(r.x) : "f"(w.x));
+  asm("min.xorsign.abs.f32 %0, %1, 0f7F7FFFFF;" : "=f"(r.y) : "f"(w.y));
+  return r;
+}
+
 // The sum of x over a warp, or over the block (`shared` as in row_sum).  A block's first
 // steps are between so many partial sums that their roundings average out.
 template <bool kWarp, int kThreads>
@@ -369,10 +378,24 @@ __global__ void __maxnreg__(kThreads > 512 ? 64 : !kAligned ? 72 : sizeof(T) == 
 #pragma unroll
         for (int i = 0; i < M; ++i) {
           const F a = mul2(f[i], high), rest = fma2(f[i], low, fma2(f[i], high, minus(a)));
-          f[i] = fma2(a, w[i], mul2(rest, w[i]));
+          f[i] = fma2(a, w[i], mul2(rest, kFormat == A2AV_PLAIN ? finite(w[i]) : w[i]));
         }
       }
+      const float top = kFormat == A2AV_PLAIN ? 0.0f : largest(f);
       if (plain) {
+        // (of a packed row's block nothing is left where a weight is infinite, so that the plain
+        // row alone is put right: finite() for every value cost 5 us of 533)
+        if (kFormat != A2AV_PLAIN && isnan(top)) {
+          F w[M], x[M];
+          take_weight<T, kAligned, kVectors>(w, P, v);
+          Q::unpack(s[u], x);
+#pragma unroll
+          for (int i = 0; i < M; ++i) {
+            const F y = mul2(mul2(x[i], high), w[i]);
+            if (isinf(y.x)) f[i].x = y.x;
+            if (isinf(y.y)) f[i].y = y.y;
+          }
+        }
         V y[1] = {Q::pack(f)};
         if constexpr (kSpread) Loose<T>::gather(y, place);
         give_row<T, kAligned>(out, y, v, 0, P.H);
@@ -396,7 +419,7 @@ __global__ void __maxnreg__(kThreads > 512 ? 64 : !kAligned ? 72 : sizeof(T) == 
           return any;
         };
         if (u * threads < np)
-          mx_store<kFormat, N>(packed, P.row.values, v, f, __float_as_uint(largest(f)), v < np, above);
+          mx_store<kFormat, N>(packed, P.row.values, v, f, __float_as_uint(top), v < np, above);
       }
     }
     if constexpr (kFormat != A2AV_PLAIN) {
