@@ -20,6 +20,8 @@
 #include "mma.cuh"
 #include "mx_device.cuh"
 
+#include <algorithm>
+
 namespace {
 
 struct NormParams {
@@ -984,7 +986,7 @@ int pack_call(a2av_handle* h, int64_t features, int dtype, int format, const voi
     return A2AV_ERR_INVALID_ARG;
   rc = current_device(h);
   if (rc != A2AV_OK) return rc;
-  if (P.first[h->W] == 0) return A2AV_OK;
+  if (P.first[h->W] == 0 && splits == nullptr) return A2AV_OK;  // (splits are checked all the same)
   P.W = h->W;
   P.D = (int)features;
   P.splits = reinterpret_cast<const long long*>(splits);
@@ -1000,7 +1002,7 @@ int pack_call(a2av_handle* h, int64_t features, int dtype, int format, const voi
   const long long vectors = (features * size + 15) / 16, warps = kPackThreads / 32;
   const long long slice = 32 * kPackVectors;
   const long long slices = (vectors + slice - 1) / slice;
-  const long long want = (P.first[h->W] * slices + warps - 1) / warps, most = (long long)fit * h->sms;
+  const long long want = std::max(1LL, (P.first[h->W] * slices + warps - 1) / warps), most = (long long)fit * h->sms;
   const cudaError_t e = launch_chained(kernel, dim3((unsigned)(want < most ? want : most)), kPackThreads, 0,
                                        static_cast<cudaStream_t>(stream), h->pdl, P);
   return e != cudaSuccess || cudaGetLastError() != cudaSuccess ? A2AV_ERR_CUDA : A2AV_OK;
