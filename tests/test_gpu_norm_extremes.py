@@ -1,5 +1,5 @@
 """The norm and its gradients at the ends of their ranges: infinite weights, rows
-whose squares leave 32 bits on either side."""
+whose squares leave 32 bits on either side, the largest eps."""
 import numpy as np
 import pytest
 import torch
@@ -129,3 +129,13 @@ def test_no_length_at_all():
     s = torch.zeros(3, 64, device="cuda")
     s[1], s[2, 0] = 1e-30, -1e-30
     assert _norm(s, torch.ones(64, device="cuda"), 0.0).isnan().all()
+
+
+def test_largest_eps():
+    eps = float(np.finfo(np.float32).max)
+    x, w = torch.randn(7, 96, device="cuda"), torch.ones(96, device="cuda")
+    y = mx.norm(moe.f64(x), moe.f64(w), eps)
+    moe.close(_norm(x, w, eps), y, mx.norm_error(96) * np.abs(y), "f32", "y")
+    dx, _ = _norm_backward(x, w, x, eps)
+    d, _, size = mx.norm_backward(moe.f64(x), moe.f64(w), moe.f64(x), eps)
+    moe.close(dx, d, 4 * mx.norm_error(96) * size, "f32", "d_x")

@@ -21,6 +21,7 @@
 #include "mx_device.cuh"
 
 #include <algorithm>
+#include <cfloat>
 
 namespace {
 
@@ -941,7 +942,7 @@ cudaError_t launch_norm(const a2av_handle* h, K kernel_of, NormForm f, int row_b
 int norm_ok(const a2av_handle* h, int64_t features, int dtype, float eps, const void* x,
             const int64_t* tokens, const float* weight, const void* out) {
   if (h == nullptr || x == nullptr || tokens == nullptr || weight == nullptr || out == nullptr ||
-      features < 1 || dtype_bytes(dtype) == 0 || !(eps >= 0.0f) || eps > 3.4e38f || !aligned_to(weight, 4))
+      features < 1 || dtype_bytes(dtype) == 0 || !(eps >= 0.0f) || eps > FLT_MAX || !aligned_to(weight, 4))
     return A2AV_ERR_INVALID_ARG;
   return features > A2AV_MAX_NORM_FEATURES ? A2AV_ERR_UNSUPPORTED : A2AV_OK;
 }
