@@ -59,9 +59,10 @@ int64_t a2av_mx_row_bytes(int64_t features, int format);
  *   s = x + residual, rounded to dtype and kept    (without residual: s = x)
  *   y = s / sqrt(mean(s^2) + eps) * weight
  *
- * y is rounded once, to dtype or to a packed row.  The norm is that of the rounded
- * s, which is all that the backward pass needs.  A row of NaN or infinities
- * stays within its own results; squares are summed in 32 bits, so that a row whose
+ * y is rounded from 32 bits, to dtype or to the codes of a packed row; the scale of a row's
+ * block goes by its largest value as it was before the rounding to 32 bits.  The norm is
+ * that of the rounded s, which is all that the backward pass needs.  A row of NaN or
+ * infinities stays within its own results; squares are summed in 32 bits, so that a row whose
  * squares' sum passes 2^128 counts as one of infinite length (y = 0 where s is finite).
  * Squares below 2^-126 keep fewer bits the smaller they are, and where all of a row's are 0
  * (values below 2^-75) and eps is 0 as well, y is NaN.  Both are for eps to prevent.

@@ -15,13 +15,14 @@
 // two tiles' sums, enough for the scales of one stage each.
 //
 // What it reaches: a decoding step's weights (256 rows for 64 gated experts, 7168 -> 2 x
-// 2048, 1 GB of 4 bits) in 157 to 165 us, 90 % of the copy rate, 552 in 16 bits; 131,072
-// Zipf-skewed rows of the same in 1.50 to 1.53 ms, 5.1 PFLOP/s (16 bits: 4.96 to 5.15 ms);
-// 16,384 skewed rows, 2048 -> 7168, of 8 bits 300 us (467 to 490).
+// 2048, 1 GB of 4 bits) in 162 to 167 us, 90 % of the copy rate, 552 in 16 bits; 131,072
+// Zipf-skewed rows of the same in 1.50 to 1.54 ms, 5.1 PFLOP/s (16 bits: 4.96 to 5.15 ms);
+// 16,384 skewed rows, 2048 -> 7168, of 8 bits 276 to 309 us (467 to 490).
 // What bounds it: shared memory.  A stage of 256 x 216 is written by the copies and
 // read by the products once, 60 KB a CTA, which at 128 bytes a cycle is 0.25 us, and its products
-// take 0.236 us at the tensor cores' 9.1 PFLOP/s (4 bits); it takes 0.32 to 0.34.  With parts
-// left out, of 360 us (4 bits, 32,768 rows, gated): the rows' copies cost 25 us, the
+// 0.27 us at 7.85 PFLOP/s (4 bits: four times the 16-bit rate measured, at which the tensor
+// cores would be busy throughout); it takes 0.32 to 0.34, with the tensor pipe busy 56 to 59 % of
+// the time.  With parts left out, of 360 us (4 bits, 32,768 rows, gated): the rows' copies cost 25 us, the
 // weights' 17, storing the scales 14, copying them to TMEM 14; four stages instead of five
 // 9.  A tile costs 1 to 1.5 us besides: its epilogue is not hidden behind fewer than some 14
 // stages (64 -> 2048, a stage a tile, writes its results at 2.3 TB/s).

@@ -4,7 +4,7 @@
 //
 // All are bound by memory: what a row has is read once and written once.  Of 65,536
 // rows of 7168 in bf16, at a copy rate of 6.68 TB/s: the norm with a residual, 8-bit results
-// 528 to 543 us (91 to 93 %); its gradients, 616 to 640 us (88 to 91 %); rows to 8 bits 214 us (99 %), 131,072
+// 529 to 543 us (91 to 93 %); its gradients, 618 to 640 us (88 to 91 %); rows to 8 bits 214 us (99 %), 131,072
 // of them back 467 us (91 %); 458,752 rows of 2048 to 4 bits and back 785 us (91 %).
 //
 // The norm: a block (a warp, for short rows) takes a row, holds it in registers
@@ -13,7 +13,10 @@
 // they are needed took 627 and 1441 us instead, cp.async by each thread 523 and 841, with two
 // registers of addresses for each array in every thread), and the weight is read from L1
 // for each row, because 32 registers less are a block more on an SM.  (A spill costs far more
-// than a block: its loads miss the little L1 that the rows leave, 1730 us.)
+// than a block: its loads miss the little L1 that the rows leave, 1730 us.  The gradients of
+// rows above 8192 features spill all the same where a block needs 1024 threads, which leaves each
+// 64 registers: f32, and rows that take no vectors.  8192 rows of 16,384 in f32 547 us, of
+// 16,383 708, of 16,383 in bf16 517; floors 321, 321 and 161.)
 //
 // Instructions count as well: values are multiplied in pairs, magnitudes of 16-bit rows
 // compared in pairs, ranks and slices followed without divisions.
